@@ -1,13 +1,23 @@
 """w4a16_decode_amd: INT4 group-wise RTN weight quantization and the fused
 W4A16 GEMV / skinny GEMM for AMD MI355X (gfx950), plus per-channel INT8
-weights with the W8A16 GEMV.
+weights with the W8A16 GEMV, and the attention side of a decoder layer on a paged
+INT4 KV cache.
 
 Every computation runs in the HIP kernels of ``libq4.so`` behind the C ABI
-declared in ``include/q4.h``, ``include/q8.h`` and ``include/q4_kv.h``; this package only marshals torch tensors
-(device memory, the current HIP stream) into those calls. There is no CPU
+declared under ``include/``; this package only marshals torch tensors (device
+memory, the current HIP stream) into those calls. There is no CPU
 fallback: without the built library or a GPU the calls raise.
 """
 
+from .attention import (  # noqa: F401
+    PagedKVCache4,
+    paged_kv_alloc,
+    paged_kv_append,
+    paged_kv_dequant,
+    qk_norm_rope,
+    qk_norm_rope_append,
+    rope_table,
+)
 from .ops import (  # noqa: F401
     ActOrderWeight,
     KVCache4,
@@ -53,5 +63,7 @@ __all__ = [
     "QuantizedWeight8", "q8_quantize_pack", "q8_gemm", "q8_gemm_config", "q8_to_canonical", "q8_from_canonical",
     "q8_packed_bytes", "q8_workspace_bytes",
     "ActOrderWeight", "actorder_perm", "quantize_pack_perm", "gemm_perm", "workspace_bytes_perm",
-    "KVCache4", "kv_cache_alloc", "kv_quantize_pack", "kv_dequant", "read_probe", "rtn_check",
+    "KVCache4", "kv_cache_alloc", "kv_quantize_pack", "kv_dequant",
+    "PagedKVCache4", "paged_kv_alloc", "paged_kv_append", "paged_kv_dequant", "rope_table", "qk_norm_rope",
+    "qk_norm_rope_append", "read_probe", "rtn_check",
 ]

@@ -50,6 +50,15 @@ SIGNATURES = {
     "q4_rtn_check": (ctypes.c_int, [_P, _P]),
     "q4_kv_quantize_pack": (ctypes.c_int, [_P, _I64, _I64, _I64, _I32, _P, _P, _I64, _I64, _P]),
     "q4_kv_dequant": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _I32, _I64, _I64, _P, _P]),
+    "q4_paged_codes_bytes": (_SZ, [_I64, _I32, _I32, _I32]),
+    "q4_paged_scales_count": (_SZ, [_I64, _I32, _I32, _I32, _I32]),
+    "q4_rope_table": (ctypes.c_int, [_I64, _I32, ctypes.c_double, _P, _P]),
+    "q4_qk_norm_rope": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _I32, _I32, _I32, _P, _P, ctypes.c_float, _P, _P, _I64,
+                                       _I32, _I32, _P, _I64, _P, _I64, _P]),
+    "q4_qk_norm_rope_append": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _I64, _I32, _P, _P, ctypes.c_float, _P, _P,
+                                              _I64, _I32, _I32, _P, _I64, _P, _P, _P]),
+    "q4_paged_kv_append": (ctypes.c_int, [_P, _I64, _P, _I64, _I64, _P, _P, _P]),
+    "q4_paged_kv_dequant": (ctypes.c_int, [_P, _P, _I64, _P, _P, _P]),
     "q8_packed_bytes": (_SZ, [_I64, _I64]),
     "q8_scales_count": (_SZ, [_I64]),
     "q8_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
@@ -59,6 +68,15 @@ SIGNATURES = {
     "q8_to_canonical": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _P]),
     "q8_from_canonical": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _P]),
 }
+
+
+
+class PagedKV(ctypes.Structure):
+    """q4_paged_kv (include/q4_attn.h)."""
+
+    _fields_ = [("k_codes", _P), ("k_scales", _P), ("v_codes", _P), ("v_scales", _P), ("pages", _I64),
+                ("page_size", _I32), ("kv_heads", _I32), ("head_dim", _I32), ("group", _I32)]
+
 
 _lib = None
 

@@ -16,13 +16,14 @@
 #include "../../include/q4.h"
 #include "../../include/q8.h"
 #include "../../include/q4_kv.h"
+#include "q4_check.h"
 #include "q4_internal.h"
 
+namespace q4 {
 namespace {
-
 thread_local char g_last_error[256] = "";
+}  // namespace
 
-q4_status fail(q4_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 q4_status fail(q4_status st, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -36,14 +37,24 @@ q4_status ok() {
   return Q4_OK;
 }
 
-constexpr int64_t kMaxDim = int64_t(1) << 30;
+q4_status hip_status(hipError_t e, const char* what) {
+  if (e != hipSuccess) return fail(Q4_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+  return ok();
+}
+}  // namespace q4
+
+namespace {
+
+using q4::aligned;
+using q4::fail;
+using q4::hip_status;
+using q4::kMaxDim;
+using q4::ok;
+using q4::round_up;
+
 static_assert(Q4_NOALLOC_SCRATCH_BYTES == q4::kNoAllocScratchBytes, "q4.h and the scratch array agree");
 
 bool group_ok(int32_t g) { return g == 32 || g == 64 || (g >= 128 && g % 128 == 0); }
-
-int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 struct Dims {
   int N, K, group, Np, Kp, Gp;
@@ -63,11 +74,6 @@ q4_status check_dims(int64_t out, int64_t in, int32_t group, Dims* d) {
   if ((int64_t)d->Np * d->Kp / 2 > (int64_t(1) << 40))
     return fail(Q4_ERR_SHAPE, "matrix too large");
   return Q4_OK;
-}
-
-q4_status hip_status(hipError_t e, const char* what) {
-  if (e != hipSuccess) return fail(Q4_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-  return ok();
 }
 
 // Launch shape for y = x W^T with B rows (the kernels are described at the top of
@@ -377,7 +383,7 @@ const char* q4_status_str(int status) {
   }
 }
 
-const char* q4_last_error(void) { return g_last_error; }
+const char* q4_last_error(void) { return q4::g_last_error; }
 
 #ifndef Q4_SOURCE_HASH
 #define Q4_SOURCE_HASH "unknown"

@@ -1,0 +1,178 @@
+// C ABI front end of the attention side (include/q4_attn.h): argument validation and
+// launch-shape selection on the host, before any HIP call.
+#include <algorithm>
+
+#include <hip/hip_runtime.h>
+
+#include "../../include/q4_attn.h"
+#include "q4_check.h"
+#include "q4_internal.h"
+
+using q4::aligned;
+using q4::fail;
+using q4::hip_status;
+using q4::kMaxDim;
+using q4::ok;
+
+namespace {
+
+q4_status check_paged_dims(int64_t pages, int32_t page_size, int32_t kv_heads, int32_t head_dim,
+                                  int32_t group) {
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return fail(Q4_ERR_UNSUPPORTED, "head_dim=%d: the paged cache takes 64, 128 or 256", (int)head_dim);
+  if (group != 32 && group != 64 && group != 128)
+    return fail(Q4_ERR_GROUP, "KV group %d unsupported (32, 64 or 128)", (int)group);
+  if (head_dim % group != 0)
+    return fail(Q4_ERR_GROUP, "head_dim=%d must be a multiple of group %d", (int)head_dim, (int)group);
+  if (pages <= 0 || pages >= kMaxDim || kv_heads <= 0 || kv_heads > 65535)
+    return fail(Q4_ERR_SHAPE, "pages=%lld, kv_heads=%d out of range", (long long)pages, (int)kv_heads);
+  if (page_size <= 0 || page_size % 16 != 0)
+    return fail(Q4_ERR_SHAPE, "page_size=%d must be a positive multiple of 16", (int)page_size);
+  if (pages * page_size >= (int64_t(1) << 31))
+    return fail(Q4_ERR_SHAPE, "pages * page_size = %lld must be below 2^31", (long long)(pages * page_size));
+  return Q4_OK;
+}
+
+q4_status check_paged(const q4_paged_kv* cache, q4::PagedArgs* c) {
+  if (!cache) return fail(Q4_ERR_NULL, "cache must be non-NULL");
+  q4_status st = check_paged_dims(cache->pages, cache->page_size, cache->kv_heads, cache->head_dim, cache->group);
+  if (st != Q4_OK) return st;
+  if (!cache->k_codes || !cache->k_scales || !cache->v_codes || !cache->v_scales)
+    return fail(Q4_ERR_NULL, "the cache's k_codes, k_scales, v_codes, v_scales must be non-NULL");
+  if (!aligned(cache->k_codes, 16) || !aligned(cache->v_codes, 16) || !aligned(cache->k_scales, 8) ||
+      !aligned(cache->v_scales, 8))
+    return fail(Q4_ERR_ALIGN, "the cache's codes need 16-byte, its scales 8-byte alignment");
+  *c = q4::PagedArgs{cache->k_codes, cache->k_scales, cache->v_codes,  cache->v_scales, cache->pages,
+                     cache->page_size, cache->kv_heads, cache->head_dim, cache->group};
+  return Q4_OK;
+}
+
+// A [tokens][heads][head_dim] operand: strides cover a row and keep 16-byte rows.
+q4_status check_rows(const char* name, const void* p, int64_t stride, int64_t heads, int64_t head_dim) {
+  if (!p) return fail(Q4_ERR_NULL, "%s must be non-NULL", name);
+  if (stride < heads * head_dim || stride >= (int64_t(1) << 40))
+    return fail(Q4_ERR_SHAPE, "%s: stride %lld is not in [heads * head_dim = %lld, 2^40)", name, (long long)stride,
+                (long long)(heads * head_dim));
+  if (stride % 8 != 0 || !aligned(p, 16))
+    return fail(Q4_ERR_ALIGN, "%s needs 16-byte alignment and a stride that is a multiple of 8", name);
+  return Q4_OK;
+}
+
+// Checks and launch shared by the norm / rotation entry points; a.cache.head_dim etc.
+// are set where a.append.
+q4_status rope_common(q4::RopeArgs& a, void* stream) {
+  if (a.tokens < 0 || a.tokens >= kMaxDim) return fail(Q4_ERR_SHAPE, "tokens=%lld out of range", (long long)a.tokens);
+  if (a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256)
+    return fail(Q4_ERR_UNSUPPORTED, "head_dim=%d unsupported (64, 128 or 256)", a.head_dim);
+  if (a.q_heads < 0 || a.kv_heads < 0 || a.q_heads > 65535 || a.kv_heads > 65535)
+    return fail(Q4_ERR_SHAPE, "q_heads=%d, kv_heads=%d out of range", a.q_heads, a.kv_heads);
+  if (!a.table) a.rot = 0;
+  if (a.rot < 0 || a.rot > a.head_dim || a.rot % 16 != 0)
+    return fail(Q4_ERR_UNSUPPORTED, "rot_dim=%d must be a multiple of 16 in [0, head_dim]", a.rot);
+  if (a.rot > 0 && (a.table_positions <= 0 || a.table_positions >= kMaxDim))
+    return fail(Q4_ERR_SHAPE, "table_positions=%lld out of range", (long long)a.table_positions);
+  if ((a.q_weight || a.k_weight) && !(a.eps >= 0.0f && a.eps <= 3.0e38f))
+    return fail(Q4_ERR_SHAPE, "eps must be a finite number >= 0");
+  if (a.tokens == 0 || (a.q_heads == 0 && a.kv_heads == 0)) return ok();
+  q4_status st;
+  if (a.q_heads > 0) {
+    if ((st = check_rows("q", a.q, a.q_stride, a.q_heads, a.head_dim)) != Q4_OK) return st;
+    if ((st = check_rows("q_out", a.q_out, a.q_out_stride, a.q_heads, a.head_dim)) != Q4_OK) return st;
+  }
+  if (a.kv_heads > 0) {
+    if ((st = check_rows("k", a.k, a.k_stride, a.kv_heads, a.head_dim)) != Q4_OK) return st;
+    if (a.append) {
+      if ((st = check_rows("v", a.v, a.v_stride, a.kv_heads, a.head_dim)) != Q4_OK) return st;
+    } else if ((st = check_rows("k_out", a.k_out, a.k_out_stride, a.kv_heads, a.head_dim)) != Q4_OK) {
+      return st;
+    }
+  }
+  if (a.append && !a.slots) return fail(Q4_ERR_NULL, "slots must be non-NULL");
+  if (a.rot > 0 && !a.positions) return fail(Q4_ERR_NULL, "positions must be non-NULL");
+  if ((a.q_weight && !aligned(a.q_weight, 16)) || (a.k_weight && !aligned(a.k_weight, 16)) ||
+      (a.rot > 0 && (!aligned(a.table, 16) || !aligned(a.positions, 4))) || (a.append && !aligned(a.slots, 4)))
+    return fail(Q4_ERR_ALIGN, "weights and table need 16-byte, positions and slots 4-byte alignment");
+  return hip_status(q4::launch_rope(a, static_cast<hipStream_t>(stream)), "norm and rotation launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t q4_paged_codes_bytes(int64_t pages, int32_t page_size, int32_t kv_heads, int32_t head_dim) {
+  if (check_paged_dims(pages, page_size, kv_heads, head_dim, 32) != Q4_OK) return 0;
+  return (size_t)pages * page_size * kv_heads * (head_dim / 2);
+}
+
+size_t q4_paged_scales_count(int64_t pages, int32_t page_size, int32_t kv_heads, int32_t head_dim, int32_t group) {
+  if (check_paged_dims(pages, page_size, kv_heads, head_dim, group) != Q4_OK) return 0;
+  return (size_t)pages * page_size * kv_heads * (head_dim / group);
+}
+
+q4_status q4_rope_table(int64_t positions, int32_t rot_dim, double theta, float* table, void* stream) {
+  if (positions < 0 || positions >= kMaxDim) return fail(Q4_ERR_SHAPE, "positions=%lld out of range", (long long)positions);
+  if (rot_dim <= 0 || rot_dim % 16 != 0 || rot_dim > 256)
+    return fail(Q4_ERR_UNSUPPORTED, "rot_dim=%d must be a multiple of 16 in [16, 256]", (int)rot_dim);
+  if (!(theta > 0.0) || theta > 1e300) return fail(Q4_ERR_SHAPE, "theta must be positive and finite");
+  if (positions == 0) return ok();
+  if (!table) return fail(Q4_ERR_NULL, "table must be non-NULL");
+  if (!aligned(table, 16)) return fail(Q4_ERR_ALIGN, "table needs 16-byte alignment");
+  return hip_status(q4::launch_rope_table(positions, rot_dim, theta, table, static_cast<hipStream_t>(stream)),
+                    "rope table launch");
+}
+
+q4_status q4_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int64_t tokens,
+                          int32_t q_heads, int32_t kv_heads, int32_t head_dim, const void* q_weight,
+                          const void* k_weight, float eps, const int32_t* positions, const float* table,
+                          int64_t table_positions, int32_t rot_dim, int32_t interleaved, void* q_out,
+                          int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream) {
+  q4::RopeArgs a{};
+  a.q = q, a.k = k, a.q_stride = q_stride, a.k_stride = k_stride;
+  a.tokens = tokens, a.q_heads = q_heads, a.kv_heads = kv_heads, a.head_dim = head_dim;
+  a.q_weight = q_weight, a.k_weight = k_weight, a.eps = eps;
+  a.positions = positions, a.table = table, a.table_positions = table_positions, a.rot = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.q_out = q_out, a.k_out = k_out, a.q_out_stride = q_out_stride, a.k_out_stride = k_out_stride;
+  return rope_common(a, stream);
+}
+
+q4_status q4_qk_norm_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                 int64_t v_stride, int64_t tokens, int32_t q_heads, const void* q_weight,
+                                 const void* k_weight, float eps, const int32_t* positions, const float* table,
+                                 int64_t table_positions, int32_t rot_dim, int32_t interleaved, void* q_out,
+                                 int64_t q_out_stride, const q4_paged_kv* cache, const int32_t* slots,
+                                 void* stream) {
+  q4::RopeArgs a{};
+  q4_status st = check_paged(cache, &a.cache);
+  if (st != Q4_OK) return st;
+  a.q = q, a.k = k, a.v = v, a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+  a.tokens = tokens, a.q_heads = q_heads, a.kv_heads = a.cache.kv_heads, a.head_dim = a.cache.head_dim;
+  a.q_weight = q_weight, a.k_weight = k_weight, a.eps = eps;
+  a.positions = positions, a.table = table, a.table_positions = table_positions, a.rot = rot_dim;
+  a.interleaved = interleaved != 0;
+  a.q_out = q_out, a.q_out_stride = q_out_stride;
+  a.append = true, a.slots = slots;
+  return rope_common(a, stream);
+}
+
+q4_status q4_paged_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t tokens,
+                             const q4_paged_kv* cache, const int32_t* slots, void* stream) {
+  return q4_qk_norm_rope_append(nullptr, 0, k, k_stride, v, v_stride, tokens, 0, nullptr, nullptr, 0.0f, nullptr,
+                                nullptr, 0, 0, 0, nullptr, 0, cache, slots, stream);
+}
+
+q4_status q4_paged_kv_dequant(const q4_paged_kv* cache, const int32_t* slots, int64_t tokens, void* k_out,
+                              void* v_out, void* stream) {
+  q4::PagedArgs c;
+  q4_status st = check_paged(cache, &c);
+  if (st != Q4_OK) return st;
+  if (tokens < 0 || tokens >= kMaxDim) return fail(Q4_ERR_SHAPE, "tokens=%lld out of range", (long long)tokens);
+  if (tokens == 0) return ok();
+  if (!slots || !k_out || !v_out) return fail(Q4_ERR_NULL, "slots, k_out, v_out must be non-NULL");
+  if (!aligned(slots, 4) || !aligned(k_out, 16) || !aligned(v_out, 16))
+    return fail(Q4_ERR_ALIGN, "slots need 4-byte, k_out and v_out 16-byte alignment");
+  return hip_status(q4::launch_paged_dequant(c, slots, tokens, k_out, v_out, static_cast<hipStream_t>(stream)),
+                    "paged dequant launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,22 @@
+// Argument checks and error reporting shared by the C ABI front ends (q4_api.cpp,
+// q4_attn_api.cpp). Host code only.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/q4.h"
+
+namespace q4 {
+
+constexpr int64_t kMaxDim = int64_t(1) << 30;
+
+// Record the calling thread's last error and return its status; ok() clears it.
+q4_status fail(q4_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+q4_status ok();
+q4_status hip_status(hipError_t e, const char* what);
+
+inline int64_t round_up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+}  // namespace q4

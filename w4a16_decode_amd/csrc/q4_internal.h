@@ -77,6 +77,44 @@ struct KvArgs {
   void* dst;
 };
 
+// Paged INT4 KV cache (include/q4_attn.h).
+struct PagedArgs {
+  void* k_codes;
+  void* k_scales;
+  void* v_codes;
+  void* v_scales;
+  int64_t pages;
+  int page_size, kv_heads, head_dim, group;
+};
+
+// Norm and rotation of q and k rows; with `append` k and v go into the cache's slots.
+struct RopeArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;  // elements from token to token
+  int64_t tokens;
+  int q_heads, kv_heads, head_dim;
+  const void* q_weight;  // NULL: no norm
+  const void* k_weight;
+  float eps;
+  const int32_t* positions;
+  const float* table;
+  int64_t table_positions;
+  int rot;  // 0: no rotation
+  bool interleaved;
+  void* q_out;
+  void* k_out;
+  int64_t q_out_stride, k_out_stride;
+  bool append;
+  PagedArgs cache;
+  const int32_t* slots;
+};
+
+hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
+hipError_t launch_paged_dequant(const PagedArgs& c, const int32_t* slots, int64_t tokens, void* k_out, void* v_out,
+                                hipStream_t stream);
+hipError_t launch_rope_table(int64_t positions, int rot, double theta, float* table, hipStream_t stream);
 hipError_t launch_kv_quantize(const KvArgs& a, hipStream_t stream);
 // Read `pieces` x 8 KiB from buf with one workgroup of 4 wavefronts per CU.
 hipError_t launch_read_probe(const void* buf, int64_t pieces, void* sink, int cus, hipStream_t stream);
