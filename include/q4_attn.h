@@ -108,6 +108,36 @@ q4_status q4_paged_kv_append(const void* k, int64_t k_stride, const void* v, int
 q4_status q4_paged_kv_dequant(const q4_paged_kv* cache, const int32_t* slots, int64_t tokens, void* k_out,
                               void* v_out, void* stream);
 
+/* Attention of each sequence's newest tokens over its pages, causal:
+ *   o = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q . k_t),
+ * k and v the cache's code * scale unrounded. Rows q_offsets[n] .. q_offsets[n + 1] - 1
+ * of q are sequence n's, the last of its kv_lens[n] tokens, whose k and v are in the
+ * cache already: row i of n_q sees the keys t <= p = kv_lens[n] - n_q + i, and with
+ * window > 0 only those with t > p - window. A decode step has one row a sequence, a
+ * chunk of a prompt many; both may be mixed in a call. Token t of sequence n lies in
+ * page block_table[n][t / page_size]; entries behind the length are not read. Pages may
+ * be shared between sequences.
+ *   q: float16 [tokens][q_heads][head_dim], q_stride elements from token to token;
+ *   out: the same shape, contiguous, 8-byte aligned; block_table: int32 [seqs]
+ *   [max_blocks]; q_offsets: int32 [seqs + 1], ascending; kv_lens: int32 [seqs].
+ *   max_q and max_kv bound the rows and the length of every sequence; they size the
+ *   launch and the workspace, so a captured graph serves any lengths up to them.
+ * A row that sees no key (an empty sequence, a row ahead of its sequence's start) is
+ * zero. Rows of no sequence are left as they were. Lengths, offsets and rows beyond
+ * the bounds are cut to them, and the keys of a page number outside [0, pages) count as
+ * hidden, so no contents of these arrays lead outside the buffers. q . k and the
+ * softmax are held in float32, the weights rounded to float16 with the V scale in
+ * them before they meet the codes, out rounded once. The result does not depend on
+ * timing: partial results of a split context are joined in a fixed order.
+ * `workspace` (16-byte aligned) must hold q4_paged_attention_workspace_bytes() bytes
+ * (NULL when that is 0, else Q4_ERR_WORKSPACE); contents as q4_gemm's. */
+size_t q4_paged_attention_workspace_bytes(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv,
+                                          int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t window);
+q4_status q4_paged_attention(const void* q, int64_t q_stride, const q4_paged_kv* cache, const int32_t* block_table,
+                             int64_t max_blocks, const int32_t* q_offsets, const int32_t* kv_lens, int64_t seqs,
+                             int64_t tokens, int64_t max_q, int64_t max_kv, int32_t q_heads, float scale,
+                             int64_t window, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

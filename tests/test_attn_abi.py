@@ -125,3 +125,18 @@ def test_oracle_attention_closed_forms():
     assert np.allclose(y[0], 3) and np.allclose(y[1], 4)
     y = oracle.paged.attention(q, [k[0][:1]], [v[0][:1]], [1], [0, 2], 1.0)
     assert np.all(y[0] == 0) and np.allclose(y[1], 0)
+
+
+def test_attention_refusals(lib):
+    def f(q=FAKE, qs=1024, cache=None, tab=FAKE, mb=4, off=FAKE, lens=FAKE, seqs=2, n=3, mq=2, mkv=100, hq=8, scale=0.1,
+          window=0, out=FAKE, ws=FAKE, wsb=1 << 30):
+        return lib.q4_paged_attention(q, qs, cache or _cache(), tab, mb, off, lens, seqs, n, mq, mkv, hq, scale, window,
+                                      out, ws, wsb, None)
+
+    assert f(q=None) == 1 and f(tab=None) == 1 and f(off=None) == 1 and f(lens=None) == 1 and f(out=None) == 1
+    assert f(hq=7) == 2 and f(hq=0) == 2 and f(seqs=-1) == 2 and f(n=-1) == 2 and f(mq=-1) == 2 and f(mkv=-1) == 2
+    assert f(window=-1) == 2 and f(scale=float("inf")) == 2 and f(mb=-1) == 2
+    assert f(seqs=1 << 25, n=1 << 28, mq=1 << 20) == 2
+    assert f(qs=1000) == 2 and f(qs=1028) == 4 and f(q=FAKE + 8) == 4 and f(out=FAKE + 4) == 4 and f(off=FAKE + 2) == 4
+    assert f(cache=_cache(page_size=20)) == 2 and f(cache=_cache(codes=None)) == 1
+    assert f(seqs=0, q=None) == 0 and f(n=0, q=None) == 0 and f(mq=0, q=None) == 0

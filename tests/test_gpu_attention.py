@@ -1,0 +1,275 @@
+"""Attention over the paged INT4 cache against the oracle in float64.
+
+Bound of an output's error, from the arithmetic. With A = sum_t p_t |v_t| (p the exact
+softmax), Z = max_t sum_c |q_c k_tc| * scale:
+ - each weight, times its V scale, is rounded to float16: 2^-11 A;
+ - a score is a float32 dot product of D / 32 matrix steps plus the scaling, the
+   subtraction of the maximum and the exponential: (D / 32 + 8) roundings of 2^-23
+   relative to Z + 1, which changes a weight by that much of itself, and the sum of
+   the weights by no more: 2 (D / 32 + 8) 2^-23 (Z + 1) A;
+ - float32 sums over n keys in steps of 32 and up to a few hundred joins: (n / 32 + 32)
+   2^-24 A twice;
+ - the result is rounded to float16: 2^-11 |o| (subnormal: 2^-25).
+"""
+
+import numpy as np
+import pytest
+
+import oracle
+from gpu_util import say, to_gpu, to_np
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def q4():
+    import torch
+
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import w4a16_decode_amd as q4mod
+
+    say("libq4", q4mod.version())
+    return q4mod
+
+
+class Batch:
+    """Sequences with their keys in a paged cache; every slot that no length covers, and
+    every unused page, holds random codes and NaN scales."""
+
+    def __init__(self, q4, lens, news, hq, hkv, d, g, page, seed=0, spread=1.0, extra_rows=0, v_scale=1.0):
+        import torch
+
+        r = np.random.default_rng(seed)
+        self.q4, self.lens, self.page, self.d = q4, list(lens), page, d
+        self.offsets = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+        blocks = max(1, max(-(-n // page) for n in lens))
+        pages = len(lens) * blocks + 3
+        self.table = r.permutation(pages)[:len(lens) * blocks].reshape(len(lens), blocks).astype(np.int32)
+        rows = int(self.offsets[-1]) + extra_rows
+        self.q = (spread * r.standard_normal((rows, hq, d))).astype(np.float16)
+        self.cache = q4.paged_kv_alloc(pages, page, hkv, d, g)
+        for t in (self.cache.k_codes, self.cache.v_codes):
+            t.copy_(torch.randint(0, 256, t.shape, dtype=torch.uint8))
+        for t in (self.cache.k_scales, self.cache.v_scales):
+            t.fill_(float("nan"))
+        self.k, self.v, self.k16, self.v16 = [], [], [], []
+        for n, length in enumerate(lens):
+            k16 = (r.standard_normal((length, hkv, d)) * np.exp(0.4 * r.standard_normal((1, hkv, d)))).astype(np.float16)
+            v16 = (v_scale * r.standard_normal((length, hkv, d))).astype(np.float16)
+            self.k16.append(k16), self.v16.append(v16)
+            self.k.append(oracle.paged.store(k16, g)[2] if length else np.zeros((0, hkv, d)))
+            self.v.append(oracle.paged.store(v16, g)[2] if length else np.zeros((0, hkv, d)))
+            if length:
+                self.put(n, k16, v16)
+
+    def slots(self, n, length):
+        t = np.arange(length)
+        return (self.table[n][t // self.page] * self.page + t % self.page).astype(np.int32)
+
+    def put(self, n, k16, v16):
+        self.q4.paged_kv_append(to_gpu(k16), to_gpu(v16), self.cache, to_gpu(self.slots(n, len(k16))))
+
+    def run(self, window=0, scale=None, table=None, **kw):
+        news = np.diff(self.offsets)
+        args = dict(max_q=int(news.max()), max_kv=max(self.lens))
+        args.update(kw)
+        q = args.pop("q", None)
+        out = self.q4.paged_attention(to_gpu(self.q) if q is None else q, self.cache,
+                                      to_gpu(self.table if table is None else table), to_gpu(self.offsets),
+                                      to_gpu(np.array(self.lens, np.int32)), window=window, scale=scale, **args)
+        return out
+
+    def check(self, got, window=0, scale=None, what="", rows=None, ref=None):
+        s = self.d ** -0.5 if scale is None else scale
+        got = to_np(got).astype(np.float64)
+        worst = 0.0
+        for n, length in enumerate(self.lens):
+            a, b = self.offsets[n], self.offsets[n + 1]
+            if a == b:
+                continue
+            share = self.q.shape[1] // self.k[n].shape[1]
+            off = [0, b - a]
+            ref = oracle.paged.attention(self.q[a:b], [self.k[n]], [self.v[n]], [length], off, s, window)
+            mag = oracle.paged.attention(self.q[a:b], [self.k[n]], [np.abs(self.v[n])], [length], off, s, window)
+            z = 1.0
+            if length:
+                kk = np.abs(self.k[n]).max(axis=0)
+                z += np.abs(s) * (np.abs(self.q[a:b].astype(np.float64)) * np.repeat(kk, share, axis=0)).sum(-1).max()
+            rel = 2.0 ** -11 + 2 * (self.d / 32 + 8) * 2.0 ** -23 * z + 2 * (length / 32 + 32) * 2.0 ** -24
+            bound = rel * mag + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25
+            err = np.abs(got[a:b] - ref)
+            assert np.all(np.isfinite(got[a:b])), (what, n)
+            assert np.all(err <= bound), (what, n, length, (err / bound).max())
+            worst = max(worst, (err / bound).max())
+        return worst
+
+
+SHAPES = [  # hq, hkv, d, g, page
+    (8, 1, 128, 128, 16),
+    (4, 4, 64, 64, 16),
+    (14, 2, 128, 64, 48),
+    (6, 2, 256, 128, 32),
+    (16, 2, 64, 32, 64),
+    (8, 1, 128, 32, 32),
+    (3, 1, 256, 32, 16),
+    (20, 1, 256, 64, 16),
+]
+
+
+@pytest.mark.parametrize("hq,hkv,d,g,page", SHAPES)
+def test_decode(q4, hq, hkv, d, g, page):
+    """One row a sequence, lengths around every tile, step and page border."""
+    say("decode", hq, hkv, d, g, page)
+    lens = [1, 2, 15, 16, 17, 31, 32, 33, 47, 48, 49, 63, 64, 65, 200, 1000]
+    b = Batch(q4, lens, [1] * len(lens), hq, hkv, d, g, page, seed=d + g)
+    say("  worst share of the bound", b.check(b.run()))
+    say("  window 16", b.check(b.run(window=16), window=16))
+
+
+@pytest.mark.parametrize("hq,hkv,d,g,page", SHAPES)
+def test_chunks(q4, hq, hkv, d, g, page):
+    """Prompts, chunks over a context, single rows, and sequences without rows, in one call."""
+    say("chunks", hq, hkv, d, g, page)
+    lens, news = [40, 300, 77, 5, 130, 64, 97], [40, 33, 1, 0, 129, 2, 64]
+    b = Batch(q4, lens, news, hq, hkv, d, g, page, seed=d + g + 1)
+    say("  worst share of the bound", b.check(b.run()))
+    say("  window 33", b.check(b.run(window=33), window=33))
+    say("  window 1", b.check(b.run(window=1), window=1))
+
+
+@pytest.mark.parametrize("new", [1, 3, 70])
+def test_long_context(q4, new):
+    b = Batch(q4, [9001, 4500], [new, new], 8, 2, 128, 128, 32, seed=new)
+    say("long context", new, b.check(b.run()))
+    say("  bounds larger than the lengths", b.check(b.run(max_q=new + 5, max_kv=20000)))
+
+
+def test_large_scores_and_small_values(q4):
+    """A softmax close to one-hot, and V scales among float16's subnormals: the weights
+    keep their precision."""
+    b = Batch(q4, [500, 70], [4, 4], 8, 2, 128, 64, 16, seed=5, spread=30.0)
+    say("sharp", b.check(b.run()))
+    b = Batch(q4, [700], [3], 8, 2, 128, 128, 16, seed=6, v_scale=2.0 ** -13)
+    say("small v", b.check(b.run()))
+    b = Batch(q4, [700], [3], 8, 2, 128, 128, 16, seed=6, v_scale=4000.0)
+    say("large v", b.check(b.run()))
+    b = Batch(q4, [300], [3], 8, 2, 128, 128, 16, seed=7)
+    say("negative scale", b.check(b.run(scale=-0.3), scale=-0.3))
+    b.check(b.run(scale=0.0), scale=0.0)
+
+
+def test_rows_that_see_nothing_and_rows_of_no_sequence(q4):
+    """Empty sequences and rows ahead of a sequence's start are zero; rows behind the last
+    sequence keep their contents."""
+    import torch
+
+    b = Batch(q4, [0, 3, 20], [2, 8, 1], 8, 2, 128, 128, 16, seed=8, extra_rows=5)
+    out = torch.full((16, 8, 128), 3.0, dtype=torch.float16, device="cuda")
+    b.run(out=out)
+    b.check(out)
+    got = to_np(out)
+    assert not got[:2].any() and not got[2:7].any()          # length 0; rows ahead of a length of 3
+    assert np.all(got[11:] == 3.0)
+    b = Batch(q4, [0, 0], [1, 1], 8, 2, 128, 128, 16, seed=9)
+    assert not to_np(b.run()).any()
+    assert not to_np(b.run(max_kv=64)).any()
+
+
+def test_hidden_infinities(q4):
+    """A new token's K and V hold infinities (their groups' scales are infinite): rows that do not
+    see it are as without it, in the same tile too."""
+    b = Batch(q4, [40], [10], 8, 2, 128, 128, 16, seed=10)
+    clean = to_np(b.run())
+    k16, v16 = b.k16[0].copy(), b.v16[0].copy()
+    k16[36:, :, 3] = np.inf
+    v16[36:, :, 5] = -np.inf
+    b.put(0, k16, v16)
+    got = to_np(b.run())
+    assert np.array_equal(got[:6].view(np.uint16), clean[:6].view(np.uint16))
+    assert not np.isfinite(got[6:]).any()
+
+
+def test_pages_outside_the_cache(q4):
+    """Keys of a bad page number are hidden; entries behind the length may hold anything."""
+    b = Batch(q4, [100, 40], [2, 1], 8, 2, 128, 64, 16, seed=11)
+    table = b.table.copy()
+    table[1, 3:] = [-7, 2 ** 31 - 1, b.cache.pages, -1][:table.shape[1] - 3]
+    assert np.array_equal(to_np(b.run(table=table)), to_np(b.run()))
+    table[0, 2] = b.cache.pages
+    table[0, 4] = -1
+    got = b.run(table=table)
+    keep = np.array([t for t in range(100) if t // 16 not in (2, 4)])
+    c = Batch(q4, [100], [2], 8, 2, 128, 64, 16, seed=11)
+    for i in range(2):          # row i of the two newest tokens: neither sits on a bad page
+        seen = keep[keep <= 98 + i]
+        c.lens, c.offsets, c.q = [len(seen)], np.array([0, 1]), b.q[i:i + 1]
+        c.k, c.v = [b.k[0][seen]], [b.v[0][seen]]
+        c.check(got[i:i + 1], what="bad page")
+
+
+def test_lengths_cut_to_the_bounds(q4):
+    """Lengths beyond max_kv or the table, offsets beyond the rows: cut, in bounds."""
+    import torch
+
+    b = Batch(q4, [48, 48], [1, 1], 8, 2, 128, 128, 16, seed=12)
+    lens = to_gpu(np.array([48, 2 ** 31 - 1], np.int32))
+    args = (to_gpu(b.q), b.cache, to_gpu(b.table))
+    got = q4.paged_attention(*args, to_gpu(b.offsets), lens, 1, 48)
+    assert torch.equal(got, b.run())
+    got = q4.paged_attention(*args, to_gpu(b.offsets), to_gpu(np.array([48, -3], np.int32)), 1, 48)
+    assert torch.equal(got[0], b.run()[0]) and not got[1].any()
+    out = torch.full((2, 8, 128), 5.0, dtype=torch.float16, device="cuda")
+    q4.paged_attention(*args, to_gpu(np.array([0, 2 ** 31 - 1, -4], np.int32)), lens, 2, 48, out=out)
+    torch.cuda.synchronize()
+
+
+def test_shared_pages_strided_queries_and_order(q4):
+    """Two sequences on the same pages; q as slices of fused rows; batch order does not matter."""
+    import torch
+
+    b = Batch(q4, [150, 90], [1, 30], 8, 2, 128, 128, 16, seed=13)
+    ref = b.run()
+    wide = torch.zeros((31, 12, 128), dtype=torch.float16, device="cuda")
+    wide[:, :8] = to_gpu(b.q)
+    assert torch.equal(b.run(q=wide[:, :8]), ref)
+    twice = q4.paged_attention(to_gpu(np.concatenate([b.q[:1], b.q[:1]])), b.cache, to_gpu(b.table[[0, 0]]),
+                               to_gpu(np.array([0, 1, 2], np.int32)), to_gpu(np.array([150, 150], np.int32)), 1, 150)
+    assert torch.equal(twice[0], twice[1])
+    assert torch.equal(b.run(), ref)                          # the same bits again
+
+
+def test_empty_calls(q4):
+    import torch
+
+    b = Batch(q4, [20], [1], 8, 2, 128, 128, 16, seed=14)
+    e = torch.zeros((0, 8, 128), dtype=torch.float16, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    assert q4.paged_attention(e, b.cache, torch.zeros((0, 4), **i32), torch.zeros(1, **i32), torch.zeros(0, **i32), 1,
+                              8).shape == (0, 8, 128)
+    out = torch.full((1, 8, 128), 2.0, dtype=torch.float16, device="cuda")
+    q4.paged_attention(to_gpu(b.q), b.cache, torch.zeros((1, 0), **i32), to_gpu(b.offsets), torch.zeros(1, **i32), 1, 0,
+                       out=out)
+    assert not out.any()
+
+
+def test_refusals(q4):
+    import torch
+
+    b = Batch(q4, [20], [1], 8, 2, 128, 128, 16, seed=15)
+    q, tab, off, lens = to_gpu(b.q), to_gpu(b.table), to_gpu(b.offsets), to_gpu(np.array([20], np.int32))
+    with pytest.raises(TypeError):
+        q4.paged_attention(q.float(), b.cache, tab, off, lens, 1, 20)
+    with pytest.raises(ValueError):
+        q4.paged_attention(q[..., :64], b.cache, tab, off, lens, 1, 20)
+    with pytest.raises(TypeError):
+        q4.paged_attention(q, b.cache, tab.long(), off, lens, 1, 20)
+    with pytest.raises(ValueError):
+        q4.paged_attention(q, b.cache, tab, off[:1], lens, 1, 20)
+    with pytest.raises(q4.Q4Error):
+        q4.paged_attention(q[:, :7], b.cache, tab, off, lens, 1, 20)          # 7 heads over 2
+    with pytest.raises(q4.Q4Error):
+        q4.paged_attention(q, b.cache, tab, off, lens, 1, 20, window=-1)
+    with pytest.raises(q4.Q4Error):
+        q4.paged_attention(q, b.cache, tab, off, lens, 1, 20, scale=float("nan"))
+    with pytest.raises(ValueError):
+        q4.paged_attention(q, b.cache, tab, off, lens, 1, 20, out=torch.empty_like(q)[:, :4])

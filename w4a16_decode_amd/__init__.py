@@ -11,6 +11,8 @@ fallback: without the built library or a GPU the calls raise.
 
 from .attention import (  # noqa: F401
     PagedKVCache4,
+    paged_attention,
+    paged_attention_workspace_bytes,
     paged_kv_alloc,
     paged_kv_append,
     paged_kv_dequant,
@@ -65,5 +67,5 @@ __all__ = [
     "ActOrderWeight", "actorder_perm", "quantize_pack_perm", "gemm_perm", "workspace_bytes_perm",
     "KVCache4", "kv_cache_alloc", "kv_quantize_pack", "kv_dequant",
     "PagedKVCache4", "paged_kv_alloc", "paged_kv_append", "paged_kv_dequant", "rope_table", "qk_norm_rope",
-    "qk_norm_rope_append", "read_probe", "rtn_check",
+    "qk_norm_rope_append", "paged_attention", "paged_attention_workspace_bytes", "read_probe", "rtn_check",
 ]

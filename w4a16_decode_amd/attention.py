@@ -13,7 +13,7 @@ import ctypes
 from dataclasses import dataclass
 
 from . import _lib
-from .ops import Q4Error, _check, _require_gpu, _stream
+from .ops import Q4Error, _check, _require_gpu, _stream, _workspace
 
 
 def _on(t):
@@ -232,3 +232,49 @@ def paged_kv_dequant(cache: PagedKVCache4, slots):
         _check(_lib.load().q4_paged_kv_dequant(cache._c(), slots.data_ptr(), n, k.data_ptr(), v.data_ptr(),
                                                _stream(k)))
     return k, v
+
+
+def paged_attention_workspace_bytes(seqs: int, tokens: int, max_q: int, max_kv: int, q_heads: int, kv_heads: int,
+                                    head_dim: int, window: int = 0) -> int:
+    return int(_lib.load().q4_paged_attention_workspace_bytes(seqs, tokens, max_q, max_kv, q_heads, kv_heads, head_dim,
+                                                              window))
+
+
+def paged_attention(q, cache: PagedKVCache4, block_table, q_offsets, kv_lens, max_q: int, max_kv: int,
+                    scale: float | None = None, window: int = 0, out=None, workspace=None):
+    """q4_paged_attention: causal attention of each sequence's newest tokens over its pages.
+
+    q: float16 [tokens, q_heads, head_dim], sequence n's rows q_offsets[n] ..
+    q_offsets[n + 1] - 1 being the last of its kv_lens[n] tokens (k and v appended
+    before); block_table: int32 [seqs, max_blocks], the page of each page_size tokens;
+    max_q, max_kv: bounds of the rows and the length of any sequence. scale defaults to
+    1 / sqrt(head_dim); window > 0 hides keys more than window - 1 positions back. Returns
+    float16 [tokens, q_heads, head_dim]; rows of no sequence keep what `out` held (an
+    `out` made here holds anything there)."""
+    import torch
+
+    n, hq, d, qs = _rows(q, "q")
+    if d != cache.head_dim:
+        raise ValueError(f"q must have the cache's head_dim {cache.head_dim}")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [seqs, max_blocks]")
+    seqs, blocks = block_table.shape
+    _ints(block_table, "block_table", (seqs, blocks))
+    _ints(q_offsets, "q_offsets", (seqs + 1,))
+    _ints(kv_lens, "kv_lens", (seqs,))
+    _same_device(q, "q", {"the cache": cache, "block_table": block_table, "q_offsets": q_offsets, "kv_lens": kv_lens})
+    if out is None:
+        out = torch.empty((n, hq, d), dtype=torch.float16, device=q.device)
+    else:
+        _require_gpu(out, "out", torch.float16)
+        if tuple(out.shape) != (n, hq, d) or out.device != q.device:
+            raise ValueError(f"out must be {[n, hq, d]} on {q.device}")
+    lib = _lib.load()
+    with _on(q):
+        need = int(lib.q4_paged_attention_workspace_bytes(seqs, n, max_q, max_kv, hq, cache.kv_heads, d, window))
+        ws_ptr, ws_bytes = _workspace(q, need, workspace)
+        _check(lib.q4_paged_attention(q.data_ptr(), qs, cache._c(), block_table.data_ptr(), blocks,
+                                      q_offsets.data_ptr(), kv_lens.data_ptr(), seqs, n, max_q, max_kv, hq,
+                                      d ** -0.5 if scale is None else scale, window, out.data_ptr(), ws_ptr, ws_bytes,
+                                      _stream(q)))
+    return out

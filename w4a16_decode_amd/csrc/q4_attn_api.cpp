@@ -95,6 +95,23 @@ q4_status rope_common(q4::RopeArgs& a, void* stream) {
   return hip_status(q4::launch_rope(a, static_cast<hipStream_t>(stream)), "norm and rotation launch");
 }
 
+// Sizes of an attention call; q_heads in whole shares of kv_heads.
+q4_status check_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv, int32_t q_heads, int32_t kv_heads,
+                     int64_t window) {
+  if (seqs < 0 || tokens < 0 || max_q < 0 || max_kv < 0 || seqs >= kMaxDim || tokens >= kMaxDim || max_q >= kMaxDim ||
+      max_kv >= kMaxDim)
+    return fail(Q4_ERR_SHAPE, "seqs=%lld, tokens=%lld, max_q=%lld, max_kv=%lld out of range", (long long)seqs,
+                (long long)tokens, (long long)max_q, (long long)max_kv);
+  if (window < 0 || window >= kMaxDim) return fail(Q4_ERR_SHAPE, "window=%lld out of range", (long long)window);
+  if (kv_heads <= 0 || q_heads <= 0 || q_heads > 65535 || q_heads % kv_heads != 0)
+    return fail(Q4_ERR_SHAPE, "q_heads=%d must be a positive multiple of kv_heads=%d", (int)q_heads, (int)kv_heads);
+  // row tiles of all sequences and heads index the grid
+  const int64_t rows = std::min(max_q, tokens) * (q_heads / kv_heads);
+  if (rows >= kMaxDim || (rows / 16 + 1) * kv_heads >= kMaxDim / std::max<int64_t>(seqs, 1))
+    return fail(Q4_ERR_SHAPE, "seqs * heads * max_q too large for one call");
+  return Q4_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -173,6 +190,45 @@ q4_status q4_paged_kv_dequant(const q4_paged_kv* cache, const int32_t* slots, in
     return fail(Q4_ERR_ALIGN, "slots need 4-byte, k_out and v_out 16-byte alignment");
   return hip_status(q4::launch_paged_dequant(c, slots, tokens, k_out, v_out, static_cast<hipStream_t>(stream)),
                     "paged dequant launch");
+}
+
+size_t q4_paged_attention_workspace_bytes(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv,
+                                          int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t window) {
+  if (check_attn(seqs, tokens, max_q, max_kv, q_heads, kv_heads, window) != Q4_OK) return 0;
+  return 0;
+}
+
+q4_status q4_paged_attention(const void* q, int64_t q_stride, const q4_paged_kv* cache, const int32_t* block_table,
+                             int64_t max_blocks, const int32_t* q_offsets, const int32_t* kv_lens, int64_t seqs,
+                             int64_t tokens, int64_t max_q, int64_t max_kv, int32_t q_heads, float scale,
+                             int64_t window, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  q4::AttnArgs a{};
+  q4_status st = check_paged(cache, &a.cache);
+  if (st != Q4_OK) return st;
+  if ((st = check_attn(seqs, tokens, max_q, max_kv, q_heads, a.cache.kv_heads, window)) != Q4_OK) return st;
+  if (max_blocks < 0 || max_blocks >= kMaxDim)
+    return fail(Q4_ERR_SHAPE, "max_blocks=%lld out of range", (long long)max_blocks);
+  if (!(scale > -3.0e38f && scale < 3.0e38f)) return fail(Q4_ERR_SHAPE, "scale must be finite");
+  if (seqs == 0 || tokens == 0 || max_q == 0) return ok();
+  if ((st = check_rows("q", q, q_stride, q_heads, a.cache.head_dim)) != Q4_OK) return st;
+  if (!q_offsets || !kv_lens || !out || (!block_table && max_blocks > 0 && max_kv > 0))
+    return fail(Q4_ERR_NULL, "block_table, q_offsets, kv_lens, out must be non-NULL");
+  if (!aligned(out, 8) || !aligned(block_table, 4) || !aligned(q_offsets, 4) || !aligned(kv_lens, 4))
+    return fail(Q4_ERR_ALIGN, "out needs 8-byte, block_table, q_offsets and kv_lens 4-byte alignment");
+  a.q = q, a.q_stride = q_stride, a.block_table = block_table, a.max_blocks = (int)max_blocks;
+  a.q_offsets = q_offsets, a.kv_lens = kv_lens, a.seqs = (int)seqs, a.tokens = (int)tokens;
+  a.max_q = (int)std::min(max_q, tokens), a.max_kv = (int)max_kv, a.q_heads = q_heads;
+  a.scale = scale, a.window = (int)window, a.out = out;
+  const size_t need = q4_paged_attention_workspace_bytes(seqs, tokens, max_q, max_kv, q_heads, a.cache.kv_heads,
+                                                         a.cache.head_dim, window);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need)
+      return fail(Q4_ERR_WORKSPACE, "this call needs %zu bytes of workspace (q4_paged_attention_workspace_bytes), got %zu",
+                  need, workspace ? workspace_bytes : (size_t)0);
+    if (!aligned(workspace, 16)) return fail(Q4_ERR_ALIGN, "workspace needs 16-byte alignment");
+  }
+  a.workspace = workspace;
+  return hip_status(q4::launch_attention(a, static_cast<hipStream_t>(stream)), "attention launch");
 }
 
 }  // extern "C"

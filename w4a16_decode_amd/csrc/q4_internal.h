@@ -111,6 +111,23 @@ struct RopeArgs {
   const int32_t* slots;
 };
 
+// Attention of the last rows of each sequence over its paged keys (include/q4_attn.h).
+struct AttnArgs {
+  const void* q;  // [tokens][q_heads][head_dim], tokens q_stride elements apart
+  int64_t q_stride;
+  PagedArgs cache;
+  const int32_t* block_table;  // [seqs][max_blocks]
+  int max_blocks;
+  const int32_t* q_offsets;  // [seqs + 1]
+  const int32_t* kv_lens;    // [seqs]
+  int seqs, tokens, max_q, max_kv, q_heads;
+  float scale;
+  int window;  // 0: none
+  void* out;   // [tokens][q_heads][head_dim]
+  void* workspace;
+};
+
+hipError_t launch_attention(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
 hipError_t launch_paged_dequant(const PagedArgs& c, const int32_t* slots, int64_t tokens, void* k_out, void* v_out,
                                 hipStream_t stream);
