@@ -1,0 +1,144 @@
+"""The product with adapters on the GPU against the oracle (float64).
+
+With all-zero weights the result is the adapters' part alone. Its bound: A x is a float32 sum
+of in / 32 matrix steps and up to 32 joins, B t one of rank terms after a product with
+the scaling: (in / 32 + 32 + rank + 2) 2^-23 relative to scaling * sum_r |B| sum_k |A| |x|,
+then half a float16 step 2^-11 (subnormal: 2^-25). With real weights the suite's
+tolerance of a product holds (gpu_util), and a row without an adapter has gemm's bits.
+"""
+
+import numpy as np
+import pytest
+
+import oracle
+import synth
+from gpu_util import assert_close, say, to_gpu, to_np
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def q4():
+    import torch
+
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import w4a16_decode_amd as q4mod
+
+    say("libq4", q4mod.version())
+    return q4mod
+
+
+def _adapters(n, rank, N, K, seed):
+    r = np.random.default_rng(seed)
+    a = (r.standard_normal((n, rank, K)) / np.sqrt(K)).astype(np.float16)
+    b = (0.3 * r.standard_normal((n, N, rank))).astype(np.float16)
+    return a, b, (0.5 + r.random(n)).astype(np.float32)
+
+
+def _ids(B, n, kind, seed):
+    r = np.random.default_rng(seed)
+    if kind == "same":
+        return np.zeros(B, np.int32)
+    if kind == "runs":
+        return np.repeat(r.integers(-1, n, B), 5)[:B].astype(np.int32)
+    ids = r.integers(-1, n, B).astype(np.int32)
+    if B > 3:
+        ids[1], ids[3] = n, 2 ** 31 - 1                # outside the adapters
+    return ids
+
+
+SHAPES = [  # B, N, K, g, rank, adapters, ids
+    (1, 256, 256, 128, 8, 1, "same"),
+    (1, 4096, 4096, 128, 16, 3, "mixed"),
+    (2, 17, 96, 32, 16, 2, "mixed"),
+    (3, 8192, 8192, 128, 24, 4, "mixed"),
+    (4, 1000, 1024, 64, 32, 5, "mixed"),
+    (13, 515, 2048, 128, 64, 20, "mixed"),
+    (16, 300, 7168, 128, 128, 16, "mixed"),
+    (17, 1037, 512, 128, 16, 3, "runs"),
+    (50, 640, 1152, 128, 40, 7, "mixed"),
+    (100, 2048, 4096, 128, 16, 30, "mixed"),
+    (200, 515, 1024, 32, 64, 4, "runs"),
+]
+
+
+@pytest.mark.parametrize("B,N,K,g,rank,n,kind", SHAPES)
+def test_adapters_alone(q4, B, N, K, g, rank, n, kind):
+    import torch
+
+    say("adapters alone", B, N, K, g, rank, n, kind)
+    a, b, s = _adapters(n, rank, N, K, seed=B + N)
+    ids = _ids(B, n, kind, seed=B)
+    x = synth.activation(B, K, seed=B)
+    qw = q4.quantize_pack(torch.zeros((N, K), dtype=torch.float16, device="cuda"), g)
+    y = to_np(q4.gemm_lora(to_gpu(x), qw, q4.LoraAdapters(to_gpu(a), to_gpu(b), to_gpu(s)), to_gpu(ids)))
+    ref = oracle.lora.lora_delta(x, a, b, s, ids)
+    mag = oracle.lora.lora_delta(np.abs(x), np.abs(a), np.abs(b), s, ids)
+    bound = (K / 32 + 32 + rank + 2) * 2.0 ** -23 * mag + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25
+    err = np.abs(y.astype(np.float64) - ref)
+    assert np.all(err <= bound), (err / bound).max()
+    say("  worst share of the bound", (err / bound).max())
+
+
+@pytest.mark.parametrize("asym", [False, True])
+@pytest.mark.parametrize("B,N,K,g,rank,n,kind", SHAPES)
+def test_beside_the_product(q4, B, N, K, g, rank, n, kind, asym):
+    import torch
+
+    say("beside the product", B, N, K, g, rank, n, kind, asym)
+    W = synth.weight(N, K, seed=N)
+    a, b, s = _adapters(n, rank, N, K, seed=B + N)
+    ids = _ids(B, n, kind, seed=B)
+    x = to_gpu(synth.activation(B, K, seed=B + 1))
+    qw = q4.quantize_pack(to_gpu(W), g, asym)
+    y = q4.gemm_lora(x, qw, q4.LoraAdapters(to_gpu(a), to_gpu(b), to_gpu(s)), to_gpu(ids))
+    plain = q4.gemm(x, qw)
+    without = torch.from_numpy((ids < 0) | (ids >= n)).cuda()
+    assert torch.equal(y[without], plain[without])
+    if asym:
+        w_hat = oracle.dequant_asym(*oracle.quantize_asym(W, g), g)
+    else:
+        w_hat = oracle.dequant_sym(*oracle.quantize_sym(W, g), g)
+    ref = oracle.gemm_ref(to_np(x), w_hat) + oracle.lora.lora_delta(to_np(x), a, b, s, ids)
+    assert_close(to_np(y), ref, "beside the product")
+    again = q4.gemm_lora(x, qw, q4.LoraAdapters(to_gpu(a), to_gpu(b), to_gpu(s)), to_gpu(ids))
+    assert torch.equal(y, again)
+
+
+def test_no_adapters_and_no_rows(q4):
+    import torch
+
+    x = to_gpu(synth.activation(5, 256, seed=1))
+    qw = q4.quantize_pack(to_gpu(synth.weight(64, 256, seed=2)), 128)
+    e = q4.LoraAdapters(torch.empty((0, 8, 256), dtype=torch.float16, device="cuda"),
+                        torch.empty((0, 64, 8), dtype=torch.float16, device="cuda"),
+                        torch.empty(0, dtype=torch.float32, device="cuda"))
+    ids = torch.zeros(5, dtype=torch.int32, device="cuda")
+    assert torch.equal(q4.gemm_lora(x, qw, e, ids), q4.gemm(x, qw))
+    a = q4.LoraAdapters(*(to_gpu(t) for t in _adapters(2, 8, 64, 256, 0)))
+    assert q4.gemm_lora(x[:0], qw, a, ids[:0]).shape == (0, 64)
+
+
+def test_workspace_and_refusals(q4):
+    import torch
+
+    x = to_gpu(synth.activation(5, 256, seed=1))
+    qw = q4.quantize_pack(to_gpu(synth.weight(64, 256, seed=2)), 128)
+    a = q4.LoraAdapters(*(to_gpu(t) for t in _adapters(2, 8, 64, 256, 0)))
+    ids = torch.tensor([0, 1, -1, 1, 0], dtype=torch.int32, device="cuda")
+    need = q4.workspace_bytes_lora(5, 64, 256, 128, 8)
+    ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+    y = q4.gemm_lora(x, qw, a, ids, workspace=ws)
+    assert torch.equal(y, q4.gemm_lora(x, qw, a, ids))
+    assert bool((ws[need:] == 0xFF).all())
+    with pytest.raises(q4.Q4Error):
+        q4.gemm_lora(x, qw, a, ids, workspace=ws[:need - 16])
+    with pytest.raises(ValueError):
+        q4.gemm_lora(x, qw, a, ids[:4])
+    with pytest.raises(TypeError):
+        q4.gemm_lora(x, qw, a, ids.long())
+    with pytest.raises(ValueError):
+        q4.gemm_lora(x, qw, q4.LoraAdapters(a.a, a.b[:, :32].contiguous(), a.scaling), ids)
+    bad = [to_gpu(t) for t in _adapters(2, 12, 64, 256, 0)]
+    with pytest.raises(q4.Q4Error):
+        q4.gemm_lora(x, qw, q4.LoraAdapters(*bad), ids)                  # rank 12

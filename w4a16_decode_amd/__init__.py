@@ -23,6 +23,7 @@ from .attention import (  # noqa: F401
 from .ops import (  # noqa: F401
     ActOrderWeight,
     KVCache4,
+    LoraAdapters,
     Q4Error,
     QuantizedWeight,
     QuantizedWeight8,
@@ -30,6 +31,7 @@ from .ops import (  # noqa: F401
     from_canonical,
     gemm,
     gemm_config,
+    gemm_lora,
     gemm_noalloc,
     gemm_perm,
     gemm_shape,
@@ -56,6 +58,7 @@ from .ops import (  # noqa: F401
     to_canonical,
     version,
     workspace_bytes,
+    workspace_bytes_lora,
     workspace_bytes_perm,
 )
 
@@ -65,6 +68,7 @@ __all__ = [
     "QuantizedWeight8", "q8_quantize_pack", "q8_gemm", "q8_gemm_config", "q8_to_canonical", "q8_from_canonical",
     "q8_packed_bytes", "q8_workspace_bytes",
     "ActOrderWeight", "actorder_perm", "quantize_pack_perm", "gemm_perm", "workspace_bytes_perm",
+    "LoraAdapters", "gemm_lora", "workspace_bytes_lora",
     "KVCache4", "kv_cache_alloc", "kv_quantize_pack", "kv_dequant",
     "PagedKVCache4", "paged_kv_alloc", "paged_kv_append", "paged_kv_dequant", "rope_table", "qk_norm_rope",
     "qk_norm_rope_append", "paged_attention", "paged_attention_workspace_bytes", "read_probe", "rtn_check",

@@ -62,6 +62,9 @@ SIGNATURES = {
     "q4_paged_attention_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I32, _I32, _I32, _I64]),
     "q4_paged_attention": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I32, ctypes.c_float,
                                           _I64, _P, _P, _SZ, _P]),
+    "q4_workspace_bytes_lora": (_SZ, [_I64, _I64, _I64, _I32, _I32]),
+    "q4_gemm_lora": (ctypes.c_int, [_P, _I64, _P, _P, _P, _I64, _I64, _I32, _P, _P, _P, _I64, _I32, _P, _P, _P, _SZ,
+                                    _P]),
     "q8_packed_bytes": (_SZ, [_I64, _I64]),
     "q8_scales_count": (_SZ, [_I64]),
     "q8_workspace_bytes": (_SZ, [_I64, _I64, _I64]),

@@ -471,38 +471,65 @@ q4_status q4_quantize_pack_clip(const void* W, int64_t out, int64_t in, int32_t 
   return quantize_common(W, out, in, group, packed, scales, nullptr, false, min_percent, stream);
 }
 
+}  // extern "C"
+
+namespace q4 {
+
+q4_status gemm_args(const void* x, int64_t B, const void* packed, const void* scales, const void* zeros, bool asym,
+                    int64_t out, int64_t in, int32_t group, void* y, GemmArgs* a) {
+  if (B < 0 || B >= kMaxDim) return fail(Q4_ERR_SHAPE, "B=%lld out of range", (long long)B);
+  Dims d;
+  q4_status st = check_dims(out, in, group, &d);
+  if (st != Q4_OK) return st;
+  if (B == 0) return Q4_OK;
+  if (!x || !packed || !scales || !y || (asym && !zeros))
+    return fail(Q4_ERR_NULL, "x, packed, scales, y%s must be non-NULL", asym ? ", zeros" : "");
+  if (!aligned(x, 16) || !aligned(packed, 16) || !aligned(scales, 8) || !aligned(y, 2))
+    return fail(Q4_ERR_ALIGN, "x and packed need 16-byte, scales 8-byte, y 2-byte alignment");
+  if (B * in >= (int64_t(1) << 40) || B * out >= (int64_t(1) << 40))
+    return fail(Q4_ERR_SHAPE, "B*in or B*out too large");
+  a->x = x;
+  a->B = (int)B;
+  a->packed = packed;
+  a->scales = scales;
+  a->zeros = zeros;
+  a->asym = asym;
+  a->N = d.N;
+  a->K = d.K;
+  a->group = d.group;
+  a->Np = d.Np;
+  a->Kp = d.Kp;
+  a->Gp = d.Gp;
+  a->y = y;
+  pick_shape((int)B, d, a);
+  return Q4_OK;
+}
+
+int gemm_splits(int64_t B, int64_t out, int64_t in, int32_t group, bool asym) {
+  Dims d;
+  if (B <= 0 || B >= kMaxDim || check_dims(out, in, group, &d) != Q4_OK) return 0;
+  GemmArgs a{};
+  a.B = (int)B;
+  a.N = d.N;
+  a.asym = asym;
+  pick_shape((int)B, d, &a);
+  return a.k_splits;
+}
+
+}  // namespace q4
+
+extern "C" {
+
 static q4_status gemm_common(const void* x, int64_t B, const void* packed, const void* scales, const void* zeros,
                              bool asym, int64_t out, int64_t in, int32_t group, void* y, int rows_per_wave,
                              int waves_per_group, int k_splits, int col_tiles, void* workspace,
                              size_t workspace_bytes, void* stream, const int32_t* perm = nullptr,
                              bool noalloc = false) {
-  if (B < 0 || B >= kMaxDim) return fail(Q4_ERR_SHAPE, "B=%lld out of range", (long long)B);
-  Dims d;
-  q4_status st = check_dims(out, in, group, &d);
+  q4::GemmArgs a{};
+  q4_status st = q4::gemm_args(x, B, packed, scales, zeros, asym, out, in, group, y, &a);
   if (st != Q4_OK) return st;
   if (B == 0) return ok();
-  if (!x || !packed || !scales || !y || (asym && !zeros))
-    return fail(Q4_ERR_NULL, "x, packed, scales, y%s must be non-NULL", asym ? ", zeros" : "");
-  if (!aligned(x, 16) || !aligned(packed, 16) || !aligned(scales, 8) || !aligned(y, 2))
-    return fail(Q4_ERR_ALIGN, "x and packed need 16-byte, scales 8-byte, y 2-byte alignment");
-  if ((int64_t)B * in >= (int64_t(1) << 40) || (int64_t)B * out >= (int64_t(1) << 40))
-    return fail(Q4_ERR_SHAPE, "B*in or B*out too large");
-  q4::GemmArgs a{};
-  a.x = x;
-  a.B = (int)B;
-  a.packed = packed;
-  a.scales = scales;
-  a.zeros = zeros;
-  a.asym = asym;
-  a.N = d.N;
-  a.K = d.K;
-  a.group = d.group;
-  a.Np = d.Np;
-  a.Kp = d.Kp;
-  a.Gp = d.Gp;
-  a.y = y;
   a.perm = perm;
-  pick_shape((int)B, d, &a);
   if (rows_per_wave > 0 || waves_per_group > 0 || k_splits > 0 || col_tiles > 0) {
     if (rows_per_wave != 1 && rows_per_wave != 2 && rows_per_wave != 4)
       return fail(Q4_ERR_UNSUPPORTED, "rows_per_wave must be 1, 2 or 4");
@@ -513,14 +540,14 @@ static q4_status gemm_common(const void* x, int64_t B, const void* packed, const
       a.lds_limit = lds_per_block();
       // the streaming kernel (two row tiles, B <= 3, no split) stages no activation slice
       const bool streamed = q4::gemv_streams_x(
-          (int)B, d.Kp, rows_per_wave, k_splits,
-          q4::gemv_stream_burst_ok(d.Np, d.group, asym != 0, false, q4::device_cu_count_cached()));
+          (int)B, a.Kp, rows_per_wave, k_splits,
+          q4::gemv_stream_burst_ok(a.Np, a.group, asym != 0, false, q4::device_cu_count_cached()));
       if (!streamed &&
-          !gemv_shape_ok((int)B, d.Kp / 128, k_splits, waves_per_group, rows_per_wave, d.group, asym, a.lds_limit))
+          !gemv_shape_ok((int)B, a.Kp / 128, k_splits, waves_per_group, rows_per_wave, a.group, asym, a.lds_limit))
         return fail(Q4_ERR_UNSUPPORTED, "k_splits=%d, waves_per_group=%d: more splits than 128-channel blocks, "
                     "or the activation slice of B=%lld does not fit LDS or the copy",
                     (int)k_splits, (int)waves_per_group, (long long)B);
-    } else if (!mfma_shape_ok(rows_per_wave, waves_per_group, k_splits, col_tiles, d.group, d.Kp / 128)) {
+    } else if (!mfma_shape_ok(rows_per_wave, waves_per_group, k_splits, col_tiles, a.group, a.Kp / 128)) {
       return fail(Q4_ERR_UNSUPPORTED, "for B > 16: waves_per_group must be 4 or 8 (8 only with rows_per_wave <= 2), "
                   "col_tiles 2, 3, 4, 6 or 8 (within LDS), "
                   "rows_per_wave * col_tiles * max(1, 128 / group) <= 16, k_splits at most the chunks of "

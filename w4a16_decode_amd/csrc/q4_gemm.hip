@@ -178,11 +178,11 @@ __device__ __forceinline__ void gemv_store_x(const uint4 (&xr)[XCH], uint16_t* x
 
 // Step 4 of the staged GEMVs (after the barrier that ends the streaming): the units'
 // partial sums, parked in LDS as [unit = i * CH + c][r][b][16 rows], added in chunk
-// order for every row block i of the workgroup -> y, or with KS > 1 -> the k-split's
-// float32 slice of the workspace; e = ((i * R + r) * B + b) * 16 + row.
+// order for every row block i of the workgroup -> y, or where y is NULL (a k-split, a
+// caller that adds to the sums) -> the k-split's float32 slice of the workspace; e = ((i * R + r) * B + b) * 16 + row.
 template <int R>
 __device__ __forceinline__ void gemv_write_units(const float* part0, int n_rb, int CH, int B, int N, int rb_first,
-                                                 int rb_stride, int KS, int ks, uint16_t* __restrict__ y,
+                                                 int rb_stride, int ks, uint16_t* __restrict__ y,
                                                  float* __restrict__ ws) {
   const int nout = n_rb * R * 16 * B;
   for (int e = threadIdx.x; e < nout; e += blockDim.x) {
@@ -196,7 +196,7 @@ __device__ __forceinline__ void gemv_write_units(const float* part0, int n_rb, i
     for (int c = 0; c < CH; ++c) sum += pp[(size_t)c * R * 16 * B];
     const int n = ((rb_first + i * rb_stride) * R + r) * 16 + row;
     if (n < N) {
-      if (KS == 1) y[(size_t)b * N + n] = __builtin_bit_cast(uint16_t, (_Float16)sum);
+      if (y) y[(size_t)b * N + n] = __builtin_bit_cast(uint16_t, (_Float16)sum);
       else ws[((size_t)ks * B + b) * N + n] = sum;
     }
   }
@@ -445,7 +445,7 @@ void gemv_kernel(const uint16_t* __restrict__ x, int B, const uint4* __restrict_
 
   // 4. results of all row blocks -> y (or the k-split workspace)
   lds_barrier();
-  gemv_write_units<R>(part0, n_rb, CH, B, N, rb_first, rb_stride, KS, ks, y, ws);
+  gemv_write_units<R>(part0, n_rb, CH, B, N, rb_first, rb_stride, ks, y, ws);
 }
 
 // ---------------------------------------------------------------------------------
@@ -661,7 +661,7 @@ void gemv_burst_kernel(const uint16_t* __restrict__ x, int B, const uint4* __res
 
   // 4. results of all row blocks -> y (or the k-split workspace)
   lds_barrier();
-  gemv_write_units<1>(part0, n_rb, CH, B, N, rb_first, rb_stride, KS, ks, y, ws);
+  gemv_write_units<1>(part0, n_rb, CH, B, N, rb_first, rb_stride, ks, y, ws);
 }
 
 __global__ void reduce_splits_kernel(const float* __restrict__ ws, int KS, int64_t BN, uint16_t* __restrict__ y) {
@@ -696,6 +696,11 @@ __global__ void reduce_splits8_kernel(const float* __restrict__ ws, int KS, int6
     }
     *reinterpret_cast<uint4*>(y + 8 * i) = __builtin_bit_cast(uint4, h);
   }
+}
+
+// Where a product's kernels write: y, or NULL for float32 sums in the workspace.
+uint16_t* sum_out(const GemmArgs& a) {
+  return a.k_splits > 1 || a.partials ? nullptr : static_cast<uint16_t*>(a.y);
 }
 
 // Adds the KS float32 partial products in the workspace, split by split, into y.
@@ -761,7 +766,8 @@ template <int R, int GSUB, bool ASYM, int P, int BMAX = 1>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(BMAX == 1 && GSUB == 1 ? 4 : 1, 8)))
 void gemv_stream_kernel(const uint16_t* __restrict__ x, int B, const uint4* __restrict__ packed,
                         const uint16_t* __restrict__ scales, const uint8_t* __restrict__ zeros, int N, int K,
-                        int T, int S, int Gp, int J, int nRB, uint16_t* __restrict__ y) {
+                        int T, int S, int Gp, int J, int nRB, uint16_t* __restrict__ y,
+                        float* __restrict__ ws) {
   static_assert(P - 1 <= kUnitBlocks, "a unit must outlast the blocks in flight");
   // BMAX: batch rows the unit's x registers and LDS slice are sized for (B <= BMAX)
   extern __shared__ __align__(16) unsigned char smem[];
@@ -986,7 +992,7 @@ void gemv_stream_kernel(const uint16_t* __restrict__ x, int B, const uint4* __re
 
   // results: the units' partials added in chunk order -> y
   lds_barrier();
-  gemv_write_units<R>(part0, n_rb, CH, B, N, rb_first, rb_stride, 1, 0, y, nullptr);
+  gemv_write_units<R>(part0, n_rb, CH, B, N, rb_first, rb_stride, 0, y, ws);
 }
 
 // ---------------------------------------------------------------------------------
@@ -1008,7 +1014,7 @@ template <int BMAX>
 __global__ __launch_bounds__(512)
 void gemv_stream_burst_kernel(const uint16_t* __restrict__ x, int B, const uint4* __restrict__ packed,
                               const uint16_t* __restrict__ scales, int N, int K, int T, int S, int Gp, int nRB,
-                              uint16_t* __restrict__ y) {
+                              uint16_t* __restrict__ y, float* __restrict__ ws) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int R = 2;                        // row tiles per wavefront
   constexpr int NB = 2;                       // blocks per burst
@@ -1228,7 +1234,7 @@ void gemv_stream_burst_kernel(const uint16_t* __restrict__ x, int B, const uint4
 
   // results: the units' partials added in chunk order -> y
   lds_barrier();
-  gemv_write_units<R>(part0, n_rb, CH, B, N, rb_first, rb_stride, 1, 0, y, nullptr);
+  gemv_write_units<R>(part0, n_rb, CH, B, N, rb_first, rb_stride, 0, y, ws);
 }
 
 template <int R, int GSUB, bool ASYM, int XCH, bool Q8 = false>
@@ -1300,13 +1306,13 @@ hipError_t launch_gemv_t(const GemmArgs& a, hipStream_t stream) {
         hipLaunchKernelGGL((gemv_burst_kernel<XCH, 2, Q8>), dim3(grid), dim3(W * kWave), lds, stream,
                            static_cast<const uint16_t*>(a.x), a.B, static_cast<const uint4*>(a.packed),
                            static_cast<const uint16_t*>(a.scales), a.N, a.K, S, a.Gp, KS, nRB, CH,
-                           static_cast<uint16_t*>(a.y), static_cast<float*>(a.workspace));
+                           sum_out(a), static_cast<float*>(a.workspace));
       else
         hipLaunchKernelGGL((gemv_burst_kernel<XCH, 4, Q8>), dim3(grid), dim3(W * kWave), lds, stream,
                            static_cast<const uint16_t*>(a.x), a.B, static_cast<const uint4*>(a.packed),
                            static_cast<const uint16_t*>(a.scales), a.N, a.K, S, a.Gp, KS, nRB, CH,
-                           static_cast<uint16_t*>(a.y), static_cast<float*>(a.workspace));
-      if (KS > 1)
+                           sum_out(a), static_cast<float*>(a.workspace));
+      if (KS > 1 && !a.partials)
         launch_reduce_splits(static_cast<const float*>(a.workspace), KS, (int64_t)a.B * a.N,
                              static_cast<uint16_t*>(a.y), stream);
       return hipGetLastError();
@@ -1315,8 +1321,8 @@ hipError_t launch_gemv_t(const GemmArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((gemv_kernel<R, GSUB, ASYM, P, XCH, Q8>), dim3(grid), dim3(W * kWave), lds, stream,
                      static_cast<const uint16_t*>(a.x), a.B, static_cast<const uint4*>(a.packed),
                      static_cast<const uint16_t*>(a.scales), static_cast<const uint8_t*>(a.zeros), a.N, a.K, T, S,
-                     a.Gp, J, KS, nRB, CH, static_cast<uint16_t*>(a.y), static_cast<float*>(a.workspace));
-  if (KS > 1)
+                     a.Gp, J, KS, nRB, CH, sum_out(a), static_cast<float*>(a.workspace));
+  if (KS > 1 && !a.partials)
     launch_reduce_splits(static_cast<const float*>(a.workspace), KS, (int64_t)a.B * a.N, static_cast<uint16_t*>(a.y),
                          stream);
   return hipGetLastError();
@@ -1376,14 +1382,14 @@ hipError_t launch_gemv_stream_t(const GemmArgs& a, hipStream_t stream) {
       hipLaunchKernelGGL((gemv_stream_burst_kernel<BMAX>), dim3((unsigned)grid), dim3(W * kWave), lds, stream,
                          static_cast<const uint16_t*>(a.x), a.B, static_cast<const uint4*>(a.packed),
                          static_cast<const uint16_t*>(a.scales), a.N, a.K, T, S, a.Gp, nRB,
-                         static_cast<uint16_t*>(a.y));
+                         sum_out(a), static_cast<float*>(a.workspace));
       return hipGetLastError();
     }
   }
   hipLaunchKernelGGL((gemv_stream_kernel<R, GSUB, ASYM, P, BMAX>), dim3((unsigned)grid), dim3(W * kWave), lds,
                      stream, static_cast<const uint16_t*>(a.x), a.B, static_cast<const uint4*>(a.packed),
                      static_cast<const uint16_t*>(a.scales), static_cast<const uint8_t*>(a.zeros), a.N, a.K, T, S,
-                     a.Gp, J, nRB, static_cast<uint16_t*>(a.y));
+                     a.Gp, J, nRB, sum_out(a), static_cast<float*>(a.workspace));
   return hipGetLastError();
 }
 
@@ -1614,7 +1620,7 @@ __global__ __launch_bounds__(WV * 64) void gemm_mfma_kernel(const uint16_t* __re
       for (int i = 0; i < 4; ++i) {
         const int n = (tile0 + r) * 16 + crow + i;
         if (n >= N) continue;
-        if (KS == 1) y[(size_t)b * N + n] = __builtin_bit_cast(uint16_t, (_Float16)acc[r][c][i]);
+        if (y) y[(size_t)b * N + n] = __builtin_bit_cast(uint16_t, (_Float16)acc[r][c][i]);
         else ws[((size_t)ks * B + b) * N + n] = acc[r][c][i];
       }
     }
@@ -1634,8 +1640,8 @@ hipError_t launch_mfma_t(const GemmArgs& a, hipStream_t stream) {
   hipLaunchKernelGGL((gemm_mfma_kernel<RT, CT, GSUB, ASYM, NB, WV, Q8>), grid, dim3(WV * 64), lds, stream,
                      static_cast<const uint16_t*>(a.x), a.B, static_cast<const uint4*>(a.packed),
                      static_cast<const uint16_t*>(a.scales), static_cast<const uint8_t*>(a.zeros), a.N, a.K, T, S,
-                     a.Gp, J, static_cast<uint16_t*>(a.y), static_cast<float*>(a.workspace));
-  if (KS > 1)
+                     a.Gp, J, sum_out(a), static_cast<float*>(a.workspace));
+  if (KS > 1 && !a.partials)
     launch_reduce_splits(static_cast<const float*>(a.workspace), KS, (int64_t)a.B * a.N, static_cast<uint16_t*>(a.y),
                          stream);
   return hipGetLastError();

@@ -52,6 +52,7 @@ struct GemmArgs {
   int k_splits;         // workgroups splitting the channels; > 1 needs workspace
   void* workspace;      // float32 [k_splits][B][N] partial sums when k_splits > 1
   int grid_limit;       // B <= 16: cap on the persistent grid (0 = as many as are resident)
+  bool partials;        // write float32 sums to the workspace even without a split; no reduction into y
   size_t lds_limit;     // B <= 16: LDS a workgroup may use (sizes the per-workgroup result buffer)
 };
 
@@ -127,6 +128,25 @@ struct AttnArgs {
   void* workspace;
 };
 
+// Adapters beside a product (include/q4_lora.h). phase 0: A x into t; phase 1: y from the
+// product's partial sums and B t.
+struct LoraArgs {
+  const void* x;
+  int B, N, K;
+  const void* lora_a;
+  const void* lora_b;
+  const float* scaling;
+  const int32_t* ids;
+  int adapters, rank;
+  float* t;               // [lora_splits(K)][B][rank]
+  const float* partials;  // [gemm_splits][B][N]
+  int gemm_splits;
+  void* y;
+  int phase;
+};
+
+int lora_splits(int K);  // slices of the channel range of A x
+hipError_t launch_lora(const LoraArgs& a, hipStream_t stream);
 hipError_t launch_attention(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
 hipError_t launch_paged_dequant(const PagedArgs& c, const int32_t* slots, int64_t tokens, void* k_out, void* v_out,
