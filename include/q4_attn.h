@@ -33,7 +33,8 @@
  *   K and V scale of group j: float16 element (tile * D / group + j) * 16 + t.
  * Codes are stored offset-binary (q + 8). Rounding is q4_kv.h's: scale =
  * float16_rne(float32(amax) / 7), q = clamp(rint_half_even(x / scale), -8, 7), 0 for a
- * zero scale. group is 32, 64 or 128 and divides head_dim; pages * page_size < 2^31.
+ * zero scale; a group that holds an infinity or a NaN gets a NaN scale. group is 32, 64
+ * or 128 and divides head_dim; pages * page_size < 2^31.
  * Nothing reads the contents of a slot that no sequence's length covers.
  */
 #ifndef Q4_ATTN_H

@@ -218,3 +218,20 @@ def test_wrapper_refusals(q4):
         q4.paged_kv_alloc(2, 8, 1, 128)
     with pytest.raises(q4.Q4Error):
         q4.rope_table(8, 20)
+
+
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+def test_non_finite_groups(q4, bad):
+    """A group that holds an infinity or a NaN reads back as NaN, the others are unharmed."""
+    x = _qkv(4, 0, 2, 128, seed=21)
+    x[1, 0, 40], x[2, 3, 127] = bad, bad
+    cache = q4.paged_kv_alloc(1, 16, 2, 128, 32)
+    slots = to_gpu(np.arange(4, dtype=np.int32))
+    q4.paged_kv_append(to_gpu(x[:, :2]), to_gpu(x[:, 2:]), cache, slots)
+    k, v = (to_np(t) for t in q4.paged_kv_dequant(cache, slots))
+    clean = x.copy()
+    clean[1, 0, 40] = clean[2, 3, 127] = 0
+    want_k, want_v = (oracle.paged.store(clean[:, s], 32)[2] for s in (slice(0, 2), slice(2, 4)))
+    want_k[1, 0, 32:64] = want_v[2, 1, 96:] = np.nan
+    assert np.array_equal(k.astype(np.float64), want_k.astype(np.float16).astype(np.float64), equal_nan=True)
+    assert np.array_equal(v.astype(np.float64), want_v.astype(np.float16).astype(np.float64), equal_nan=True)

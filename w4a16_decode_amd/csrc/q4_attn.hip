@@ -20,12 +20,22 @@
 //     eight (4c + i of tile 0, then of tile 1) makes the scores the operand without a
 //     shuffle; the cache keeps V in that order.
 //
+// Maximum. All that has to hold is that the weights neither overflow nor vanish, so the
+// held maximum m is raised (a reduction over the row's four lanes, a rescaling of l and O)
+// only when some score exceeds it by more than kSlack binades: after a row's first few
+// steps almost never.
+//
+// Split. Where rows are few (decode), the four wavefronts of a workgroup share the rows and
+// take every fourth step of its keys, joined in LDS; long contexts are split further over
+// workgroups, whose partial results (O, m + E, l in float32) a second kernel joins in
+// order. Where rows are many, each wavefront has rows of its own.
+//
 // Range of the weights. P = p * vs is rounded to float16 before the product (half a
 // step, 2^-11 of each weight; its errors are independent and average over the keys).
 // p lies in [0, 1] relative to the row's maximum, but vs can be anything a float16
 // can be, and small products would fall among the subnormals. The exponent is
 // therefore taken relative to m + E, E the exponent of the largest V scale so far minus
-// kHeadroom: P stays in [0, 2^kHeadroom], 26 binades of full precision below its
+// kHeadroom: P stays in [0, 2^(kHeadroom + kSlack)], 26 binades of full precision below its
 // maximum. (Infinite scales do not count: their rows are not finite, others' unharmed.) The sum l carries the same factor, so it cancels in o = O / l.
 #include <algorithm>
 
@@ -36,6 +46,7 @@ namespace {
 
 constexpr int kStep = 2 * kTokTile;  // keys per step (MFMA K of the second product)
 constexpr float kHeadroom = 12.0f;
+constexpr float kSlack = 3.0f;  // binades a score may exceed the held maximum by
 constexpr float kLowest = -3.4028234663852886e38f;
 
 __device__ __forceinline__ float4_t mfma(half8_t a, half8_t b, float4_t c) {
@@ -43,6 +54,27 @@ __device__ __forceinline__ float4_t mfma(half8_t a, half8_t b, float4_t c) {
 }
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// Eight codes of the K operand, biased: fields of a dword are moved to bits 2..5 and 6..9
+// of the half-words, where OR with 256.0h and 16.0h makes 256 + n and 16 + n: two shifts
+// and four v_and_or_b32 for eight codes, no subtraction. The biases times the query's
+// channels (264 = 256 + 8 on elements 0, 1, 4, 5, 24 on the others) are the start value of
+// the dot product's accumulator instead.
+struct KRegs {
+  uint32_t m2, m6, b2, b6;
+  __device__ __forceinline__ static KRegs make() {
+    return KRegs{vreg_const(0x003C003Cu), vreg_const(0x03C003C0u), vreg_const(0x5C005C00u), vreg_const(0x4C004C00u)};
+  }
+};
+
+__device__ __forceinline__ half8_t k_operand(uint32_t w, const KRegs& k) {
+  const uint32_t a = w << 2, b = w >> 6;
+  const half2_t p0 = as_half2((a & k.m2) | k.b2), p1 = as_half2((a & k.m6) | k.b6);
+  const half2_t p2 = as_half2((b & k.m2) | k.b2), p3 = as_half2((b & k.m6) | k.b6);
+  const half4_t lo = __builtin_shufflevector(p0, p1, 0, 1, 2, 3);
+  const half4_t hi = __builtin_shufflevector(p2, p3, 0, 1, 2, 3);
+  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+}
 
 // Eight codes of the V operand: four tokens of each of two tiles. HI picks the channel
 // in the high nibble.
@@ -96,127 +128,242 @@ __device__ __forceinline__ void load_tile(Tile<D, GC>& t, const PagedArgs& c, in
   }
 }
 
-// Rows of one wavefront: sequence n's rows r0 .. r0 + 16 QT - 1 for KV head h.
-template <int D, int GC, int QT>
-struct Rows {
-  static constexpr int KB = D / 32;       // 32-channel blocks
-  static constexpr int BPG = KB / GC;     // of them per scale group
-  half8_t q[QT][KB];
-  int pos[QT];      // position of the lane's row (its own last visible key); -1: no row
-  float m[QT];      // running maximum of the scores (times log2 e)
-  float base[QT];   // m + E: what exponents are relative to
-  float l[QT];      // the lane's share of the sum
-  float4_t acc[QT][2 * KB];
+// What a workgroup works on.
+struct Job {
+  int first, rows, len, nq;  // the sequence's first row of q, rows = nq * share, length
+  int seq, head, share;
 };
 
-template <int D, int GC, int QT>
-__global__ __launch_bounds__(256) void attn_kernel(AttnArgs a, unsigned tiles) {
-  using R = Rows<D, GC, QT>;
-  constexpr int KB = R::KB, BPG = R::BPG;
+__device__ __forceinline__ bool make_job(const AttnArgs& a, int seq, int head, Job* w) {
+  // kept inside what the arguments promise
+  w->seq = seq;
+  w->head = head;
+  w->share = a.q_heads / a.cache.kv_heads;
+  w->first = min(max(a.q_offsets[seq], 0), a.tokens);
+  w->nq = min(min(max(a.q_offsets[seq + 1], w->first), a.tokens) - w->first, a.max_q);
+  w->len = min(max(a.kv_lens[seq], 0), a.max_kv);
+  w->rows = w->nq * w->share;
+  return w->rows > 0;
+}
+
+// Keys that rows r0 .. r0 + n - 1 see: [first (a multiple of kStep), last).
+struct Span {
+  int pos_lo, pos_hi, window, first, last;
+};
+
+__device__ __forceinline__ Span span_of(const AttnArgs& a, const Job& w, int r0, int n) {
+  Span s;
+  s.pos_lo = w.len - w.nq + r0 / w.share;
+  s.pos_hi = w.len - w.nq + (min(r0 + n, w.rows) - 1) / w.share;
+  s.last = s.pos_hi + 1;
+  s.window = a.window > 0 ? a.window : s.last + 1;
+  s.first = max(0, s.pos_lo - s.window + 1) / kStep * kStep;
+  return s;
+}
+
+// Walks 16-key tiles of a sequence's pages without a division per step (all scalar).
+struct Walk {
+  int tile, block, in_page;  // tile of the sequence, its page table entry, tile of the page
+};
+
+template <int D, int GC, int QT, bool TOK>
+struct Attn {
+  static constexpr int KB = D / 32;    // 32-channel blocks
+  static constexpr int BPG = KB / GC;  // of them per scale group
+  static constexpr int kWaves = 4;
+  static constexpr int kRowsWave = 16 * QT;
+  static constexpr int kRowsGroup = TOK ? kRowsWave : kWaves * kRowsWave;
+  // wavefronts per SIMD the registers are budgeted for: the most without spills
+  static constexpr int kWavesSimd = D == 64    ? (QT == 1 ? 4 - GC / 2 : 4 - GC)
+                                    : D == 128 ? (QT == 1 ? (GC == 1 ? 3 : 2) : (GC <= 2 ? 2 : 1))
+                                               : 1;
+
+  struct Step {
+    Tile<D, GC> t[2];
+    bool there[2];
+  };
+};
+
+template <int D, int GC, int QT, bool TOK>
+__global__ __launch_bounds__(256, (Attn<D, GC, QT, TOK>::kWavesSimd)) void attn_kernel(AttnArgs a, int tiles) {
+  using C = Attn<D, GC, QT, TOK>;
+  using Step = typename C::Step;
+  constexpr int KB = C::KB, BPG = C::BPG;
   const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, c4 = lane >> 4;
-  const int head = (int)(blockIdx.x / tiles % a.cache.kv_heads), seq = (int)(blockIdx.x / tiles / a.cache.kv_heads);
-  const int share = a.q_heads / a.cache.kv_heads;
+  // blocks: split fastest, then row tile (last rows, the longest spans, first), head, sequence
+  unsigned at = blockIdx.x;
+  const int split = (int)(at % (unsigned)a.splits);
+  at /= (unsigned)a.splits;
+  const int tile_q = tiles - 1 - (int)(at % (unsigned)tiles);
+  at /= (unsigned)tiles;
+  Job w;
+  if (!make_job(a, (int)(at / (unsigned)a.cache.kv_heads), (int)(at % (unsigned)a.cache.kv_heads), &w)) return;
+  const int r0 = tile_q * C::kRowsGroup + (TOK ? 0 : wave * C::kRowsWave);
+  if (tile_q * C::kRowsGroup >= w.rows) return;
+  const bool idle = r0 >= w.rows;  // a wavefront without rows (only where rows are its own)
+  if (!TOK && idle) return;        // no barrier follows there
 
-  // the sequence's rows and length, kept inside what the arguments promise
-  const int first = min(max(a.q_offsets[seq], 0), a.tokens);
-  const int nq = min(min(max(a.q_offsets[seq + 1], first), a.tokens) - first, a.max_q);
-  const int len = min(max(a.kv_lens[seq], 0), a.max_kv);
-  const int rows = nq * share;
-  const int r0 = (int)(blockIdx.x % tiles * 4 + threadIdx.x / kWave) * 16 * QT;
-  if (r0 >= rows) return;
-
-  R r;
+  half8_t q[QT][KB];
+  float bias[QT][GC];  // -(264 * sum of q over elements 0, 1, 4, 5 + 24 * the others), per scale group
+  int pos[QT];         // position of the lane's row: its own last visible key; -1: no row
+  float m[QT], base[QT], l[QT];
+  float4_t acc[QT][2 * KB];
 #pragma unroll
   for (int t = 0; t < QT; ++t) {
-    const int m = r0 + 16 * t + col;
-    const bool real = m < rows;
-    const int i = min(m, rows - 1) / share, hs = min(m, rows - 1) - i * share;
-    r.pos[t] = real ? len - nq + i : -1;
-    const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(first + i) * a.q_stride +
-                          (int64_t)(head * share + hs) * D + 8 * c4;
+    const int row = r0 + 16 * t + col;
+    const int i = min(row, w.rows - 1) / w.share, hs = min(row, w.rows - 1) - i * w.share;
+    pos[t] = row < w.rows ? w.len - w.nq + i : -1;
+    const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.first + i) * a.q_stride +
+                          (int64_t)(w.head * w.share + hs) * D + 8 * c4;
 #pragma unroll
-    for (int b = 0; b < KB; ++b) r.q[t][b] = as_half8(*reinterpret_cast<const uint4*>(src + 32 * b));
-    r.m[t] = r.base[t] = kLowest;
-    r.l[t] = 0.0f;
+    for (int b = 0; b < KB; ++b) q[t][b] = as_half8(*reinterpret_cast<const uint4*>(src + 32 * b));
 #pragma unroll
-    for (int b = 0; b < 2 * KB; ++b) r.acc[t][b] = float4_t{0.f, 0.f, 0.f, 0.f};
+    for (int g = 0; g < GC; ++g) {
+      float s2 = 0.0f, s6 = 0.0f;
+#pragma unroll
+      for (int b = g * BPG; b < (g + 1) * BPG; ++b)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) (e & 2 ? s6 : s2) += (float)q[t][b][e];
+      float sum = 264.0f * s2 + 24.0f * s6;
+      sum += __shfl_xor(sum, 16, 64);
+      sum += __shfl_xor(sum, 32, 64);
+      bias[t][g] = -sum;
+    }
+    m[t] = base[t] = kLowest;
+    l[t] = 0.0f;
+#pragma unroll
+    for (int b = 0; b < 2 * KB; ++b) acc[t][b] = float4_t{0.f, 0.f, 0.f, 0.f};
   }
 
-  // keys any of the rows sees: [t_first, t_last)
-  const int pos_lo = len - nq + r0 / share;
-  const int pos_hi = len - nq + (min(r0 + 16 * QT, rows) - 1) / share;
-  const int t_last = pos_hi + 1;
-  const int window = a.window > 0 ? a.window : t_last + 1;
-  const int t_first = max(0, pos_lo - window + 1) / kStep * kStep;
-  const int page_size = a.cache.page_size, tpp = page_size / kTokTile;
-  const int32_t* table = a.block_table + (int64_t)seq * a.max_blocks;
+  const Span sp = span_of(a, w, r0, C::kRowsWave);
+  // this workgroup's part of the keys
+  const int t_first = sp.first + split * a.chunk;
+  const int t_last = a.splits > 1 ? min(sp.last, t_first + a.chunk) : sp.last;
+  const int tpp = a.cache.page_size / kTokTile;
+  const int32_t* table = a.block_table + (int64_t)w.seq * a.max_blocks;
   const float scale = a.scale * 1.4426950408889634f;
   const DequantRegs dq = DequantRegs::make();
+  const KRegs kr = KRegs::make();
   float exp_v = -64.0f;  // E (wave-uniform)
   uint32_t cap_v = 0;    // largest V scale that E covers, as float16 bits
 
-  for (int t0 = t_first; t0 < t_last; t0 += kStep) {
-    Tile<D, GC> tile[2];
-    bool there[2];
+  constexpr int kStride = TOK ? C::kWaves * 2 : 2;  // tiles from one step of a wavefront to the next
+  const int stride_block = kStride / tpp, stride_rem = kStride - stride_block * tpp;
+  const int last_tile = max(t_last - 1, 0) / kTokTile;
+  Walk next;
+  next.tile = t_first / kTokTile + (TOK ? 2 * wave : 0);
+  next.block = next.tile / tpp;
+  next.in_page = next.tile - next.block * tpp;
+  int page[2];      // page numbers of `next`'s two tiles
+  int in_page2;     // and where the second lies in its page
+  auto fetch_pages = [&]() __attribute__((always_inline)) {
+    const bool wraps = next.in_page + 1 == tpp;
+    in_page2 = wraps ? 0 : next.in_page + 1;
+    const int b2 = next.block + (wraps ? 1 : 0);
+    // entries behind the last key's are not read
+    page[0] = next.tile <= last_tile && next.block < a.max_blocks ? table[next.block] : -1;
+    page[1] = next.tile + 1 <= last_tile && b2 < a.max_blocks ? table[b2] : -1;
+  };
+  // Loads of the step at `next`, which then moves on. A tile behind the last key or of a
+  // page outside the cache is read from page 0 and masked.
+  auto load = [&](Step& s) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      // a tile behind the last key, or of a page outside the cache, is read from a
-      // valid place and masked
-      const int key = min(t0 + 16 * j, (t_last - 1) / kTokTile * kTokTile);
-      const int block = key / page_size;
-      const int page = block < a.max_blocks ? table[block] : -1;
-      there[j] = page >= 0 && page < a.cache.pages && t0 + 16 * j < t_last;
-      const int64_t at = ((int64_t)(there[j] ? page : 0) * a.cache.kv_heads + head) * tpp + (key - block * page_size) / kTokTile;
-      load_tile<D, GC>(tile[j], a.cache, at, lane);
+      s.there[j] = (unsigned)page[j] < (unsigned)a.cache.pages;
+      const int64_t tile =
+          ((int64_t)(s.there[j] ? page[j] : 0) * a.cache.kv_heads + w.head) * tpp + (j ? in_page2 : next.in_page);
+      load_tile<D, GC>(s.t[j], a.cache, tile, lane);
     }
-    const bool edge = t0 + kStep > pos_lo + 1 || t0 <= pos_hi - window || !there[0] || !there[1];
+    next.tile += kStride;
+    next.block += stride_block;
+    next.in_page += stride_rem;
+    if (next.in_page >= tpp) {
+      next.in_page -= tpp;
+      ++next.block;
+    }
+    fetch_pages();
+  };
 
-    // scores, base 2
-    float ks[2][GC][4], vs[2][GC][4];
+  auto compute = [&](Step& st, int t0) __attribute__((always_inline)) {
+    const bool edge =
+        t0 + kStep > sp.pos_lo + 1 || t0 <= sp.pos_hi - sp.window || t0 + kStep > t_last || !st.there[0] || !st.there[1];
+    if (edge) {
+      // what no row sees may hold anything: 0 * NaN must not arise
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int g = 0; g < GC; ++g) {
+          half4_t kh = __builtin_bit_cast(half4_t, st.t[j].ks[g]), vh = __builtin_bit_cast(half4_t, st.t[j].vs[g]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int key = t0 + 16 * j + 4 * c4 + i;
+            const bool seen = st.there[j] && key < t_last && key > sp.pos_lo - sp.window;
+            kh[i] = seen ? kh[i] : (_Float16)0.0f;
+            vh[i] = seen ? vh[i] : (_Float16)0.0f;
+          }
+          st.t[j].ks[g] = __builtin_bit_cast(uint2, kh);
+          st.t[j].vs[g] = __builtin_bit_cast(uint2, vh);
+        }
+    }
+    uint32_t hidden[QT] = {};  // keys of the lane that its row does not see
+    // E, where a V scale exceeds what it covers
     uint32_t vmax = 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int g = 0; g < GC; ++g) {
-        const half4_t kh = __builtin_bit_cast(half4_t, tile[j].ks[g]), vh = __builtin_bit_cast(half4_t, tile[j].vs[g]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // an infinite scale makes its key's score NaN (0 codes times infinity), not +-inf
-          ks[j][g][i] = __builtin_fmaf((float)kh[i], scale, (float)kh[i] * 0.0f);
-          const int key = t0 + 16 * j + 4 * c4 + i;
-          const bool seen = !edge || (there[j] && key < t_last && key > pos_lo - window);
-          // what no row sees may hold anything: 0 * NaN must not arise
-          vs[j][g][i] = seen ? (float)vh[i] : 0.0f;
-          const uint32_t bits = __builtin_bit_cast(uint16_t, vh[i]);
-          vmax = max(vmax, seen && bits < 0x7C00u ? bits : 0u);
-        }
+        const uint2 r = st.t[j].vs[g];
+        vmax = max(vmax, max(max(r.x & 0xFFFFu, r.x >> 16), max(r.y & 0xFFFFu, r.y >> 16)));
       }
     if (__any(vmax > cap_v)) {
+      // the largest finite one, up to the end of its binade
+      vmax = cap_v;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int g = 0; g < GC; ++g)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t bits = ((i < 2 ? st.t[j].vs[g].x : st.t[j].vs[g].y) >> (16 * (i & 1))) & 0xFFFFu;
+            vmax = max(vmax, bits < 0x7C00u ? bits : 0u);
+          }
 #pragma unroll
       for (int s = 1; s < 64; s <<= 1) vmax = max(vmax, (uint32_t)__shfl_xor((int)vmax, s, 64));
-      cap_v = vmax | 0x3FFu;  // up to the end of its binade
+      cap_v = vmax | 0x3FFu;
       exp_v = (float)(int)(cap_v >> 10) - 14.0f - kHeadroom;
+#pragma unroll
+      for (int t = 0; t < QT; ++t) {
+        const float b = m[t] + exp_v, alpha = exp2_fast(base[t] - b);
+        base[t] = b;
+        l[t] *= alpha;
+#pragma unroll
+        for (int c = 0; c < 2 * KB; ++c) acc[t][c] *= alpha;
+      }
     }
 
+    // scores, base 2
     float s[QT][2][4];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       half8_t ka[KB];
-      const half2_t lo_bias = {(_Float16)-1032.0f, (_Float16)-1032.0f};
-      const half2_t hi_bias = {(_Float16)-72.0f, (_Float16)-72.0f};
 #pragma unroll
-      for (int b = 0; b < KB; ++b) ka[b] = dequant8r(tile[j].k[b], dq, lo_bias, hi_bias);
+      for (int b = 0; b < KB; ++b) ka[b] = k_operand(st.t[j].k[b], kr);
 #pragma unroll
-      for (int t = 0; t < QT; ++t) {
+      for (int g = 0; g < GC; ++g) {
+        const half4_t kh = __builtin_bit_cast(half4_t, st.t[j].ks[g]);
+        float ks[4];
 #pragma unroll
-        for (int g = 0; g < GC; ++g) {
-          float4_t part = {0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < 4; ++i) ks[i] = (float)kh[i] * scale;
 #pragma unroll
-          for (int b = 0; b < BPG; ++b) part = mfma(ka[g * BPG + b], r.q[t][g * BPG + b], part);
+        for (int t = 0; t < QT; ++t) {
+          float4_t part = {bias[t][g], bias[t][g], bias[t][g], bias[t][g]};
+#pragma unroll
+          for (int b = 0; b < BPG; ++b) part = mfma(ka[g * BPG + b], q[t][g * BPG + b], part);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            s[t][j][i] = g == 0 ? part[i] * ks[j][g][i] : __builtin_fmaf(part[i], ks[j][g][i], s[t][j][i]);
+            s[t][j][i] = g == 0 ? part[i] * ks[i] : __builtin_fmaf(part[i], ks[i], s[t][j][i]);
         }
       }
     }
@@ -228,77 +375,218 @@ __global__ __launch_bounds__(256) void attn_kernel(AttnArgs a, unsigned tiles) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int key = t0 + 16 * j + 4 * c4 + i;
-            if (!there[j] || key > r.pos[t] || key <= r.pos[t] - window) s[t][j][i] = -__builtin_inff();
+            if (!st.there[j] || key >= t_last || key > pos[t] || key <= pos[t] - sp.window) {
+              s[t][j][i] = -__builtin_inff();
+              hidden[t] |= 1u << (4 * j + i);
+            }
           }
     }
 
-    // softmax step, weights to float16
-    half8_t p[QT][GC];
+    // a score far above a row's held maximum?
+    float mx[QT];
+    bool raise = false;
 #pragma unroll
     for (int t = 0; t < QT; ++t) {
-      float mx = r.m[t];
+      float v = s[t][0][0];
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int e = 1; e < 8; ++e) v = fmaxf(v, s[t][e >> 2][e & 3]);
+      mx[t] = v;
+      raise |= v > m[t] + kSlack;
+    }
+    if (__any(raise)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[t][j][i]);
-      mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-      const float base = mx + exp_v;
-      const float alpha = exp2_fast(r.base[t] - base);
-      r.m[t] = mx;
-      r.base[t] = base;
-      r.l[t] *= alpha;
+      for (int t = 0; t < QT; ++t) {
+        float v = fmaxf(mx[t], m[t]);
+        v = fmaxf(v, __shfl_xor(v, 16, 64));
+        v = fmaxf(v, __shfl_xor(v, 32, 64));
+        const float b = v + exp_v, alpha = exp2_fast(base[t] - b);
+        m[t] = v;
+        base[t] = b;
+        l[t] *= alpha;
 #pragma unroll
-      for (int b = 0; b < 2 * KB; ++b) r.acc[t][b] *= alpha;
+        for (int c = 0; c < 2 * KB; ++c) acc[t][c] *= alpha;
+      }
+    }
+
+    // weights, to float16 with the V scale in them
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float e = exp2_fast(s[t][j][i] - base);
-          r.l[t] += e;
-#pragma unroll
-          for (int g = 0; g < GC; ++g)  // a key that this row does not see may have an infinite scale
-            p[t][g][4 * j + i] = (_Float16)(edge && s[t][j][i] == -__builtin_inff() ? 0.0f : e * vs[j][g][i]);
+          s[t][j][i] = exp2_fast(s[t][j][i] - base[t]);
+          l[t] += s[t][j][i];
         }
+    half8_t p[QT][GC];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int g = 0; g < GC; ++g) {
+        const half4_t vh = __builtin_bit_cast(half4_t, st.t[j].vs[g]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float vs = (float)vh[i];
+#pragma unroll
+          for (int t = 0; t < QT; ++t) p[t][g][4 * j + i] = (_Float16)(s[t][j][i] * vs);
+        }
+      }
+    if (edge) {
+      // a key that one row sees and another does not may have an infinite scale
+#pragma unroll
+      for (int t = 0; t < QT; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int g = 0; g < GC; ++g)
+              if (hidden[t] >> (4 * j + i) & 1u) p[t][g][4 * j + i] = (_Float16)0.0f;
     }
 
 #pragma unroll
     for (int b = 0; b < KB; ++b) {
-      const half8_t lo = v_operand<false>(tile[0].v[b], tile[1].v[b], dq);
-      const half8_t hi = v_operand<true>(tile[0].v[b], tile[1].v[b], dq);
+      const half8_t lo = v_operand<false>(st.t[0].v[b], st.t[1].v[b], dq);
+      const half8_t hi = v_operand<true>(st.t[0].v[b], st.t[1].v[b], dq);
 #pragma unroll
       for (int t = 0; t < QT; ++t) {
-        r.acc[t][2 * b] = mfma(lo, p[t][b / BPG], r.acc[t][2 * b]);
-        r.acc[t][2 * b + 1] = mfma(hi, p[t][b / BPG], r.acc[t][2 * b + 1]);
+        acc[t][2 * b] = mfma(lo, p[t][b / BPG], acc[t][2 * b]);
+        acc[t][2 * b + 1] = mfma(hi, p[t][b / BPG], acc[t][2 * b + 1]);
+      }
+    }
+  };
+
+  // one step in flight while the one before is computed
+  const int t_own = t_first + (TOK ? kStep * wave : 0);
+  if (t_own < t_last) {
+    Step s0, s1;
+    fetch_pages();
+    load(s0);
+    for (int t0 = t_own;;) {
+      load(s1);
+      compute(s0, t0);
+      if ((t0 += kStride * kTokTile) >= t_last) break;
+      load(s0);
+      compute(s1, t0);
+      if ((t0 += kStride * kTokTile) >= t_last) break;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < QT; ++t) {
+    l[t] += __shfl_xor(l[t], 16, 64);
+    l[t] += __shfl_xor(l[t], 32, 64);
+  }
+
+  // Result of row `row`, channels 16 c + 4 c4 .. + 3: the output, or the split's part.
+  auto store = [&](int row, int c, float4_t o, float sum, float b) __attribute__((always_inline)) {
+    if (row >= w.rows) return;
+    const int i = row / w.share, hs = row - i * w.share;
+    const int64_t r = (int64_t)(w.first + i) * a.q_heads + w.head * w.share + hs;
+    if (a.splits > 1) {
+      const int64_t rs = r * a.splits + split;
+      *reinterpret_cast<float4_t*>(a.part_o + rs * D + 16 * c + 4 * c4) = o;
+      if (c == 0 && c4 == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * rs) = make_float2(b, sum);
+      return;
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    half4_t h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = (_Float16)(o[e] * inv);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + r * D + 16 * c + 4 * c4) = __builtin_bit_cast(uint2, h);
+  };
+
+  if constexpr (!TOK) {
+#pragma unroll
+    for (int t = 0; t < QT; ++t)
+#pragma unroll
+      for (int c = 0; c < 2 * KB; ++c) store(r0 + 16 * t + col, c, acc[t][c], l[t], base[t]);
+  } else {
+    // the four wavefronts' parts of the same rows, added in order
+    __shared__ float4_t buf[C::kWaves][2 * KB][kWave];
+    __shared__ float2 ml[C::kWaves][16];
+#pragma unroll
+    for (int t = 0; t < QT; ++t) {
+      if (t > 0) __syncthreads();
+#pragma unroll
+      for (int c = 0; c < 2 * KB; ++c) buf[wave][c][lane] = acc[t][c];
+      if (c4 == 0) ml[wave][col] = make_float2(base[t], l[t]);
+      __syncthreads();
+      float top = ml[0][col].x, sum = 0.0f, f[C::kWaves];
+#pragma unroll
+      for (int v = 1; v < C::kWaves; ++v) top = fmaxf(top, ml[v][col].x);
+#pragma unroll
+      for (int v = 0; v < C::kWaves; ++v) {
+        f[v] = exp2_fast(ml[v][col].x - top);
+        sum = __builtin_fmaf(ml[v][col].y, f[v], sum);
+      }
+      for (int c = wave; c < 2 * KB; c += C::kWaves) {
+        float4_t o = buf[0][c][lane] * f[0];
+#pragma unroll
+        for (int v = 1; v < C::kWaves; ++v) o += buf[v][c][lane] * f[v];
+        store(r0 + 16 * t + col, c, o, sum, top);
       }
     }
   }
+}
 
+// Joins the splits of a row, in order: one wavefront half, quarter ... (D / 4 lanes) a row.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows_group, int64_t rows) {
+  constexpr int LPR = D / 4;
+  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;  // (sequence, head, row)
+  const int ch = 4 * (threadIdx.x % LPR);
+  const int64_t sh = at / rows;
+  const int row = (int)(at - sh * rows);
+  if (sh >= (int64_t)a.seqs * a.cache.kv_heads) return;
+  Job w;
+  if (!make_job(a, (int)(sh / a.cache.kv_heads), (int)(sh % a.cache.kv_heads), &w) || row >= w.rows) return;
+  // the row's tile decides which splits had keys
+  const Span sp = span_of(a, w, row / rows_group * rows_group, rows_group);
+  const int n = min((max(sp.last - sp.first, 0) + a.chunk - 1) / a.chunk, a.splits);
+  const int i = row / w.share, hs = row - i * w.share;
+  const int64_t r = (int64_t)(w.first + i) * a.q_heads + w.head * w.share + hs;
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + r * a.splits;
+  const float* po = a.part_o + r * a.splits * D + ch;
+  float top = kLowest;
+  for (int s = 0; s < n; ++s) top = fmaxf(top, ml[s].x);
+  float sum = 0.0f;
+  float4_t o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) {
+    const float f = exp2_fast(ml[s].x - top);
+    sum = __builtin_fmaf(ml[s].y, f, sum);
+    o += *reinterpret_cast<const float4_t*>(po + (int64_t)s * D) * f;
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  half4_t h;
 #pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    float l = r.l[t];
-    l += __shfl_xor(l, 16, 64);
-    l += __shfl_xor(l, 32, 64);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    const int m = r0 + 16 * t + col;
-    if (m >= rows) continue;
-    const int i = m / share, hs = m - i * share;
-    uint16_t* dst = static_cast<uint16_t*>(a.out) + ((int64_t)(first + i) * a.q_heads + head * share + hs) * D + 4 * c4;
-#pragma unroll
-    for (int b = 0; b < 2 * KB; ++b) {
-      half4_t h;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) h[e] = (_Float16)(r.acc[t][b][e] * inv);
-      *reinterpret_cast<uint2*>(dst + 16 * b) = __builtin_bit_cast(uint2, h);
-    }
+  for (int e = 0; e < 4; ++e) h[e] = (_Float16)(o[e] * inv);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + r * D + ch) = __builtin_bit_cast(uint2, h);
+}
+
+template <int D, int GC, int QT, bool TOK>
+void launch_q(const AttnArgs& a, hipStream_t stream) {
+  using C = Attn<D, GC, QT, TOK>;
+  const int64_t rows = (int64_t)a.max_q * (a.q_heads / a.cache.kv_heads);
+  const int tiles = (int)((rows + C::kRowsGroup - 1) / C::kRowsGroup);
+  const int64_t blocks = (int64_t)a.splits * tiles * a.cache.kv_heads * a.seqs;
+  hipLaunchKernelGGL((attn_kernel<D, GC, QT, TOK>), dim3((unsigned)blocks), dim3(256), 0, stream, a, tiles);
+  if (a.splits > 1) {
+    const int64_t threads = rows * a.cache.kv_heads * a.seqs * (D / 4);
+    hipLaunchKernelGGL(attn_join_kernel<D>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, a,
+                       C::kRowsWave, rows);
   }
 }
 
 template <int D, int GC>
 hipError_t launch_t(const AttnArgs& a, hipStream_t stream) {
-  const int64_t rows = (int64_t)a.max_q * (a.q_heads / a.cache.kv_heads);
-  const unsigned tiles = (unsigned)((rows + 63) / 64);
-  hipLaunchKernelGGL((attn_kernel<D, GC, 1>), dim3(tiles * a.cache.kv_heads * a.seqs), dim3(256), 0, stream, a, tiles);
+  if constexpr (D < 256) {  // at 256 channels two row tiles do not fit the registers
+    if (a.tiles_wave == 2) {
+      a.tok ? launch_q<D, GC, 2, true>(a, stream) : launch_q<D, GC, 2, false>(a, stream);
+      return hipGetLastError();
+    }
+  }
+  a.tok ? launch_q<D, GC, 1, true>(a, stream) : launch_q<D, GC, 1, false>(a, stream);
   return hipGetLastError();
 }
 

@@ -125,7 +125,13 @@ struct AttnArgs {
   float scale;
   int window;  // 0: none
   void* out;   // [tokens][q_heads][head_dim]
-  void* workspace;
+  // launch shape
+  bool tok;        // the wavefronts of a workgroup share rows and split the keys
+  int tiles_wave;  // tiles of 16 rows per wavefront: 1 or 2
+  int splits;      // workgroups splitting a row tile's keys, `chunk` each (a multiple of 128)
+  int chunk;
+  float* part_o;   // splits > 1: float32 [tokens][q_heads][splits][head_dim]
+  float* part_ml;  // and [tokens][q_heads][splits][2]: what exponents are relative to, sum
 };
 
 // Adapters beside a product (include/q4_lora.h). phase 0: A x into t; phase 1: y from the

@@ -116,22 +116,25 @@ __device__ __forceinline__ half8_t norm_rope(half8_t x, const uint16_t* weight, 
 }
 
 // INT4 codes of a lane's 8 values (one nibble each, element 0 lowest, two's complement
-// q) and the float16 scale of its group of GL lanes: the KV cache's rule (q4_kv.hip).
+// q) and the float16 scale of its group of GL lanes: the KV cache's rule (q4_kv.hip). The
+// group's largest magnitude is taken over float16 bit patterns, which order as the
+// values do with infinity and NaN on top; such a group gets a NaN scale.
 __device__ __forceinline__ uint32_t quantize8(half8_t h, int GL, _Float16* scale) {
-  float v[8];
-  float a = 0.0f;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    v[e] = (float)h[e];
-    a = fmaxf(a, fabsf(v[e]));
-  }
-  for (int m = 1; m < GL; m <<= 1) a = fmaxf(a, __shfl_xor(a, m, 64));
-  const _Float16 s16 = (_Float16)(fmaxf(a, 1e-12f) * (1.0f / 7.0f));
+  typedef uint16_t us2 __attribute__((ext_vector_type(2)));
+  const uint4 bits = __builtin_bit_cast(uint4, h);
+  auto mag = [](uint32_t w) { return __builtin_bit_cast(us2, w & 0x7FFF7FFFu); };
+  us2 a2 = __builtin_elementwise_max(__builtin_elementwise_max(mag(bits.x), mag(bits.y)),
+                                     __builtin_elementwise_max(mag(bits.z), mag(bits.w)));
+  int a = max((int)a2.x, (int)a2.y);
+  for (int m = 1; m < GL; m <<= 1) a = max(a, __shfl_xor(a, m, 64));
+  const float amax = (float)__builtin_bit_cast(_Float16, (uint16_t)a);
+  const _Float16 s16 =
+      a < 0x7C00 ? (_Float16)(fmaxf(amax, 1e-12f) * (1.0f / 7.0f)) : __builtin_bit_cast(_Float16, (uint16_t)0x7E00);
   const float rcp = rtn_recip((float)s16);
   uint32_t word = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int q = (int)fminf(fmaxf(rtn_quot(v[e], rcp), -8.0f), 7.0f);
+    const int q = (int)fminf(fmaxf(rtn_quot((float)h[e], rcp), -8.0f), 7.0f);
     word |= (uint32_t)(q & 0xF) << (4 * e);
   }
   *scale = s16;
