@@ -128,6 +128,12 @@ __device__ __forceinline__ void load_tile(Tile<D, GC>& t, const PagedArgs& c, in
   }
 }
 
+// Read-only int32 arrays at uniform indexes go through the scalar cache: a vector load
+// would have to be waited for behind the tile loads issued before it (they return in
+// order), which would leave none in flight.
+typedef const __attribute__((address_space(4))) int32_t* ScalarInts;
+__device__ __forceinline__ ScalarInts scalar_ints(const int32_t* p) { return (ScalarInts)(uintptr_t)p; }
+
 // What a workgroup works on.
 struct Job {
   int first, rows, len, nq;  // the sequence's first row of q, rows = nq * share, length
@@ -139,9 +145,10 @@ __device__ __forceinline__ bool make_job(const AttnArgs& a, int seq, int head, J
   w->seq = seq;
   w->head = head;
   w->share = a.q_heads / a.cache.kv_heads;
-  w->first = min(max(a.q_offsets[seq], 0), a.tokens);
-  w->nq = min(min(max(a.q_offsets[seq + 1], w->first), a.tokens) - w->first, a.max_q);
-  w->len = min(max(a.kv_lens[seq], 0), a.max_kv);
+  const ScalarInts offsets = scalar_ints(a.q_offsets);
+  w->first = min(max(offsets[seq], 0), a.tokens);
+  w->nq = min(min(max(offsets[seq + 1], w->first), a.tokens) - w->first, a.max_q);
+  w->len = min(max(scalar_ints(a.kv_lens)[seq], 0), a.max_kv);
   w->rows = w->nq * w->share;
   return w->rows > 0;
 }
@@ -242,7 +249,7 @@ __global__ __launch_bounds__(256, (Attn<D, GC, QT, TOK>::kWavesSimd)) void attn_
   const int t_first = sp.first + split * a.chunk;
   const int t_last = a.splits > 1 ? min(sp.last, t_first + a.chunk) : sp.last;
   const int tpp = a.cache.page_size / kTokTile;
-  const int32_t* table = a.block_table + (int64_t)w.seq * a.max_blocks;
+  const ScalarInts table = scalar_ints(a.block_table + (int64_t)w.seq * a.max_blocks);
   const float scale = a.scale * 1.4426950408889634f;
   const DequantRegs dq = DequantRegs::make();
   const KRegs kr = KRegs::make();
@@ -529,39 +536,57 @@ __global__ __launch_bounds__(256, (Attn<D, GC, QT, TOK>::kWavesSimd)) void attn_
   }
 }
 
-// Joins the splits of a row, in order: one wavefront half, quarter ... (D / 4 lanes) a row.
+// Joins the splits of a row: a workgroup per row, D / 4 lanes a group of channels, the
+// 1024 / D groups taking every such split and then added in order (one group walking all
+// splits of a 100K context took as long as a quarter of the attention itself).
 template <int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows_group, int64_t rows) {
-  constexpr int LPR = D / 4;
-  const int64_t at = ((int64_t)blockIdx.x * 256 + threadIdx.x) / LPR;  // (sequence, head, row)
-  const int ch = 4 * (threadIdx.x % LPR);
-  const int64_t sh = at / rows;
-  const int row = (int)(at - sh * rows);
-  if (sh >= (int64_t)a.seqs * a.cache.kv_heads) return;
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows_group, unsigned rows) {
+  constexpr int LPR = D / 4, G = 256 / LPR;
+  __shared__ float4_t buf[G][LPR];
+  __shared__ float2 part[G];
+  const int lane = threadIdx.x % LPR, g = threadIdx.x / LPR;
+  const unsigned sh = blockIdx.x / rows;  // sequence and head
+  const int row = (int)(blockIdx.x - sh * rows);
   Job w;
-  if (!make_job(a, (int)(sh / a.cache.kv_heads), (int)(sh % a.cache.kv_heads), &w) || row >= w.rows) return;
+  if (!make_job(a, (int)(sh / (unsigned)a.cache.kv_heads), (int)(sh % (unsigned)a.cache.kv_heads), &w) || row >= w.rows)
+    return;
   // the row's tile decides which splits had keys
   const Span sp = span_of(a, w, row / rows_group * rows_group, rows_group);
   const int n = min((max(sp.last - sp.first, 0) + a.chunk - 1) / a.chunk, a.splits);
   const int i = row / w.share, hs = row - i * w.share;
   const int64_t r = (int64_t)(w.first + i) * a.q_heads + w.head * w.share + hs;
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + r * a.splits;
-  const float* po = a.part_o + r * a.splits * D + ch;
-  float top = kLowest;
-  for (int s = 0; s < n; ++s) top = fmaxf(top, ml[s].x);
-  float sum = 0.0f;
+  const float* po = a.part_o + r * a.splits * D + 4 * lane;
+  float top = kLowest, sum = 0.0f;
   float4_t o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-  for (int s = 0; s < n; ++s) {
-    const float f = exp2_fast(ml[s].x - top);
-    sum = __builtin_fmaf(ml[s].y, f, sum);
+  for (int s = g; s < n; s += G) top = fmaxf(top, ml[s].x);
+#pragma unroll 2
+  for (int s = g; s < n; s += G) {
+    const float2 v = ml[s];
+    const float f = exp2_fast(v.x - top);
+    sum = __builtin_fmaf(v.y, f, sum);
     o += *reinterpret_cast<const float4_t*>(po + (int64_t)s * D) * f;
+  }
+  buf[g][lane] = o;
+  if (lane == 0) part[g] = make_float2(top, sum);
+  __syncthreads();
+  if (g > 0) return;
+  float all = part[0].x, f[G];
+#pragma unroll
+  for (int v = 1; v < G; ++v) all = fmaxf(all, part[v].x);
+  sum = 0.0f;
+  o = float4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int v = 0; v < G; ++v) {
+    f[v] = exp2_fast(part[v].x - all);
+    sum = __builtin_fmaf(part[v].y, f[v], sum);
+    o += buf[v][lane] * f[v];
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   half4_t h;
 #pragma unroll
   for (int e = 0; e < 4; ++e) h[e] = (_Float16)(o[e] * inv);
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + r * D + ch) = __builtin_bit_cast(uint2, h);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + r * D + 4 * lane) = __builtin_bit_cast(uint2, h);
 }
 
 template <int D, int GC, int QT, bool TOK>
@@ -572,9 +597,8 @@ void launch_q(const AttnArgs& a, hipStream_t stream) {
   const int64_t blocks = (int64_t)a.splits * tiles * a.cache.kv_heads * a.seqs;
   hipLaunchKernelGGL((attn_kernel<D, GC, QT, TOK>), dim3((unsigned)blocks), dim3(256), 0, stream, a, tiles);
   if (a.splits > 1) {
-    const int64_t threads = rows * a.cache.kv_heads * a.seqs * (D / 4);
-    hipLaunchKernelGGL(attn_join_kernel<D>, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, stream, a,
-                       C::kRowsWave, rows);
+    const int64_t all = rows * a.cache.kv_heads * a.seqs;
+    hipLaunchKernelGGL(attn_join_kernel<D>, dim3((unsigned)all), dim3(256), 0, stream, a, C::kRowsWave, (unsigned)rows);
   }
 }
 
