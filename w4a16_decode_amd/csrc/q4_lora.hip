@@ -87,25 +87,28 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void lora_shrink_kernel(LoraArgs
   }
 }
 
-// y = the product's split sums + scaling * B t, for 16 rows and 256 outputs a workgroup.
+// y = the product's split sums + scaling * B t, for `rows` (at most 16) rows and 256
+// outputs a workgroup; a thread owns one output channel and keeps its B row while the
+// adapter stays the same.
 template <int RT>
-__global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int splits, int n_blocks) {
+__global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int splits, int n_blocks, int rows) {
   __shared__ float t[16][16 * RT];
   __shared__ int ids[16];
   const int nb = blockIdx.x % n_blocks;
-  const int b0 = (int)(blockIdx.x / n_blocks) * 16;
-  const int nrows = min(16, a.B - b0);
-  if (threadIdx.x < 16) {
-    const int id = (int)threadIdx.x < nrows ? a.ids[b0 + threadIdx.x] : -1;
-    ids[threadIdx.x] = id < a.adapters ? id : -1;
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < 16 * 16 * RT; e += 256) {
+  const int b0 = (int)(blockIdx.x / n_blocks) * rows;
+  const int nrows = min(rows, a.B - b0);
+  for (int e = threadIdx.x; e < nrows * 16 * RT; e += 256) {
     const int i = e / (16 * RT), r = e % (16 * RT);
+    const int id = a.ids[b0 + i];
+    const bool real = id >= 0 && id < a.adapters;
+    if (r == 0) ids[i] = real ? id : -1;
     float sum = 0.0f;
-    if (ids[i] >= 0 && r < a.rank) {
-      for (int s = 0; s < splits; ++s) sum += a.t[((int64_t)s * a.B + b0 + i) * a.rank + r];
-      sum *= a.scaling[ids[i]];
+    if (real && r < a.rank) {
+      const float* src = a.t + (int64_t)(b0 + i) * a.rank + r;
+      const int64_t stride = (int64_t)a.B * a.rank;
+#pragma unroll 8
+      for (int s = 0; s < splits; ++s) sum += src[s * stride];
+      sum *= a.scaling[id];
     }
     t[i][r] = sum;
   }
@@ -113,29 +116,41 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int splits
   const int n = nb * 256 + threadIdx.x;
   if (n >= a.N) return;
   uint16_t* y = static_cast<uint16_t*>(a.y);
+  const int64_t split_stride = (int64_t)a.B * a.N;
   half8_t w[2 * RT];
   int held = -1;
-  for (int i = 0; i < nrows; ++i) {
-    const int64_t at = (int64_t)(b0 + i) * a.N + n;
-    float sum = 0.0f;
-    for (int k = 0; k < a.gemm_splits; ++k) sum += a.partials[(int64_t)k * a.B * a.N + at];
-    const int id = ids[i];
-    if (id >= 0) {
-      if (id != held) {
-        const uint16_t* src = static_cast<const uint16_t*>(a.lora_b) + ((int64_t)id * a.N + n) * a.rank;
+  for (int i0 = 0; i0 < nrows; i0 += 4) {
+    // four rows' sums in flight
+    float sum[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float* src = a.partials + (int64_t)(b0 + min(i0 + u, nrows - 1)) * a.N + n;
+      sum[u] = 0.0f;
+#pragma unroll 2
+      for (int k = 0; k < a.gemm_splits; ++k) sum[u] += src[k * split_stride];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = i0 + u;
+      if (i >= nrows) break;
+      const int id = ids[i];
+      if (id >= 0) {
+        if (id != held) {
+          const uint16_t* src = static_cast<const uint16_t*>(a.lora_b) + ((int64_t)id * a.N + n) * a.rank;
+#pragma unroll
+          for (int q = 0; q < 2 * RT; ++q)
+            w[q] = as_half8(*reinterpret_cast<const uint4*>(src + 8 * min(q, a.rank / 8 - 1)));
+          held = id;
+        }
+        float d = 0.0f;
 #pragma unroll
         for (int q = 0; q < 2 * RT; ++q)
-          w[q] = as_half8(*reinterpret_cast<const uint4*>(src + 8 * min(q, a.rank / 8 - 1)));
-        held = id;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) d = __builtin_fmaf((float)w[q][e], t[i][8 * q + e], d);
+        sum[u] += d;
       }
-      float d = 0.0f;
-#pragma unroll
-      for (int q = 0; q < 2 * RT; ++q)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d = __builtin_fmaf((float)w[q][e], t[i][8 * q + e], d);
-      sum += d;
+      y[(int64_t)(b0 + i) * a.N + n] = __builtin_bit_cast(uint16_t, (_Float16)sum[u]);
     }
-    y[at] = __builtin_bit_cast(uint16_t, (_Float16)sum);
   }
 }
 
@@ -154,9 +169,14 @@ void launch_t(const LoraArgs& a, hipStream_t stream) {
   if (a.phase == 0)
     hipLaunchKernelGGL(lora_shrink_kernel<RT>, dim3((unsigned)(tiles * slots * splits)), dim3(kShrinkWaves * 64), 0,
                        stream, a, splits, slots, per);
-  else
-    hipLaunchKernelGGL(lora_expand_kernel<RT>, dim3((unsigned)(tiles * n_blocks)), dim3(256), 0, stream, a, splits,
-                       n_blocks);
+  else {
+    // rows a workgroup takes: 16 where that still fills the chip (a B row then serves a run
+    // of rows of one request), fewer in a decode batch, whose rows each bring their own
+    int rows = 16;
+    while (rows > 1 && (a.B + rows - 1) / rows * (int64_t)n_blocks < 2 * device_cu_count_cached()) rows /= 2;
+    hipLaunchKernelGGL(lora_expand_kernel<RT>, dim3((unsigned)((a.B + rows - 1) / rows * (int64_t)n_blocks)), dim3(256),
+                       0, stream, a, splits, n_blocks, rows);
+  }
 }
 
 }  // namespace
