@@ -20,10 +20,10 @@ from .attention import (  # noqa: F401
     qk_norm_rope_append,
     rope_table,
 )
+from .lora import LoraAdapters, gemm_lora, workspace_bytes_lora  # noqa: F401
 from .ops import (  # noqa: F401
     ActOrderWeight,
     KVCache4,
-    LoraAdapters,
     Q4Error,
     QuantizedWeight,
     QuantizedWeight8,
@@ -31,7 +31,6 @@ from .ops import (  # noqa: F401
     from_canonical,
     gemm,
     gemm_config,
-    gemm_lora,
     gemm_noalloc,
     gemm_perm,
     gemm_shape,
@@ -58,7 +57,6 @@ from .ops import (  # noqa: F401
     to_canonical,
     version,
     workspace_bytes,
-    workspace_bytes_lora,
     workspace_bytes_perm,
 )
 

@@ -47,7 +47,7 @@ q4_status q4_gemm_lora(const void* x, int64_t B, const void* packed, const void*
     return fail(Q4_ERR_NULL, "lora_a, lora_b, scaling, ids must be non-NULL");
   if (adapters > 0 && (!aligned(lora_a, 16) || !aligned(lora_b, 16) || !aligned(scaling, 4) || !aligned(ids, 4)))
     return fail(Q4_ERR_ALIGN, "lora_a and lora_b need 16-byte, scaling and ids 4-byte alignment");
-  const size_t need = q4_workspace_bytes_lora(B, out, in, group, rank);
+  const size_t need = product_bytes(g.k_splits, B, out) + t_bytes(B, in, rank);
   if (!workspace || workspace_bytes < need)
     return fail(Q4_ERR_WORKSPACE, "this shape needs %zu bytes of workspace (q4_workspace_bytes_lora), got %zu", need,
                 workspace ? workspace_bytes : (size_t)0);

@@ -381,58 +381,6 @@ def gemm_perm(x, aw: ActOrderWeight, out=None, workspace=None):
     return out
 
 
-# ---- low-rank adapters beside a product, include/q4_lora.h -------------------------
-
-
-@dataclass
-class LoraAdapters:
-    """Adapters of one matrix: a float16 [adapters, rank, in_features], b float16
-    [adapters, out_features, rank], scaling float32 [adapters], contiguous on one GPU."""
-
-    a: object
-    b: object
-    scaling: object
-
-    @property
-    def count(self) -> int:
-        return self.a.shape[0]
-
-    @property
-    def rank(self) -> int:
-        return self.a.shape[1]
-
-
-def workspace_bytes_lora(batch: int, out_features: int, in_features: int, group: int, rank: int) -> int:
-    return int(_lib.load().q4_workspace_bytes_lora(batch, out_features, in_features, group, rank))
-
-
-def gemm_lora(x, qw: QuantizedWeight, adapters: LoraAdapters, ids, out=None, workspace=None):
-    """q4_gemm_lora: gemm plus scaling[i] * B_i (A_i x[b]) with i = ids[b] (int32 [B]; an id
-    outside the adapters, -1 say, is a row without one)."""
-    import torch
-
-    B, out = _prep_gemm(x, qw, out)
-    a, b, s = adapters.a, adapters.b, adapters.scaling
-    for t, name, dtype in ((a, "adapters.a", torch.float16), (b, "adapters.b", torch.float16),
-                           (s, "adapters.scaling", torch.float32), (ids, "ids", torch.int32)):
-        _require_gpu(t, name, dtype)
-        if t.device != x.device:
-            raise ValueError(f"{name} ({t.device}) must be on x's GPU ({x.device})")
-    if a.dim() != 3 or a.shape[2] != qw.in_features:
-        raise ValueError(f"adapters.a must be [adapters, rank, {qw.in_features}]")
-    n, rank = a.shape[:2]
-    if tuple(b.shape) != (n, qw.out_features, rank) or tuple(s.shape) != (n,) or tuple(ids.shape) != (B,):
-        raise ValueError(f"adapters.b must be {[n, qw.out_features, rank]}, scaling [{n}] and ids [{B}]")
-    lib = _lib.load()
-    need = int(lib.q4_workspace_bytes_lora(B, qw.out_features, qw.in_features, qw.group, rank)) if B > 0 else 0
-    ws_ptr, ws_bytes = _workspace(x, need, workspace)
-    _check(lib.q4_gemm_lora(x.data_ptr(), B, qw.packed.data_ptr(), qw.scales.data_ptr(),
-                            qw.zeros.data_ptr() if qw.asym else None, qw.out_features, qw.in_features, qw.group,
-                            a.data_ptr(), b.data_ptr(), s.data_ptr(), n, rank, ids.data_ptr(), out.data_ptr(), ws_ptr,
-                            ws_bytes, _stream(x)))
-    return out
-
-
 # ---- INT4 KV cache, include/q4_kv.h ------------------------------------------------
 
 
