@@ -20,20 +20,40 @@
 namespace q4 {
 namespace {
 
-struct Row8 {
-  half8_t x;
-  bool real;
-};
+// 1 / sqrt(v): v_rsq_f64 (about 26 bits) and one Newton step.
+__device__ __forceinline__ double inv_sqrt(double v) {
+  const double y = __builtin_amdgcn_rsq(v);
+  return __builtin_fma(0.5 * y, __builtin_fma(-v * y, y, 1.0), y);
+}
 
-// Float16 of a float64, rounded once.
-__device__ __forceinline__ _Float16 to_half(double v) { return (_Float16)v; }
-__device__ __forceinline__ _Float16 to_half(float v) { return (_Float16)v; }
+// v plus the value of another lane of the same 16, picked by a DPP control (no LDS).
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+template <int CTRL>
+__device__ __forceinline__ double add_dpp(double v) {
+  const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, 0xF, 0xF, true);
+  const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, 0xF, 0xF, true);
+  return v + __hiloint2double(hi, lo);
+}
 
-__device__ __forceinline__ float inv_sqrt(float v) { return 1.0f / sqrtf(v); }
-__device__ __forceinline__ double inv_sqrt(double v) { return 1.0 / sqrt(v); }
+// Sum over a head's LPH lanes: neighbours, pairs, then mirrored halves of 8 and 16 lanes
+// (whose quads, resp. eights, are equal by then).
+template <int LPH, typename T>
+__device__ __forceinline__ T head_sum(T v) {
+  v = add_dpp<0xB1>(v);   // quad_perm [1, 0, 3, 2]
+  v = add_dpp<0x4E>(v);   // quad_perm [2, 3, 0, 1]
+  v = add_dpp<0x141>(v);  // row_half_mirror
+  if (LPH >= 16) v = add_dpp<0x140>(v);  // row_mirror
+  if (LPH >= 32) v += __shfl_xor(v, 16, 64);
+  return v;
+}
 
 // Rotation factors of a lane's 8 channels: out[e] = h[e] * c[e] + partner[e] * s[e],
-// s carrying the sign. `turn` is false for channels behind rot_dim.
+// s carrying the sign. `turn` is false for channels behind rot_dim (c = 1, s = 0).
+constexpr int kAhead = 4;
+
 struct Turn {
   float c[8], s[8];
   int partner;  // lane of the partner's chunk (half-split pairs)
@@ -41,13 +61,11 @@ struct Turn {
 };
 
 template <int D>
-__device__ __forceinline__ Turn load_turn(const RopeArgs& a, int64_t token, int lane) {
+__device__ __forceinline__ void load_turn(const RopeArgs& a, int64_t token, int lane, Turn& t) {
   constexpr int LPH = D / 8;
-  Turn t;
   const int ch = 8 * (lane & (LPH - 1));
   t.turn = ch < a.rot;
-  t.partner = lane;
-  if (!t.turn) return t;
+  if (!t.turn) return;
   const int64_t pos = min(max((int64_t)a.positions[token], (int64_t)0), a.table_positions - 1);
   const float* row = a.table + pos * a.rot;
   if (a.interleaved) {
@@ -59,7 +77,7 @@ __device__ __forceinline__ Turn load_turn(const RopeArgs& a, int64_t token, int 
       t.c[e] = v[(e & 2)];
       t.s[e] = (e & 1) ? v[(e & 2) + 1] : -v[(e & 2) + 1];
     }
-    return t;
+    return;
   }
   const bool first = ch < a.rot / 2;
   t.partner = lane + (first ? a.rot / 16 : -(a.rot / 16));
@@ -72,45 +90,88 @@ __device__ __forceinline__ Turn load_turn(const RopeArgs& a, int64_t token, int 
     t.s[2 * i] = first ? -v[1] : v[1];
     t.s[2 * i + 1] = first ? -v[3] : v[3];
   }
-  return t;
 }
 
-// Norm and rotation of one head row chunk, arithmetic in T.
-template <int D, typename T>
-__device__ __forceinline__ half8_t norm_rope(half8_t x, const uint16_t* weight, float eps, const Turn& t,
-                                             bool interleaved, bool rotate, int lane) {
+// A norm's weights for a lane's channels and for its rotation partner's.
+struct Weights {
+  half8_t own, other;
+};
+
+// The two halves of every dword swapped: adjacent channels.
+__device__ __forceinline__ uint4 swap_pairs(uint4 r) {
+  return make_uint4(r.x >> 16 | r.x << 16, r.y >> 16 | r.y << 16, r.z >> 16 | r.z << 16, r.w >> 16 | r.w << 16);
+}
+
+template <int D>
+__device__ __forceinline__ Weights load_weights(const void* w, int lane, int partner, bool interleaved) {
   constexpr int LPH = D / 8;
-  float h[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) h[e] = (float)x[e];
-  T r = (T)1;
-  if (weight) {
-    T sum = (T)0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum += (T)(h[e] * h[e]);
-#pragma unroll
-    for (int m = 1; m < LPH; m <<= 1) sum += __shfl_xor(sum, m, 64);
-    r = inv_sqrt(sum / (T)D + (T)eps);
-    const half8_t w = as_half8(*reinterpret_cast<const uint4*>(weight + 8 * (lane & (LPH - 1))));
-#pragma unroll
-    for (int e = 0; e < 8; ++e) h[e] *= (float)w[e];
+  const uint4* p = static_cast<const uint4*>(w);
+  const uint4 own = p[lane & (LPH - 1)];
+  return Weights{as_half8(own), as_half8(interleaved ? swap_pairs(own) : p[partner & (LPH - 1)])};
+}
+
+// The rotation partners of a lane's 8 channels; zeros where there is no rotation (the
+// lane's own values would bring infinities into a product with sine 0).
+__device__ __forceinline__ half8_t partners(half8_t x, const Turn& t, bool interleaved) {
+  uint4 r = __builtin_bit_cast(uint4, x);
+  if (interleaved) {
+    r = swap_pairs(r);
+  } else {
+    r = make_uint4(__shfl(r.x, t.partner, 64), __shfl(r.y, t.partner, 64), __shfl(r.z, t.partner, 64),
+                   __shfl(r.w, t.partner, 64));
   }
-  float other[8];
-  if (rotate) {
-    if (interleaved) {
+  const uint32_t keep = t.turn ? 0xFFFFFFFFu : 0u;
+  return as_half8(make_uint4(r.x & keep, r.y & keep, r.z & keep, r.w & keep));
+}
+
+// q: norm and rotation in float32, with the weights already in c and s:
+// (x (w c) + y (w' s)) / rms. About 55 instructions for 8 channels a lane.
+template <int D>
+__device__ __forceinline__ half8_t q_row(half8_t x, half8_t y, bool norm, float eps, const Turn& t) {
+  float r = 1.0f;
+  if (norm) {
+    float sum = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) other[e] = h[e ^ 1];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) other[e] = __shfl(h[e], t.partner, 64);
+    for (int e = 0; e < 8; e += 2) {
+      const half2_t v = {x[e], x[e + 1]};
+      sum = __builtin_amdgcn_fdot2(v, v, sum, false);
     }
+    r = __builtin_amdgcn_rsqf(head_sum<D / 8>(sum) * (1.0f / D) + eps);  // within one ulp
   }
   half8_t out;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    T v = (T)h[e];
-    if (rotate && t.turn) v = v * (T)t.c[e] + (T)other[e] * (T)t.s[e];
-    out[e] = weight ? to_half(v * r) : to_half(v);
+    const float v = __builtin_fmaf((float)y[e], t.s[e], (float)x[e] * t.c[e]);
+    out[e] = (_Float16)(v * r);
+  }
+  return out;
+}
+
+// k: the same in float64, rounded once. Through float32, the second rounding errs only
+// where the first lands on a tie of the second (or, below 2^-14, on a subnormal's): those
+// few lanes are rounded from the float64 directly.
+template <int D>
+__device__ __forceinline__ half8_t k_row(half8_t x, half8_t y, bool norm, const Weights& w, float eps, const Turn& t,
+                                         bool rotate) {
+  double r = 1.0;
+  if (norm) {
+    double sum = 0.0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += (double)((float)x[e] * (float)x[e]);  // 22 bits: exact in float32
+    r = inv_sqrt(head_sum<D / 8>(sum) * (1.0 / D) + (double)eps);
+  }
+  half8_t out;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    double v = (double)(norm ? (float)x[e] * (float)w.own[e] : (float)x[e]);  // exact too
+    if (rotate) {
+      const double o = (double)(norm ? (float)y[e] * (float)w.other[e] : (float)y[e]);
+      v = v * (double)t.c[e] + o * (double)t.s[e];
+    }
+    if (norm) v *= r;
+    const float f = (float)v;
+    out[e] = (_Float16)f;
+    if ((__float_as_uint(f) & 0x1FFFu) == 0x1000u || fabsf(f) < 0x1p-14f) out[e] = (_Float16)v;
   }
   return out;
 }
@@ -141,87 +202,125 @@ __device__ __forceinline__ uint32_t quantize8(half8_t h, int GL, _Float16* scale
   return word;
 }
 
-// Heads of a token in units of RPW heads: q's, then k's, then (append) v's.
+// Codes and scale of a lane's 8 channels of a token (row tt of its tile) into the cache.
+template <int D, bool IS_V>
+__device__ __forceinline__ void store_codes(const PagedArgs& c, half8_t x, uint32_t slot, bool stored, int head,
+                                            int chunk) {
+  constexpr int LPH = D / 8;
+  _Float16 scale;
+  const int GL = c.group / 8;
+  const uint32_t word = quantize8(x, GL, &scale);
+  const uint32_t partner = IS_V ? __shfl_xor(word, 2, 64) : 0u;  // channels + 16
+  if (!stored) return;
+  const int64_t tile = slot_tile(slot, c.page_size, c.kv_heads, head);
+  const int tt = (int)(slot % (uint32_t)kTokTile);  // page_size is a multiple of the tile
+  if (chunk % GL == 0) {
+    uint16_t* sc = static_cast<uint16_t*>(IS_V ? c.v_scales : c.k_scales);
+    sc[(tile * (LPH / GL) + chunk / GL) * kTokTile + tt] = __builtin_bit_cast(uint16_t, scale);
+  }
+  const uint32_t off = word ^ 0x88888888u;  // q + 8
+  if (!IS_V) {
+    uint32_t dw = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw |= ((off >> (4 * e)) & 0xFu) << (4 * nibble_of(e));
+    static_cast<uint32_t*>(c.k_codes)[tile * (2 * D) + tile_dword<D>(chunk / 4, tt + 16 * (chunk & 3))] = dw;
+  } else {
+    // a byte holds channels 32m + r and 32m + 16 + r: the lanes of the two halves
+    // write four of their eight bytes each
+    const uint32_t po = partner ^ 0x88888888u;
+    const int hi = (chunk >> 1) & 1;
+    const uint32_t lo_word = hi ? po : off, hi_word = hi ? off : po;
+    uint8_t* vc = static_cast<uint8_t*>(c.v_codes) + tile * (8 * D) + v_byte(tt & 3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * hi + i;
+      const int r = 8 * (chunk & 1) + e;
+      vc[tile_dword<D>(chunk / 4, r + 16 * (tt >> 2)) * 4] =
+          (uint8_t)(((lo_word >> (4 * e)) & 0xFu) | (((hi_word >> (4 * e)) & 0xFu) << 4));
+    }
+  }
+}
+
+// Heads of a token in units of RPW heads: k's, then (append) v's, then q's.
 template <int D, bool APPEND>
-__global__ __launch_bounds__(256) void rope_kernel(RopeArgs a, int segs, int units_per_seg) {
+__global__ __launch_bounds__(256, 6) void rope_kernel(RopeArgs a, int segs, int units_per_seg) {
   constexpr int LPH = D / 8;
   constexpr int RPW = kWave / LPH;
   const int lane = threadIdx.x & 63;
-  const int64_t wave = (int64_t)blockIdx.x * (blockDim.x / kWave) + threadIdx.x / kWave;
+  const int64_t wave = (int64_t)blockIdx.x * (blockDim.x / kWave) + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int64_t token = wave / segs;
   if (token >= a.tokens) return;
-  const int nq = (a.q_heads + RPW - 1) / RPW, nk = (a.kv_heads + RPW - 1) / RPW;
-  const int units = nq + nk + (APPEND ? nk : 0);
+  const int nk = (a.kv_heads + RPW - 1) / RPW, nq = (a.q_heads + RPW - 1) / RPW;
+  const int v0 = nk, q0 = APPEND ? 2 * nk : nk;  // first units of v and q
   const int u0 = (int)(wave - token * segs) * units_per_seg;
-  const int u1 = min(u0 + units_per_seg, units);
+  const int u1 = min(u0 + units_per_seg, q0 + nq);
   const int sub = lane / LPH, chunk = lane & (LPH - 1);
   const bool rotate = a.rot > 0;
+  auto fetch = [&](const void* p, int64_t stride, int head, int heads) __attribute__((always_inline)) {
+    return head < heads ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + token * stride + head * D + 8 * chunk)
+                        : make_uint4(0u, 0u, 0u, 0u);
+  };
+  auto store = [&](void* p, int64_t stride, int head, int heads, half8_t x) __attribute__((always_inline)) {
+    if (head < heads)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + token * stride + head * D + 8 * chunk) =
+          __builtin_bit_cast(uint4, x);
+  };
   Turn t;
   t.turn = false;
-  if (rotate) t = load_turn<D>(a, token, lane);
-  uint32_t slot = 0xFFFFFFFFu;
-  if (APPEND) slot = (uint32_t)a.slots[token];
-  const bool stored = APPEND && (int64_t)slot < a.cache.pages * a.cache.page_size;
-  for (int u = u0; u < u1; ++u) {
-    // kind 0: q, 1: k, 2: v (uniform)
-    const int kind = u < nq ? 0 : u < nq + nk ? 1 : 2;
-    const int head = (kind == 0 ? u : kind == 1 ? u - nq : u - nq - nk) * RPW + sub;
-    const bool real = head < (kind == 0 ? a.q_heads : a.kv_heads);
-    const uint16_t* src = kind == 0 ? static_cast<const uint16_t*>(a.q) + token * a.q_stride
-                          : kind == 1 ? static_cast<const uint16_t*>(a.k) + token * a.k_stride
-                                      : static_cast<const uint16_t*>(a.v) + token * a.v_stride;
-    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    if (real) raw = *reinterpret_cast<const uint4*>(src + head * D + 8 * chunk);
-    half8_t x = as_half8(raw);
-    if (kind == 0) {
-      x = norm_rope<D, float>(x, static_cast<const uint16_t*>(a.q_weight), a.eps, t, a.interleaved, rotate, lane);
-      if (real)
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.q_out) + token * a.q_out_stride + head * D + 8 * chunk) =
-            __builtin_bit_cast(uint4, x);
-      continue;
-    }
-    if (kind == 1) {
-      x = norm_rope<D, double>(x, static_cast<const uint16_t*>(a.k_weight), a.eps, t, a.interleaved, rotate, lane);
-      if (!APPEND) {
-        if (real)
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.k_out) + token * a.k_out_stride + head * D + 8 * chunk) =
-              __builtin_bit_cast(uint4, x);
-        continue;
-      }
-    }
-    if (!APPEND) continue;
-    _Float16 scale;
-    const int GL = a.cache.group / 8;
-    const uint32_t word = quantize8(x, GL, &scale);
-    const uint32_t partner = __shfl_xor(word, 2, 64);  // channels + 16 (V bytes)
-    if (!stored || !real) continue;
-    const int64_t tile = slot_tile(slot, a.cache.page_size, a.cache.kv_heads, head);
-    const int tt = (int)(slot % (uint32_t)kTokTile);  // page_size is a multiple of the tile
-    if (chunk % GL == 0) {
-      uint16_t* sc = static_cast<uint16_t*>(kind == 1 ? a.cache.k_scales : a.cache.v_scales);
-      sc[(tile * (LPH / GL) + chunk / GL) * kTokTile + tt] = __builtin_bit_cast(uint16_t, scale);
-    }
-    const uint32_t off = word ^ 0x88888888u;  // q + 8
-    if (kind == 1) {
-      uint32_t dw = 0;
+  t.partner = lane;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dw |= ((off >> (4 * e)) & 0xFu) << (4 * nibble_of(e));
-      static_cast<uint32_t*>(a.cache.k_codes)[tile * (2 * D) + tile_dword<D>(chunk / 4, tt + 16 * (chunk & 3))] = dw;
-    } else {
-      // a byte holds channels 32m + r and 32m + 16 + r: the lanes of the two halves
-      // write four of their eight bytes each
-      const uint32_t po = partner ^ 0x88888888u;
-      const int hi = (chunk >> 1) & 1;
-      const uint32_t lo_word = hi ? po : off, hi_word = hi ? off : po;
-      uint8_t* vc = static_cast<uint8_t*>(a.cache.v_codes) + tile * (8 * D);
-      const int byte = v_byte(tt & 3);
+  for (int e = 0; e < 8; ++e) t.c[e] = 1.0f, t.s[e] = 0.0f;
+  if (rotate) load_turn<D>(a, token, lane, t);
+  uint32_t slot = 0;
+  bool stored = false;
+  if (APPEND) {
+    slot = (uint32_t)a.slots[token];
+    stored = (int64_t)slot < a.cache.pages * a.cache.page_size;
+  }
+
+  if (u0 < nk) {
+    Weights w{};
+    if (a.k_weight) w = load_weights<D>(a.k_weight, lane, t.partner, a.interleaved);
+    for (int u = u0; u < min(u1, nk); ++u) {
+      const int head = u * RPW + sub;
+      const half8_t x = as_half8(fetch(a.k, a.k_stride, head, a.kv_heads));
+      half8_t y = x;
+      if (rotate) y = partners(x, t, a.interleaved);
+      const half8_t k = k_row<D>(x, y, a.k_weight != nullptr, w, a.eps, t, rotate);
+      if (APPEND) store_codes<D, false>(a.cache, k, slot, stored && head < a.kv_heads, head, chunk);
+      else store(a.k_out, a.k_out_stride, head, a.kv_heads, k);
+    }
+  }
+  if (APPEND) {
+    for (int u = max(u0, v0); u < min(u1, q0); ++u) {
+      const int head = (u - v0) * RPW + sub;
+      const half8_t x = as_half8(fetch(a.v, a.v_stride, head, a.kv_heads));
+      store_codes<D, true>(a.cache, x, slot, stored && head < a.kv_heads, head, chunk);
+    }
+  }
+  if (u1 <= q0) return;
+  if (a.q_weight) {
+    const Weights w = load_weights<D>(a.q_weight, lane, t.partner, a.interleaved);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = 4 * hi + i;
-        const int r = 8 * (chunk & 1) + e;
-        vc[tile_dword<D>(chunk / 4, r + 16 * (tt >> 2)) * 4 + byte] =
-            (uint8_t)(((lo_word >> (4 * e)) & 0xFu) | (((hi_word >> (4 * e)) & 0xFu) << 4));
-      }
+    for (int e = 0; e < 8; ++e) t.c[e] *= (float)w.own[e], t.s[e] *= (float)w.other[e];
+  }
+  // the next kAhead units' loads are in flight while kAhead are computed
+  const int first = max(u0, q0) - q0, last = u1 - q0;
+  uint4 raw[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) raw[i] = fetch(a.q, a.q_stride, (first + i) * RPW + sub, a.q_heads);
+  for (int u = first; u < last; u += kAhead) {
+    uint4 next[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) next[i] = fetch(a.q, a.q_stride, (u + kAhead + i) * RPW + sub, a.q_heads);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (u + i >= last) break;
+      const half8_t x = as_half8(raw[i]);
+      half8_t y = x;
+      if (rotate) y = partners(x, t, a.interleaved);
+      store(a.q_out, a.q_out_stride, (u + i) * RPW + sub, a.q_heads, q_row<D>(x, y, a.q_weight != nullptr, a.eps, t));
+      raw[i] = next[i];
     }
   }
 }
