@@ -54,6 +54,13 @@ __device__ __forceinline__ float4_t mfma(half8_t a, half8_t b, float4_t c) {
 }
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// Larger halves of two pairs of unsigned 16-bit numbers.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  typedef uint16_t us2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2, a), __builtin_bit_cast(us2, b)));
+}
 
 // Eight codes of the K operand, biased: fields of a dword are moved to bits 2..5 and 6..9
 // of the half-words, where OR with 256.0h and 16.0h makes 256 + n and 16 + n: two shifts
@@ -173,13 +180,32 @@ struct Walk {
   int tile, block, in_page;  // tile of the sequence, its page table entry, tile of the page
 };
 
-template <int D, int GC, int QT, bool TOK>
+// Result of row `row`, channels ch .. ch + 3: the output, or the split's part.
+template <int D>
+__device__ __forceinline__ void store_row(const AttnArgs& a, const Job& w, int split, int row, int ch, float4_t o,
+                                          float sum, float base) {
+  if (row >= w.rows) return;
+  const int i = row / w.share, hs = row - i * w.share;
+  const int64_t r = (int64_t)(w.first + i) * a.q_heads + w.head * w.share + hs;
+  if (a.splits > 1) {
+    const int64_t rs = r * a.splits + split;
+    *reinterpret_cast<float4_t*>(a.part_o + rs * D + ch) = o;
+    if (ch == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * rs) = make_float2(base, sum);
+    return;
+  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  half4_t h;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = (_Float16)(o[e] * inv);
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + r * D + ch) = __builtin_bit_cast(uint2, h);
+}
+
+template <int D, int GC, int QT>
 struct Attn {
   static constexpr int KB = D / 32;    // 32-channel blocks
   static constexpr int BPG = KB / GC;  // of them per scale group
   static constexpr int kWaves = 4;
-  static constexpr int kRowsWave = 16 * QT;
-  static constexpr int kRowsGroup = TOK ? kRowsWave : kWaves * kRowsWave;
+  static constexpr int kRows = 16 * QT;
   // wavefronts per SIMD the registers are budgeted for: the most without spills
   static constexpr int kWavesSimd = D == 64    ? (QT == 1 ? 4 - GC / 2 : 4 - GC)
                                     : D == 128 ? (QT == 1 ? (GC == 1 ? 3 : 2) : (GC <= 2 ? 2 : 1))
@@ -191,9 +217,10 @@ struct Attn {
   };
 };
 
-template <int D, int GC, int QT, bool TOK>
-__global__ __launch_bounds__(256, (Attn<D, GC, QT, TOK>::kWavesSimd)) void attn_kernel(AttnArgs a, int tiles) {
-  using C = Attn<D, GC, QT, TOK>;
+// Few rows: all four wavefronts have the same ones and split the keys.
+template <int D, int GC, int QT>
+__global__ __launch_bounds__(256, (Attn<D, GC, QT>::kWavesSimd)) void attn_kernel(AttnArgs a, int tiles) {
+  using C = Attn<D, GC, QT>;
   using Step = typename C::Step;
   constexpr int KB = C::KB, BPG = C::BPG;
   const int lane = threadIdx.x & 63;
@@ -207,10 +234,8 @@ __global__ __launch_bounds__(256, (Attn<D, GC, QT, TOK>::kWavesSimd)) void attn_
   at /= (unsigned)tiles;
   Job w;
   if (!make_job(a, (int)(at / (unsigned)a.cache.kv_heads), (int)(at % (unsigned)a.cache.kv_heads), &w)) return;
-  const int r0 = tile_q * C::kRowsGroup + (TOK ? 0 : wave * C::kRowsWave);
-  if (tile_q * C::kRowsGroup >= w.rows) return;
-  const bool idle = r0 >= w.rows;  // a wavefront without rows (only where rows are its own)
-  if (!TOK && idle) return;        // no barrier follows there
+  const int r0 = tile_q * C::kRows;
+  if (r0 >= w.rows) return;
 
   half8_t q[QT][KB];
   float bias[QT][GC];  // -(264 * sum of q over elements 0, 1, 4, 5 + 24 * the others), per scale group
@@ -244,7 +269,7 @@ __global__ __launch_bounds__(256, (Attn<D, GC, QT, TOK>::kWavesSimd)) void attn_
     for (int b = 0; b < 2 * KB; ++b) acc[t][b] = float4_t{0.f, 0.f, 0.f, 0.f};
   }
 
-  const Span sp = span_of(a, w, r0, C::kRowsWave);
+  const Span sp = span_of(a, w, r0, C::kRows);
   // this workgroup's part of the keys
   const int t_first = sp.first + split * a.chunk;
   const int t_last = a.splits > 1 ? min(sp.last, t_first + a.chunk) : sp.last;
@@ -256,11 +281,11 @@ __global__ __launch_bounds__(256, (Attn<D, GC, QT, TOK>::kWavesSimd)) void attn_
   float exp_v = -64.0f;  // E (wave-uniform)
   uint32_t cap_v = 0;    // largest V scale that E covers, as float16 bits
 
-  constexpr int kStride = TOK ? C::kWaves * 2 : 2;  // tiles from one step of a wavefront to the next
+  constexpr int kStride = C::kWaves * 2;  // tiles from one step of a wavefront to the next
   const int stride_block = kStride / tpp, stride_rem = kStride - stride_block * tpp;
   const int last_tile = max(t_last - 1, 0) / kTokTile;
   Walk next;
-  next.tile = t_first / kTokTile + (TOK ? 2 * wave : 0);
+  next.tile = t_first / kTokTile + 2 * wave;
   next.block = next.tile / tpp;
   next.in_page = next.tile - next.block * tpp;
   int page[2];      // page numbers of `next`'s two tiles
@@ -464,7 +489,7 @@ __global__ __launch_bounds__(256, (Attn<D, GC, QT, TOK>::kWavesSimd)) void attn_
   };
 
   // one step in flight while the one before is computed
-  const int t_own = t_first + (TOK ? kStep * wave : 0);
+  const int t_own = t_first + kStep * wave;
   if (t_own < t_last) {
     Step s0, s1;
     fetch_pages();
@@ -484,54 +509,390 @@ __global__ __launch_bounds__(256, (Attn<D, GC, QT, TOK>::kWavesSimd)) void attn_
     l[t] += __shfl_xor(l[t], 32, 64);
   }
 
-  // Result of row `row`, channels 16 c + 4 c4 .. + 3: the output, or the split's part.
-  auto store = [&](int row, int c, float4_t o, float sum, float b) __attribute__((always_inline)) {
-    if (row >= w.rows) return;
-    const int i = row / w.share, hs = row - i * w.share;
-    const int64_t r = (int64_t)(w.first + i) * a.q_heads + w.head * w.share + hs;
-    if (a.splits > 1) {
-      const int64_t rs = r * a.splits + split;
-      *reinterpret_cast<float4_t*>(a.part_o + rs * D + 16 * c + 4 * c4) = o;
-      if (c == 0 && c4 == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * rs) = make_float2(b, sum);
-      return;
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    half4_t h;
+  // the four wavefronts' parts of the same rows, added in order
+  __shared__ float4_t buf[C::kWaves][2 * KB][kWave];
+  __shared__ float2 ml[C::kWaves][16];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = (_Float16)(o[e] * inv);
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + r * D + 16 * c + 4 * c4) = __builtin_bit_cast(uint2, h);
+  for (int t = 0; t < QT; ++t) {
+    if (t > 0) __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 2 * KB; ++c) buf[wave][c][lane] = acc[t][c];
+    if (c4 == 0) ml[wave][col] = make_float2(base[t], l[t]);
+    __syncthreads();
+    float top = ml[0][col].x, sum = 0.0f, f[C::kWaves];
+#pragma unroll
+    for (int v = 1; v < C::kWaves; ++v) top = fmaxf(top, ml[v][col].x);
+#pragma unroll
+    for (int v = 0; v < C::kWaves; ++v) {
+      f[v] = exp2_fast(ml[v][col].x - top);
+      sum = __builtin_fmaf(ml[v][col].y, f[v], sum);
+    }
+    for (int c = wave; c < 2 * KB; c += C::kWaves) {
+      float4_t o = buf[0][c][lane] * f[0];
+#pragma unroll
+      for (int v = 1; v < C::kWaves; ++v) o += buf[v][c][lane] * f[v];
+      store_row<D>(a, w, split, r0 + 16 * t + col, 16 * c + 4 * c4, o, sum, top);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// More than 16 rows: tiles of 32 rows on v_mfma_f32_32x32x16_f16. At equal rate it holds the
+// issue port half as often as the 16x16 form, and next to the softmax's vector work
+// that counts: 131072 products beside 32 vector instructions took 195 cycles with it, 230 to
+// 257 without (two wavefronts on a SIMD).
+//
+// The cache's tiles serve this shape too. K: lane (key, c), key < 32, c < 2, takes what lanes
+// key % 16 + 16 c and + 32 of the key's tile own: channels 8c .. 8c + 7 of the even and the odd
+// 16-channel steps. The scores come out with keys 8 (i / 4) + 4c + i % 4 in register i, so one
+// tile's 16 keys are eight registers of both lane halves, and a V operand of 16 keys is the
+// dwords of cache lanes r + 16 c and r + 32 + 16 c; channels 0..15 of a block are their low
+// nibbles, 16..31 the high ones: lanes 16..31 read the same dwords with other masks.
+//
+// With ROWS every wavefront has 32 rows of its own and walks all their keys (the four
+// wavefronts of a workgroup read the same tiles at nearly the same time, from the
+// L1); without, four wavefronts share 32 rows and split the keys. Staging converted
+// operands in LDS for all four saves two thirds of the conversion, but its barriers cost
+// more than that (16x16 form, four 509-token chunks: 616 against 610 us).
+typedef float float16_t __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ float16_t mfma32(half8_t a, half8_t b, float16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
+// Four V codes of a dword for this lane's channel: low or high nibbles by mask and magic.
+struct VRegs {
+  uint32_t mask, magic;
+  half2_t bias;
+};
+__device__ __forceinline__ half4_t v_codes4(uint32_t w, const VRegs& k) {
+  const half2_t a = as_half2((w & k.mask) | k.magic) + k.bias;
+  const half2_t b = as_half2(((w >> 8) & k.mask) | k.magic) + k.bias;
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3);
+}
+
+template <int D, int GC, bool ROWS>
+__global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_kernel(AttnArgs a, int tiles,
+                                                                                       int swizzle) {
+  constexpr int KB = D / 32, BPG = KB / GC;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 31, c = lane >> 5, r16 = lane & 15;
+  // blocks: split fastest, then row tile (last rows, the longest spans, first), head, sequence; with
+  // `swizzle` the eight XCDs, which take blocks in turn, each keep whole heads (their L2 then
+  // holds the keys all of a head's tiles read)
+  const unsigned inner = (unsigned)(a.splits * tiles);
+  unsigned group = blockIdx.x / inner, at = blockIdx.x % inner;
+  if (swizzle) {
+    const unsigned x = blockIdx.x % 8, y = blockIdx.x / 8;
+    group = x + 8 * (y / inner);
+    at = y % inner;
+  }
+  const int split = (int)(at % (unsigned)a.splits);
+  const int tile_q = tiles - 1 - (int)(at / (unsigned)a.splits);
+  Job w;
+  if (!make_job(a, (int)(group / (unsigned)a.cache.kv_heads), (int)(group % (unsigned)a.cache.kv_heads), &w)) return;
+  constexpr int kGroup = ROWS ? 128 : 32;
+  const int g0 = tile_q * kGroup;
+  const int r0 = g0 + (ROWS ? 32 * wave : 0);
+  if (r0 >= w.rows) return;  // no barrier follows where wavefronts differ in this
+
+  const int row = r0 + col;
+  half8_t q[2 * KB];
+  int pos;  // position of the lane's row: its own last visible key; -1: no row
+  float16_t start = {};  // what a dot product starts at: see k_operand
+  {
+    const int i = min(row, w.rows - 1) / w.share, hs = min(row, w.rows - 1) - i * w.share;
+    pos = row < w.rows ? w.len - w.nq + i : -1;
+    const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.first + i) * a.q_stride +
+                          (int64_t)(w.head * w.share + hs) * D + 8 * c;
+    float s2 = 0.0f, s6 = 0.0f;
+#pragma unroll
+    for (int b = 0; b < 2 * KB; ++b) {
+      q[b] = as_half8(*reinterpret_cast<const uint4*>(src + 16 * b));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) (e & 2 ? s6 : s2) += (float)q[b][e];
+    }
+    if (GC == 1) {
+      const float own = -(264.0f * s2 + 24.0f * s6);
+      const float both = own + __shfl_xor(own, 32, 64);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) start[e] = both;
+    }
+  }
+  // base: m + E. A score more than `limit` above it makes m rise; a row that has seen no key
+  // yet has base 0 and limit -infinity, and its first key sets m.
+  float base = 0.0f, limit = -__builtin_inff(), l = 0.0f;
+  float16_t acc[KB];
+#pragma unroll
+  for (int b = 0; b < KB; ++b) acc[b] = float16_t{};
+
+  // the keys of the rows that decide the split, and those of this wavefront's rows
+  const Span all = span_of(a, w, g0, kGroup);
+  const Span sp = ROWS ? span_of(a, w, r0, 32) : all;
+  const int s_first = all.first + split * a.chunk;
+  const int t_last = a.splits > 1 ? min(sp.last, s_first + a.chunk) : sp.last;
+  const int t_first = max(s_first, sp.first) + (ROWS ? 0 : kStep * wave);
+  constexpr int kStride = ROWS ? 2 : 8;  // tiles from one step of a wavefront to the next
+  const float scale = a.scale * 1.4426950408889634f;
+  const DequantRegs dq = DequantRegs::make();
+  const KRegs kr = KRegs::make();
+  VRegs vr;
+  vr.mask = lane & 16 ? 0x00F000F0u : 0x000F000Fu;   // 64 + n, or 1024 + n
+  vr.magic = lane & 16 ? 0x54005400u : 0x64006400u;
+  vr.bias = as_half2(lane & 16 ? 0xD480D480u : 0xE408E408u);  // -72, -1032
+  float exp_v = -64.0f;  // E (wave-uniform)
+  uint32_t cap_v = 0;    // largest V scale that E covers, as float16 bits
+
+  const int tpp = a.cache.page_size / kTokTile;
+  const ScalarInts table = scalar_ints(a.block_table + (int64_t)w.seq * a.max_blocks);
+  const int stride_block = kStride / tpp, stride_rem = kStride - stride_block * tpp;
+  const int last_tile = max(t_last - 1, 0) / kTokTile;
+  Walk next;
+  next.tile = t_first / kTokTile;
+  next.block = next.tile / tpp;
+  next.in_page = next.tile - next.block * tpp;
+  // tiles of the step whose K is loaded, and whether their pages lie in the cache
+  int64_t tile[2], tile_n[2];
+  bool there[2], there_n[2];
+  auto walk = [&]() __attribute__((always_inline)) {
+    const bool wraps = next.in_page + 1 == tpp;
+    const int in2 = wraps ? 0 : next.in_page + 1, b2 = next.block + (wraps ? 1 : 0);
+    const int p0 = next.tile <= last_tile && next.block < a.max_blocks ? table[next.block] : -1;
+    const int p1 = next.tile + 1 <= last_tile && b2 < a.max_blocks ? table[b2] : -1;
+    there_n[0] = (unsigned)p0 < (unsigned)a.cache.pages;
+    there_n[1] = (unsigned)p1 < (unsigned)a.cache.pages;
+    // a tile behind the last key or of a page outside the cache is read from page 0 and masked
+    tile_n[0] = ((int64_t)(there_n[0] ? p0 : 0) * a.cache.kv_heads + w.head) * tpp + next.in_page;
+    tile_n[1] = ((int64_t)(there_n[1] ? p1 : 0) * a.cache.kv_heads + w.head) * tpp + in2;
+    next.tile += kStride;
+    next.block += stride_block;
+    next.in_page += stride_rem;
+    if (next.in_page >= tpp) {
+      next.in_page -= tpp;
+      ++next.block;
+    }
+  };
+  uint32_t kw[2][KB];  // K codes: even and odd 16-channel steps
+  uint2 ks[2][GC][2];  // scales of keys 8u + 4c .. + 3 of tile j: [j][g][u]
+  auto load_k = [&]() __attribute__((always_inline)) {
+    const int64_t mine = lane & 16 ? tile_n[1] : tile_n[0];
+    const uint32_t* p = static_cast<const uint32_t*>(a.cache.k_codes) + mine * (2 * D);
+    load_codes<D>(kw[0], p, r16 + 16 * c);
+    load_codes<D>(kw[1], p, r16 + 16 * c + 32);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint16_t* sc = static_cast<const uint16_t*>(a.cache.k_scales) + tile_n[j] * (GC * kTokTile) + 4 * c;
+#pragma unroll
+      for (int g = 0; g < GC; ++g)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) ks[j][g][u] = *reinterpret_cast<const uint2*>(sc + g * kTokTile + 8 * u);
+      tile[j] = tile_n[j];
+      there[j] = there_n[j];
+    }
   };
 
-  if constexpr (!TOK) {
+  auto step = [&](int t0) __attribute__((always_inline)) {
+    // V of this step: needed only after the softmax
+    uint32_t vw[2][2][KB];  // [tile][cache lanes r + 16 c, + 32]
+    uint2 vs[2][GC][2];
 #pragma unroll
-    for (int t = 0; t < QT; ++t)
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t* p = static_cast<const uint32_t*>(a.cache.v_codes) + tile[j] * (2 * D);
+      load_codes<D>(vw[j][0], p, r16 + 16 * c);
+      load_codes<D>(vw[j][1], p, r16 + 16 * c + 32);
+      const uint16_t* sc = static_cast<const uint16_t*>(a.cache.v_scales) + tile[j] * (GC * kTokTile) + 4 * c;
 #pragma unroll
-      for (int c = 0; c < 2 * KB; ++c) store(r0 + 16 * t + col, c, acc[t][c], l[t], base[t]);
+      for (int g = 0; g < GC; ++g)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) vs[j][g][u] = *reinterpret_cast<const uint2*>(sc + g * kTokTile + 8 * u);
+    }
+    const bool there0 = there[0], there1 = there[1];
+    const bool edge =
+        t0 + kStep > sp.pos_lo + 1 || t0 <= sp.pos_hi - sp.window || t0 + kStep > t_last || !there0 || !there1;
+    auto key_of = [&](int i) __attribute__((always_inline)) { return t0 + 8 * (i >> 2) + 4 * c + (i & 3); };
+
+    // scores, base 2, relative to m + E
+    float s[16];
+#pragma unroll
+    for (int g = 0; g < GC; ++g) {
+      float16_t part = start;
+#pragma unroll
+      for (int b = g * BPG; b < (g + 1) * BPG; ++b)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const half2_t lo_bias = {(_Float16)-1032.0f, (_Float16)-1032.0f};
+          const half2_t hi_bias = {(_Float16)-72.0f, (_Float16)-72.0f};
+          // one group a head: biased codes against `start`; more: exact codes
+          const half8_t k = GC == 1 ? k_operand(kw[u][b], kr) : dequant8r(kw[u][b], dq, lo_bias, hi_bias);
+          part = mfma32(k, q[2 * b + u], part);
+        }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const half4_t kh = __builtin_bit_cast(half4_t, ks[i >> 3][g][(i >> 2) & 1]);
+        s[i] = g == 0 ? part[i] * (float)kh[i & 3] : __builtin_fmaf(part[i], (float)kh[i & 3], s[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) s[i] = __builtin_fmaf(s[i], scale, -base);
+    // the next step's K while the rest of this one runs
+    load_k();
+    walk();
+
+    uint32_t hidden = 0;  // keys of the lane that its row does not see
+    if (edge) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int key = key_of(i);
+        if (!(i < 8 ? there0 : there1) || key >= t_last || key > pos || key <= pos - sp.window) {
+          s[i] = -__builtin_inff();
+          hidden |= 1u << i;
+        }
+      }
+      // what no row sees may hold anything: 0 * NaN must not arise
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int g = 0; g < GC; ++g)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            half4_t vh = __builtin_bit_cast(half4_t, vs[j][g][u]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = key_of(8 * j + 4 * u + i);
+              vh[i] = (j ? there1 : there0) && key < t_last && key > sp.pos_lo - sp.window ? vh[i] : (_Float16)0.0f;
+            }
+            vs[j][g][u] = __builtin_bit_cast(uint2, vh);
+          }
+    }
+    // E, where a V scale exceeds what it covers
+    uint32_t vmax = 0;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int g = 0; g < GC; ++g)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) vmax = max_u16x2(vmax, max_u16x2(vs[j][g][u].x, vs[j][g][u].y));
+    vmax = max(vmax & 0xFFFFu, vmax >> 16);
+    if (__any(vmax > cap_v)) {
+      // the largest finite one, up to the end of its binade
+      vmax = cap_v;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int g = 0; g < GC; ++g)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint2 r = vs[j][g][i >> 2];
+            const uint32_t bits = ((i & 2 ? r.y : r.x) >> (16 * (i & 1))) & 0xFFFFu;
+            vmax = max(vmax, bits < 0x7C00u ? bits : 0u);
+          }
+#pragma unroll
+      for (int i = 1; i < 64; i <<= 1) vmax = max(vmax, (uint32_t)__shfl_xor((int)vmax, i, 64));
+      cap_v = vmax | 0x3FFu;
+      const float up = (float)(int)(cap_v >> 10) - 14.0f - kHeadroom - exp_v, alpha = exp2_fast(-up);
+      exp_v += up;
+      if (limit > -__builtin_inff()) {
+        base += up;
+        limit = kSlack - exp_v;
+        l *= alpha;
+#pragma unroll
+        for (int b = 0; b < KB; ++b) acc[b] *= alpha;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] -= up;
+      }
+    }
+    // one score far above its row's held maximum?
+    float mx = max3(s[0], s[1], s[2]);
+#pragma unroll
+    for (int i = 3; i < 15; i += 2) mx = max3(mx, s[i], s[i + 1]);
+    mx = fmaxf(mx, s[15]);
+    if (__any(mx > limit)) {
+      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+      if (mx > -__builtin_inff()) {
+        const bool first = limit == -__builtin_inff();
+        const float up = first ? mx + exp_v : fmaxf(mx + exp_v, 0.0f);
+        const float alpha = first ? 1.0f : exp2_fast(-up);
+        base += up;
+        limit = kSlack - exp_v;
+        l *= alpha;
+#pragma unroll
+        for (int b = 0; b < KB; ++b) acc[b] *= alpha;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[i] -= up;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[i] = exp2_fast(s[i]);
+      l += s[i];
+    }
+    // weights, to float16 with the V scale in them, and O += V P, a tile's 16 keys at a time
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      half8_t p[GC];
+#pragma unroll
+      for (int g = 0; g < GC; ++g)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const half4_t vh = __builtin_bit_cast(half4_t, vs[j][g][i >> 2]);
+          p[g][i] = (_Float16)(s[8 * j + i] * (float)vh[i & 3]);
+        }
+      if (edge) {
+        // a key that one row sees and another does not may have an infinite scale
+#pragma unroll
+        for (int g = 0; g < GC; ++g)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (hidden >> (8 * j + i) & 1u) p[g][i] = (_Float16)0.0f;
+      }
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        const half4_t v0 = v_codes4(vw[j][0][b], vr), v1 = v_codes4(vw[j][1][b], vr);
+        acc[b] = mfma32(__builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7), p[b / BPG], acc[b]);
+      }
+    }
+  };
+
+  if (t_first < t_last) {
+    walk();
+    load_k();
+    walk();
+    for (int t0 = t_first; t0 < t_last; t0 += kStride * kTokTile) step(t0);
+  }
+  l += __shfl_xor(l, 32, 64);
+  if (limit == -__builtin_inff()) base = kLowest;
+
+  if constexpr (ROWS) {
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        store_row<D>(a, w, split, row, 32 * b + 8 * u + 4 * c,
+                     float4_t{acc[b][4 * u], acc[b][4 * u + 1], acc[b][4 * u + 2], acc[b][4 * u + 3]}, l, base);
   } else {
     // the four wavefronts' parts of the same rows, added in order
-    __shared__ float4_t buf[C::kWaves][2 * KB][kWave];
-    __shared__ float2 ml[C::kWaves][16];
+    __shared__ float4_t buf[4][4][kWave];
+    __shared__ float2 ml[4][32];
+    if (c == 0) ml[wave][col] = make_float2(base, l);
 #pragma unroll
-    for (int t = 0; t < QT; ++t) {
-      if (t > 0) __syncthreads();
+    for (int b = 0; b < KB; ++b) {
+      if (b > 0) __syncthreads();
 #pragma unroll
-      for (int c = 0; c < 2 * KB; ++c) buf[wave][c][lane] = acc[t][c];
-      if (c4 == 0) ml[wave][col] = make_float2(base[t], l[t]);
+      for (int u = 0; u < 4; ++u)
+        buf[wave][u][lane] = float4_t{acc[b][4 * u], acc[b][4 * u + 1], acc[b][4 * u + 2], acc[b][4 * u + 3]};
       __syncthreads();
-      float top = ml[0][col].x, sum = 0.0f, f[C::kWaves];
+      float top = ml[0][col].x, sum = 0.0f;
 #pragma unroll
-      for (int v = 1; v < C::kWaves; ++v) top = fmaxf(top, ml[v][col].x);
+      for (int v = 1; v < 4; ++v) top = fmaxf(top, ml[v][col].x);
+      float4_t o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int v = 0; v < C::kWaves; ++v) {
-        f[v] = exp2_fast(ml[v][col].x - top);
-        sum = __builtin_fmaf(ml[v][col].y, f[v], sum);
+      for (int v = 0; v < 4; ++v) {
+        const float f = exp2_fast(ml[v][col].x - top);
+        sum = __builtin_fmaf(ml[v][col].y, f, sum);
+        o += buf[v][wave][lane] * f;
       }
-      for (int c = wave; c < 2 * KB; c += C::kWaves) {
-        float4_t o = buf[0][c][lane] * f[0];
-#pragma unroll
-        for (int v = 1; v < C::kWaves; ++v) o += buf[v][c][lane] * f[v];
-        store(r0 + 16 * t + col, c, o, sum, top);
-      }
+      store_row<D>(a, w, split, row, 32 * b + 8 * wave + 4 * c, o, sum, top);
     }
   }
 }
@@ -589,28 +950,27 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows_gro
   *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + r * D + 4 * lane) = __builtin_bit_cast(uint2, h);
 }
 
-template <int D, int GC, int QT, bool TOK>
-void launch_q(const AttnArgs& a, hipStream_t stream) {
-  using C = Attn<D, GC, QT, TOK>;
-  const int64_t rows = (int64_t)a.max_q * (a.q_heads / a.cache.kv_heads);
-  const int tiles = (int)((rows + C::kRowsGroup - 1) / C::kRowsGroup);
-  const int64_t blocks = (int64_t)a.splits * tiles * a.cache.kv_heads * a.seqs;
-  hipLaunchKernelGGL((attn_kernel<D, GC, QT, TOK>), dim3((unsigned)blocks), dim3(256), 0, stream, a, tiles);
-  if (a.splits > 1) {
-    const int64_t all = rows * a.cache.kv_heads * a.seqs;
-    hipLaunchKernelGGL(attn_join_kernel<D>, dim3((unsigned)all), dim3(256), 0, stream, a, C::kRowsWave, (unsigned)rows);
-  }
+// rows_group: the rows whose keys decide which splits there are.
+template <int D>
+void launch_join(const AttnArgs& a, int rows_group, int64_t rows, hipStream_t stream) {
+  if (a.splits <= 1) return;
+  const int64_t all = rows * a.cache.kv_heads * a.seqs;
+  hipLaunchKernelGGL(attn_join_kernel<D>, dim3((unsigned)all), dim3(256), 0, stream, a, rows_group, (unsigned)rows);
 }
 
 template <int D, int GC>
 hipError_t launch_t(const AttnArgs& a, hipStream_t stream) {
-  if constexpr (D < 256) {  // at 256 channels two row tiles do not fit the registers
-    if (a.tiles_wave == 2) {
-      a.tok ? launch_q<D, GC, 2, true>(a, stream) : launch_q<D, GC, 2, false>(a, stream);
-      return hipGetLastError();
-    }
+  const int64_t rows = (int64_t)a.max_q * (a.q_heads / a.cache.kv_heads);
+  const int tiles = (int)((rows + a.rows_group - 1) / a.rows_group);
+  const int64_t groups = (int64_t)a.cache.kv_heads * a.seqs;
+  const dim3 grid((unsigned)(a.splits * tiles * groups));
+  const int swizzle = groups % 8 == 0 && tiles > 1;
+  switch (a.rows_group) {
+    case 16: hipLaunchKernelGGL((attn_kernel<D, GC, 1>), grid, dim3(256), 0, stream, a, tiles); break;
+    case 32: hipLaunchKernelGGL((attn32_kernel<D, GC, false>), grid, dim3(256), 0, stream, a, tiles, swizzle); break;
+    default: hipLaunchKernelGGL((attn32_kernel<D, GC, true>), grid, dim3(256), 0, stream, a, tiles, swizzle); break;
   }
-  a.tok ? launch_q<D, GC, 1, true>(a, stream) : launch_q<D, GC, 1, false>(a, stream);
+  launch_join<D>(a, a.rows_group, rows, stream);
   return hipGetLastError();
 }
 

@@ -116,12 +116,10 @@ q4_status check_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv
 void pick_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv, int32_t q_heads, int32_t kv_heads,
                int32_t head_dim, int64_t window, q4::AttnArgs* a) {
   const int64_t rows = std::min(max_q, tokens) * (q_heads / kv_heads);
-  a->tiles_wave = rows > 16 && head_dim < 256 ? 2 : 1;
-  a->tok = rows <= 128;
-  const int64_t rows_group = 16 * a->tiles_wave * (a->tok ? 1 : 4);
-  const int64_t groups = (rows + rows_group - 1) / rows_group * kv_heads * seqs;
-  const int64_t span = std::min(max_kv, window > 0 ? window + rows_group + 32 : max_kv);
-  const int64_t want = (int64_t)q4::device_cu_count_cached() * 8;  // workgroups
+  a->rows_group = rows <= 16 ? 16 : rows <= 128 ? 32 : 128;
+  const int64_t groups = (rows + a->rows_group - 1) / a->rows_group * kv_heads * seqs;
+  const int64_t span = std::min(max_kv, window > 0 ? window + a->rows_group + 32 : max_kv);
+  const int64_t want = (int64_t)q4::device_cu_count_cached() * (a->rows_group < 128 ? 4 : 1);  // workgroups
   int64_t splits = std::max<int64_t>(1, std::min<int64_t>(want / std::max<int64_t>(groups, 1), (span + 511) / 512));
   const int64_t chunk = q4::round_up((span + splits - 1) / splits, 128);
   splits = std::max<int64_t>(1, (span + chunk - 1) / std::max<int64_t>(chunk, 1));

@@ -126,8 +126,7 @@ struct AttnArgs {
   int window;  // 0: none
   void* out;   // [tokens][q_heads][head_dim]
   // launch shape
-  bool tok;        // the wavefronts of a workgroup share rows and split the keys
-  int tiles_wave;  // tiles of 16 rows per wavefront: 1 or 2
+  int rows_group;  // rows of a workgroup: 16 or 32 (its wavefronts split the keys), or 128
   int splits;      // workgroups splitting a row tile's keys, `chunk` each (a multiple of 128)
   int chunk;
   float* part_o;   // splits > 1: float32 [tokens][q_heads][splits][head_dim]
