@@ -730,7 +730,7 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const half4_t kh = __builtin_bit_cast(half4_t, ks[i >> 3][g][(i >> 2) & 1]);
-        s[i] = g == 0 ? part[i] * (float)kh[i & 3] : __builtin_fmaf(part[i], (float)kh[i & 3], s[i]);
+        s[i] = __builtin_fmaf(part[i], (float)kh[i & 3], g == 0 ? 0.0f : s[i]);  // one v_fma_mix
       }
     }
 #pragma unroll
@@ -836,7 +836,7 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const half4_t vh = __builtin_bit_cast(half4_t, vs[j][g][i >> 2]);
-          p[g][i] = (_Float16)(s[8 * j + i] * (float)vh[i & 3]);
+          p[g][i] = (_Float16)__builtin_fmaf(s[8 * j + i], (float)vh[i & 3], 0.0f);  // one v_fma_mix
         }
       if (edge) {
         // a key that one row sees and another does not may have an infinite scale
@@ -895,6 +895,298 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_
       store_row<D>(a, w, split, row, 32 * b + 8 * wave + 4 * c, o, sum, top);
     }
   }
+}
+
+// ---------------------------------------------------------------------------------
+// Many rows: 128 a workgroup, 32 a wavefront, all reading the same keys. Two of the
+// wavefronts convert the K codes of the next 64 keys to float16 operands in LDS, two the V
+// codes, with their scales as floats (K's with the softmax scale in them; both zeroed where
+// no row sees the key), so that a wavefront's vector work is the softmax and a quarter of
+// the conversion, and its registers (no raw codes) leave room for three wavefronts on a
+// SIMD, which cover each other's barriers: one buffer and two barriers per 64 keys. With two
+// wavefronts (a second buffer, one barrier) the barriers cost what the sharing saves.
+template <int D, int GC>
+struct Shared {
+  static constexpr int KB = D / 32;
+  static constexpr int kKeys = 64;
+  half8_t k[2][2 * KB][kWave];  // [32-key pair][16-channel step]
+  half8_t v[2][2][KB][kWave];   // [pair][tile][32-channel block]
+  float ks[GC][kKeys], vs[GC][kKeys];
+  int there[4];  // whether a tile's page lies in the cache
+  int vmax[2];   // largest finite V scale of a pair (float16 bits)
+  int pad[2];
+};
+
+template <int D, int GC>
+__global__ __launch_bounds__(256, (D < 256 ? 3 : 1)) void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
+  using S = Shared<D, GC>;
+  constexpr int KB = S::KB, BPG = KB / GC, kKeys = S::kKeys;
+  extern __shared__ __align__(16) unsigned char smem[];
+  S& lds = *reinterpret_cast<S*>(smem);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int col = lane & 31, c = lane >> 5;
+  // blocks: split fastest, then row tile (last rows, the longest spans, first), head, sequence; with
+  // `swizzle` the eight XCDs, which take blocks in turn, each keep whole heads (their L2 then
+  // holds the keys all of a head's tiles read)
+  const unsigned inner = (unsigned)(a.splits * tiles);
+  unsigned group = blockIdx.x / inner, at = blockIdx.x % inner;
+  if (swizzle) {
+    const unsigned x = blockIdx.x % 8, y = blockIdx.x / 8;
+    group = x + 8 * (y / inner);
+    at = y % inner;
+  }
+  const int split = (int)(at % (unsigned)a.splits);
+  const int tile_q = tiles - 1 - (int)(at / (unsigned)a.splits);
+  Job w;
+  if (!make_job(a, (int)(group / (unsigned)a.cache.kv_heads), (int)(group % (unsigned)a.cache.kv_heads), &w)) return;
+  constexpr int kGroup = 128;
+  const int g0 = tile_q * kGroup, r0 = g0 + 32 * wave;
+  if (g0 >= w.rows) return;  // the whole workgroup; a wavefront without rows still converts
+  const bool idle = r0 >= w.rows;
+
+  const int row = r0 + col;
+  half8_t q[2 * KB];
+  int pos;  // position of the lane's row: its own last visible key; -1: no row
+  {
+    const int i = min(row, w.rows - 1) / w.share, hs = min(row, w.rows - 1) - i * w.share;
+    pos = row < w.rows ? w.len - w.nq + i : -1;
+    const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.first + i) * a.q_stride +
+                          (int64_t)(w.head * w.share + hs) * D + 8 * c;
+#pragma unroll
+    for (int b = 0; b < 2 * KB; ++b) q[b] = as_half8(*reinterpret_cast<const uint4*>(src + 16 * b));
+  }
+  // base: m + E. A score more than `limit` above it makes m rise; a row that has seen no key
+  // yet has base 0 and limit -infinity, and its first key sets m.
+  float base = 0.0f, limit = -__builtin_inff(), l = 0.0f;
+  float16_t acc[KB];
+#pragma unroll
+  for (int b = 0; b < KB; ++b) acc[b] = float16_t{};
+
+  const Span all = span_of(a, w, g0, kGroup);                   // the workgroup's keys
+  const Span own = span_of(a, w, min(r0, w.rows - 1), 32);      // those of this wavefront's rows
+  const int t_first = all.first + split * a.chunk;
+  const int t_last = a.splits > 1 ? min(all.last, t_first + a.chunk) : all.last;
+  const float scale = a.scale * 1.4426950408889634f;
+  float exp_v = -64.0f;  // E (wave-uniform)
+  int cap_v = 0;         // largest V scale that E covers, as float16 bits
+
+  // --- producer: one pair of tiles of K (wavefronts 0, 1) or of V (2, 3) every 64 keys
+  const DequantRegs dq = DequantRegs::make();
+  const bool is_v = wave >= 2;
+  const int pair = wave & 1;
+  const uint32_t* codes = static_cast<const uint32_t*>(is_v ? a.cache.v_codes : a.cache.k_codes);
+  const uint16_t* scales = static_cast<const uint16_t*>(is_v ? a.cache.v_scales : a.cache.k_scales);
+  const ScalarInts table = scalar_ints(a.block_table + (int64_t)w.seq * a.max_blocks);
+  const int tpp = a.cache.page_size / kTokTile;
+  const int stride_block = 4 / tpp, stride_rem = 4 - stride_block * tpp;
+  const int last_tile = max(t_last - 1, 0) / kTokTile;
+  Walk next;
+  next.tile = t_first / kTokTile + 2 * pair;
+  next.block = next.tile / tpp;
+  next.in_page = next.tile - next.block * tpp;
+  uint32_t raw[2][KB];  // codes of the 64 keys after those in LDS
+  uint16_t raw_s[GC];   // scale of key lane % 32
+  bool raw_there[2];
+  int raw_t0 = t_first;
+  int page[2], in_page2;
+  int top_v = 0;  // largest V scale this wavefront has converted
+  auto fetch_pages = [&]() __attribute__((always_inline)) {
+    const bool wraps = next.in_page + 1 == tpp;
+    in_page2 = wraps ? 0 : next.in_page + 1;
+    const int b2 = next.block + (wraps ? 1 : 0);
+    page[0] = next.tile <= last_tile && next.block < a.max_blocks ? table[next.block] : -1;
+    page[1] = next.tile + 1 <= last_tile && b2 < a.max_blocks ? table[b2] : -1;
+  };
+  auto load = [&]() __attribute__((always_inline)) {
+    int64_t tile[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      // a tile behind the last key or of a page outside the cache is read from page 0 and hidden
+      raw_there[j] = (unsigned)page[j] < (unsigned)a.cache.pages;
+      tile[j] = ((int64_t)(raw_there[j] ? page[j] : 0) * a.cache.kv_heads + w.head) * tpp + (j ? in_page2 : next.in_page);
+      load_codes<D>(raw[j], codes + tile[j] * (2 * D), lane);
+    }
+    const uint16_t* sc = scales + ((lane & 16) ? tile[1] : tile[0]) * (GC * kTokTile) + (lane & 15);
+#pragma unroll
+    for (int g = 0; g < GC; ++g) raw_s[g] = sc[g * kTokTile];
+    next.tile += 4;
+    next.block += stride_block;
+    next.in_page += stride_rem;
+    if (next.in_page >= tpp) {
+      next.in_page -= tpp;
+      ++next.block;
+    }
+    fetch_pages();
+  };
+  auto convert = [&]() __attribute__((always_inline)) {
+    const int r16 = lane & 15, c4 = lane >> 4;
+    if (is_v) {
+      // four tokens of channels r and 16 + r: half of an operand of lanes r, 16 + r (+ 32)
+      VRegs lo{0x000F000Fu, 0x64006400u, as_half2(0xE408E408u)}, hi{0x00F000F0u, 0x54005400u, as_half2(0xD480D480u)};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int b = 0; b < KB; ++b) {
+          half4_t* to = reinterpret_cast<half4_t*>(&lds.v[pair][j][b][r16 + 32 * (c4 & 1)]) + (c4 >> 1);
+          to[0] = v_codes4(raw[j][b], lo);
+          to[2 * 16] = v_codes4(raw[j][b], hi);
+        }
+    } else {
+      const half2_t lo_bias = {(_Float16)-1032.0f, (_Float16)-1032.0f};
+      const half2_t hi_bias = {(_Float16)-72.0f, (_Float16)-72.0f};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int b = 0; b < KB; ++b)
+          lds.k[pair][2 * b + (c4 >> 1)][r16 + 16 * j + 32 * (c4 & 1)] = dequant8r(raw[j][b], dq, lo_bias, hi_bias);
+    }
+    // what no row sees may hold anything: 0 * NaN must not arise
+    const int key = raw_t0 + 32 * pair + (lane & 31);
+    const bool seen = ((lane & 16) ? raw_there[1] : raw_there[0]) && key < t_last && key > all.pos_lo - all.window;
+    int top = 0;
+#pragma unroll
+    for (int g = 0; g < GC; ++g) {
+      const uint32_t bits = seen ? raw_s[g] : 0u;
+      const float f = (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+      if (lane < 32) (is_v ? lds.vs : lds.ks)[g][32 * pair + lane] = is_v ? f : f * scale;
+      top = max(top, bits < 0x7C00u ? (int)bits : 0);
+    }
+    if (is_v) {
+      if (__any(top > top_v)) {
+#pragma unroll
+        for (int i = 1; i < 32; i <<= 1) top = max(top, __shfl_xor(top, i, 64));
+        top_v = max(top_v, __builtin_amdgcn_readfirstlane(top));
+      }
+      if (lane == 0) lds.vmax[pair] = top_v;
+    } else if (lane < 2) {
+      lds.there[2 * pair + lane] = lane ? raw_there[1] : raw_there[0];
+    }
+    raw_t0 += kKeys;
+  };
+
+  auto compute = [&](int t0) __attribute__((always_inline)) {
+    const int vmax = __builtin_amdgcn_readfirstlane(max(lds.vmax[0], lds.vmax[1]));
+    if (vmax > cap_v) {
+      cap_v = vmax | 0x3FF;  // up to the end of its binade
+      const float up = (float)(cap_v >> 10) - 14.0f - kHeadroom - exp_v, alpha = exp2_fast(-up);
+      exp_v += up;
+      if (limit > -__builtin_inff()) {
+        base += up;
+        limit = kSlack - exp_v;
+        l *= alpha;
+#pragma unroll
+        for (int b = 0; b < KB; ++b) acc[b] *= alpha;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int th = t0 + kStep * h;
+      if (th > own.pos_hi || th + kStep <= own.first) continue;  // none of these rows sees any (uniform)
+      const bool there0 = __builtin_amdgcn_readfirstlane(lds.there[2 * h]);
+      const bool there1 = __builtin_amdgcn_readfirstlane(lds.there[2 * h + 1]);
+      const bool edge =
+          th + kStep > own.pos_lo + 1 || th <= own.pos_hi - own.window || th + kStep > t_last || !there0 || !there1;
+
+      // scores, base 2, relative to m + E
+      float s[16];
+#pragma unroll
+      for (int g = 0; g < GC; ++g) {
+        float16_t part = {};
+#pragma unroll
+        for (int b = 2 * g * BPG; b < 2 * (g + 1) * BPG; ++b) part = mfma32(lds.k[h][b][lane], q[b], part);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float4_t ks = *reinterpret_cast<const float4_t*>(&lds.ks[g][32 * h + 8 * u + 4 * c]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[4 * u + i] = __builtin_fmaf(part[4 * u + i], ks[i], g == 0 ? -base : s[4 * u + i]);
+        }
+      }
+      uint32_t hidden = 0;  // keys of the lane that its row does not see
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int key = th + 8 * (i >> 2) + 4 * c + (i & 3);
+          if (!(i < 8 ? there0 : there1) || key >= t_last || key > pos || key <= pos - own.window) {
+            s[i] = -__builtin_inff();
+            hidden |= 1u << i;
+          }
+        }
+      }
+      // one far above its row's held maximum?
+      float mx = max3(s[0], s[1], s[2]);
+#pragma unroll
+      for (int i = 3; i < 15; i += 2) mx = max3(mx, s[i], s[i + 1]);
+      mx = fmaxf(mx, s[15]);
+      if (__any(mx > limit)) {
+        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+        if (mx > -__builtin_inff()) {
+          const bool first = limit == -__builtin_inff();
+          const float up = first ? mx + exp_v : fmaxf(mx + exp_v, 0.0f);
+          const float alpha = first ? 1.0f : exp2_fast(-up);
+          base += up;
+          limit = kSlack - exp_v;
+          l *= alpha;
+#pragma unroll
+          for (int b = 0; b < KB; ++b) acc[b] *= alpha;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[i] -= up;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[i] = exp2_fast(s[i]);
+        l += s[i];
+      }
+      // weights, to float16 with the V scale in them, and O += V P, a tile's 16 keys at a time
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        half8_t p[GC];
+#pragma unroll
+        for (int g = 0; g < GC; ++g)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float4_t vs = *reinterpret_cast<const float4_t*>(&lds.vs[g][32 * h + 16 * j + 8 * u + 4 * c]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[g][4 * u + i] = (_Float16)(s[8 * j + 4 * u + i] * vs[i]);
+          }
+        if (edge) {
+          // a key that one row sees and another does not may have an infinite scale
+#pragma unroll
+          for (int g = 0; g < GC; ++g)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (hidden >> (8 * j + i) & 1u) p[g][i] = (_Float16)0.0f;
+        }
+#pragma unroll
+        for (int b = 0; b < KB; ++b) acc[b] = mfma32(lds.v[h][j][b][lane], p[b / BPG], acc[b]);
+      }
+    }
+  };
+
+  if (t_first < t_last) {
+    fetch_pages();
+    load();
+    convert();
+    load();
+    lds_barrier();
+    for (int t0 = t_first;;) {
+      if (!idle) compute(t0);
+      if ((t0 += kKeys) >= t_last) break;
+      lds_barrier();  // all have read these keys
+      convert();
+      load();
+      lds_barrier();
+    }
+  }
+  l += __shfl_xor(l, 32, 64);
+  if (limit == -__builtin_inff()) base = kLowest;
+#pragma unroll
+  for (int b = 0; b < KB; ++b)
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      store_row<D>(a, w, split, row, 32 * b + 8 * u + 4 * c,
+                   float4_t{acc[b][4 * u], acc[b][4 * u + 1], acc[b][4 * u + 2], acc[b][4 * u + 3]}, l, base);
 }
 
 // Joins the splits of a row: a workgroup per row, D / 4 lanes a group of channels, the
@@ -968,7 +1260,7 @@ hipError_t launch_t(const AttnArgs& a, hipStream_t stream) {
   switch (a.rows_group) {
     case 16: hipLaunchKernelGGL((attn_kernel<D, GC, 1>), grid, dim3(256), 0, stream, a, tiles); break;
     case 32: hipLaunchKernelGGL((attn32_kernel<D, GC, false>), grid, dim3(256), 0, stream, a, tiles, swizzle); break;
-    default: hipLaunchKernelGGL((attn32_kernel<D, GC, true>), grid, dim3(256), 0, stream, a, tiles, swizzle); break;
+    default: hipLaunchKernelGGL((attn_rows_kernel<D, GC>), grid, dim3(256), sizeof(Shared<D, GC>), stream, a, tiles, swizzle); break;
   }
   launch_join<D>(a, a.rows_group, rows, stream);
   return hipGetLastError();
