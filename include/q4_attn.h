@@ -133,7 +133,8 @@ q4_status q4_paged_kv_dequant(const q4_paged_kv* cache, const int32_t* slots, in
  * `workspace` (16-byte aligned) must hold q4_paged_attention_workspace_bytes() bytes
  * (NULL when that is 0, else Q4_ERR_WORKSPACE); contents as q4_gemm's. */
 size_t q4_paged_attention_workspace_bytes(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv,
-                                          int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t window);
+                                          int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t group,
+                                          int64_t window);
 q4_status q4_paged_attention(const void* q, int64_t q_stride, const q4_paged_kv* cache, const int32_t* block_table,
                              int64_t max_blocks, const int32_t* q_offsets, const int32_t* kv_lens, int64_t seqs,
                              int64_t tokens, int64_t max_q, int64_t max_kv, int32_t q_heads, float scale,

@@ -196,9 +196,9 @@ def paged_kv_dequant(cache: PagedKVCache4, slots):
 
 
 def paged_attention_workspace_bytes(seqs: int, tokens: int, max_q: int, max_kv: int, q_heads: int, kv_heads: int,
-                                    head_dim: int, window: int = 0) -> int:
+                                    head_dim: int, group: int, window: int = 0) -> int:
     return int(_lib.load().q4_paged_attention_workspace_bytes(seqs, tokens, max_q, max_kv, q_heads, kv_heads, head_dim,
-                                                              window))
+                                                              group, window))
 
 
 def paged_attention(q, cache: PagedKVCache4, block_table, q_offsets, kv_lens, max_q: int, max_kv: int,
@@ -232,7 +232,7 @@ def paged_attention(q, cache: PagedKVCache4, block_table, q_offsets, kv_lens, ma
     lib = _lib.load()
     cur = enter(dev)  # the split, and with it the workspace, depends on the device
     try:
-        need = lib.q4_paged_attention_workspace_bytes(seqs, n, max_q, max_kv, hq, heads, d, window)
+        need = lib.q4_paged_attention_workspace_bytes(seqs, n, max_q, max_kv, hq, heads, d, cache.group, window)
     finally:
         if cur != dev:
             torch.cuda.set_device(cur)

@@ -151,7 +151,7 @@ __device__ __forceinline__ bool make_job(const AttnArgs& a, int seq, int head, J
   // kept inside what the arguments promise
   w->seq = seq;
   w->head = head;
-  w->share = a.q_heads / a.cache.kv_heads;
+  w->share = __builtin_amdgcn_readfirstlane(a.q_heads / a.cache.kv_heads);
   const ScalarInts offsets = scalar_ints(a.q_offsets);
   w->first = min(max(offsets[seq], 0), a.tokens);
   w->nq = min(min(max(offsets[seq + 1], w->first), a.tokens) - w->first, a.max_q);
@@ -167,8 +167,8 @@ struct Span {
 
 __device__ __forceinline__ Span span_of(const AttnArgs& a, const Job& w, int r0, int n) {
   Span s;
-  s.pos_lo = w.len - w.nq + r0 / w.share;
-  s.pos_hi = w.len - w.nq + (min(r0 + n, w.rows) - 1) / w.share;
+  s.pos_lo = w.len - w.nq + __builtin_amdgcn_readfirstlane(r0 / w.share);
+  s.pos_hi = w.len - w.nq + __builtin_amdgcn_readfirstlane((min(r0 + n, w.rows) - 1) / w.share);
   s.last = s.pos_hi + 1;
   s.window = a.window > 0 ? a.window : s.last + 1;
   s.first = max(0, s.pos_lo - s.window + 1) / kStep * kStep;
@@ -180,36 +180,232 @@ struct Walk {
   int tile, block, in_page;  // tile of the sequence, its page table entry, tile of the page
 };
 
-// Result of row `row`, channels ch .. ch + 3: the output, or the split's part.
-template <int D>
-__device__ __forceinline__ void store_row(const AttnArgs& a, const Job& w, int split, int row, int ch, float4_t o,
-                                          float sum, float base) {
-  if (row >= w.rows) return;
-  const int i = row / w.share, hs = row - i * w.share;
-  const int64_t r = (int64_t)(w.first + i) * a.q_heads + w.head * w.share + hs;
-  if (a.splits > 1) {
-    const int64_t rs = r * a.splits + split;
-    *reinterpret_cast<float4_t*>(a.part_o + rs * D + ch) = o;
-    if (ch == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * rs) = make_float2(base, sum);
-    return;
-  }
+// Float16 row from sums.
+__device__ __forceinline__ uint2 to_row(float4_t o, float sum) {
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   half4_t h;
 #pragma unroll
   for (int e = 0; e < 4; ++e) h[e] = (_Float16)(o[e] * inv);
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + r * D + ch) = __builtin_bit_cast(uint2, h);
+  return __builtin_bit_cast(uint2, h);
 }
 
-template <int D, int GC, int QT>
+// Address of channel ch of row `row` of a job in the output.
+template <int D>
+__device__ __forceinline__ uint2* out_at(const AttnArgs& a, const Job& w, int row, int ch) {
+  const int i = row / w.share, hs = row - i * w.share;
+  const int64_t r = (int64_t)(w.first + i) * a.q_heads + w.head * w.share + hs;
+  return reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + r * D + ch);
+}
+
+// ---------------------------------------------------------------------------------
+// Work shares. Where the wavefronts of a workgroup split the keys, a job (RG rows of a sequence
+// and KV head) is cut into units of 128 keys, all jobs' units form one line (sequence,
+// row tile, head, keys), and each of the resident workgroups takes an equal share of it: the
+// chip is full to the end whatever the lengths are, which only the device knows. A share
+// may begin and end inside a job; those two pieces are partial results (slot 0: the piece
+// does not begin its job, slot 1: it begins it and is cut), the jobs between are whole.
+constexpr int kUnit = 128;
+constexpr int kMinUnits = 4;  // units a share has at least: fewer workgroups for little work
+
+struct SeqWork {
+  int units, tiles, key0;  // units of a job, row tiles, first key (a multiple of kStep)
+};
+
+__device__ __forceinline__ SeqWork seq_work(const AttnArgs& a, int nq, int len, int rows, int rg) {
+  SeqWork s;
+  const int window = a.window > 0 ? a.window : len + 1;
+  s.key0 = max(0, len - nq - window + 1) / kStep * kStep;
+  s.units = max(1, (max(len - s.key0, 0) + kUnit - 1) / kUnit);
+  s.tiles = (rows + rg - 1) / rg;
+  return s;
+}
+
+// Units of the sequences `base + lane`.
+__device__ __forceinline__ int64_t lane_work(const AttnArgs& a, int seq, int rg) {
+  if (seq >= a.seqs) return 0;
+  const int first = min(max(a.q_offsets[seq], 0), a.tokens);
+  const int nq = min(min(max(a.q_offsets[seq + 1], first), a.tokens) - first, a.max_q);
+  const int len = min(max(a.kv_lens[seq], 0), a.max_kv);
+  const SeqWork s = seq_work(a, nq, len, nq * (a.q_heads / a.cache.kv_heads), rg);
+  return (int64_t)s.tiles * a.cache.kv_heads * s.units;
+}
+
+// Values that are the same in every lane but were computed on the vector unit (divisions, lane
+// operations), moved to scalar registers: addresses and branches made of them then stay scalar.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
+  return (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ int64_t total_work(const AttnArgs& a, int rg, int lane) {
+  long long sum = 0;
+  for (int base = 0; base < a.seqs; base += kWave) sum += lane_work(a, base + lane, rg);
+#pragma unroll
+  for (int m = 1; m < kWave; m <<= 1) sum += __shfl_xor(sum, m, 64);
+  return uniform64(sum);
+}
+
+// The sequence that holds unit `unit` (below the total), and the units before it.
+__device__ __forceinline__ int find_seq(const AttnArgs& a, int rg, int lane, int64_t unit, int64_t* before) {
+  long long acc = 0;
+  for (int base = 0; base < a.seqs; base += kWave) {
+    const long long own = lane_work(a, base + lane, rg);
+    long long incl = own;
+#pragma unroll
+    for (int m = 1; m < kWave; m <<= 1) {
+      const long long up = __shfl_up(incl, m, 64);
+      if (lane >= m) incl += up;
+    }
+    const uint64_t past = __ballot(acc + incl > unit);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      *before = uniform64(acc + __shfl(incl - own, at, 64));
+      return base + at;
+    }
+    acc += __shfl(incl, kWave - 1, 64);
+  }
+  *before = acc;  // not reached
+  return a.seqs - 1;
+}
+
+__device__ __forceinline__ int64_t shares_of(const AttnArgs& a, int64_t total) {
+  const int64_t want = total / kMinUnits;
+  return uniform64(want < 1 ? 1 : want < a.shares ? want : a.shares);
+}
+
+// One piece of work: rows r0 .. of a job, keys [key0, key1) of it (key1 < 0: to the end);
+// slot < 0: the whole job.
+struct Piece {
+  Job w;
+  int r0, key0, key1, slot;
+};
+
+// `p` with every field in scalar registers.
+__device__ __forceinline__ Piece uniform_piece(const Piece& p) {
+  return Piece{Job{uniform(p.w.first), uniform(p.w.rows), uniform(p.w.len), uniform(p.w.nq), uniform(p.w.seq),
+                   uniform(p.w.head), uniform(p.w.share)},
+               uniform(p.r0), uniform(p.key0), uniform(p.key1), uniform(p.slot)};
+}
+
+struct Shares {
+  int64_t at, end, total, count;
+  int64_t before, seq_end;  // units before the current sequence and before the next
+  int64_t cut_end;          // end of the job this share begins and does not end (0: none)
+  Job w;
+  SeqWork s;
+  bool whole;  // no shares: one job a workgroup
+
+  __device__ __forceinline__ void enter(const AttnArgs& a, int rg, int seq) {
+    make_job(a, seq, 0, &w);
+    s = seq_work(a, w.nq, w.len, w.rows, rg);
+    seq_end = before + (int64_t)s.tiles * a.cache.kv_heads * s.units;
+  }
+
+  __device__ __forceinline__ bool begin(const AttnArgs& a, int rg, int lane) {
+    whole = a.shares == 0;
+    if (whole) {
+      at = blockIdx.x;
+      return true;
+    }
+    long long own = 0, incl = 0;
+    if (a.seqs <= kWave) {  // one pass finds the total and the place
+      own = incl = lane_work(a, lane, rg);
+#pragma unroll
+      for (int m = 1; m < kWave; m <<= 1) {
+        const long long up = __shfl_up(incl, m, 64);
+        if (lane >= m) incl += up;
+      }
+      total = uniform64(__shfl(incl, kWave - 1, 64));
+    } else {
+      total = total_work(a, rg, lane);
+    }
+    count = shares_of(a, total);
+    cut_end = 0;
+    if ((int64_t)blockIdx.x >= count) return false;
+    at = uniform64((int64_t)blockIdx.x * total / count);
+    end = uniform64(((int64_t)blockIdx.x + 1) * total / count);
+    if (at >= end) return false;
+    int seq;
+    if (a.seqs <= kWave) {
+      seq = __builtin_ctzll(__ballot(incl > at));
+      before = uniform64(__shfl(incl - own, seq, 64));
+    } else {
+      seq = find_seq(a, rg, lane, at, &before);
+    }
+    enter(a, rg, uniform(seq));
+    return true;
+  }
+
+  __device__ __forceinline__ bool next(const AttnArgs& a, int rg, int lane, int tiles, Piece* p) {
+    if (whole) {
+      if (at < 0) return false;
+      const unsigned j = (unsigned)at, heads = (unsigned)a.cache.kv_heads;
+      at = -1;
+      const int group = uniform((int)(j / heads));
+      const int seq = uniform((int)((unsigned)group / (unsigned)tiles));
+      if (!make_job(a, seq, (int)j - group * (int)heads, &p->w)) return false;
+      p->r0 = (group - seq * tiles) * rg;
+      p->key0 = 0;
+      p->key1 = -1;
+      p->slot = -1;
+      return p->r0 < p->w.rows;
+    }
+    if (at >= end) return false;
+    if (at >= seq_end) {
+      const int seq = find_seq(a, rg, lane, at, &before);
+      enter(a, rg, uniform(seq));
+    }
+    const int64_t off = at - before;
+    const int64_t job = uniform64(off / s.units);
+    const int k0 = (int)(off - job * s.units);
+    const int k1 = (int)(s.units - k0 < end - at ? s.units : k0 + (end - at));
+    const int tile = uniform((int)(job / a.cache.kv_heads));
+    p->w = w;
+    p->w.head = (int)(job - (int64_t)tile * a.cache.kv_heads);
+    p->r0 = tile * rg;
+    p->key0 = s.key0 + k0 * kUnit;
+    p->key1 = k1 == s.units ? -1 : s.key0 + k1 * kUnit;
+    p->slot = k0 == 0 && k1 == s.units ? -1 : k0 > 0 ? 0 : 1;
+    if (p->slot == 1) cut_end = at + s.units;
+    at += k1 - k0;
+    return true;
+  }
+
+  // For the join: the job that this share begins and does not end, and its pieces.
+  __device__ __forceinline__ void finish(const AttnArgs& a, const Piece& last) const {
+    if (whole || threadIdx.x != 0) return;
+    const int n = cut_end > 0 ? (int)((cut_end * count - 1) / total) - (int)blockIdx.x + 1 : 0;
+    int4* to = reinterpret_cast<int4*>(a.cuts) + 2 * blockIdx.x;
+    to[0] = make_int4(n, last.w.first, last.w.rows, last.w.head);
+    to[1] = make_int4(last.r0, 0, 0, 0);
+  }
+};
+
+// Channels ch .. ch + 3 of a piece's row r0 + local: the output, or the piece's slot.
+template <int D, int RG>
+__device__ __forceinline__ void store_piece(const AttnArgs& a, const Piece& p, int local, int ch, float4_t o, float sum,
+                                            float base) {
+  if (p.slot < 0) {
+    if (p.r0 + local < p.w.rows) *out_at<D>(a, p.w, p.r0 + local, ch) = to_row(o, sum);
+    return;
+  }
+  const int64_t at = ((int64_t)blockIdx.x * 2 + p.slot) * RG + local;
+  *reinterpret_cast<float4_t*>(a.part_o + at * D + ch) = o;
+  if (ch == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(base, sum);
+}
+
+template <int D, int GC>
 struct Attn {
   static constexpr int KB = D / 32;    // 32-channel blocks
   static constexpr int BPG = KB / GC;  // of them per scale group
-  static constexpr int kWaves = 4;
-  static constexpr int kRows = 16 * QT;
-  // wavefronts per SIMD the registers are budgeted for: the most without spills
-  static constexpr int kWavesSimd = D == 64    ? (QT == 1 ? 4 - GC / 2 : 4 - GC)
-                                    : D == 128 ? (QT == 1 ? (GC == 1 ? 3 : 2) : (GC <= 2 ? 2 : 1))
-                                               : 1;
+  static constexpr int kRows = 16;
+  // Steps of 32 keys a wavefront has in registers (one computed, the other in flight; three and
+  // four stages were 3 us slower at 48 x 8K keys), and wavefronts per SIMD the registers are
+  // budgeted for (three with two stages spill at 128 channels: 68 -> 86 us).
+  static constexpr int kStages = 2;
+  static constexpr int kWavesSimd = D == 64 ? 3 : D == 128 ? 2 : 1;
 
   struct Step {
     Tile<D, GC> t[2];
@@ -217,323 +413,274 @@ struct Attn {
   };
 };
 
-// Few rows: all four wavefronts have the same ones and split the keys.
-template <int D, int GC, int QT>
-__global__ __launch_bounds__(256, (Attn<D, GC, QT>::kWavesSimd)) void attn_kernel(AttnArgs a, int tiles) {
-  using C = Attn<D, GC, QT>;
+// At most 16 rows: all four wavefronts have the same ones and split the keys.
+template <int D, int GC>
+__global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(AttnArgs a, int tiles) {
+  using C = Attn<D, GC>;
   using Step = typename C::Step;
   constexpr int KB = C::KB, BPG = C::BPG;
+  __shared__ float4_t buf[4][2 * KB][kWave];
+  __shared__ float2 ml[4][16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, c4 = lane >> 4;
-  // blocks: split fastest, then row tile (last rows, the longest spans, first), head, sequence
-  unsigned at = blockIdx.x;
-  const int split = (int)(at % (unsigned)a.splits);
-  at /= (unsigned)a.splits;
-  const int tile_q = tiles - 1 - (int)(at % (unsigned)tiles);
-  at /= (unsigned)tiles;
-  Job w;
-  if (!make_job(a, (int)(at / (unsigned)a.cache.kv_heads), (int)(at % (unsigned)a.cache.kv_heads), &w)) return;
-  const int r0 = tile_q * C::kRows;
-  if (r0 >= w.rows) return;
-
-  half8_t q[QT][KB];
-  float bias[QT][GC];  // -(264 * sum of q over elements 0, 1, 4, 5 + 24 * the others), per scale group
-  int pos[QT];         // position of the lane's row: its own last visible key; -1: no row
-  float m[QT], base[QT], l[QT];
-  float4_t acc[QT][2 * KB];
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    const int row = r0 + 16 * t + col;
-    const int i = min(row, w.rows - 1) / w.share, hs = min(row, w.rows - 1) - i * w.share;
-    pos[t] = row < w.rows ? w.len - w.nq + i : -1;
-    const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.first + i) * a.q_stride +
-                          (int64_t)(w.head * w.share + hs) * D + 8 * c4;
-#pragma unroll
-    for (int b = 0; b < KB; ++b) q[t][b] = as_half8(*reinterpret_cast<const uint4*>(src + 32 * b));
-#pragma unroll
-    for (int g = 0; g < GC; ++g) {
-      float s2 = 0.0f, s6 = 0.0f;
-#pragma unroll
-      for (int b = g * BPG; b < (g + 1) * BPG; ++b)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) (e & 2 ? s6 : s2) += (float)q[t][b][e];
-      float sum = 264.0f * s2 + 24.0f * s6;
-      sum += __shfl_xor(sum, 16, 64);
-      sum += __shfl_xor(sum, 32, 64);
-      bias[t][g] = -sum;
-    }
-    m[t] = base[t] = kLowest;
-    l[t] = 0.0f;
-#pragma unroll
-    for (int b = 0; b < 2 * KB; ++b) acc[t][b] = float4_t{0.f, 0.f, 0.f, 0.f};
-  }
-
-  const Span sp = span_of(a, w, r0, C::kRows);
-  // this workgroup's part of the keys
-  const int t_first = sp.first + split * a.chunk;
-  const int t_last = a.splits > 1 ? min(sp.last, t_first + a.chunk) : sp.last;
-  const int tpp = a.cache.page_size / kTokTile;
-  const ScalarInts table = scalar_ints(a.block_table + (int64_t)w.seq * a.max_blocks);
   const float scale = a.scale * 1.4426950408889634f;
   const DequantRegs dq = DequantRegs::make();
   const KRegs kr = KRegs::make();
-  float exp_v = -64.0f;  // E (wave-uniform)
-  uint32_t cap_v = 0;    // largest V scale that E covers, as float16 bits
-
-  constexpr int kStride = C::kWaves * 2;  // tiles from one step of a wavefront to the next
+  const int tpp = a.cache.page_size / kTokTile;
+  constexpr int kStride = 8;  // tiles from one step of a wavefront to the next
   const int stride_block = kStride / tpp, stride_rem = kStride - stride_block * tpp;
-  const int last_tile = max(t_last - 1, 0) / kTokTile;
-  Walk next;
-  next.tile = t_first / kTokTile + 2 * wave;
-  next.block = next.tile / tpp;
-  next.in_page = next.tile - next.block * tpp;
-  int page[2];      // page numbers of `next`'s two tiles
-  int in_page2;     // and where the second lies in its page
-  auto fetch_pages = [&]() __attribute__((always_inline)) {
-    const bool wraps = next.in_page + 1 == tpp;
-    in_page2 = wraps ? 0 : next.in_page + 1;
-    const int b2 = next.block + (wraps ? 1 : 0);
-    // entries behind the last key's are not read
-    page[0] = next.tile <= last_tile && next.block < a.max_blocks ? table[next.block] : -1;
-    page[1] = next.tile + 1 <= last_tile && b2 < a.max_blocks ? table[b2] : -1;
-  };
-  // Loads of the step at `next`, which then moves on. A tile behind the last key or of a
-  // page outside the cache is read from page 0 and masked.
-  auto load = [&](Step& s) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      s.there[j] = (unsigned)page[j] < (unsigned)a.cache.pages;
-      const int64_t tile =
-          ((int64_t)(s.there[j] ? page[j] : 0) * a.cache.kv_heads + w.head) * tpp + (j ? in_page2 : next.in_page);
-      load_tile<D, GC>(s.t[j], a.cache, tile, lane);
-    }
-    next.tile += kStride;
-    next.block += stride_block;
-    next.in_page += stride_rem;
-    if (next.in_page >= tpp) {
-      next.in_page -= tpp;
-      ++next.block;
-    }
-    fetch_pages();
-  };
+  Shares shares;
+  Piece pc{};
+  bool more = uniform(shares.begin(a, 16, lane));
+  for (bool again = false; more; again = true) {
+    Piece next_piece;
+    if (!uniform(shares.next(a, 16, lane, tiles, &next_piece))) break;
+    pc = uniform_piece(next_piece);
+    if (again) __syncthreads();  // buf of the piece before has been read
+    const Job& w = pc.w;
 
-  auto compute = [&](Step& st, int t0) __attribute__((always_inline)) {
-    const bool edge =
-        t0 + kStep > sp.pos_lo + 1 || t0 <= sp.pos_hi - sp.window || t0 + kStep > t_last || !st.there[0] || !st.there[1];
-    if (edge) {
-      // what no row sees may hold anything: 0 * NaN must not arise
+    const int row = pc.r0 + col;
+    half8_t q[KB];
+    float bias[GC];  // -(264 * sum of q over elements 0, 1, 4, 5 + 24 * the others), per scale group
+    int pos;         // position of the lane's row: its own last visible key; -1: no row
+    {
+      const int i = min(row, w.rows - 1) / w.share, hs = min(row, w.rows - 1) - i * w.share;
+      pos = row < w.rows ? w.len - w.nq + i : -1;
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.first + i) * a.q_stride +
+                            (int64_t)(w.head * w.share + hs) * D + 8 * c4;
+#pragma unroll
+      for (int b = 0; b < KB; ++b) q[b] = as_half8(*reinterpret_cast<const uint4*>(src + 32 * b));
+    }
+    // base: m + E. A score more than `limit` above it makes m rise; a row that has seen no key
+    // yet has base 0 and limit -infinity, and its first key sets m.
+    float base = 0.0f, limit = -__builtin_inff(), l = 0.0f;
+    float4_t acc[2 * KB];
+#pragma unroll
+    for (int b = 0; b < 2 * KB; ++b) acc[b] = float4_t{0.f, 0.f, 0.f, 0.f};
+
+    const Span sp = span_of(a, w, pc.r0, 16);
+    const int t_first = max(pc.key0, sp.first);
+    const int t_last = pc.key1 < 0 ? sp.last : min(sp.last, pc.key1);
+    const ScalarInts table = scalar_ints(a.block_table + (int64_t)w.seq * a.max_blocks);
+    float exp_v = -64.0f;  // E (wave-uniform)
+    uint32_t cap_v = 0;    // largest V scale that E covers, as float16 bits
+
+    const int last_tile = max(t_last - 1, 0) / kTokTile;
+    Walk next;
+    next.tile = t_first / kTokTile + 2 * wave;
+    next.block = next.tile / tpp;
+    next.in_page = next.tile - next.block * tpp;
+    int page[2];   // page numbers of `next`'s two tiles
+    int in_page2;  // and where the second lies in its page
+    auto fetch_pages = [&]() __attribute__((always_inline)) {
+      const bool wraps = next.in_page + 1 == tpp;
+      in_page2 = wraps ? 0 : next.in_page + 1;
+      const int b2 = next.block + (wraps ? 1 : 0);
+      // entries behind the last key's are not read
+      page[0] = next.tile <= last_tile && next.block < a.max_blocks ? table[next.block] : -1;
+      page[1] = next.tile + 1 <= last_tile && b2 < a.max_blocks ? table[b2] : -1;
+    };
+    // Loads of the step at `next`, which then moves on. A tile behind the last key or of a
+    // page outside the cache is read from page 0 and masked.
+    auto load = [&](Step& s) __attribute__((always_inline)) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        s.there[j] = (unsigned)page[j] < (unsigned)a.cache.pages;
+        const int64_t tile =
+            ((int64_t)(s.there[j] ? page[j] : 0) * a.cache.kv_heads + w.head) * tpp + (j ? in_page2 : next.in_page);
+        load_tile<D, GC>(s.t[j], a.cache, tile, lane);
+      }
+      next.tile += kStride;
+      next.block += stride_block;
+      next.in_page += stride_rem;
+      if (next.in_page >= tpp) {
+        next.in_page -= tpp;
+        ++next.block;
+      }
+      fetch_pages();
+    };
+
+    auto compute = [&](Step& st, int t0) __attribute__((always_inline)) {
+      const bool edge = t0 + kStep > sp.pos_lo + 1 || t0 <= sp.pos_hi - sp.window || t0 + kStep > t_last ||
+                        !st.there[0] || !st.there[1];
+      auto key_of = [&](int e) __attribute__((always_inline)) { return t0 + 16 * (e >> 2) + 4 * c4 + (e & 3); };
+      // scores, base 2, relative to m + E
+      float s[8];
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int g = 0; g < GC; ++g) {
-          half4_t kh = __builtin_bit_cast(half4_t, st.t[j].ks[g]), vh = __builtin_bit_cast(half4_t, st.t[j].vs[g]);
+          float4_t part = {bias[g], bias[g], bias[g], bias[g]};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = t0 + 16 * j + 4 * c4 + i;
-            const bool seen = st.there[j] && key < t_last && key > sp.pos_lo - sp.window;
-            kh[i] = seen ? kh[i] : (_Float16)0.0f;
-            vh[i] = seen ? vh[i] : (_Float16)0.0f;
-          }
-          st.t[j].ks[g] = __builtin_bit_cast(uint2, kh);
-          st.t[j].vs[g] = __builtin_bit_cast(uint2, vh);
+          for (int b = g * BPG; b < (g + 1) * BPG; ++b) part = mfma(k_operand(st.t[j].k[b], kr), q[b], part);
+          const half4_t kh = __builtin_bit_cast(half4_t, st.t[j].ks[g]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)  // one v_fma_mix
+            s[4 * j + i] = __builtin_fmaf(part[i], (float)kh[i], g == 0 ? 0.0f : s[4 * j + i]);
         }
-    }
-    uint32_t hidden[QT] = {};  // keys of the lane that its row does not see
-    // E, where a V scale exceeds what it covers
-    uint32_t vmax = 0;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+      for (int e = 0; e < 8; ++e) s[e] = __builtin_fmaf(s[e], scale, -base);
+      uint32_t hidden = 0;  // keys of the lane that its row does not see
+      if (edge) {
 #pragma unroll
-      for (int g = 0; g < GC; ++g) {
-        const uint2 r = st.t[j].vs[g];
-        vmax = max(vmax, max(max(r.x & 0xFFFFu, r.x >> 16), max(r.y & 0xFFFFu, r.y >> 16)));
+        for (int e = 0; e < 8; ++e) {
+          const int key = key_of(e);
+          if (!st.there[e >> 2] || key >= t_last || key > pos || key <= pos - sp.window) {
+            s[e] = -__builtin_inff();
+            hidden |= 1u << e;
+          }
+        }
+        // what no row sees may hold anything: 0 * NaN must not arise
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int g = 0; g < GC; ++g) {
+            half4_t vh = __builtin_bit_cast(half4_t, st.t[j].vs[g]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = key_of(4 * j + i);
+              vh[i] = st.there[j] && key < t_last && key > sp.pos_lo - sp.window ? vh[i] : (_Float16)0.0f;
+            }
+            st.t[j].vs[g] = __builtin_bit_cast(uint2, vh);
+          }
       }
-    if (__any(vmax > cap_v)) {
-      // the largest finite one, up to the end of its binade
-      vmax = cap_v;
+      // E, where a V scale exceeds what it covers
+      uint32_t vmax = 0;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int g = 0; g < GC; ++g) vmax = max_u16x2(vmax, max_u16x2(st.t[j].vs[g].x, st.t[j].vs[g].y));
+      vmax = max(vmax & 0xFFFFu, vmax >> 16);
+      if (__any(vmax > cap_v)) {
+        // the largest finite one, up to the end of its binade
+        vmax = cap_v;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int g = 0; g < GC; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t bits = ((i < 2 ? st.t[j].vs[g].x : st.t[j].vs[g].y) >> (16 * (i & 1))) & 0xFFFFu;
+              vmax = max(vmax, bits < 0x7C00u ? bits : 0u);
+            }
+#pragma unroll
+        for (int i = 1; i < 64; i <<= 1) vmax = max(vmax, (uint32_t)__shfl_xor((int)vmax, i, 64));
+        cap_v = vmax | 0x3FFu;
+        const float up = (float)(int)(cap_v >> 10) - 14.0f - kHeadroom - exp_v, alpha = exp2_fast(-up);
+        exp_v += up;
+        if (limit > -__builtin_inff()) {
+          base += up;
+          limit = kSlack - exp_v;
+          l *= alpha;
+#pragma unroll
+          for (int c = 0; c < 2 * KB; ++c) acc[c] *= alpha;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[e] -= up;
+        }
+      }
+      // a score far above its row's held maximum?
+      float mx = fmaxf(max3(max3(s[0], s[1], s[2]), s[3], s[4]), max3(s[5], s[6], s[7]));
+      if (__any(mx > limit)) {
+        mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+        if (mx > -__builtin_inff()) {
+          const bool first = limit == -__builtin_inff();
+          const float up = first ? mx + exp_v : fmaxf(mx + exp_v, 0.0f);
+          const float alpha = first ? 1.0f : exp2_fast(-up);
+          base += up;
+          limit = kSlack - exp_v;
+          l *= alpha;
+#pragma unroll
+          for (int c = 0; c < 2 * KB; ++c) acc[c] *= alpha;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[e] -= up;
+        }
+      }
+      // weights, to float16 with the V scale in them
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s[e] = exp2_fast(s[e]);
+        l += s[e];
+      }
+      half8_t p[GC];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int g = 0; g < GC; ++g) {
+          const half4_t vh = __builtin_bit_cast(half4_t, st.t[j].vs[g]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            p[g][4 * j + i] = (_Float16)__builtin_fmaf(s[4 * j + i], (float)vh[i], 0.0f);  // one v_fma_mix
+        }
+      if (edge) {
+        // a key that one row sees and another does not may have an infinite scale
 #pragma unroll
         for (int g = 0; g < GC; ++g)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t bits = ((i < 2 ? st.t[j].vs[g].x : st.t[j].vs[g].y) >> (16 * (i & 1))) & 0xFFFFu;
-            vmax = max(vmax, bits < 0x7C00u ? bits : 0u);
-          }
-#pragma unroll
-      for (int s = 1; s < 64; s <<= 1) vmax = max(vmax, (uint32_t)__shfl_xor((int)vmax, s, 64));
-      cap_v = vmax | 0x3FFu;
-      exp_v = (float)(int)(cap_v >> 10) - 14.0f - kHeadroom;
-#pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        const float b = m[t] + exp_v, alpha = exp2_fast(base[t] - b);
-        base[t] = b;
-        l[t] *= alpha;
-#pragma unroll
-        for (int c = 0; c < 2 * KB; ++c) acc[t][c] *= alpha;
+          for (int e = 0; e < 8; ++e)
+            if (hidden >> e & 1u) p[g][e] = (_Float16)0.0f;
       }
-    }
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        acc[2 * b] = mfma(v_operand<false>(st.t[0].v[b], st.t[1].v[b], dq), p[b / BPG], acc[2 * b]);
+        acc[2 * b + 1] = mfma(v_operand<true>(st.t[0].v[b], st.t[1].v[b], dq), p[b / BPG], acc[2 * b + 1]);
+      }
+    };
 
-    // scores, base 2
-    float s[QT][2][4];
+    // kStages - 1 steps in flight while one is computed
+    const int t_own = t_first + kStep * wave;
+    if (t_own < t_last) {
+      Step ring[C::kStages];
+      fetch_pages();
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      half8_t ka[KB];
-#pragma unroll
-      for (int b = 0; b < KB; ++b) ka[b] = k_operand(st.t[j].k[b], kr);
+      for (int i = 0; i + 1 < C::kStages; ++i) load(ring[i]);
 #pragma unroll
       for (int g = 0; g < GC; ++g) {
-        const half4_t kh = __builtin_bit_cast(half4_t, st.t[j].ks[g]);
-        float ks[4];
+        float s2 = 0.0f, s6 = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ks[i] = (float)kh[i] * scale;
+        for (int b = g * BPG; b < (g + 1) * BPG; ++b)
 #pragma unroll
-        for (int t = 0; t < QT; ++t) {
-          float4_t part = {bias[t][g], bias[t][g], bias[t][g], bias[t][g]};
+          for (int e = 0; e < 8; ++e) (e & 2 ? s6 : s2) += (float)q[b][e];
+        float sum = 264.0f * s2 + 24.0f * s6;
+        sum += __shfl_xor(sum, 16, 64);
+        sum += __shfl_xor(sum, 32, 64);
+        bias[g] = -sum;
+      }
+      for (int t0 = t_own; t0 < t_last;) {
 #pragma unroll
-          for (int b = 0; b < BPG; ++b) part = mfma(ka[g * BPG + b], q[t][g * BPG + b], part);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            s[t][j][i] = g == 0 ? part[i] * ks[i] : __builtin_fmaf(part[i], ks[i], s[t][j][i]);
+        for (int i = 0; i < C::kStages; ++i) {
+          load(ring[(i + C::kStages - 1) % C::kStages]);
+          if (t0 < t_last) compute(ring[i], t0);
+          t0 += kStride * kTokTile;
         }
       }
     }
-    if (edge) {
-#pragma unroll
-      for (int t = 0; t < QT; ++t)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = t0 + 16 * j + 4 * c4 + i;
-            if (!st.there[j] || key >= t_last || key > pos[t] || key <= pos[t] - sp.window) {
-              s[t][j][i] = -__builtin_inff();
-              hidden[t] |= 1u << (4 * j + i);
-            }
-          }
-    }
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    if (limit == -__builtin_inff()) base = kLowest;
 
-    // a score far above a row's held maximum?
-    float mx[QT];
-    bool raise = false;
+    // the four wavefronts' parts of the same rows, added in order
 #pragma unroll
-    for (int t = 0; t < QT; ++t) {
-      float v = s[t][0][0];
-#pragma unroll
-      for (int e = 1; e < 8; ++e) v = fmaxf(v, s[t][e >> 2][e & 3]);
-      mx[t] = v;
-      raise |= v > m[t] + kSlack;
-    }
-    if (__any(raise)) {
-#pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        float v = fmaxf(mx[t], m[t]);
-        v = fmaxf(v, __shfl_xor(v, 16, 64));
-        v = fmaxf(v, __shfl_xor(v, 32, 64));
-        const float b = v + exp_v, alpha = exp2_fast(base[t] - b);
-        m[t] = v;
-        base[t] = b;
-        l[t] *= alpha;
-#pragma unroll
-        for (int c = 0; c < 2 * KB; ++c) acc[t][c] *= alpha;
-      }
-    }
-
-    // weights, to float16 with the V scale in them
-#pragma unroll
-    for (int t = 0; t < QT; ++t)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[t][j][i] = exp2_fast(s[t][j][i] - base[t]);
-          l[t] += s[t][j][i];
-        }
-    half8_t p[QT][GC];
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int g = 0; g < GC; ++g) {
-        const half4_t vh = __builtin_bit_cast(half4_t, st.t[j].vs[g]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float vs = (float)vh[i];
-#pragma unroll
-          for (int t = 0; t < QT; ++t) p[t][g][4 * j + i] = (_Float16)(s[t][j][i] * vs);
-        }
-      }
-    if (edge) {
-      // a key that one row sees and another does not may have an infinite scale
-#pragma unroll
-      for (int t = 0; t < QT; ++t)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int g = 0; g < GC; ++g)
-              if (hidden[t] >> (4 * j + i) & 1u) p[t][g][4 * j + i] = (_Float16)0.0f;
-    }
-
-#pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      const half8_t lo = v_operand<false>(st.t[0].v[b], st.t[1].v[b], dq);
-      const half8_t hi = v_operand<true>(st.t[0].v[b], st.t[1].v[b], dq);
-#pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        acc[t][2 * b] = mfma(lo, p[t][b / BPG], acc[t][2 * b]);
-        acc[t][2 * b + 1] = mfma(hi, p[t][b / BPG], acc[t][2 * b + 1]);
-      }
-    }
-  };
-
-  // one step in flight while the one before is computed
-  const int t_own = t_first + kStep * wave;
-  if (t_own < t_last) {
-    Step s0, s1;
-    fetch_pages();
-    load(s0);
-    for (int t0 = t_own;;) {
-      load(s1);
-      compute(s0, t0);
-      if ((t0 += kStride * kTokTile) >= t_last) break;
-      load(s0);
-      compute(s1, t0);
-      if ((t0 += kStride * kTokTile) >= t_last) break;
-    }
-  }
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    l[t] += __shfl_xor(l[t], 16, 64);
-    l[t] += __shfl_xor(l[t], 32, 64);
-  }
-
-  // the four wavefronts' parts of the same rows, added in order
-  __shared__ float4_t buf[C::kWaves][2 * KB][kWave];
-  __shared__ float2 ml[C::kWaves][16];
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    if (t > 0) __syncthreads();
-#pragma unroll
-    for (int c = 0; c < 2 * KB; ++c) buf[wave][c][lane] = acc[t][c];
-    if (c4 == 0) ml[wave][col] = make_float2(base[t], l[t]);
+    for (int c = 0; c < 2 * KB; ++c) buf[wave][c][lane] = acc[c];
+    if (c4 == 0) ml[wave][col] = make_float2(base, l);
     __syncthreads();
-    float top = ml[0][col].x, sum = 0.0f, f[C::kWaves];
+    float top = ml[0][col].x, sum = 0.0f, f[4];
 #pragma unroll
-    for (int v = 1; v < C::kWaves; ++v) top = fmaxf(top, ml[v][col].x);
+    for (int v = 1; v < 4; ++v) top = fmaxf(top, ml[v][col].x);
 #pragma unroll
-    for (int v = 0; v < C::kWaves; ++v) {
+    for (int v = 0; v < 4; ++v) {
       f[v] = exp2_fast(ml[v][col].x - top);
       sum = __builtin_fmaf(ml[v][col].y, f[v], sum);
     }
-    for (int c = wave; c < 2 * KB; c += C::kWaves) {
+    for (int c = wave; c < 2 * KB; c += 4) {
       float4_t o = buf[0][c][lane] * f[0];
 #pragma unroll
-      for (int v = 1; v < C::kWaves; ++v) o += buf[v][c][lane] * f[v];
-      store_row<D>(a, w, split, r0 + 16 * t + col, 16 * c + 4 * c4, o, sum, top);
+      for (int v = 1; v < 4; ++v) o += buf[v][c][lane] * f[v];
+      store_piece<D, 16>(a, pc, col, 16 * c + 4 * c4, o, sum, top);
     }
   }
+  shares.finish(a, pc);
 }
 
 // ---------------------------------------------------------------------------------
@@ -549,11 +696,7 @@ __global__ __launch_bounds__(256, (Attn<D, GC, QT>::kWavesSimd)) void attn_kerne
 // dwords of cache lanes r + 16 c and r + 32 + 16 c; channels 0..15 of a block are their low
 // nibbles, 16..31 the high ones: lanes 16..31 read the same dwords with other masks.
 //
-// With ROWS every wavefront has 32 rows of its own and walks all their keys (the four
-// wavefronts of a workgroup read the same tiles at nearly the same time, from the
-// L1); without, four wavefronts share 32 rows and split the keys. Staging converted
-// operands in LDS for all four saves two thirds of the conversion, but its barriers cost
-// more than that (16x16 form, four 509-token chunks: 616 against 610 us).
+// The four wavefronts of a workgroup share 32 rows and split the keys.
 typedef float float16_t __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ float16_t mfma32(half8_t a, half8_t b, float16_t c) {
@@ -571,31 +714,34 @@ __device__ __forceinline__ half4_t v_codes4(uint32_t w, const VRegs& k) {
   return __builtin_shufflevector(a, b, 0, 1, 2, 3);
 }
 
-template <int D, int GC, bool ROWS>
-__global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_kernel(AttnArgs a, int tiles,
-                                                                                       int swizzle) {
+template <int D, int GC>
+__global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_kernel(AttnArgs a, int tiles) {
   constexpr int KB = D / 32, BPG = KB / GC;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, c = lane >> 5, r16 = lane & 15;
-  // blocks: split fastest, then row tile (last rows, the longest spans, first), head, sequence; with
-  // `swizzle` the eight XCDs, which take blocks in turn, each keep whole heads (their L2 then
-  // holds the keys all of a head's tiles read)
-  const unsigned inner = (unsigned)(a.splits * tiles);
-  unsigned group = blockIdx.x / inner, at = blockIdx.x % inner;
-  if (swizzle) {
-    const unsigned x = blockIdx.x % 8, y = blockIdx.x / 8;
-    group = x + 8 * (y / inner);
-    at = y % inner;
-  }
-  const int split = (int)(at % (unsigned)a.splits);
-  const int tile_q = tiles - 1 - (int)(at / (unsigned)a.splits);
-  Job w;
-  if (!make_job(a, (int)(group / (unsigned)a.cache.kv_heads), (int)(group % (unsigned)a.cache.kv_heads), &w)) return;
-  constexpr int kGroup = ROWS ? 128 : 32;
-  const int g0 = tile_q * kGroup;
-  const int r0 = g0 + (ROWS ? 32 * wave : 0);
-  if (r0 >= w.rows) return;  // no barrier follows where wavefronts differ in this
+  __shared__ float4_t buf[4][4][kWave];
+  __shared__ float2 ml[4][32];
+  const float scale = a.scale * 1.4426950408889634f;
+  const DequantRegs dq = DequantRegs::make();
+  const KRegs kr = KRegs::make();
+  VRegs vr;
+  vr.mask = lane & 16 ? 0x00F000F0u : 0x000F000Fu;   // 64 + n, or 1024 + n
+  vr.magic = lane & 16 ? 0x54005400u : 0x64006400u;
+  vr.bias = as_half2(lane & 16 ? 0xD480D480u : 0xE408E408u);  // -72, -1032
+  const int tpp = a.cache.page_size / kTokTile;
+  constexpr int kStride = 8;  // tiles from one step of a wavefront to the next
+  const int stride_block = kStride / tpp, stride_rem = kStride - stride_block * tpp;
+  Shares shares;
+  Piece pc{};
+  bool more = uniform(shares.begin(a, 32, lane));
+  for (bool again = false; more; again = true) {
+  Piece next_piece;
+  if (!uniform(shares.next(a, 32, lane, tiles, &next_piece))) break;
+  pc = uniform_piece(next_piece);
+  if (again) __syncthreads();  // buf of the piece before has been read
+  const Job& w = pc.w;
+  const int r0 = pc.r0;
 
   const int row = r0 + col;
   half8_t q[2 * KB];
@@ -627,29 +773,16 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_
 #pragma unroll
   for (int b = 0; b < KB; ++b) acc[b] = float16_t{};
 
-  // the keys of the rows that decide the split, and those of this wavefront's rows
-  const Span all = span_of(a, w, g0, kGroup);
-  const Span sp = ROWS ? span_of(a, w, r0, 32) : all;
-  const int s_first = all.first + split * a.chunk;
-  const int t_last = a.splits > 1 ? min(sp.last, s_first + a.chunk) : sp.last;
-  const int t_first = max(s_first, sp.first) + (ROWS ? 0 : kStep * wave);
-  constexpr int kStride = ROWS ? 2 : 8;  // tiles from one step of a wavefront to the next
-  const float scale = a.scale * 1.4426950408889634f;
-  const DequantRegs dq = DequantRegs::make();
-  const KRegs kr = KRegs::make();
-  VRegs vr;
-  vr.mask = lane & 16 ? 0x00F000F0u : 0x000F000Fu;   // 64 + n, or 1024 + n
-  vr.magic = lane & 16 ? 0x54005400u : 0x64006400u;
-  vr.bias = as_half2(lane & 16 ? 0xD480D480u : 0xE408E408u);  // -72, -1032
+  const Span sp = span_of(a, w, r0, 32);
+  const int t_own = max(pc.key0, sp.first) + kStep * wave;
+  const int t_last = pc.key1 < 0 ? sp.last : min(sp.last, pc.key1);
   float exp_v = -64.0f;  // E (wave-uniform)
   uint32_t cap_v = 0;    // largest V scale that E covers, as float16 bits
 
-  const int tpp = a.cache.page_size / kTokTile;
   const ScalarInts table = scalar_ints(a.block_table + (int64_t)w.seq * a.max_blocks);
-  const int stride_block = kStride / tpp, stride_rem = kStride - stride_block * tpp;
   const int last_tile = max(t_last - 1, 0) / kTokTile;
   Walk next;
-  next.tile = t_first / kTokTile;
+  next.tile = t_own / kTokTile;
   next.block = next.tile / tpp;
   next.in_page = next.tile - next.block * tpp;
   // tiles of the step whose K is loaded, and whether their pages lie in the cache
@@ -854,47 +987,38 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_
     }
   };
 
-  if (t_first < t_last) {
+  if (t_own < t_last) {
     walk();
     load_k();
     walk();
-    for (int t0 = t_first; t0 < t_last; t0 += kStride * kTokTile) step(t0);
+    for (int t0 = t_own; t0 < t_last; t0 += kStride * kTokTile) step(t0);
   }
   l += __shfl_xor(l, 32, 64);
   if (limit == -__builtin_inff()) base = kLowest;
 
-  if constexpr (ROWS) {
+  // the four wavefronts' parts of the same rows, added in order
+  if (c == 0) ml[wave][col] = make_float2(base, l);
 #pragma unroll
-    for (int b = 0; b < KB; ++b)
+  for (int b = 0; b < KB; ++b) {
+    if (b > 0) __syncthreads();
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        store_row<D>(a, w, split, row, 32 * b + 8 * u + 4 * c,
-                     float4_t{acc[b][4 * u], acc[b][4 * u + 1], acc[b][4 * u + 2], acc[b][4 * u + 3]}, l, base);
-  } else {
-    // the four wavefronts' parts of the same rows, added in order
-    __shared__ float4_t buf[4][4][kWave];
-    __shared__ float2 ml[4][32];
-    if (c == 0) ml[wave][col] = make_float2(base, l);
+    for (int u = 0; u < 4; ++u)
+      buf[wave][u][lane] = float4_t{acc[b][4 * u], acc[b][4 * u + 1], acc[b][4 * u + 2], acc[b][4 * u + 3]};
+    __syncthreads();
+    float top = ml[0][col].x, sum = 0.0f;
 #pragma unroll
-    for (int b = 0; b < KB; ++b) {
-      if (b > 0) __syncthreads();
+    for (int v = 1; v < 4; ++v) top = fmaxf(top, ml[v][col].x);
+    float4_t o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        buf[wave][u][lane] = float4_t{acc[b][4 * u], acc[b][4 * u + 1], acc[b][4 * u + 2], acc[b][4 * u + 3]};
-      __syncthreads();
-      float top = ml[0][col].x, sum = 0.0f;
-#pragma unroll
-      for (int v = 1; v < 4; ++v) top = fmaxf(top, ml[v][col].x);
-      float4_t o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const float f = exp2_fast(ml[v][col].x - top);
-        sum = __builtin_fmaf(ml[v][col].y, f, sum);
-        o += buf[v][wave][lane] * f;
-      }
-      store_row<D>(a, w, split, row, 32 * b + 8 * wave + 4 * c, o, sum, top);
+    for (int v = 0; v < 4; ++v) {
+      const float f = exp2_fast(ml[v][col].x - top);
+      sum = __builtin_fmaf(ml[v][col].y, f, sum);
+      o += buf[v][wave][lane] * f;
     }
+    store_piece<D, 32>(a, pc, col, 32 * b + 8 * wave + 4 * c, o, sum, top);
   }
+  }
+  shares.finish(a, pc);
 }
 
 // ---------------------------------------------------------------------------------
@@ -926,18 +1050,16 @@ __global__ __launch_bounds__(256, (D < 256 ? 3 : 1)) void attn_rows_kernel(AttnA
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, c = lane >> 5;
-  // blocks: split fastest, then row tile (last rows, the longest spans, first), head, sequence; with
+  // blocks: row tile fastest (last rows, the longest spans, first), then head, sequence; with
   // `swizzle` the eight XCDs, which take blocks in turn, each keep whole heads (their L2 then
-  // holds the keys all of a head's tiles read)
-  const unsigned inner = (unsigned)(a.splits * tiles);
-  unsigned group = blockIdx.x / inner, at = blockIdx.x % inner;
+  // holds the keys all of a head's tiles read: a 4001-token prompt 390 -> 311 us)
+  unsigned group = blockIdx.x / (unsigned)tiles, at = blockIdx.x % (unsigned)tiles;
   if (swizzle) {
     const unsigned x = blockIdx.x % 8, y = blockIdx.x / 8;
-    group = x + 8 * (y / inner);
-    at = y % inner;
+    group = x + 8 * (y / (unsigned)tiles);
+    at = y % (unsigned)tiles;
   }
-  const int split = (int)(at % (unsigned)a.splits);
-  const int tile_q = tiles - 1 - (int)(at / (unsigned)a.splits);
+  const int tile_q = tiles - 1 - (int)at;
   Job w;
   if (!make_job(a, (int)(group / (unsigned)a.cache.kv_heads), (int)(group % (unsigned)a.cache.kv_heads), &w)) return;
   constexpr int kGroup = 128;
@@ -965,8 +1087,7 @@ __global__ __launch_bounds__(256, (D < 256 ? 3 : 1)) void attn_rows_kernel(AttnA
 
   const Span all = span_of(a, w, g0, kGroup);                   // the workgroup's keys
   const Span own = span_of(a, w, min(r0, w.rows - 1), 32);      // those of this wavefront's rows
-  const int t_first = all.first + split * a.chunk;
-  const int t_last = a.splits > 1 ? min(all.last, t_first + a.chunk) : all.last;
+  const int t_first = all.first, t_last = all.last;
   const float scale = a.scale * 1.4426950408889634f;
   float exp_v = -64.0f;  // E (wave-uniform)
   int cap_v = 0;         // largest V scale that E covers, as float16 bits
@@ -1180,74 +1301,57 @@ __global__ __launch_bounds__(256, (D < 256 ? 3 : 1)) void attn_rows_kernel(AttnA
     }
   }
   l += __shfl_xor(l, 32, 64);
-  if (limit == -__builtin_inff()) base = kLowest;
+  if (row >= w.rows) return;
 #pragma unroll
   for (int b = 0; b < KB; ++b)
 #pragma unroll
     for (int u = 0; u < 4; ++u)
-      store_row<D>(a, w, split, row, 32 * b + 8 * u + 4 * c,
-                   float4_t{acc[b][4 * u], acc[b][4 * u + 1], acc[b][4 * u + 2], acc[b][4 * u + 3]}, l, base);
+      *out_at<D>(a, w, row, 32 * b + 8 * u + 4 * c) =
+          to_row(float4_t{acc[b][4 * u], acc[b][4 * u + 1], acc[b][4 * u + 2], acc[b][4 * u + 3]}, l);
 }
 
-// Joins the splits of a row: a workgroup per row, D / 4 lanes a group of channels, the
-// 1024 / D groups taking every such split and then added in order (one group walking all
-// splits of a 100K context took as long as a quarter of the attention itself).
+// Joins the pieces of the job that share blockIdx.x / (RG / 4) begins and does not end: a
+// wavefront per row, D / 4 lanes a group of channels, the 256 / D groups taking every such piece
+// and added in order.
 template <int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rows_group, unsigned rows) {
-  constexpr int LPR = D / 4, G = 256 / LPR;
-  __shared__ float4_t buf[G][LPR];
-  __shared__ float2 part[G];
-  const int lane = threadIdx.x % LPR, g = threadIdx.x / LPR;
-  const unsigned sh = blockIdx.x / rows;  // sequence and head
-  const int row = (int)(blockIdx.x - sh * rows);
-  Job w;
-  if (!make_job(a, (int)(sh / (unsigned)a.cache.kv_heads), (int)(sh % (unsigned)a.cache.kv_heads), &w) || row >= w.rows)
-    return;
-  // the row's tile decides which splits had keys
-  const Span sp = span_of(a, w, row / rows_group * rows_group, rows_group);
-  const int n = min((max(sp.last - sp.first, 0) + a.chunk - 1) / a.chunk, a.splits);
-  const int i = row / w.share, hs = row - i * w.share;
-  const int64_t r = (int64_t)(w.first + i) * a.q_heads + w.head * w.share + hs;
-  const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + r * a.splits;
-  const float* po = a.part_o + r * a.splits * D + 4 * lane;
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rg) {
+  constexpr int LPR = D / 4, G = kWave / LPR;
+  const int lane = threadIdx.x & 63;
+  const int per = rg / 4;
+  const int share = (int)(blockIdx.x / (unsigned)per);
+  const int local = (int)(blockIdx.x - (unsigned)(share * per)) * 4 + uniform(threadIdx.x >> 6);
+  const int4* cut = reinterpret_cast<const int4*>(a.cuts) + 2 * share;
+  const int4 c0 = cut[0];
+  const int n = c0.x;  // pieces: this share's slot 1, the next ones' slot 0
+  const int row = cut[1].x + local;
+  if (n == 0 || row >= c0.z) return;
+  Job w{};
+  w.first = c0.y;
+  w.head = c0.w;
+  w.share = a.q_heads / a.cache.kv_heads;
+  const int g = lane / LPR, ch = 4 * (lane % LPR);
+  auto at = [&](int i) __attribute__((always_inline)) { return ((int64_t)(share + i) * 2 + (i == 0)) * rg + local; };
+  const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
   float top = kLowest, sum = 0.0f;
   float4_t o = {0.f, 0.f, 0.f, 0.f};
-  for (int s = g; s < n; s += G) top = fmaxf(top, ml[s].x);
-#pragma unroll 2
-  for (int s = g; s < n; s += G) {
-    const float2 v = ml[s];
+#pragma unroll 4
+  for (int i = g; i < n; i += G) top = fmaxf(top, ml[at(i)].x);
+#pragma unroll
+  for (int m = LPR; m < kWave; m <<= 1) top = fmaxf(top, __shfl_xor(top, m, 64));
+#pragma unroll 4
+  for (int i = g; i < n; i += G) {
+    const float2 v = ml[at(i)];
     const float f = exp2_fast(v.x - top);
     sum = __builtin_fmaf(v.y, f, sum);
-    o += *reinterpret_cast<const float4_t*>(po + (int64_t)s * D) * f;
+    o += *reinterpret_cast<const float4_t*>(a.part_o + at(i) * D + ch) * f;
   }
-  buf[g][lane] = o;
-  if (lane == 0) part[g] = make_float2(top, sum);
-  __syncthreads();
-  if (g > 0) return;
-  float all = part[0].x, f[G];
 #pragma unroll
-  for (int v = 1; v < G; ++v) all = fmaxf(all, part[v].x);
-  sum = 0.0f;
-  o = float4_t{0.f, 0.f, 0.f, 0.f};
+  for (int m = LPR; m < kWave; m <<= 1) {
+    sum += __shfl_xor(sum, m, 64);
 #pragma unroll
-  for (int v = 0; v < G; ++v) {
-    f[v] = exp2_fast(part[v].x - all);
-    sum = __builtin_fmaf(part[v].y, f[v], sum);
-    o += buf[v][lane] * f[v];
+    for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], m, 64);
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  half4_t h;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) h[e] = (_Float16)(o[e] * inv);
-  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + r * D + 4 * lane) = __builtin_bit_cast(uint2, h);
-}
-
-// rows_group: the rows whose keys decide which splits there are.
-template <int D>
-void launch_join(const AttnArgs& a, int rows_group, int64_t rows, hipStream_t stream) {
-  if (a.splits <= 1) return;
-  const int64_t all = rows * a.cache.kv_heads * a.seqs;
-  hipLaunchKernelGGL(attn_join_kernel<D>, dim3((unsigned)all), dim3(256), 0, stream, a, rows_group, (unsigned)rows);
+  if (g == 0) *out_at<D>(a, w, row, ch) = to_row(o, sum);
 }
 
 template <int D, int GC>
@@ -1255,28 +1359,52 @@ hipError_t launch_t(const AttnArgs& a, hipStream_t stream) {
   const int64_t rows = (int64_t)a.max_q * (a.q_heads / a.cache.kv_heads);
   const int tiles = (int)((rows + a.rows_group - 1) / a.rows_group);
   const int64_t groups = (int64_t)a.cache.kv_heads * a.seqs;
-  const dim3 grid((unsigned)(a.splits * tiles * groups));
-  const int swizzle = groups % 8 == 0 && tiles > 1;
+  const dim3 grid((unsigned)(a.shares > 0 ? a.shares : tiles * groups));
   switch (a.rows_group) {
-    case 16: hipLaunchKernelGGL((attn_kernel<D, GC, 1>), grid, dim3(256), 0, stream, a, tiles); break;
-    case 32: hipLaunchKernelGGL((attn32_kernel<D, GC, false>), grid, dim3(256), 0, stream, a, tiles, swizzle); break;
-    default: hipLaunchKernelGGL((attn_rows_kernel<D, GC>), grid, dim3(256), sizeof(Shared<D, GC>), stream, a, tiles, swizzle); break;
+    case 16: hipLaunchKernelGGL((attn16_kernel<D, GC>), grid, dim3(256), 0, stream, a, tiles); break;
+    case 32: hipLaunchKernelGGL((attn32_kernel<D, GC>), grid, dim3(256), 0, stream, a, tiles); break;
+    default:
+      hipLaunchKernelGGL((attn_rows_kernel<D, GC>), grid, dim3(256), sizeof(Shared<D, GC>), stream, a, tiles,
+                         (int)(groups % 8 == 0 && tiles > 1));
   }
-  launch_join<D>(a, a.rows_group, rows, stream);
+  if (a.shares > 0)
+    hipLaunchKernelGGL(attn_join_kernel<D>, dim3((unsigned)(a.shares * (a.rows_group / 4))), dim3(256), 0, stream, a,
+                       a.rows_group);
   return hipGetLastError();
+}
+
+template <int D, int GC>
+int resident_t(int rows_group) {
+  const void* fn = rows_group == 16 ? reinterpret_cast<const void*>(&attn16_kernel<D, GC>)
+                                    : reinterpret_cast<const void*>(&attn32_kernel<D, GC>);
+  return resident_grid(fn, 256);
 }
 
 }  // namespace
 
-hipError_t launch_attention(const AttnArgs& a, hipStream_t stream) {
-  const int gc = a.cache.head_dim / a.cache.group;
-  switch (a.cache.head_dim) {
-    case 64: return gc == 1 ? launch_t<64, 1>(a, stream) : launch_t<64, 2>(a, stream);
-    case 128:
-      return gc == 1 ? launch_t<128, 1>(a, stream) : gc == 2 ? launch_t<128, 2>(a, stream) : launch_t<128, 4>(a, stream);
-    default:
-      return gc == 2 ? launch_t<256, 2>(a, stream) : gc == 4 ? launch_t<256, 4>(a, stream) : launch_t<256, 8>(a, stream);
+// CALL(head_dim, scale groups a head) for the cache's sizes.
+#define Q4_ATTN_DISPATCH(head_dim, group, CALL)                                       \
+  switch ((head_dim) * 8 + (head_dim) / (group)) {                                    \
+    case 64 * 8 + 1: return CALL(64, 1);                                              \
+    case 64 * 8 + 2: return CALL(64, 2);                                              \
+    case 128 * 8 + 1: return CALL(128, 1);                                            \
+    case 128 * 8 + 2: return CALL(128, 2);                                            \
+    case 128 * 8 + 4: return CALL(128, 4);                                            \
+    case 256 * 8 + 2: return CALL(256, 2);                                            \
+    case 256 * 8 + 4: return CALL(256, 4);                                            \
+    default: return CALL(256, 8);                                                     \
   }
+
+int attention_resident(int head_dim, int group, int rows_group) {
+#define Q4_CALL(D, GC) resident_t<D, GC>(rows_group)
+  Q4_ATTN_DISPATCH(head_dim, group, Q4_CALL)
+#undef Q4_CALL
+}
+
+hipError_t launch_attention(const AttnArgs& a, hipStream_t stream) {
+#define Q4_CALL(D, GC) launch_t<D, GC>(a, stream)
+  Q4_ATTN_DISPATCH(a.cache.head_dim, a.cache.group, Q4_CALL)
+#undef Q4_CALL
 }
 
 }  // namespace q4

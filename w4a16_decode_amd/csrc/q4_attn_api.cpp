@@ -112,19 +112,23 @@ q4_status check_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv
   return Q4_OK;
 }
 
-// Launch shape (q4_attn.hip): rows a KV head's new tokens have, and how far keys are split.
+// Launch shape (q4_attn.hip), from the bounds alone. Rows that a KV head's new tokens of a
+// sequence have: up to 16 take the 16-row kernel; tiles of 128 rows where they fill the chip;
+// between them tiles of 32. The first and last kind split the keys of short contexts
+// (512 keys or less) not at all and others in equal shares of all the work.
 void pick_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv, int32_t q_heads, int32_t kv_heads,
-               int32_t head_dim, int64_t window, q4::AttnArgs* a) {
+               int32_t head_dim, int32_t group, int64_t window, q4::AttnArgs* a) {
   const int64_t rows = std::min(max_q, tokens) * (q_heads / kv_heads);
-  a->rows_group = rows <= 16 ? 16 : rows <= 128 ? 32 : 128;
-  const int64_t groups = (rows + a->rows_group - 1) / a->rows_group * kv_heads * seqs;
-  const int64_t span = std::min(max_kv, window > 0 ? window + a->rows_group + 32 : max_kv);
-  const int64_t want = (int64_t)q4::device_cu_count_cached() * (a->rows_group < 128 ? 4 : 1);  // workgroups
-  int64_t splits = std::max<int64_t>(1, std::min<int64_t>(want / std::max<int64_t>(groups, 1), (span + 511) / 512));
-  const int64_t chunk = q4::round_up((span + splits - 1) / splits, 128);
-  splits = std::max<int64_t>(1, (span + chunk - 1) / std::max<int64_t>(chunk, 1));
-  a->splits = (int)splits;
-  a->chunk = (int)chunk;
+  const int64_t groups = kv_heads * seqs;
+  const bool fill = (rows + 127) / 128 * groups >= 2 * q4::device_cu_count_cached();
+  a->rows_group = rows <= 16 ? 16 : rows > 32 && fill ? 128 : 32;
+  const int64_t span = window > 0 ? std::min(max_kv, window + std::min(max_q, tokens)) : max_kv;
+  a->shares = a->rows_group == 128 || span <= 512 ? 0 : q4::attention_resident(head_dim, group, a->rows_group);
+}
+
+size_t attn_parts(const q4::AttnArgs& a) { return (size_t)a.shares * 2 * a.rows_group; }
+size_t attn_workspace(const q4::AttnArgs& a, int32_t head_dim) {
+  return attn_parts(a) * (head_dim + 2) * 4 + (size_t)a.shares * 32;
 }
 
 }  // namespace
@@ -208,11 +212,12 @@ q4_status q4_paged_kv_dequant(const q4_paged_kv* cache, const int32_t* slots, in
 }
 
 size_t q4_paged_attention_workspace_bytes(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv,
-                                          int32_t q_heads, int32_t kv_heads, int32_t head_dim, int64_t window) {
+                                          int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t group, int64_t window) {
   if (check_attn(seqs, tokens, max_q, max_kv, q_heads, kv_heads, window) != Q4_OK) return 0;
+  if (check_paged_dims(1, 16, kv_heads, head_dim, group) != Q4_OK) return 0;
   q4::AttnArgs a{};
-  pick_attn(seqs, tokens, max_q, max_kv, q_heads, kv_heads, head_dim, window, &a);
-  return a.splits > 1 ? (size_t)tokens * q_heads * a.splits * (head_dim + 2) * 4 : 0;
+  pick_attn(seqs, tokens, max_q, max_kv, q_heads, kv_heads, head_dim, group, window, &a);
+  return attn_workspace(a, head_dim);
 }
 
 q4_status q4_paged_attention(const void* q, int64_t q_stride, const q4_paged_kv* cache, const int32_t* block_table,
@@ -236,16 +241,16 @@ q4_status q4_paged_attention(const void* q, int64_t q_stride, const q4_paged_kv*
   a.q_offsets = q_offsets, a.kv_lens = kv_lens, a.seqs = (int)seqs, a.tokens = (int)tokens;
   a.max_q = (int)std::min(max_q, tokens), a.max_kv = (int)max_kv, a.q_heads = q_heads;
   a.scale = scale, a.window = (int)window, a.out = out;
-  pick_attn(seqs, tokens, max_q, max_kv, q_heads, a.cache.kv_heads, a.cache.head_dim, window, &a);
-  if (a.splits > 1) {
-    const size_t parts = (size_t)tokens * q_heads * a.splits;
-    const size_t need = parts * (a.cache.head_dim + 2) * 4;
+  pick_attn(seqs, tokens, max_q, max_kv, q_heads, a.cache.kv_heads, a.cache.head_dim, a.cache.group, window, &a);
+  if (a.shares > 0) {
+    const size_t parts = attn_parts(a), need = attn_workspace(a, a.cache.head_dim);
     if (!workspace || workspace_bytes < need)
       return fail(Q4_ERR_WORKSPACE, "this call needs %zu bytes of workspace (q4_paged_attention_workspace_bytes), got %zu",
                   need, workspace ? workspace_bytes : (size_t)0);
     if (!aligned(workspace, 16)) return fail(Q4_ERR_ALIGN, "workspace needs 16-byte alignment");
     a.part_o = static_cast<float*>(workspace);
     a.part_ml = a.part_o + parts * a.cache.head_dim;
+    a.cuts = reinterpret_cast<int32_t*>(a.part_ml + 2 * parts);
   }
   return hip_status(q4::launch_attention(a, static_cast<hipStream_t>(stream)), "attention launch");
 }

@@ -127,12 +127,14 @@ struct AttnArgs {
   void* out;   // [tokens][q_heads][head_dim]
   // launch shape
   int rows_group;  // rows of a workgroup: 16 or 32 (its wavefronts split the keys), or 128
-  int splits;      // workgroups splitting a row tile's keys, `chunk` each (a multiple of 128)
-  int chunk;
-  float* part_o;   // splits > 1: float32 [tokens][q_heads][splits][head_dim]
-  float* part_ml;  // and [tokens][q_heads][splits][2]: what exponents are relative to, sum
+  int shares;      // > 0: workgroups that take equal shares of all keys (rows_group 16 or 32)
+  float* part_o;   // shares > 0: float32 [shares][2][rows_group][head_dim]
+  float* part_ml;  // and [shares][2][rows_group][2]: what exponents are relative to, sum
+  int32_t* cuts;   // and int32 [shares][8]: the job a share begins and does not end
 };
 
+// Workgroups of the kernel for rows_group 16 or 32 that the current device holds at once.
+int attention_resident(int head_dim, int group, int rows_group);
 // Adapters beside a product (include/q4_lora.h). phase 0: A x into t; phase 1: y from the
 // product's partial sums and B t.
 struct LoraArgs {
