@@ -1042,7 +1042,7 @@ struct Shared {
 };
 
 template <int D, int GC>
-__global__ __launch_bounds__(256, (D < 256 ? 3 : 1)) void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
+__global__ __launch_bounds__(256, (D == 256 ? 1 : D == 128 && GC == 2 ? 3 : 2)) void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
   using S = Shared<D, GC>;
   constexpr int KB = S::KB, BPG = KB / GC, kKeys = S::kKeys;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -1360,12 +1360,13 @@ hipError_t launch_t(const AttnArgs& a, hipStream_t stream) {
   const int tiles = (int)((rows + a.rows_group - 1) / a.rows_group);
   const int64_t groups = (int64_t)a.cache.kv_heads * a.seqs;
   const dim3 grid((unsigned)(a.shares > 0 ? a.shares : tiles * groups));
-  switch (a.rows_group) {
-    case 16: hipLaunchKernelGGL((attn16_kernel<D, GC>), grid, dim3(256), 0, stream, a, tiles); break;
-    case 32: hipLaunchKernelGGL((attn32_kernel<D, GC>), grid, dim3(256), 0, stream, a, tiles); break;
-    default:
-      hipLaunchKernelGGL((attn_rows_kernel<D, GC>), grid, dim3(256), sizeof(Shared<D, GC>), stream, a, tiles,
-                         (int)(groups % 8 == 0 && tiles > 1));
+  if (a.rows_group == 128) {
+    hipLaunchKernelGGL((attn_rows_kernel<D, GC>), grid, dim3(256), sizeof(Shared<D, GC>), stream, a, tiles,
+                       (int)(groups % 8 == 0 && tiles > 1));
+  } else if (a.rows_group == 16) {
+    hipLaunchKernelGGL((attn16_kernel<D, GC>), grid, dim3(256), 0, stream, a, tiles);
+  } else if constexpr (has_attn32(D, GC)) {
+    hipLaunchKernelGGL((attn32_kernel<D, GC>), grid, dim3(256), 0, stream, a, tiles);
   }
   if (a.shares > 0)
     hipLaunchKernelGGL(attn_join_kernel<D>, dim3((unsigned)(a.shares * (a.rows_group / 4))), dim3(256), 0, stream, a,
@@ -1375,9 +1376,10 @@ hipError_t launch_t(const AttnArgs& a, hipStream_t stream) {
 
 template <int D, int GC>
 int resident_t(int rows_group) {
-  const void* fn = rows_group == 16 ? reinterpret_cast<const void*>(&attn16_kernel<D, GC>)
-                                    : reinterpret_cast<const void*>(&attn32_kernel<D, GC>);
-  return resident_grid(fn, 256);
+  if constexpr (has_attn32(D, GC)) {
+    if (rows_group == 32) return resident_grid(reinterpret_cast<const void*>(&attn32_kernel<D, GC>), 256);
+  }
+  return resident_grid(reinterpret_cast<const void*>(&attn16_kernel<D, GC>), 256);
 }
 
 }  // namespace

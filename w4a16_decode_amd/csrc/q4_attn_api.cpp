@@ -114,14 +114,14 @@ q4_status check_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv
 
 // Launch shape (q4_attn.hip), from the bounds alone. Rows that a KV head's new tokens of a
 // sequence have: up to 16 take the 16-row kernel; tiles of 128 rows where they fill the chip;
-// between them tiles of 32. The first and last kind split the keys of short contexts
+// between them tiles of 32 (16 where those are not built). The first and last kind split the keys of short contexts
 // (512 keys or less) not at all and others in equal shares of all the work.
 void pick_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv, int32_t q_heads, int32_t kv_heads,
                int32_t head_dim, int32_t group, int64_t window, q4::AttnArgs* a) {
   const int64_t rows = std::min(max_q, tokens) * (q_heads / kv_heads);
   const int64_t groups = kv_heads * seqs;
   const bool fill = (rows + 127) / 128 * groups >= 2 * q4::device_cu_count_cached();
-  a->rows_group = rows <= 16 ? 16 : rows > 32 && fill ? 128 : 32;
+  a->rows_group = rows > 32 && fill ? 128 : rows <= 16 || !q4::has_attn32(head_dim, head_dim / group) ? 16 : 32;
   const int64_t span = window > 0 ? std::min(max_kv, window + std::min(max_q, tokens)) : max_kv;
   a->shares = a->rows_group == 128 || span <= 512 ? 0 : q4::attention_resident(head_dim, group, a->rows_group);
 }

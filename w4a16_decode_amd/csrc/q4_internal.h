@@ -133,6 +133,10 @@ struct AttnArgs {
   int32_t* cuts;   // and int32 [shares][8]: the job a share begins and does not end
 };
 
+// Whether tiles of 32 rows whose wavefronts split the keys are built: 256 channels, or four
+// scale groups a head, do not fit the registers next to them (five rows of each of eight
+// sequences over 8K keys at 256 channels, groups of 64: 330 us with spills).
+constexpr bool has_attn32(int head_dim, int groups) { return head_dim <= 128 && groups <= 2; }
 // Workgroups of the kernel for rows_group 16 or 32 that the current device holds at once.
 int attention_resident(int head_dim, int group, int rows_group);
 // Adapters beside a product (include/q4_lora.h). phase 0: A x into t; phase 1: y from the
