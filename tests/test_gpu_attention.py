@@ -79,7 +79,16 @@ class Batch:
                                       to_gpu(np.array(self.lens, np.int32)), window=window, scale=scale, **args)
         return out
 
-    def check(self, got, window=0, scale=None, what="", rows=None, ref=None):
+    def check(self, got, window=0, scale=None, what="", heads=None):
+        """`heads`: the query heads to look at (all by default)."""
+        if heads is not None:
+            worst, share = 0.0, self.q.shape[1] // self.k[0].shape[1]
+            for h in heads:
+                one = Batch.__new__(Batch)
+                one.lens, one.offsets, one.d, one.q = self.lens, self.offsets, self.d, self.q[:, h:h + 1]
+                one.k, one.v = ([t[:, h // share:h // share + 1] for t in kv] for kv in (self.k, self.v))
+                worst = max(worst, one.check(got[:, h:h + 1], window, scale, (what, h)))
+            return worst
         s = self.d ** -0.5 if scale is None else scale
         got = to_np(got).astype(np.float64)
         worst = 0.0
@@ -273,3 +282,53 @@ def test_refusals(q4):
         q4.paged_attention(q, b.cache, tab, off, lens, 1, 20, scale=float("nan"))
     with pytest.raises(ValueError):
         q4.paged_attention(q, b.cache, tab, off, lens, 1, 20, out=torch.empty_like(q)[:, :4])
+
+
+@pytest.mark.parametrize("d,g,page", [(64, 32, 16), (64, 64, 48), (128, 128, 32), (128, 64, 16), (128, 32, 64),
+                                      (256, 128, 16), (256, 64, 32), (256, 32, 48)])
+def test_many_rows(q4, d, g, page):
+    """Enough rows and heads that tiles of 128 rows fill the chip: chunks over contexts, a prompt, a
+    ragged last tile, a sequence without rows, windows."""
+    say("many rows", d, g, page)
+    lens, news = [193, 700, 260, 9, 450], [193, 150, 199, 0, 1]
+    b = Batch(q4, lens, news, 64, 32, d, g, page, seed=d + 3 * g, extra_rows=3)
+    heads = [0, 1, 33, 63]
+    say("  worst share of the bound", b.check(b.run(), heads=heads))
+    say("  window 70", b.check(b.run(window=70), window=70, heads=heads))
+    say("  window 1", b.check(b.run(window=1), window=1, heads=[5]))
+
+
+def test_many_rows_hidden(q4):
+    """Hidden infinities, bad pages and rows that see nothing, in tiles of 128 rows."""
+    lens, news = [220, 30, 300, 210, 0], [200, 60, 250, 199, 5]
+    b = Batch(q4, lens, news, 64, 32, 128, 128, 16, seed=31)
+    clean = to_np(b.run())
+    b.check(clean_t := b.run(), heads=[2, 40])
+    assert np.array_equal(to_np(clean_t).view(np.uint16), clean.view(np.uint16))
+    assert not clean[200:230].any() and not clean[-5:].any()
+    k16, v16 = b.k16[0].copy(), b.v16[0].copy()
+    k16[150:, :, 3], v16[150:, :, 5] = np.inf, -np.inf
+    b.put(0, k16, v16)
+    got = to_np(b.run())
+    assert np.array_equal(got[:130].view(np.uint16), clean[:130].view(np.uint16))     # positions 20 .. 149
+    assert not np.isfinite(got[130:200]).any()
+    assert np.array_equal(got[200:].view(np.uint16), clean[200:].view(np.uint16))
+    b.put(0, b.k16[0], b.v16[0])
+    table = b.table.copy()
+    table[3, 2] = b.cache.pages + 5
+    got = to_np(b.run(table=table)).astype(np.float64)
+    keep = np.array([t for t in range(210) if t // 16 != 2])
+    first = int(b.offsets[3])
+    for i in (0, 60, 120, 198):
+        pos = 210 - 199 + i
+        if pos // 16 == 2:
+            continue
+        seen = keep[keep <= pos]
+        ref = oracle.paged.attention(b.q[first + i:first + i + 1, :1], [b.k[3][seen][:, :1]], [b.v[3][seen][:, :1]],
+                                     [len(seen)], [0, 1], 128 ** -0.5)
+        assert np.abs(got[first + i, 0] - ref[0, 0]).max() <= 2.0 ** -9 * max(1.0, np.abs(ref).max())
+
+
+def test_many_rows_sharp(q4):
+    b = Batch(q4, [400, 300], [200, 200], 128, 64, 64, 32, 16, seed=33, spread=20.0, v_scale=2.0 ** -12)
+    say("sharp, small v", b.check(b.run(), heads=[0, 77]))
