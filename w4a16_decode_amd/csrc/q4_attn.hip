@@ -25,10 +25,17 @@
 // only when some score exceeds it by more than kSlack binades: after a row's first few
 // steps almost never.
 //
-// Split. Where rows are few (decode), the four wavefronts of a workgroup share the rows and
-// take every fourth step of its keys, joined in LDS; long contexts are split further over
-// workgroups, whose partial results (O, m + E, l in float32) a second kernel joins in
-// order. Where rows are many, each wavefront has rows of its own.
+// Split. In the first two kernels the four wavefronts of a workgroup have the same rows and
+// take every fourth step of its keys, joined in LDS; the keys of all sequences and heads are
+// cut into equal shares, one for each workgroup that fits on the chip (below), and a second
+// kernel joins the partial results (O, m + E, l in float32) of what was cut, in order. In
+// the third each wavefront has rows of its own and nothing is cut.
+//
+// What bounds it. Few rows: the cache's bytes, read once (48 rows over 8K contexts of 8 heads
+// at 128 channels, 276 MB, in 64 us: 4.3 TB/s, a copy's read + write rate is 4.8). Many rows:
+// the matrix products and, beside them on the same issue ports, the softmax's vector work:
+// four 509-token chunks in contexts of up to 8190 tokens, 64 heads over 8, 430 GFLOP, in 610 to
+// 650 us, 16 of them at 880 TFLOP/s (an 8192^3 library product in float16: 1148).
 //
 // Range of the weights. P = p * vs is rounded to float16 before the product (half a
 // step, 2^-11 of each weight; its errors are independent and average over the keys).
@@ -36,13 +43,16 @@
 // can be, and small products would fall among the subnormals. The exponent is
 // therefore taken relative to m + E, E the exponent of the largest V scale so far minus
 // kHeadroom: P stays in [0, 2^(kHeadroom + kSlack)], 26 binades of full precision below its
-// maximum. (Infinite scales do not count: their rows are not finite, others' unharmed.) The sum l carries the same factor, so it cancels in o = O / l.
+// maximum. (Infinite scales do not count: their rows are not finite, others' unharmed.)
+// The sum l carries the same factor, so it cancels in o = O / l.
 #include <algorithm>
 
 #include "q4_paged.h"
 
 namespace q4 {
 namespace {
+
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kStep = 2 * kTokTile;  // keys per step (MFMA K of the second product)
 constexpr float kHeadroom = 12.0f;
@@ -107,25 +117,30 @@ struct Tile {
   uint2 ks[GC], vs[GC];
 };
 
-template <int D>
+// ONCE: read by this workgroup alone, so not to be kept (nontemporal).
+template <int D, bool ONCE = false>
 __device__ __forceinline__ void load_codes(uint32_t (&w)[D / 32], const uint32_t* base, int lane) {
+  auto get = [](auto* p) __attribute__((always_inline)) {
+    if constexpr (ONCE) return __builtin_nontemporal_load(p);
+    return *p;
+  };
   if constexpr (D == 64) {
-    const uint2 r = *reinterpret_cast<const uint2*>(base + 2 * lane);
-    w[0] = r.x, w[1] = r.y;
+    const auto r = get(reinterpret_cast<const u32x2_t*>(base + 2 * lane));
+    w[0] = r[0], w[1] = r[1];
   } else {
 #pragma unroll
     for (int i = 0; i < D / 128; ++i) {
-      const uint4 r = *reinterpret_cast<const uint4*>(base + (i * kWave + lane) * 4);
-      w[4 * i] = r.x, w[4 * i + 1] = r.y, w[4 * i + 2] = r.z, w[4 * i + 3] = r.w;
+      const auto r = get(reinterpret_cast<const u32x4_t*>(base + (i * kWave + lane) * 4));
+      w[4 * i] = r[0], w[4 * i + 1] = r[1], w[4 * i + 2] = r[2], w[4 * i + 3] = r[3];
     }
   }
 }
 
 // `tile` of the cache (D * 8 bytes of codes, GC * 16 scales, for K and for V).
-template <int D, int GC>
+template <int D, int GC, bool ONCE>
 __device__ __forceinline__ void load_tile(Tile<D, GC>& t, const PagedArgs& c, int64_t tile, int lane) {
-  load_codes<D>(t.k, static_cast<const uint32_t*>(c.k_codes) + tile * (2 * D), lane);
-  load_codes<D>(t.v, static_cast<const uint32_t*>(c.v_codes) + tile * (2 * D), lane);
+  load_codes<D, ONCE>(t.k, static_cast<const uint32_t*>(c.k_codes) + tile * (2 * D), lane);
+  load_codes<D, ONCE>(t.v, static_cast<const uint32_t*>(c.v_codes) + tile * (2 * D), lane);
   const uint16_t* ks = static_cast<const uint16_t*>(c.k_scales) + tile * (GC * kTokTile) + 4 * (lane >> 4);
   const uint16_t* vs = static_cast<const uint16_t*>(c.v_scales) + tile * (GC * kTokTile) + 4 * (lane >> 4);
 #pragma unroll
@@ -400,7 +415,6 @@ template <int D, int GC>
 struct Attn {
   static constexpr int KB = D / 32;    // 32-channel blocks
   static constexpr int BPG = KB / GC;  // of them per scale group
-  static constexpr int kRows = 16;
   // Steps of 32 keys a wavefront has in registers (one computed, the other in flight; three and
   // four stages were 3 us slower at 48 x 8K keys), and wavefronts per SIMD the registers are
   // budgeted for (three with two stages spill at 128 channels: 68 -> 86 us).
@@ -414,7 +428,13 @@ struct Attn {
 };
 
 // At most 16 rows: all four wavefronts have the same ones and split the keys.
-template <int D, int GC>
+//
+// ONCE: no other row tile reads these keys, so their codes are loaded past the caches' normal
+// order. Caches larger than the last-level cache gain (48 rows over 8K contexts of 8 heads 69.5
+// -> 64.2 us, 128 rows 152.8 -> 142.6), 100 MB read again and again lose (35.4 -> 37.6), which a
+// model of many layers never does; three tiles over the same keys lose too (78 -> 83 us at 256
+// channels) and load normally.
+template <int D, int GC, bool ONCE>
 __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(AttnArgs a, int tiles) {
   using C = Attn<D, GC>;
   using Step = typename C::Step;
@@ -489,7 +509,7 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
         s.there[j] = (unsigned)page[j] < (unsigned)a.cache.pages;
         const int64_t tile =
             ((int64_t)(s.there[j] ? page[j] : 0) * a.cache.kv_heads + w.head) * tpp + (j ? in_page2 : next.in_page);
-        load_tile<D, GC>(s.t[j], a.cache, tile, lane);
+        load_tile<D, GC, ONCE>(s.t[j], a.cache, tile, lane);
       }
       next.tile += kStride;
       next.block += stride_block;
@@ -696,7 +716,12 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
 // dwords of cache lanes r + 16 c and r + 32 + 16 c; channels 0..15 of a block are their low
 // nibbles, 16..31 the high ones: lanes 16..31 read the same dwords with other masks.
 //
-// The four wavefronts of a workgroup share 32 rows and split the keys.
+// The four wavefronts of a workgroup share 32 rows and split the keys. V is loaded at the start
+// of its step and K of the next one behind the scores, so about half a step covers each: the
+// registers left (K, V, 64 of output, 64 of q at 128 channels) hold no whole second step. Built
+// where the operands fit in registers: with 256 channels, or four scale groups, this form
+// spills (40 rows over 8K keys, 256 channels in groups of 64: 330 us, 78 with 16-row tiles).
+// Eight sequences of 5 rows over 8K keys, 64 heads over 8, 128 channels: 45.5 us.
 typedef float float16_t __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ float16_t mfma32(half8_t a, half8_t b, float16_t c) {
@@ -736,287 +761,287 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_
   Piece pc{};
   bool more = uniform(shares.begin(a, 32, lane));
   for (bool again = false; more; again = true) {
-  Piece next_piece;
-  if (!uniform(shares.next(a, 32, lane, tiles, &next_piece))) break;
-  pc = uniform_piece(next_piece);
-  if (again) __syncthreads();  // buf of the piece before has been read
-  const Job& w = pc.w;
-  const int r0 = pc.r0;
+    Piece next_piece;
+    if (!uniform(shares.next(a, 32, lane, tiles, &next_piece))) break;
+    pc = uniform_piece(next_piece);
+    if (again) __syncthreads();  // buf of the piece before has been read
+    const Job& w = pc.w;
+    const int r0 = pc.r0;
 
-  const int row = r0 + col;
-  half8_t q[2 * KB];
-  int pos;  // position of the lane's row: its own last visible key; -1: no row
-  float16_t start = {};  // what a dot product starts at: see k_operand
-  {
-    const int i = min(row, w.rows - 1) / w.share, hs = min(row, w.rows - 1) - i * w.share;
-    pos = row < w.rows ? w.len - w.nq + i : -1;
-    const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.first + i) * a.q_stride +
-                          (int64_t)(w.head * w.share + hs) * D + 8 * c;
-    float s2 = 0.0f, s6 = 0.0f;
+    const int row = r0 + col;
+    half8_t q[2 * KB];
+    int pos;  // position of the lane's row: its own last visible key; -1: no row
+    float16_t start = {};  // what a dot product starts at: see k_operand
+    {
+      const int i = min(row, w.rows - 1) / w.share, hs = min(row, w.rows - 1) - i * w.share;
+      pos = row < w.rows ? w.len - w.nq + i : -1;
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.first + i) * a.q_stride +
+                            (int64_t)(w.head * w.share + hs) * D + 8 * c;
+      float s2 = 0.0f, s6 = 0.0f;
 #pragma unroll
-    for (int b = 0; b < 2 * KB; ++b) {
-      q[b] = as_half8(*reinterpret_cast<const uint4*>(src + 16 * b));
+      for (int b = 0; b < 2 * KB; ++b) {
+        q[b] = as_half8(*reinterpret_cast<const uint4*>(src + 16 * b));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) (e & 2 ? s6 : s2) += (float)q[b][e];
-    }
-    if (GC == 1) {
-      const float own = -(264.0f * s2 + 24.0f * s6);
-      const float both = own + __shfl_xor(own, 32, 64);
+        for (int e = 0; e < 8; ++e) (e & 2 ? s6 : s2) += (float)q[b][e];
+      }
+      if (GC == 1) {
+        const float own = -(264.0f * s2 + 24.0f * s6);
+        const float both = own + __shfl_xor(own, 32, 64);
 #pragma unroll
-      for (int e = 0; e < 16; ++e) start[e] = both;
-    }
-  }
-  // base: m + E. A score more than `limit` above it makes m rise; a row that has seen no key
-  // yet has base 0 and limit -infinity, and its first key sets m.
-  float base = 0.0f, limit = -__builtin_inff(), l = 0.0f;
-  float16_t acc[KB];
-#pragma unroll
-  for (int b = 0; b < KB; ++b) acc[b] = float16_t{};
-
-  const Span sp = span_of(a, w, r0, 32);
-  const int t_own = max(pc.key0, sp.first) + kStep * wave;
-  const int t_last = pc.key1 < 0 ? sp.last : min(sp.last, pc.key1);
-  float exp_v = -64.0f;  // E (wave-uniform)
-  uint32_t cap_v = 0;    // largest V scale that E covers, as float16 bits
-
-  const ScalarInts table = scalar_ints(a.block_table + (int64_t)w.seq * a.max_blocks);
-  const int last_tile = max(t_last - 1, 0) / kTokTile;
-  Walk next;
-  next.tile = t_own / kTokTile;
-  next.block = next.tile / tpp;
-  next.in_page = next.tile - next.block * tpp;
-  // tiles of the step whose K is loaded, and whether their pages lie in the cache
-  int64_t tile[2], tile_n[2];
-  bool there[2], there_n[2];
-  auto walk = [&]() __attribute__((always_inline)) {
-    const bool wraps = next.in_page + 1 == tpp;
-    const int in2 = wraps ? 0 : next.in_page + 1, b2 = next.block + (wraps ? 1 : 0);
-    const int p0 = next.tile <= last_tile && next.block < a.max_blocks ? table[next.block] : -1;
-    const int p1 = next.tile + 1 <= last_tile && b2 < a.max_blocks ? table[b2] : -1;
-    there_n[0] = (unsigned)p0 < (unsigned)a.cache.pages;
-    there_n[1] = (unsigned)p1 < (unsigned)a.cache.pages;
-    // a tile behind the last key or of a page outside the cache is read from page 0 and masked
-    tile_n[0] = ((int64_t)(there_n[0] ? p0 : 0) * a.cache.kv_heads + w.head) * tpp + next.in_page;
-    tile_n[1] = ((int64_t)(there_n[1] ? p1 : 0) * a.cache.kv_heads + w.head) * tpp + in2;
-    next.tile += kStride;
-    next.block += stride_block;
-    next.in_page += stride_rem;
-    if (next.in_page >= tpp) {
-      next.in_page -= tpp;
-      ++next.block;
-    }
-  };
-  uint32_t kw[2][KB];  // K codes: even and odd 16-channel steps
-  uint2 ks[2][GC][2];  // scales of keys 8u + 4c .. + 3 of tile j: [j][g][u]
-  auto load_k = [&]() __attribute__((always_inline)) {
-    const int64_t mine = lane & 16 ? tile_n[1] : tile_n[0];
-    const uint32_t* p = static_cast<const uint32_t*>(a.cache.k_codes) + mine * (2 * D);
-    load_codes<D>(kw[0], p, r16 + 16 * c);
-    load_codes<D>(kw[1], p, r16 + 16 * c + 32);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint16_t* sc = static_cast<const uint16_t*>(a.cache.k_scales) + tile_n[j] * (GC * kTokTile) + 4 * c;
-#pragma unroll
-      for (int g = 0; g < GC; ++g)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) ks[j][g][u] = *reinterpret_cast<const uint2*>(sc + g * kTokTile + 8 * u);
-      tile[j] = tile_n[j];
-      there[j] = there_n[j];
-    }
-  };
-
-  auto step = [&](int t0) __attribute__((always_inline)) {
-    // V of this step: needed only after the softmax
-    uint32_t vw[2][2][KB];  // [tile][cache lanes r + 16 c, + 32]
-    uint2 vs[2][GC][2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t* p = static_cast<const uint32_t*>(a.cache.v_codes) + tile[j] * (2 * D);
-      load_codes<D>(vw[j][0], p, r16 + 16 * c);
-      load_codes<D>(vw[j][1], p, r16 + 16 * c + 32);
-      const uint16_t* sc = static_cast<const uint16_t*>(a.cache.v_scales) + tile[j] * (GC * kTokTile) + 4 * c;
-#pragma unroll
-      for (int g = 0; g < GC; ++g)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) vs[j][g][u] = *reinterpret_cast<const uint2*>(sc + g * kTokTile + 8 * u);
-    }
-    const bool there0 = there[0], there1 = there[1];
-    const bool edge =
-        t0 + kStep > sp.pos_lo + 1 || t0 <= sp.pos_hi - sp.window || t0 + kStep > t_last || !there0 || !there1;
-    auto key_of = [&](int i) __attribute__((always_inline)) { return t0 + 8 * (i >> 2) + 4 * c + (i & 3); };
-
-    // scores, base 2, relative to m + E
-    float s[16];
-#pragma unroll
-    for (int g = 0; g < GC; ++g) {
-      float16_t part = start;
-#pragma unroll
-      for (int b = g * BPG; b < (g + 1) * BPG; ++b)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const half2_t lo_bias = {(_Float16)-1032.0f, (_Float16)-1032.0f};
-          const half2_t hi_bias = {(_Float16)-72.0f, (_Float16)-72.0f};
-          // one group a head: biased codes against `start`; more: exact codes
-          const half8_t k = GC == 1 ? k_operand(kw[u][b], kr) : dequant8r(kw[u][b], dq, lo_bias, hi_bias);
-          part = mfma32(k, q[2 * b + u], part);
-        }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const half4_t kh = __builtin_bit_cast(half4_t, ks[i >> 3][g][(i >> 2) & 1]);
-        s[i] = __builtin_fmaf(part[i], (float)kh[i & 3], g == 0 ? 0.0f : s[i]);  // one v_fma_mix
+        for (int e = 0; e < 16; ++e) start[e] = both;
       }
     }
+    // base: m + E. A score more than `limit` above it makes m rise; a row that has seen no key
+    // yet has base 0 and limit -infinity, and its first key sets m.
+    float base = 0.0f, limit = -__builtin_inff(), l = 0.0f;
+    float16_t acc[KB];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s[i] = __builtin_fmaf(s[i], scale, -base);
-    // the next step's K while the rest of this one runs
-    load_k();
-    walk();
+    for (int b = 0; b < KB; ++b) acc[b] = float16_t{};
 
-    uint32_t hidden = 0;  // keys of the lane that its row does not see
-    if (edge) {
+    const Span sp = span_of(a, w, r0, 32);
+    const int t_own = max(pc.key0, sp.first) + kStep * wave;
+    const int t_last = pc.key1 < 0 ? sp.last : min(sp.last, pc.key1);
+    float exp_v = -64.0f;  // E (wave-uniform)
+    uint32_t cap_v = 0;    // largest V scale that E covers, as float16 bits
+
+    const ScalarInts table = scalar_ints(a.block_table + (int64_t)w.seq * a.max_blocks);
+    const int last_tile = max(t_last - 1, 0) / kTokTile;
+    Walk next;
+    next.tile = t_own / kTokTile;
+    next.block = next.tile / tpp;
+    next.in_page = next.tile - next.block * tpp;
+    // tiles of the step whose K is loaded, and whether their pages lie in the cache
+    int64_t tile[2], tile_n[2];
+    bool there[2], there_n[2];
+    auto walk = [&]() __attribute__((always_inline)) {
+      const bool wraps = next.in_page + 1 == tpp;
+      const int in2 = wraps ? 0 : next.in_page + 1, b2 = next.block + (wraps ? 1 : 0);
+      const int p0 = next.tile <= last_tile && next.block < a.max_blocks ? table[next.block] : -1;
+      const int p1 = next.tile + 1 <= last_tile && b2 < a.max_blocks ? table[b2] : -1;
+      there_n[0] = (unsigned)p0 < (unsigned)a.cache.pages;
+      there_n[1] = (unsigned)p1 < (unsigned)a.cache.pages;
+      // a tile behind the last key or of a page outside the cache is read from page 0 and masked
+      tile_n[0] = ((int64_t)(there_n[0] ? p0 : 0) * a.cache.kv_heads + w.head) * tpp + next.in_page;
+      tile_n[1] = ((int64_t)(there_n[1] ? p1 : 0) * a.cache.kv_heads + w.head) * tpp + in2;
+      next.tile += kStride;
+      next.block += stride_block;
+      next.in_page += stride_rem;
+      if (next.in_page >= tpp) {
+        next.in_page -= tpp;
+        ++next.block;
+      }
+    };
+    uint32_t kw[2][KB];  // K codes: even and odd 16-channel steps
+    uint2 ks[2][GC][2];  // scales of keys 8u + 4c .. + 3 of tile j: [j][g][u]
+    auto load_k = [&]() __attribute__((always_inline)) {
+      const int64_t mine = lane & 16 ? tile_n[1] : tile_n[0];
+      const uint32_t* p = static_cast<const uint32_t*>(a.cache.k_codes) + mine * (2 * D);
+      load_codes<D>(kw[0], p, r16 + 16 * c);
+      load_codes<D>(kw[1], p, r16 + 16 * c + 32);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int key = key_of(i);
-        if (!(i < 8 ? there0 : there1) || key >= t_last || key > pos || key <= pos - sp.window) {
-          s[i] = -__builtin_inff();
-          hidden |= 1u << i;
+      for (int j = 0; j < 2; ++j) {
+        const uint16_t* sc = static_cast<const uint16_t*>(a.cache.k_scales) + tile_n[j] * (GC * kTokTile) + 4 * c;
+#pragma unroll
+        for (int g = 0; g < GC; ++g)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) ks[j][g][u] = *reinterpret_cast<const uint2*>(sc + g * kTokTile + 8 * u);
+        tile[j] = tile_n[j];
+        there[j] = there_n[j];
+      }
+    };
+
+    auto step = [&](int t0) __attribute__((always_inline)) {
+      // V of this step: needed only after the softmax
+      uint32_t vw[2][2][KB];  // [tile][cache lanes r + 16 c, + 32]
+      uint2 vs[2][GC][2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t* p = static_cast<const uint32_t*>(a.cache.v_codes) + tile[j] * (2 * D);
+        load_codes<D>(vw[j][0], p, r16 + 16 * c);
+        load_codes<D>(vw[j][1], p, r16 + 16 * c + 32);
+        const uint16_t* sc = static_cast<const uint16_t*>(a.cache.v_scales) + tile[j] * (GC * kTokTile) + 4 * c;
+#pragma unroll
+        for (int g = 0; g < GC; ++g)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) vs[j][g][u] = *reinterpret_cast<const uint2*>(sc + g * kTokTile + 8 * u);
+      }
+      const bool there0 = there[0], there1 = there[1];
+      const bool edge =
+          t0 + kStep > sp.pos_lo + 1 || t0 <= sp.pos_hi - sp.window || t0 + kStep > t_last || !there0 || !there1;
+      auto key_of = [&](int i) __attribute__((always_inline)) { return t0 + 8 * (i >> 2) + 4 * c + (i & 3); };
+
+      // scores, base 2, relative to m + E
+      float s[16];
+#pragma unroll
+      for (int g = 0; g < GC; ++g) {
+        float16_t part = start;
+#pragma unroll
+        for (int b = g * BPG; b < (g + 1) * BPG; ++b)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const half2_t lo_bias = {(_Float16)-1032.0f, (_Float16)-1032.0f};
+            const half2_t hi_bias = {(_Float16)-72.0f, (_Float16)-72.0f};
+            // one group a head: biased codes against `start`; more: exact codes
+            const half8_t k = GC == 1 ? k_operand(kw[u][b], kr) : dequant8r(kw[u][b], dq, lo_bias, hi_bias);
+            part = mfma32(k, q[2 * b + u], part);
+          }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const half4_t kh = __builtin_bit_cast(half4_t, ks[i >> 3][g][(i >> 2) & 1]);
+          s[i] = __builtin_fmaf(part[i], (float)kh[i & 3], g == 0 ? 0.0f : s[i]);  // one v_fma_mix
         }
       }
-      // what no row sees may hold anything: 0 * NaN must not arise
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = __builtin_fmaf(s[i], scale, -base);
+      // the next step's K while the rest of this one runs
+      load_k();
+      walk();
+
+      uint32_t hidden = 0;  // keys of the lane that its row does not see
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int key = key_of(i);
+          if (!(i < 8 ? there0 : there1) || key >= t_last || key > pos || key <= pos - sp.window) {
+            s[i] = -__builtin_inff();
+            hidden |= 1u << i;
+          }
+        }
+        // what no row sees may hold anything: 0 * NaN must not arise
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int g = 0; g < GC; ++g)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              half4_t vh = __builtin_bit_cast(half4_t, vs[j][g][u]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int key = key_of(8 * j + 4 * u + i);
+                vh[i] = (j ? there1 : there0) && key < t_last && key > sp.pos_lo - sp.window ? vh[i] : (_Float16)0.0f;
+              }
+              vs[j][g][u] = __builtin_bit_cast(uint2, vh);
+            }
+      }
+      // E, where a V scale exceeds what it covers
+      uint32_t vmax = 0;
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int g = 0; g < GC; ++g)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            half4_t vh = __builtin_bit_cast(half4_t, vs[j][g][u]);
+          for (int u = 0; u < 2; ++u) vmax = max_u16x2(vmax, max_u16x2(vs[j][g][u].x, vs[j][g][u].y));
+      vmax = max(vmax & 0xFFFFu, vmax >> 16);
+      if (__any(vmax > cap_v)) {
+        // the largest finite one, up to the end of its binade
+        vmax = cap_v;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int key = key_of(8 * j + 4 * u + i);
-              vh[i] = (j ? there1 : there0) && key < t_last && key > sp.pos_lo - sp.window ? vh[i] : (_Float16)0.0f;
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int g = 0; g < GC; ++g)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint2 r = vs[j][g][i >> 2];
+              const uint32_t bits = ((i & 2 ? r.y : r.x) >> (16 * (i & 1))) & 0xFFFFu;
+              vmax = max(vmax, bits < 0x7C00u ? bits : 0u);
             }
-            vs[j][g][u] = __builtin_bit_cast(uint2, vh);
-          }
-    }
-    // E, where a V scale exceeds what it covers
-    uint32_t vmax = 0;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+        for (int i = 1; i < 64; i <<= 1) vmax = max(vmax, (uint32_t)__shfl_xor((int)vmax, i, 64));
+        cap_v = vmax | 0x3FFu;
+        const float up = (float)(int)(cap_v >> 10) - 14.0f - kHeadroom - exp_v, alpha = exp2_fast(-up);
+        exp_v += up;
+        if (limit > -__builtin_inff()) {
+          base += up;
+          limit = kSlack - exp_v;
+          l *= alpha;
 #pragma unroll
-      for (int g = 0; g < GC; ++g)
+          for (int b = 0; b < KB; ++b) acc[b] *= alpha;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) vmax = max_u16x2(vmax, max_u16x2(vs[j][g][u].x, vs[j][g][u].y));
-    vmax = max(vmax & 0xFFFFu, vmax >> 16);
-    if (__any(vmax > cap_v)) {
-      // the largest finite one, up to the end of its binade
-      vmax = cap_v;
+          for (int i = 0; i < 16; ++i) s[i] -= up;
+        }
+      }
+      // one score far above its row's held maximum?
+      float mx = max3(s[0], s[1], s[2]);
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int i = 3; i < 15; i += 2) mx = max3(mx, s[i], s[i + 1]);
+      mx = fmaxf(mx, s[15]);
+      if (__any(mx > limit)) {
+        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+        if (mx > -__builtin_inff()) {
+          const bool first = limit == -__builtin_inff();
+          const float up = first ? mx + exp_v : fmaxf(mx + exp_v, 0.0f);
+          const float alpha = first ? 1.0f : exp2_fast(-up);
+          base += up;
+          limit = kSlack - exp_v;
+          l *= alpha;
+#pragma unroll
+          for (int b = 0; b < KB; ++b) acc[b] *= alpha;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[i] -= up;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        s[i] = exp2_fast(s[i]);
+        l += s[i];
+      }
+      // weights, to float16 with the V scale in them, and O += V P, a tile's 16 keys at a time
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        half8_t p[GC];
 #pragma unroll
         for (int g = 0; g < GC; ++g)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const uint2 r = vs[j][g][i >> 2];
-            const uint32_t bits = ((i & 2 ? r.y : r.x) >> (16 * (i & 1))) & 0xFFFFu;
-            vmax = max(vmax, bits < 0x7C00u ? bits : 0u);
+            const half4_t vh = __builtin_bit_cast(half4_t, vs[j][g][i >> 2]);
+            p[g][i] = (_Float16)__builtin_fmaf(s[8 * j + i], (float)vh[i & 3], 0.0f);  // one v_fma_mix
           }
+        if (edge) {
+          // a key that one row sees and another does not may have an infinite scale
 #pragma unroll
-      for (int i = 1; i < 64; i <<= 1) vmax = max(vmax, (uint32_t)__shfl_xor((int)vmax, i, 64));
-      cap_v = vmax | 0x3FFu;
-      const float up = (float)(int)(cap_v >> 10) - 14.0f - kHeadroom - exp_v, alpha = exp2_fast(-up);
-      exp_v += up;
-      if (limit > -__builtin_inff()) {
-        base += up;
-        limit = kSlack - exp_v;
-        l *= alpha;
+          for (int g = 0; g < GC; ++g)
 #pragma unroll
-        for (int b = 0; b < KB; ++b) acc[b] *= alpha;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] -= up;
-      }
-    }
-    // one score far above its row's held maximum?
-    float mx = max3(s[0], s[1], s[2]);
-#pragma unroll
-    for (int i = 3; i < 15; i += 2) mx = max3(mx, s[i], s[i + 1]);
-    mx = fmaxf(mx, s[15]);
-    if (__any(mx > limit)) {
-      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-      if (mx > -__builtin_inff()) {
-        const bool first = limit == -__builtin_inff();
-        const float up = first ? mx + exp_v : fmaxf(mx + exp_v, 0.0f);
-        const float alpha = first ? 1.0f : exp2_fast(-up);
-        base += up;
-        limit = kSlack - exp_v;
-        l *= alpha;
-#pragma unroll
-        for (int b = 0; b < KB; ++b) acc[b] *= alpha;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[i] -= up;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      s[i] = exp2_fast(s[i]);
-      l += s[i];
-    }
-    // weights, to float16 with the V scale in them, and O += V P, a tile's 16 keys at a time
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      half8_t p[GC];
-#pragma unroll
-      for (int g = 0; g < GC; ++g)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const half4_t vh = __builtin_bit_cast(half4_t, vs[j][g][i >> 2]);
-          p[g][i] = (_Float16)__builtin_fmaf(s[8 * j + i], (float)vh[i & 3], 0.0f);  // one v_fma_mix
+            for (int i = 0; i < 8; ++i)
+              if (hidden >> (8 * j + i) & 1u) p[g][i] = (_Float16)0.0f;
         }
-      if (edge) {
-        // a key that one row sees and another does not may have an infinite scale
 #pragma unroll
-        for (int g = 0; g < GC; ++g)
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (hidden >> (8 * j + i) & 1u) p[g][i] = (_Float16)0.0f;
+        for (int b = 0; b < KB; ++b) {
+          const half4_t v0 = v_codes4(vw[j][0][b], vr), v1 = v_codes4(vw[j][1][b], vr);
+          acc[b] = mfma32(__builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7), p[b / BPG], acc[b]);
+        }
       }
+    };
+
+    if (t_own < t_last) {
+      walk();
+      load_k();
+      walk();
+      for (int t0 = t_own; t0 < t_last; t0 += kStride * kTokTile) step(t0);
+    }
+    l += __shfl_xor(l, 32, 64);
+    if (limit == -__builtin_inff()) base = kLowest;
+
+    // the four wavefronts' parts of the same rows, added in order
+    if (c == 0) ml[wave][col] = make_float2(base, l);
 #pragma unroll
-      for (int b = 0; b < KB; ++b) {
-        const half4_t v0 = v_codes4(vw[j][0][b], vr), v1 = v_codes4(vw[j][1][b], vr);
-        acc[b] = mfma32(__builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7), p[b / BPG], acc[b]);
+    for (int b = 0; b < KB; ++b) {
+      if (b > 0) __syncthreads();
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        buf[wave][u][lane] = float4_t{acc[b][4 * u], acc[b][4 * u + 1], acc[b][4 * u + 2], acc[b][4 * u + 3]};
+      __syncthreads();
+      float top = ml[0][col].x, sum = 0.0f;
+#pragma unroll
+      for (int v = 1; v < 4; ++v) top = fmaxf(top, ml[v][col].x);
+      float4_t o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float f = exp2_fast(ml[v][col].x - top);
+        sum = __builtin_fmaf(ml[v][col].y, f, sum);
+        o += buf[v][wave][lane] * f;
       }
+      store_piece<D, 32>(a, pc, col, 32 * b + 8 * wave + 4 * c, o, sum, top);
     }
-  };
-
-  if (t_own < t_last) {
-    walk();
-    load_k();
-    walk();
-    for (int t0 = t_own; t0 < t_last; t0 += kStride * kTokTile) step(t0);
-  }
-  l += __shfl_xor(l, 32, 64);
-  if (limit == -__builtin_inff()) base = kLowest;
-
-  // the four wavefronts' parts of the same rows, added in order
-  if (c == 0) ml[wave][col] = make_float2(base, l);
-#pragma unroll
-  for (int b = 0; b < KB; ++b) {
-    if (b > 0) __syncthreads();
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      buf[wave][u][lane] = float4_t{acc[b][4 * u], acc[b][4 * u + 1], acc[b][4 * u + 2], acc[b][4 * u + 3]};
-    __syncthreads();
-    float top = ml[0][col].x, sum = 0.0f;
-#pragma unroll
-    for (int v = 1; v < 4; ++v) top = fmaxf(top, ml[v][col].x);
-    float4_t o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const float f = exp2_fast(ml[v][col].x - top);
-      sum = __builtin_fmaf(ml[v][col].y, f, sum);
-      o += buf[v][wave][lane] * f;
-    }
-    store_piece<D, 32>(a, pc, col, 32 * b + 8 * wave + 4 * c, o, sum, top);
-  }
   }
   shares.finish(a, pc);
 }
@@ -1042,7 +1067,8 @@ struct Shared {
 };
 
 template <int D, int GC>
-__global__ __launch_bounds__(256, (D == 256 ? 1 : D == 128 && GC == 2 ? 3 : 2)) void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
+__global__ __launch_bounds__(256, (D == 256 ? 1 : D == 128 && GC == 2 ? 3 : 2))
+void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
   using S = Shared<D, GC>;
   constexpr int KB = S::KB, BPG = KB / GC, kKeys = S::kKeys;
   extern __shared__ __align__(16) unsigned char smem[];
@@ -1363,10 +1389,12 @@ hipError_t launch_t(const AttnArgs& a, hipStream_t stream) {
   if (a.rows_group == 128) {
     hipLaunchKernelGGL((attn_rows_kernel<D, GC>), grid, dim3(256), sizeof(Shared<D, GC>), stream, a, tiles,
                        (int)(groups % 8 == 0 && tiles > 1));
-  } else if (a.rows_group == 16) {
-    hipLaunchKernelGGL((attn16_kernel<D, GC>), grid, dim3(256), 0, stream, a, tiles);
+  } else if (tiles == 1 && a.rows_group == 16) {
+    hipLaunchKernelGGL((attn16_kernel<D, GC, true>), grid, dim3(256), 0, stream, a, tiles);
   } else if constexpr (has_attn32(D, GC)) {
     hipLaunchKernelGGL((attn32_kernel<D, GC>), grid, dim3(256), 0, stream, a, tiles);
+  } else {
+    hipLaunchKernelGGL((attn16_kernel<D, GC, false>), grid, dim3(256), 0, stream, a, tiles);
   }
   if (a.shares > 0)
     hipLaunchKernelGGL(attn_join_kernel<D>, dim3((unsigned)(a.shares * (a.rows_group / 4))), dim3(256), 0, stream, a,
@@ -1379,7 +1407,7 @@ int resident_t(int rows_group) {
   if constexpr (has_attn32(D, GC)) {
     if (rows_group == 32) return resident_grid(reinterpret_cast<const void*>(&attn32_kernel<D, GC>), 256);
   }
-  return resident_grid(reinterpret_cast<const void*>(&attn16_kernel<D, GC>), 256);
+  return resident_grid(reinterpret_cast<const void*>(&attn16_kernel<D, GC, true>), 256);
 }
 
 }  // namespace

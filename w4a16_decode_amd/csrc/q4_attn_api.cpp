@@ -112,10 +112,17 @@ q4_status check_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv
   return Q4_OK;
 }
 
-// Launch shape (q4_attn.hip), from the bounds alone. Rows that a KV head's new tokens of a
-// sequence have: up to 16 take the 16-row kernel; tiles of 128 rows where they fill the chip;
-// between them tiles of 32 (16 where those are not built). The first and last kind split the keys of short contexts
-// (512 keys or less) not at all and others in equal shares of all the work.
+// Launch shape (q4_attn.hip), from the bounds alone; the rows are those that a KV head's new
+// tokens of one sequence have.
+//   up to 16: the 16-row kernel (one tile holds them all);
+//   more: 128 a workgroup where those workgroups are two or more a CU, so that nothing has to
+//     be cut (sixteen 509-token chunks of 64 heads over 8: 880 TFLOP/s, 32-row tiles 760);
+//   else 32-row tiles (8 sequences of 5 tokens over 8K: 45 us; 128-row workgroups would leave
+//     three quarters of the chip idle), or 16-row ones where the 32-row kernel is not built.
+// The 16- and 32-row kernels take equal shares of all the work, cut anywhere (48 rows over
+// unequal 8K contexts 77 -> 68 us against a fixed number of cuts); where the keys of a row are
+// at most 512, one share's smallest piece, a workgroup takes a whole job and no join
+// is launched (16 rows over 512 keys: 7.0 us, 2 us less than with the join).
 void pick_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv, int32_t q_heads, int32_t kv_heads,
                int32_t head_dim, int32_t group, int64_t window, q4::AttnArgs* a) {
   const int64_t rows = std::min(max_q, tokens) * (q_heads / kv_heads);
