@@ -142,3 +142,28 @@ def test_workspace_and_refusals(q4):
     bad = [to_gpu(t) for t in _adapters(2, 12, 64, 256, 0)]
     with pytest.raises(q4.Q4Error):
         q4.gemm_lora(x, qw, q4.LoraAdapters(*bad), ids)                  # rank 12
+
+
+@pytest.mark.parametrize("rank", [8, 16, 24, 40])
+def test_infinite_adapter_values(q4, rank):
+    """An infinity in B or A reaches the outputs that the formula gives it to, as an infinity,
+    also where the rank does not fill the kernel's registers."""
+    import torch
+
+    N, K = 300, 256
+    a, b, s = _adapters(3, rank, N, K, seed=rank)
+    x = np.abs(synth.activation(5, K, seed=rank))
+    a, s = np.abs(a), np.abs(s)
+    b[1, 7, rank - 1] = np.inf
+    b[1, 9, 0] = -np.inf
+    a[2, rank - 1, 3] = np.inf
+    x[:, 3] = 1.0
+    b[2] = np.abs(b[2]) + np.float16(2.0 ** -10)
+    ids = np.array([0, 1, 2, -1, 1], dtype=np.int32)
+    qw = q4.quantize_pack(torch.zeros((N, K), dtype=torch.float16, device="cuda"), 128)
+    y = to_np(q4.gemm_lora(to_gpu(x), qw, q4.LoraAdapters(to_gpu(a), to_gpu(b), to_gpu(s)), to_gpu(ids)))
+    assert np.isfinite(y[[0, 3]]).all() and not y[3].any()
+    for r in (1, 4):
+        assert y[r, 7] == np.inf and y[r, 9] == -np.inf
+        assert np.isfinite(np.delete(y[r], [7, 9])).all()
+    assert (y[2] == np.inf).all()

@@ -138,8 +138,8 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(LoraArgs a, int splits
         if (id != held) {
           const uint16_t* src = static_cast<const uint16_t*>(a.lora_b) + ((int64_t)id * a.N + n) * a.rank;
 #pragma unroll
-          for (int q = 0; q < 2 * RT; ++q)
-            w[q] = as_half8(*reinterpret_cast<const uint4*>(src + 8 * min(q, a.rank / 8 - 1)));
+          for (int q = 0; q < 2 * RT; ++q)  // zeros behind the rank: 0 * infinity must not arise
+            w[q] = as_half8(8 * q < a.rank ? *reinterpret_cast<const uint4*>(src + 8 * q) : make_uint4(0u, 0u, 0u, 0u));
           held = id;
         }
         float d = 0.0f;
