@@ -79,7 +79,7 @@ q4_status q4_rope_table(int64_t positions, int32_t rot_dim, double theta, float*
  * one outside [0, table_positions) is taken as the nearest inside. table NULL or
  * rot_dim 0: no rotation (positions unused). q_heads or kv_heads may be 0. q_out and
  * k_out may be q and k themselves with the same stride; any other overlap gives
- * unspecified values. */
+ * unspecified values. At most 2^26 - 4 tokens a call (here and in the append). */
 q4_status q4_qk_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int64_t tokens,
                           int32_t q_heads, int32_t kv_heads, int32_t head_dim, const void* q_weight,
                           const void* k_weight, float eps, const int32_t* positions, const float* table,
@@ -129,9 +129,13 @@ q4_status q4_paged_kv_dequant(const q4_paged_kv* cache, const int32_t* slots, in
  * hidden, so no contents of these arrays lead outside the buffers. q . k and the
  * softmax are held in float32, the weights rounded to float16 with the V scale in
  * them before they meet the codes, out rounded once. The result does not depend on
- * timing: partial results of a split context are joined in a fixed order.
+ * timing: partial results of a split context are joined in a fixed order. Where a
+ * context is split depends on the bounds, on the other sequences' lengths and on the
+ * device's size, so a row's last bits may differ between batches it is part of.
  * `workspace` (16-byte aligned) must hold q4_paged_attention_workspace_bytes() bytes
- * (NULL when that is 0, else Q4_ERR_WORKSPACE); contents as q4_gemm's. */
+ * on the device that the call runs on, taken there with the call's own bounds (NULL
+ * when that is 0, else Q4_ERR_WORKSPACE); contents as q4_gemm's. seqs, heads and max_q
+ * whose launch would need 2^24 workgroups are refused (Q4_ERR_SHAPE). */
 size_t q4_paged_attention_workspace_bytes(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv,
                                           int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t group,
                                           int64_t window);

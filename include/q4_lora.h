@@ -31,7 +31,10 @@ size_t q4_workspace_bytes_lora(int64_t B, int64_t out, int64_t in, int32_t group
  * rank is a multiple of 8 in [8, 128]. A_a x[b] is summed and kept in float32, the
  * adapter's part added to the product's float32 sum and the whole rounded once to
  * float16. Deterministic: sums are taken in a fixed order. adapters = 0 is the plain
- * product. `workspace` (16-byte aligned) must hold q4_workspace_bytes_lora() bytes. */
+ * product. `workspace` (16-byte aligned) must hold q4_workspace_bytes_lora() bytes, taken
+ * on the device that the call runs on; contents as q4_gemm's. y must not overlap x. B is bounded
+ * by the launch:
+ * ceil(B / 16) * max(16 * ceil(in / 1024), ceil(out / 256)) < 2^24 (Q4_ERR_SHAPE). */
 q4_status q4_gemm_lora(const void* x, int64_t B, const void* packed, const void* scales, const void* zeros,
                        int64_t out, int64_t in, int32_t group, const void* lora_a, const void* lora_b,
                        const float* scaling, int64_t adapters, int32_t rank, const int32_t* ids, void* y,

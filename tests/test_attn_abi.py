@@ -140,3 +140,17 @@ def test_attention_refusals(lib):
     assert f(qs=1000) == 2 and f(qs=1028) == 4 and f(q=FAKE + 8) == 4 and f(out=FAKE + 4) == 4 and f(off=FAKE + 2) == 4
     assert f(cache=_cache(page_size=20)) == 2 and f(cache=_cache(codes=None)) == 1
     assert f(seqs=0, q=None) == 0 and f(n=0, q=None) == 0 and f(mq=0, q=None) == 0
+
+
+def test_rows_beyond_a_launch(lib):
+    """A launch of 2^24 workgroups or more is refused: 4 tokens each of the norm and rotation, 16 rows
+    or one sequence's head of an attention over short contexts."""
+    f = lib.q4_qk_norm_rope
+    for n, st in ((1 << 26) - 3, 2), ((1 << 26) - 4, 1):
+        assert f(None, 512, None, 256, n, 4, 2, 128, None, None, 0.0, FAKE, FAKE, 10, 128, 0, FAKE, 512, FAKE, 256,
+                 None) == st
+    w = lib.q4_paged_attention_workspace_bytes
+    for seqs, st in (1 << 21, 2), ((1 << 21) - 1, 1):
+        assert w(seqs, seqs, 1, 512, 8, 8, 128, 128, 0) == 0
+        assert lib.q4_paged_attention(None if st == 1 else FAKE, 1024, _cache(kv_heads=8), FAKE, 4, FAKE, FAKE, seqs, seqs,
+                                      1, 512, 8, 0.1, 0, FAKE, None, 0, None) == st

@@ -32,3 +32,13 @@ def test_workspace_sizes(lib):
     assert w(3, 64, 256, 128, 16) > 0
     assert w(0, 64, 256, 128, 16) == 0 and w(3, 64, 256, 96, 16) == 0 and w(3, 64, 256, 128, 12) == 0
     assert w(3, 64, 200, 128, 16) == 0
+
+
+def test_rows_beyond_a_launch(lib):
+    """2^24 workgroups and more are refused (16 rows, 16 adapters, 4 slices of 4096 channels each)."""
+    most = ((1 << 24) - 1) // (16 * 4) * 16
+    w = lib.q4_workspace_bytes_lora
+    assert w(most, 64, 4096, 128, 16) > 0 and w(most + 1, 64, 4096, 128, 16) == 0
+    f = lambda B: lib.q4_gemm_lora(FAKE, B, FAKE, FAKE, None, 64, 4096, 128, FAKE, FAKE, FAKE, 2, 16, FAKE, FAKE, None,
+                                   0, None)
+    assert f(most) == 6 and f(most + 1) == 2

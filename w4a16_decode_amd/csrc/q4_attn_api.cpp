@@ -12,12 +12,12 @@ using q4::aligned;
 using q4::fail;
 using q4::hip_status;
 using q4::kMaxDim;
+using q4::kMaxGroups256;
 using q4::ok;
 
 namespace {
 
-q4_status check_paged_dims(int64_t pages, int32_t page_size, int32_t kv_heads, int32_t head_dim,
-                                  int32_t group) {
+q4_status check_paged_dims(int64_t pages, int32_t page_size, int32_t kv_heads, int32_t head_dim, int32_t group) {
   if (head_dim != 64 && head_dim != 128 && head_dim != 256)
     return fail(Q4_ERR_UNSUPPORTED, "head_dim=%d: the paged cache takes 64, 128 or 256", (int)head_dim);
   if (group != 32 && group != 64 && group != 128)
@@ -61,7 +61,8 @@ q4_status check_rows(const char* name, const void* p, int64_t stride, int64_t he
 // Checks and launch shared by the norm / rotation entry points; a.cache.head_dim etc.
 // are set where a.append.
 q4_status rope_common(q4::RopeArgs& a, void* stream) {
-  if (a.tokens < 0 || a.tokens >= kMaxDim) return fail(Q4_ERR_SHAPE, "tokens=%lld out of range", (long long)a.tokens);
+  if (a.tokens < 0 || a.tokens > 4 * kMaxGroups256)  // a wavefront per token or more of them
+    return fail(Q4_ERR_SHAPE, "tokens=%lld out of range", (long long)a.tokens);
   if (a.head_dim != 64 && a.head_dim != 128 && a.head_dim != 256)
     return fail(Q4_ERR_UNSUPPORTED, "head_dim=%d unsupported (64, 128 or 256)", a.head_dim);
   if (a.q_heads < 0 || a.kv_heads < 0 || a.q_heads > 65535 || a.kv_heads > 65535)
@@ -105,7 +106,6 @@ q4_status check_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv
   if (window < 0 || window >= kMaxDim) return fail(Q4_ERR_SHAPE, "window=%lld out of range", (long long)window);
   if (kv_heads <= 0 || q_heads <= 0 || q_heads > 65535 || q_heads % kv_heads != 0)
     return fail(Q4_ERR_SHAPE, "q_heads=%d must be a positive multiple of kv_heads=%d", (int)q_heads, (int)kv_heads);
-  // row tiles of all sequences and heads index the grid
   const int64_t rows = std::min(max_q, tokens) * (q_heads / kv_heads);
   if (rows >= kMaxDim || (rows / 16 + 1) * kv_heads >= kMaxDim / std::max<int64_t>(seqs, 1))
     return fail(Q4_ERR_SHAPE, "seqs * heads * max_q too large for one call");
@@ -123,14 +123,17 @@ q4_status check_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv
 // unequal 8K contexts 77 -> 68 us against a fixed number of cuts); where the keys of a row are
 // at most 512, one share's smallest piece, a workgroup takes a whole job and no join
 // is launched (16 rows over 512 keys: 7.0 us, 2 us less than with the join).
-void pick_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv, int32_t q_heads, int32_t kv_heads,
-               int32_t head_dim, int32_t group, int64_t window, q4::AttnArgs* a) {
+q4_status pick_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv, int32_t q_heads, int32_t kv_heads,
+                    int32_t head_dim, int32_t group, int64_t window, q4::AttnArgs* a) {
   const int64_t rows = std::min(max_q, tokens) * (q_heads / kv_heads);
   const int64_t groups = kv_heads * seqs;
   const bool fill = (rows + 127) / 128 * groups >= 2 * q4::device_cu_count_cached();
   a->rows_group = rows > 32 && fill ? 128 : rows <= 16 || !q4::has_attn32(head_dim, head_dim / group) ? 16 : 32;
   const int64_t span = window > 0 ? std::min(max_kv, window + std::min(max_q, tokens)) : max_kv;
   a->shares = a->rows_group == 128 || span <= 512 ? 0 : q4::attention_resident(head_dim, group, a->rows_group);
+  if (a->shares == 0 && (rows + a->rows_group - 1) / a->rows_group * groups > kMaxGroups256)
+    return fail(Q4_ERR_SHAPE, "seqs * heads * max_q too large for one call");
+  return Q4_OK;
 }
 
 size_t attn_parts(const q4::AttnArgs& a) { return (size_t)a.shares * 2 * a.rows_group; }
@@ -219,11 +222,12 @@ q4_status q4_paged_kv_dequant(const q4_paged_kv* cache, const int32_t* slots, in
 }
 
 size_t q4_paged_attention_workspace_bytes(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv,
-                                          int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t group, int64_t window) {
+                                          int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t group,
+                                          int64_t window) {
   if (check_attn(seqs, tokens, max_q, max_kv, q_heads, kv_heads, window) != Q4_OK) return 0;
   if (check_paged_dims(1, 16, kv_heads, head_dim, group) != Q4_OK) return 0;
   q4::AttnArgs a{};
-  pick_attn(seqs, tokens, max_q, max_kv, q_heads, kv_heads, head_dim, group, window, &a);
+  if (pick_attn(seqs, tokens, max_q, max_kv, q_heads, kv_heads, head_dim, group, window, &a) != Q4_OK) return 0;
   return attn_workspace(a, head_dim);
 }
 
@@ -248,7 +252,8 @@ q4_status q4_paged_attention(const void* q, int64_t q_stride, const q4_paged_kv*
   a.q_offsets = q_offsets, a.kv_lens = kv_lens, a.seqs = (int)seqs, a.tokens = (int)tokens;
   a.max_q = (int)std::min(max_q, tokens), a.max_kv = (int)max_kv, a.q_heads = q_heads;
   a.scale = scale, a.window = (int)window, a.out = out;
-  pick_attn(seqs, tokens, max_q, max_kv, q_heads, a.cache.kv_heads, a.cache.head_dim, a.cache.group, window, &a);
+  st = pick_attn(seqs, tokens, max_q, max_kv, q_heads, a.cache.kv_heads, a.cache.head_dim, a.cache.group, window, &a);
+  if (st != Q4_OK) return st;
   if (a.shares > 0) {
     const size_t parts = attn_parts(a), need = attn_workspace(a, a.cache.head_dim);
     if (!workspace || workspace_bytes < need)

@@ -10,6 +10,8 @@
 namespace q4 {
 
 constexpr int64_t kMaxDim = int64_t(1) << 30;
+// A launch has fewer than 2^32 threads: workgroups of 256 it may have.
+constexpr int64_t kMaxGroups256 = (int64_t(1) << 24) - 1;
 
 // Record the calling thread's last error and return its status; ok() clears it.
 q4_status fail(q4_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));

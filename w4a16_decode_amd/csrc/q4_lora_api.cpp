@@ -20,6 +20,11 @@ namespace {
 size_t product_bytes(int splits, int64_t B, int64_t out) { return (size_t)round_up(splits * B * out * 4, 256); }
 size_t t_bytes(int64_t B, int64_t in, int32_t rank) { return (size_t)q4::lora_splits((int)in) * B * rank * 4; }
 
+// Workgroups of the two adapter kernels (16 rows each, 16 distinct adapters, 256 outputs).
+bool grid_ok(int64_t B, int64_t out, int64_t in) {
+  return (B + 15) / 16 * std::max<int64_t>(16 * q4::lora_splits((int)in), (out + 255) / 256) <= q4::kMaxGroups256;
+}
+
 bool rank_ok(int32_t rank) { return rank >= 8 && rank <= 128 && rank % 8 == 0; }
 
 }  // namespace
@@ -30,7 +35,7 @@ size_t q4_workspace_bytes_lora(int64_t B, int64_t out, int64_t in, int32_t group
   if (B <= 0 || !rank_ok(rank)) return 0;
   int splits = 0;  // the two kinds of codes may pick different launch shapes
   for (bool asym : {false, true}) splits = std::max(splits, q4::gemm_splits(B, out, in, group, asym));
-  return splits > 0 ? product_bytes(splits, B, out) + t_bytes(B, in, rank) : 0;
+  return splits > 0 && grid_ok(B, out, in) ? product_bytes(splits, B, out) + t_bytes(B, in, rank) : 0;
 }
 
 q4_status q4_gemm_lora(const void* x, int64_t B, const void* packed, const void* scales, const void* zeros,
@@ -43,6 +48,7 @@ q4_status q4_gemm_lora(const void* x, int64_t B, const void* packed, const void*
   q4_status st = q4::gemm_args(x, B, packed, scales, zeros, zeros != nullptr, out, in, group, y, &g);
   if (st != Q4_OK) return st;
   if (B == 0) return ok();
+  if (!grid_ok(B, out, in)) return fail(Q4_ERR_SHAPE, "B=%lld: too many rows for one call", (long long)B);
   if (adapters > 0 && (!lora_a || !lora_b || !scaling || !ids))
     return fail(Q4_ERR_NULL, "lora_a, lora_b, scaling, ids must be non-NULL");
   if (adapters > 0 && (!aligned(lora_a, 16) || !aligned(lora_b, 16) || !aligned(scaling, 4) || !aligned(ids, 4)))
