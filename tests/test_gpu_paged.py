@@ -235,3 +235,26 @@ def test_non_finite_groups(q4, bad):
     want_k[1, 0, 32:64] = want_v[2, 1, 96:] = np.nan
     assert np.array_equal(k.astype(np.float64), want_k.astype(np.float16).astype(np.float64), equal_nan=True)
     assert np.array_equal(v.astype(np.float64), want_v.astype(np.float16).astype(np.float64), equal_nan=True)
+
+
+def test_caches_made_by_hand(q4):
+    """A cache's tensors are checked against its sizes, also in a copy with other fields."""
+    import dataclasses
+
+    import torch
+
+    cache = q4.paged_kv_alloc(4, 32, 2, 128, 64)
+    k = torch.randn((3, 2, 128), device="cuda").half()
+    slots = torch.tensor([0, 40, 127], dtype=torch.int32, device="cuda")
+    q4.paged_kv_append(k, k, cache, slots)
+    same = dataclasses.replace(cache, k_codes=cache.k_codes.clone())
+    assert all(torch.equal(a, b) for a, b in zip(q4.paged_kv_dequant(same, slots), q4.paged_kv_dequant(cache, slots)))
+    wrong = [dict(page_size=64), dict(head_dim=256), dict(group=32), dict(v_codes=cache.v_codes[:3]),
+             dict(k_scales=cache.k_scales[:, :1]), dict(v_scales=cache.v_scales[..., :32].contiguous()),
+             dict(v_codes=cache.v_codes.transpose(0, 1)), dict(k_codes=cache.k_codes.view(-1))]
+    for fields in wrong:
+        with pytest.raises(ValueError):
+            q4.paged_kv_append(k, k, dataclasses.replace(cache, **fields), slots)
+    for fields in (dict(v_codes=cache.v_codes.view(torch.int8)), dict(k_scales=cache.k_scales.float())):
+        with pytest.raises(TypeError):
+            q4.paged_kv_append(k, k, dataclasses.replace(cache, **fields), slots)

@@ -15,6 +15,7 @@ from . import _lib
 from ._tensors import array, call, complain, device, enter, on_device, torch_
 from .ops import Q4Error, _workspace
 
+
 def _rows(t, name: str):
     """(tokens, heads, head_dim, stride, device) of a float16 [tokens, heads, head_dim] GPU
     tensor whose heads are contiguous and whose tokens lie a fixed stride apart."""
@@ -42,7 +43,7 @@ class PagedKVCache4:
     page_size: int
     head_dim: int
     group: int
-    _struct: object = field(default=None, repr=False, compare=False)
+    _struct: object = field(default=None, init=False, repr=False, compare=False)
 
     @property
     def pages(self) -> int:
@@ -59,10 +60,23 @@ class PagedKVCache4:
     def nbytes(self) -> int:
         return 2 * (self.k_codes.numel() + 2 * self.k_scales.numel())
 
+    def _check(self) -> None:
+        """The buffers have the layout's types and sizes."""
+        torch = torch_()
+        if self.k_codes.dim() != 3:
+            raise ValueError("k_codes must be [pages, kv_heads, page_size * head_dim / 2]")
+        dev, shape = self.k_codes.get_device(), (self.pages, self.kv_heads)
+        rows = self.page_size * self.head_dim
+        codes, scales = rows // 2, rows // max(self.group, 1)
+        for name, dtype, size in (("k_codes", torch.uint8, codes), ("v_codes", torch.uint8, codes),
+                                  ("k_scales", torch.float16, scales), ("v_scales", torch.float16, scales)):
+            array(getattr(self, name), name, dtype, (*shape, size), dev)
+
     def _c(self):
         """q4_paged_kv of this cache, by reference."""
         ptrs = (self.k_codes.data_ptr(), self.k_scales.data_ptr(), self.v_codes.data_ptr(), self.v_scales.data_ptr())
         if self._struct is None or self._struct[0] != ptrs:
+            self._check()
             c = _lib.PagedKV(*ptrs, self.pages, self.page_size, self.kv_heads, self.head_dim, self.group)
             object.__setattr__(self, "_struct", (ptrs, c, ctypes.byref(c), self.kv_heads, self.k_codes.get_device()))
         return self._struct
