@@ -332,3 +332,51 @@ def test_many_rows_hidden(q4):
 def test_many_rows_sharp(q4):
     b = Batch(q4, [400, 300], [200, 200], 128, 64, 64, 32, 16, seed=33, spread=20.0, v_scale=2.0 ** -12)
     say("sharp, small v", b.check(b.run(), heads=[0, 77]))
+
+
+@pytest.mark.parametrize("d,g,page", [(64, 32, 16), (64, 64, 48), (128, 128, 32), (128, 64, 16), (128, 32, 64),
+                                      (256, 128, 16), (256, 32, 48)])
+def test_many_rows_cut(q4, d, g, page):
+    """Jobs of 128 rows left over after whole rounds of the chip, their keys cut into pieces: long and
+    short sequences, pieces without keys, a window, hidden infinities, a workspace of garbage."""
+    import torch
+
+    say("many rows, cut", d, g, page)
+    lens, news = [193, 9, 0, 450, 3900], [193, 3, 0, 140, 199]
+    b = Batch(q4, lens, news, 64, 32, d, g, page, seed=d + 5 * g, extra_rows=1000)
+    rows = b.q.shape[0]
+    heads = [0, 33, 62, 63]
+
+    def bound(window):
+        """max_q with which the launch is cut (the bounds may exceed the lengths), and its workspace."""
+        for mq in range(199, rows, 32):
+            need = q4.paged_attention_workspace_bytes(5, rows, mq, 8190, 64, 32, d, g, window)
+            if need:
+                return mq, need
+        raise AssertionError("no bound cuts a job")
+
+    for window in (0, 3300):
+        mq, need = bound(window)
+        ws = torch.full((need + 64,), 0xFF, dtype=torch.uint8, device="cuda")
+        got = b.run(window=window, max_q=mq, max_kv=8190, workspace=ws)
+        say("  window", window, "max_q", mq, "worst share of the bound", b.check(got, window=window, heads=heads))
+        assert bool((ws[need:] == 0xFF).all())
+        again = b.run(window=window, max_q=mq, max_kv=8190)
+        assert torch.equal(got[:int(b.offsets[-1])], again[:int(b.offsets[-1])])
+    mq, need = bound(0)
+    with pytest.raises(q4.Q4Error):
+        b.run(max_q=mq, max_kv=8190, workspace=ws[:need - 16])
+    first = int(b.offsets[4])
+    before = to_np(b.run(max_q=mq, max_kv=8190))[first:first + 199]
+    k16, v16 = b.k16[4].copy(), b.v16[4].copy()
+    k16[3800:, :, 3], v16[3800:, :, 5] = np.inf, -np.inf
+    b.put(4, k16, v16)
+    after = to_np(b.run(max_q=mq, max_kv=8190))[first:first + 199]
+    # Positions 3701 .. 3799 see none of it. Hidden V scales may still move the power of two that a
+    # workgroup's weights carry, and the exponents x - base (below 2^6 in size) round to 2^-24 of
+    # themselves: a weight moves by 2^-18 at most, and so by a whole float16 step, 2^-10, where that
+    # crosses a border. The weighted mean then moves by 2^-10 of the largest |v|, its rounding
+    # by another 2^-10.
+    top = np.repeat(np.abs(b.v[4]).max(axis=0), 2, axis=0)
+    assert np.all(np.abs(after[:99].astype(np.float64) - before[:99]) <= 2.0 ** -9 * top)
+    assert not np.isfinite(after[99:]).all(axis=-1).any()

@@ -29,13 +29,14 @@
 // take every fourth step of its keys, joined in LDS; the keys of all sequences and heads are
 // cut into equal shares, one for each workgroup that fits on the chip (below), and a second
 // kernel joins the partial results (O, m + E, l in float32) of what was cut, in order. In
-// the third each wavefront has rows of its own and nothing is cut.
+// the third each wavefront has rows of its own, and only the jobs of the last, partly
+// filled round of the chip are cut.
 //
 // What bounds it. Few rows: the cache's bytes, read once (48 rows over 8K contexts of 8 heads
 // at 128 channels, 276 MB, in 64 us: 4.3 TB/s, a copy's read + write rate is 4.8). Many rows:
 // the matrix products and, beside them on the same issue ports, the softmax's vector work:
-// four 509-token chunks in contexts of up to 8190 tokens, 64 heads over 8, 430 GFLOP, in 610 to
-// 650 us, 16 of them at 880 TFLOP/s (an 8192^3 library product in float16: 1148).
+// four 509-token chunks in contexts of up to 8190 tokens, 64 heads over 8, 430 GFLOP, in 511 to
+// 526 us, 16 of them in 1420 us: 820 to 870 TFLOP/s (an 8192^3 library product in float16: 1148).
 //
 // Range of the weights. P = p * vs is rounded to float16 before the product (half a
 // step, 2^-11 of each weight; its errors are independent and average over the keys).
@@ -1066,8 +1067,30 @@ struct Shared {
   int pad[2];
 };
 
-template <int D, int GC>
-__global__ __launch_bounds__(256, (D == 256 ? 1 : D == 128 && GC == 2 ? 3 : 2))
+// Row tile, head and sequence of a job. Row tile fastest (last rows, the longest spans, first),
+// then head, sequence; with `swizzle` the eight XCDs, which take workgroups in turn, each keep
+// whole heads (their L2 then holds the keys all of a head's tiles read: a 4001-token prompt
+// 390 -> 311 us).
+__device__ __forceinline__ int rows_job(const AttnArgs& a, unsigned job, int tiles, int swizzle, Job* w) {
+  unsigned group = job / (unsigned)tiles, at = job % (unsigned)tiles;
+  if (swizzle) {
+    const unsigned x = job % 8, y = job / 8;
+    group = x + 8 * (y / (unsigned)tiles);
+    at = y % (unsigned)tiles;
+  }
+  const int tile = tiles - 1 - uniform((int)at), heads = a.cache.kv_heads;
+  const int seq = uniform((int)(group / (unsigned)heads));
+  const bool any = make_job(a, seq, uniform((int)group) - seq * heads, w);
+  return any && 128 * tile < w->rows ? tile : -1;
+}
+
+//
+// Workgroups that fill the chip a whole number of times (a.whole of them) take a job each. The
+// a.tail jobs behind would leave most of it idle for as long as one job takes; CUT cuts the keys
+// of each into pieces, which a second kernel joins (four 509-token chunks, 1024 jobs on 768
+// places: 626 -> 512 us; 1.5 us slower where nothing is cut, hence two instances).
+template <int D, int GC, bool CUT>
+__global__ __launch_bounds__(256, (D == 256 ? 1 : D == 128 && (GC == 2 || (CUT && GC == 1)) ? 3 : 2))
 void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
   using S = Shared<D, GC>;
   constexpr int KB = S::KB, BPG = KB / GC, kKeys = S::kKeys;
@@ -1076,21 +1099,14 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, c = lane >> 5;
-  // blocks: row tile fastest (last rows, the longest spans, first), then head, sequence; with
-  // `swizzle` the eight XCDs, which take blocks in turn, each keep whole heads (their L2 then
-  // holds the keys all of a head's tiles read: a 4001-token prompt 390 -> 311 us)
-  unsigned group = blockIdx.x / (unsigned)tiles, at = blockIdx.x % (unsigned)tiles;
-  if (swizzle) {
-    const unsigned x = blockIdx.x % 8, y = blockIdx.x / 8;
-    group = x + 8 * (y / (unsigned)tiles);
-    at = y % (unsigned)tiles;
-  }
-  const int tile_q = tiles - 1 - (int)at;
-  Job w;
-  if (!make_job(a, (int)(group / (unsigned)a.cache.kv_heads), (int)(group % (unsigned)a.cache.kv_heads), &w)) return;
   constexpr int kGroup = 128;
+  const bool cut = CUT && blockIdx.x >= (unsigned)a.whole;  // one piece of a job's keys
+  const unsigned behind = cut ? blockIdx.x - a.whole : 0;
+  const int piece = cut ? uniform((int)(behind / (unsigned)a.tail)) : 0;
+  Job w;
+  const int tile_q = rows_job(a, blockIdx.x - (unsigned)(piece * a.tail), tiles, swizzle, &w);
+  if (tile_q < 0) return;  // the whole workgroup; a wavefront without rows still converts
   const int g0 = tile_q * kGroup, r0 = g0 + 32 * wave;
-  if (g0 >= w.rows) return;  // the whole workgroup; a wavefront without rows still converts
   const bool idle = r0 >= w.rows;
 
   const int row = r0 + col;
@@ -1113,7 +1129,14 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
 
   const Span all = span_of(a, w, g0, kGroup);                   // the workgroup's keys
   const Span own = span_of(a, w, min(r0, w.rows - 1), 32);      // those of this wavefront's rows
-  const int t_first = all.first, t_last = all.last;
+  int t_first = all.first, t_last = all.last;
+  if (cut) {
+    const int blocks = (max(t_last - t_first, 0) + kKeys - 1) / kKeys;
+    const int b0 = uniform((int)((int64_t)blocks * piece / a.pieces));
+    const int b1 = uniform((int)((int64_t)blocks * (piece + 1) / a.pieces));
+    t_last = min(t_last, t_first + kKeys * b1);
+    t_first += kKeys * b0;
+  }
   const float scale = a.scale * 1.4426950408889634f;
   float exp_v = -64.0f;  // E (wave-uniform)
   int cap_v = 0;         // largest V scale that E covers, as float16 bits
@@ -1328,6 +1351,18 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
   }
   l += __shfl_xor(l, 32, 64);
   if (row >= w.rows) return;
+  if (cut) {
+    const int64_t slot = (int64_t)behind * kGroup + 32 * wave + col;
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        *reinterpret_cast<float4_t*>(a.part_o + slot * D + 32 * b + 8 * u + 4 * c) =
+            float4_t{acc[b][4 * u], acc[b][4 * u + 1], acc[b][4 * u + 2], acc[b][4 * u + 3]};
+    if (c == 0)
+      *reinterpret_cast<float2*>(a.part_ml + 2 * slot) = make_float2(limit == -__builtin_inff() ? kLowest : base, l);
+    return;
+  }
 #pragma unroll
   for (int b = 0; b < KB; ++b)
 #pragma unroll
@@ -1336,27 +1371,13 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
           to_row(float4_t{acc[b][4 * u], acc[b][4 * u + 1], acc[b][4 * u + 2], acc[b][4 * u + 3]}, l);
 }
 
-// Joins the pieces of the job that share blockIdx.x / (RG / 4) begins and does not end: a
-// wavefront per row, D / 4 lanes a group of channels, the 256 / D groups taking every such piece
-// and added in order.
-template <int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rg) {
+// Row `row` of a job from n partial results, the i-th in place at(i): a wavefront, D / 4 lanes
+// of four channels each, the 256 / D groups taking every such piece, added in order.
+template <int D, typename At>
+__device__ __forceinline__ void join_row(const AttnArgs& a, const Job& w, int row, int n, At at) {
   constexpr int LPR = D / 4, G = kWave / LPR;
   const int lane = threadIdx.x & 63;
-  const int per = rg / 4;
-  const int share = (int)(blockIdx.x / (unsigned)per);
-  const int local = (int)(blockIdx.x - (unsigned)(share * per)) * 4 + uniform(threadIdx.x >> 6);
-  const int4* cut = reinterpret_cast<const int4*>(a.cuts) + 2 * share;
-  const int4 c0 = cut[0];
-  const int n = c0.x;  // pieces: this share's slot 1, the next ones' slot 0
-  const int row = cut[1].x + local;
-  if (n == 0 || row >= c0.z) return;
-  Job w{};
-  w.first = c0.y;
-  w.head = c0.w;
-  w.share = a.q_heads / a.cache.kv_heads;
   const int g = lane / LPR, ch = 4 * (lane % LPR);
-  auto at = [&](int i) __attribute__((always_inline)) { return ((int64_t)(share + i) * 2 + (i == 0)) * rg + local; };
   const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
   float top = kLowest, sum = 0.0f;
   float4_t o = {0.f, 0.f, 0.f, 0.f};
@@ -1380,6 +1401,37 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rg) {
   if (g == 0) *out_at<D>(a, w, row, ch) = to_row(o, sum);
 }
 
+// The job that share blockIdx.x / (rg / 4) begins and does not end.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a, int rg) {
+  const int per = rg / 4;
+  const int share = (int)(blockIdx.x / (unsigned)per);
+  const int local = (int)(blockIdx.x - (unsigned)(share * per)) * 4 + uniform(threadIdx.x >> 6);
+  const int4* cut = reinterpret_cast<const int4*>(a.cuts) + 2 * share;
+  const int4 c0 = cut[0];
+  const int n = c0.x;  // pieces: this share's slot 1, the next ones' slot 0
+  const int row = cut[1].x + local;
+  if (n == 0 || row >= c0.z) return;
+  Job w{};
+  w.first = c0.y;
+  w.head = c0.w;
+  w.share = a.q_heads / a.cache.kv_heads;
+  join_row<D>(a, w, row, n, [&](int i) __attribute__((always_inline)) {
+    return ((int64_t)(share + i) * 2 + (i == 0)) * rg + local;
+  });
+}
+
+// The cut jobs of attn_rows_kernel, a wavefront per row.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_rows_kernel(AttnArgs a, int tiles, int swizzle) {
+  const int job = (int)(blockIdx.x / 32), local = (int)(blockIdx.x % 32) * 4 + uniform(threadIdx.x >> 6);
+  Job w;
+  const int tile = rows_job(a, (unsigned)(a.whole + job), tiles, swizzle, &w);
+  if (tile < 0 || 128 * tile + local >= w.rows) return;
+  join_row<D>(a, w, 128 * tile + local, a.pieces,
+              [&](int i) __attribute__((always_inline)) { return ((int64_t)i * a.tail + job) * 128 + local; });
+}
+
 template <int D, int GC>
 hipError_t launch_t(const AttnArgs& a, hipStream_t stream) {
   const int64_t rows = (int64_t)a.max_q * (a.q_heads / a.cache.kv_heads);
@@ -1387,8 +1439,16 @@ hipError_t launch_t(const AttnArgs& a, hipStream_t stream) {
   const int64_t groups = (int64_t)a.cache.kv_heads * a.seqs;
   const dim3 grid((unsigned)(a.shares > 0 ? a.shares : tiles * groups));
   if (a.rows_group == 128) {
-    hipLaunchKernelGGL((attn_rows_kernel<D, GC>), grid, dim3(256), sizeof(Shared<D, GC>), stream, a, tiles,
-                       (int)(groups % 8 == 0 && tiles > 1));
+    const int swizzle = groups % 8 == 0 && tiles > 1;
+    if (a.tail > 0) {
+      hipLaunchKernelGGL((attn_rows_kernel<D, GC, true>), dim3((unsigned)(a.whole + a.tail * a.pieces)), dim3(256),
+                         sizeof(Shared<D, GC>), stream, a, tiles, swizzle);
+      hipLaunchKernelGGL(attn_join_rows_kernel<D>, dim3((unsigned)(a.tail * 32)), dim3(256), 0, stream, a, tiles,
+                         swizzle);
+    } else {
+      hipLaunchKernelGGL((attn_rows_kernel<D, GC, false>), grid, dim3(256), sizeof(Shared<D, GC>), stream, a, tiles,
+                         swizzle);
+    }
   } else if (tiles == 1 && a.rows_group == 16) {
     hipLaunchKernelGGL((attn16_kernel<D, GC, true>), grid, dim3(256), 0, stream, a, tiles);
   } else if constexpr (has_attn32(D, GC)) {
@@ -1404,6 +1464,9 @@ hipError_t launch_t(const AttnArgs& a, hipStream_t stream) {
 
 template <int D, int GC>
 int resident_t(int rows_group) {
+  if (rows_group == 128)
+    return resident_per_cu(reinterpret_cast<const void*>(&attn_rows_kernel<D, GC, true>), 256, sizeof(Shared<D, GC>)) *
+           device_cu_count_cached();
   if constexpr (has_attn32(D, GC)) {
     if (rows_group == 32) return resident_grid(reinterpret_cast<const void*>(&attn32_kernel<D, GC>), 256);
   }

@@ -116,13 +116,19 @@ q4_status check_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv
 // tokens of one sequence have.
 //   up to 16: the 16-row kernel (one tile holds them all);
 //   more: 128 a workgroup where those workgroups are two or more a CU, so that nothing has to
-//     be cut (sixteen 509-token chunks of 64 heads over 8: 880 TFLOP/s, 32-row tiles 760);
+//     be cut but the last round (sixteen 509-token chunks of 64 heads over 8: 870 TFLOP/s, 32-row
+//     tiles 760);
 //   else 32-row tiles (8 sequences of 5 tokens over 8K: 45 us; 128-row workgroups would leave
 //     three quarters of the chip idle), or 16-row ones where the 32-row kernel is not built.
 // The 16- and 32-row kernels take equal shares of all the work, cut anywhere (48 rows over
 // unequal 8K contexts 77 -> 68 us against a fixed number of cuts); where the keys of a row are
 // at most 512, one share's smallest piece, a workgroup takes a whole job and no join
 // is launched (16 rows over 512 keys: 7.0 us, 2 us less than with the join).
+// Workgroups of 128 rows that fill the chip a whole number of times take their jobs whole; the
+// jobs left over are cut, so that their last round is full too, into pieces of 1536 keys
+// or more by the bounds (1024 jobs of up to 8190 keys 626 -> 512 us, 896 of 4096 246 -> 204;
+// pieces of 1280 keys: 142 -> 150 us for 896 jobs of up to 2600; of 1024: 102 -> 117 us for 1024 jobs
+// of up to 2048, whose partial results cost more than the round has left to give).
 q4_status pick_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv, int32_t q_heads, int32_t kv_heads,
                     int32_t head_dim, int32_t group, int64_t window, q4::AttnArgs* a) {
   const int64_t rows = std::min(max_q, tokens) * (q_heads / kv_heads);
@@ -131,12 +137,22 @@ q4_status pick_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv,
   a->rows_group = rows > 32 && fill ? 128 : rows <= 16 || !q4::has_attn32(head_dim, head_dim / group) ? 16 : 32;
   const int64_t span = window > 0 ? std::min(max_kv, window + std::min(max_q, tokens)) : max_kv;
   a->shares = a->rows_group == 128 || span <= 512 ? 0 : q4::attention_resident(head_dim, group, a->rows_group);
-  if (a->shares == 0 && (rows + a->rows_group - 1) / a->rows_group * groups > kMaxGroups256)
-    return fail(Q4_ERR_SHAPE, "seqs * heads * max_q too large for one call");
+  const int64_t jobs = (rows + a->rows_group - 1) / a->rows_group * groups;
+  int64_t grid = a->shares > 0 ? a->shares : jobs;
+  if (a->rows_group == 128) {
+    const int64_t slots = q4::attention_resident(head_dim, group, 128), rest = jobs % slots;
+    const int64_t pieces = rest > 0 ? std::min(slots / rest, span / 1536) : 0;
+    if (pieces > 1) a->tail = (int)rest, a->pieces = (int)pieces;
+    grid = jobs - a->tail + (int64_t)a->tail * a->pieces;
+    a->whole = (int)std::min(jobs - a->tail, kMaxDim);
+  }
+  if (grid > kMaxGroups256) return fail(Q4_ERR_SHAPE, "seqs * heads * max_q too large for one call");
   return Q4_OK;
 }
 
-size_t attn_parts(const q4::AttnArgs& a) { return (size_t)a.shares * 2 * a.rows_group; }
+size_t attn_parts(const q4::AttnArgs& a) {
+  return (size_t)a.shares * 2 * a.rows_group + (size_t)a.tail * a.pieces * a.rows_group;
+}
 size_t attn_workspace(const q4::AttnArgs& a, int32_t head_dim) {
   return attn_parts(a) * (head_dim + 2) * 4 + (size_t)a.shares * 32;
 }
@@ -254,7 +270,7 @@ q4_status q4_paged_attention(const void* q, int64_t q_stride, const q4_paged_kv*
   a.scale = scale, a.window = (int)window, a.out = out;
   st = pick_attn(seqs, tokens, max_q, max_kv, q_heads, a.cache.kv_heads, a.cache.head_dim, a.cache.group, window, &a);
   if (st != Q4_OK) return st;
-  if (a.shares > 0) {
+  if (a.shares > 0 || a.tail > 0) {
     const size_t parts = attn_parts(a), need = attn_workspace(a, a.cache.head_dim);
     if (!workspace || workspace_bytes < need)
       return fail(Q4_ERR_WORKSPACE, "this call needs %zu bytes of workspace (q4_paged_attention_workspace_bytes), got %zu",

@@ -128,16 +128,19 @@ struct AttnArgs {
   // launch shape
   int rows_group;  // rows of a workgroup: 16 or 32 (its wavefronts split the keys), or 128
   int shares;      // > 0: workgroups that take equal shares of all keys (rows_group 16 or 32)
-  float* part_o;   // shares > 0: float32 [shares][2][rows_group][head_dim]
-  float* part_ml;  // and [shares][2][rows_group][2]: what exponents are relative to, sum
-  int32_t* cuts;   // and int32 [shares][8]: the job a share begins and does not end
+  int whole;       // rows_group 128: jobs that a workgroup takes whole, and
+  int tail;        // jobs behind them, each cut into
+  int pieces;      // this many pieces (tail 0: none)
+  float* part_o;   // partial results: float32 [shares][2][rows_group] or [pieces][tail][128], [head_dim]
+  float* part_ml;  // and as many [2]: what exponents are relative to, sum
+  int32_t* cuts;   // shares > 0: int32 [shares][8], the job a share begins and does not end
 };
 
 // Whether tiles of 32 rows whose wavefronts split the keys are built: 256 channels, or four
 // scale groups a head, do not fit the registers next to them (five rows of each of eight
 // sequences over 8K keys at 256 channels, groups of 64: 330 us with spills).
 constexpr bool has_attn32(int head_dim, int groups) { return head_dim <= 128 && groups <= 2; }
-// Workgroups of the kernel for rows_group 16 or 32 that the current device holds at once.
+// Workgroups of the kernel for rows_group that the current device holds at once.
 int attention_resident(int head_dim, int group, int rows_group);
 // Adapters beside a product (include/q4_lora.h). phase 0: A x into t; phase 1: y from the
 // product's partial sums and B t.

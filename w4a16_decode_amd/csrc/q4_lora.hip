@@ -9,7 +9,11 @@
 // (the others' results are discarded: the matrix work is free next to A's bytes). Slices
 // of the channels go to separate workgroups, as there are few tiles in a decode
 // batch. The second, B_a t (out x rank), is added to the product's float32 sums where
-// they are rounded.
+// they are rounded, so the product itself leaves float32 sums in the workspace.
+//
+// Bound: launches for few rows (4096 x 4096, rank 16, one row: 3.6 us A x, 5.8 the product, 2.6
+// B t), the product for many (28672 x 8192, rank 32, 192 rows: 6 + 130 + 20 us of kernel time
+// one by one, 138 together with gaps and tails overlapped; the product alone 132).
 #include <algorithm>
 
 #include "q4_device.h"

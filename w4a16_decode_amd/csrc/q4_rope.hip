@@ -7,7 +7,14 @@
 // and stay in registers for all of the token's heads. The mean square is a butterfly
 // over the head's lanes; a rotation partner that sits rot_dim / 2 channels away is
 // another lane's chunk (four dword shuffles), one that is adjacent is the lane's own.
-// Every head is read once and written once: the pass is bound by those bytes.
+// A wavefront takes its token's k heads, then v's, then q's: each loop holds only what its own
+// arithmetic needs (one loop for all three kept k's float64 values live in q's: 88 us below).
+// For q the norm's weights are folded into the cosines and sines and four loads are in flight.
+//
+// Bound: every head is read once and written once. 8191 tokens of 64 + 8 heads of 128, both
+// normed: 302 MB in 63 to 65 us, 4.7 TB/s, the rate of a large copy. The append is bound by its
+// arithmetic and by V's scattered bytes (16 tokens share a dword's neighbours): 4097 tokens
+// of 32 + 8 + 8 heads, k in float64, 26 us, 3.1 TB/s; few tokens by the launch: 3.9 us.
 //
 // Rounding: x * w is exact in float32 (11 + 11 significant bits). q continues in
 // float32; k, whose value next decides a 4-bit code, in float64, so that a code
