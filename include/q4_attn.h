@@ -73,10 +73,10 @@ q4_status q4_rope_table(int64_t positions, int32_t rot_dim, double theta, float*
  *   h = x * w / sqrt(mean(x^2) + eps)            (weight NULL: h = x),
  *   (h_a, h_b) -> (h_a c - h_b s, h_b c + h_a s)  for the pairs of the first rot_dim
  * channels, (i, i + rot_dim / 2), or (2i, 2i + 1) with `interleaved`; c, s =
- * table[position][i]. The result is rounded once, to float16 (q in float32 arithmetic,
- * k in float64: quantized next, its values decide codes). q_weight and k_weight:
- * float16 [head_dim], 16-byte aligned, each may be NULL. positions: int32 [tokens];
- * one outside [0, table_positions) is taken as the nearest inside. table NULL or
+ * table[position][i]. The result is float16: q from float32 arithmetic, k from
+ * float64 (quantized next, its values decide codes), rounded to float32 and then to
+ * float16. q_weight and k_weight: float16 [head_dim], 16-byte aligned, each may be
+ * NULL. positions: int32 [tokens]; one outside [0, table_positions) is taken as the nearest inside. table NULL or
  * rot_dim 0: no rotation (positions unused). q_heads or kv_heads may be 0. q_out and
  * k_out may be q and k themselves with the same stride; any other overlap gives
  * unspecified values. At most 2^26 - 4 tokens a call (here and in the append). */

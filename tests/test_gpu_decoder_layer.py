@@ -82,7 +82,8 @@ class Layer:
         cs = self.cos_sin[positions]
         ref_q = oracle.paged.norm_rope(qkv[:, :HQ], self.norm[0], 1e-6, cs[..., 0], cs[..., 1])
         assert np.abs(q - ref_q).max() <= 2.0 ** -10 * np.abs(ref_q).max()
-        ref_k = oracle.paged.norm_rope(qkv[:, HQ:HQ + HKV], self.norm[1], 1e-6, cs[..., 0], cs[..., 1]).astype(np.float16)
+        ref_k = oracle.paged.norm_rope(qkv[:, HQ:HQ + HKV], self.norm[1], 1e-6, cs[..., 0], cs[..., 1])
+        ref_k = ref_k.astype(np.float32).astype(np.float16)
         # what the cache holds of the new tokens, and of everything before
         k_all, v_all = [], []
         for n, length in enumerate(lens):

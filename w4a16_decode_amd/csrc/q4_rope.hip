@@ -14,7 +14,7 @@
 // Bound: every head is read once and written once. 8191 tokens of 64 + 8 heads of 128, both
 // normed: 302 MB in 63 to 65 us, 4.7 TB/s, the rate of a large copy. The append is bound by its
 // arithmetic and by V's scattered bytes (16 tokens share a dword's neighbours): 4097 tokens
-// of 32 + 8 + 8 heads, k in float64, 26 us, 3.1 TB/s; few tokens by the launch: 3.9 us.
+// of 32 + 8 + 8 heads, k in float64, 23.5 us, 3.8 TB/s; few tokens by the launch: 3.4 us.
 //
 // Rounding: x * w is exact in float32 (11 + 11 significant bits). q continues in
 // float32; k, whose value next decides a 4-bit code, in float64, so that a code
@@ -154,9 +154,10 @@ __device__ __forceinline__ half8_t q_row(half8_t x, half8_t y, bool norm, float 
   return out;
 }
 
-// k: the same in float64, rounded once. Through float32, the second rounding errs only
-// where the first lands on a tie of the second (or, below 2^-14, on a subnormal's): those
-// few lanes are rounded from the float64 directly.
+// k: the same in float64, rounded to float32 and that to float16, as a float64 array converts:
+// a program that keeps its own float64 k gets these bits. (Off by half a float16 step and 2^-24
+// of the value at most; rounding once instead differs on ties of the second rounding, one
+// value in 16000, and through them in one code of 10 million.)
 template <int D>
 __device__ __forceinline__ half8_t k_row(half8_t x, half8_t y, bool norm, const Weights& w, float eps, const Turn& t,
                                          bool rotate) {
@@ -176,9 +177,9 @@ __device__ __forceinline__ half8_t k_row(half8_t x, half8_t y, bool norm, const 
       v = v * (double)t.c[e] + o * (double)t.s[e];
     }
     if (norm) v *= r;
-    const float f = (float)v;
+    float f = (float)v;
+    asm("" : "+v"(f));  // the compiler would join the two conversions into one, in integer steps
     out[e] = (_Float16)f;
-    if ((__float_as_uint(f) & 0x1FFFu) == 0x1000u || fabsf(f) < 0x1p-14f) out[e] = (_Float16)v;
   }
   return out;
 }
