@@ -119,7 +119,8 @@ q4_status q4_paged_kv_dequant(const q4_paged_kv* cache, const int32_t* slots, in
  * page block_table[n][t / page_size]; entries behind the length are not read. Pages may
  * be shared between sequences.
  *   q: float16 [tokens][q_heads][head_dim], q_stride elements from token to token;
- *   out: the same shape, contiguous, 8-byte aligned; block_table: int32 [seqs]
+ *   out: the same shape, contiguous, 8-byte aligned, overlapping no input; scale: within
+ *   +-2e38 (0 and negative ones too); block_table: int32 [seqs]
  *   [max_blocks]; q_offsets: int32 [seqs + 1], ascending; kv_lens: int32 [seqs].
  *   max_q and max_kv bound the rows and the length of every sequence; they size the
  *   launch and the workspace, so a captured graph serves any lengths up to them.

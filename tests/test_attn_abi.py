@@ -154,3 +154,10 @@ def test_rows_beyond_a_launch(lib):
         assert w(seqs, seqs, 1, 512, 8, 8, 128, 128, 0) == 0
         assert lib.q4_paged_attention(None if st == 1 else FAKE, 1024, _cache(kv_heads=8), FAKE, 4, FAKE, FAKE, seqs, seqs,
                                       1, 512, 8, 0.1, 0, FAKE, None, 0, None) == st
+
+
+def test_scale_limits(lib):
+    f = lambda scale: lib.q4_paged_attention(None, 1024, _cache(), FAKE, 4, FAKE, FAKE, 2, 3, 2, 100, 8, scale, 0, FAKE,
+                                             None, 0, None)
+    assert f(2.5e38) == 2 and f(-2.5e38) == 2 and f(float("nan")) == 2
+    assert f(1.9e38) == 1 and f(-1.9e38) == 1 and f(0.0) == 1                          # q is NULL

@@ -380,3 +380,44 @@ def test_many_rows_cut(q4, d, g, page):
     top = np.repeat(np.abs(b.v[4]).max(axis=0), 2, axis=0)
     assert np.all(np.abs(after[:99].astype(np.float64) - before[:99]) <= 2.0 ** -9 * top)
     assert not np.isfinite(after[99:]).all(axis=-1).any()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.11, 1e-30])
+def test_scales_of_any_sign(q4, scale):
+    """Zero (the mean of what is seen), negative and tiny scales, in 16-, 32- and 128-row tiles."""
+    for lens, news, hq, hkv in (([700, 40], [1, 1], 8, 2), ([600, 90], [5, 9], 16, 2), ([400, 150], [260, 129], 64, 64)):
+        b = Batch(q4, lens, news, hq, hkv, 128, 128, 32, seed=41)
+        say("scale", scale, news, "worst share of the bound", b.check(b.run(scale=scale), scale=scale, heads=[0, hq - 1]))
+
+
+def test_many_rows_cut_captured(q4):
+    """Cut jobs in a graph, replayed with other queries and lengths beside eager work."""
+    import torch
+
+    b = Batch(q4, [193, 9, 0, 450, 2100], [193, 3, 0, 140, 199], 64, 32, 128, 128, 32, seed=51, extra_rows=1000)
+    rows = b.q.shape[0]
+    mq = next(m for m in range(199, rows, 32)
+              if q4.paged_attention_workspace_bytes(5, rows, m, 8190, 64, 32, 128, 128, 0))
+    ws = torch.empty(q4.paged_attention_workspace_bytes(5, rows, mq, 8190, 64, 32, 128, 128, 0), dtype=torch.uint8,
+                     device="cuda")
+    q, lens = to_gpu(b.q), to_gpu(np.array(b.lens, np.int32))
+    table, offsets, out = to_gpu(b.table), to_gpu(b.offsets), torch.zeros_like(to_gpu(b.q))
+
+    def call(out, ws=None):
+        return q4.paged_attention(q, b.cache, table, offsets, lens, mq, 8190, out=out, workspace=ws)
+
+    call(out, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out, ws)
+    for i in range(4):
+        q.copy_(to_gpu(np.roll(b.q, i, axis=0)))
+        lens[4] = 2100 - 300 * i
+        want = call(torch.zeros_like(out))
+        out.zero_()
+        ws.fill_(0xFF)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), i

@@ -257,7 +257,8 @@ q4_status q4_paged_attention(const void* q, int64_t q_stride, const q4_paged_kv*
   if ((st = check_attn(seqs, tokens, max_q, max_kv, q_heads, a.cache.kv_heads, window)) != Q4_OK) return st;
   if (max_blocks < 0 || max_blocks >= kMaxDim)
     return fail(Q4_ERR_SHAPE, "max_blocks=%lld out of range", (long long)max_blocks);
-  if (!(scale > -3.0e38f && scale < 3.0e38f)) return fail(Q4_ERR_SHAPE, "scale must be finite");
+  // times log2(e) it has to stay finite
+  if (!(scale > -2.0e38f && scale < 2.0e38f)) return fail(Q4_ERR_SHAPE, "scale must be within +-2e38");
   if (seqs == 0 || tokens == 0 || max_q == 0) return ok();
   if ((st = check_rows("q", q, q_stride, q_heads, a.cache.head_dim)) != Q4_OK) return st;
   if (!q_offsets || !kv_lens || !out || (!block_table && max_blocks > 0 && max_kv > 0))
