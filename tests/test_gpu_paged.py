@@ -275,3 +275,36 @@ def test_k_rounds_as_a_float64_array_converts(q4):
     assert np.array_equal(torch.from_numpy(ref).half().numpy().view(np.uint16), want.view(np.uint16))
     assert (want != ref.astype(np.float16)).any()
     assert _same_bits(to_np(k), want)
+
+
+def _norm_rope_ref(x, weight, eps, table, pos, interleaved):
+    """The formula in float64 with the arithmetic of infinities (0 * infinity is NaN)."""
+    cos, sin = (None, None) if table is None else (table[pos, :, 0], table[pos, :, 1])
+    with np.errstate(invalid="ignore"):
+        return oracle.paged.norm_rope(x, weight, eps, cos, sin, interleaved)
+
+
+def _equal_q(got, ref):
+    """q against the formula: NaN and infinities exactly, the rest within half a float16 step and 16
+    roundings of float32 (2^-24 each of the two terms of a channel, together below 64 in size here)."""
+    got = got.astype(np.float64)
+    with np.errstate(over="ignore"):
+        want = ref.astype(np.float16).astype(np.float64)
+    odd = ~np.isfinite(want)
+    assert np.array_equal(np.where(odd, got, 0), np.where(odd, want, 0), equal_nan=True)
+    err = np.abs(np.where(odd, 0, got) - np.where(odd, 0, ref))
+    assert np.all(err <= 2.0 ** -11 * np.abs(np.where(odd, 0, ref)) + 2.0 ** -25 + 16 * 2.0 ** -24 * 64), err.max()
+
+
+@pytest.mark.parametrize("rot,interleaved", [(0, False), (64, False), (64, True), (128, False), (128, True)])
+def test_infinities_in_q(q4, rot, interleaved):
+    """An infinity in q stays where the formula puts it: without a rotation and behind rot_dim it is
+    itself, inside it reaches its pair."""
+    x = np.random.default_rng(rot).standard_normal((6, 4, 128)).astype(np.float16)
+    x[1, 0, 3], x[2, 1, 70], x[3, 2, 127], x[4, 3, 100], x[5, 0, 64] = np.inf, -np.inf, np.inf, -np.inf, np.nan
+    pos = np.array([1, 2, 3, 4, 5, 6], np.int32)
+    table = _table(8, rot) if rot else None
+    g = to_gpu(x)
+    q, _ = q4.qk_norm_rope(g, g[:, :1], to_gpu(pos) if rot else None, to_gpu(table) if rot else None,
+                           interleaved=interleaved)
+    _equal_q(to_np(q), _norm_rope_ref(x, None, 0.0, table, pos, interleaved))

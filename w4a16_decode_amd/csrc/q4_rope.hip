@@ -325,7 +325,7 @@ __global__ __launch_bounds__(256, 6) void rope_kernel(RopeArgs a, int segs, int 
     for (int i = 0; i < kAhead; ++i) {
       if (u + i >= last) break;
       const half8_t x = as_half8(raw[i]);
-      half8_t y = x;
+      half8_t y{};  // no rotation: sines of 0 meet zeros, as behind rot_dim
       if (rotate) y = partners(x, t, a.interleaved);
       store(a.q_out, a.q_out_stride, (u + i) * RPW + sub, a.q_heads, q_row<D>(x, y, a.q_weight != nullptr, a.eps, t));
       raw[i] = next[i];
