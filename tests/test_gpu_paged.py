@@ -308,3 +308,38 @@ def test_infinities_in_q(q4, rot, interleaved):
     q, _ = q4.qk_norm_rope(g, g[:, :1], to_gpu(pos) if rot else None, to_gpu(table) if rot else None,
                            interleaved=interleaved)
     _equal_q(to_np(q), _norm_rope_ref(x, None, 0.0, table, pos, interleaved))
+
+
+@pytest.mark.parametrize("rot,interleaved", [(0, False), (64, False), (64, True), (128, False), (128, True)])
+def test_infinities_under_a_norm(q4, rot, interleaved):
+    """One infinity makes its head's mean square infinite: its channel (and pair) NaN, the others zero, in
+    q, in k and in the cache, where only the groups that hold a NaN read back as NaN."""
+    import torch
+
+    r = np.random.default_rng(rot + 1)
+    x = r.standard_normal((5, 8, 128)).astype(np.float16)
+    x[1, [0, 4, 6], 3], x[2, [1, 5, 7], 70], x[3, [2, 4, 6], 127] = np.inf, -np.inf, np.inf
+    w = [(1 + 0.3 * r.standard_normal(128)).astype(np.float16) for _ in range(2)]
+    pos = np.array([1, 2, 3, 4, 5], np.int32)
+    table = _table(8, rot) if rot else None
+    g = to_gpu(x)
+    rest = (to_gpu(pos) if rot else None, to_gpu(table) if rot else None)
+    q, k = q4.qk_norm_rope(g[:, :4], g[:, 4:6], *rest, to_gpu(w[0]), to_gpu(w[1]), 1e-6, interleaved)
+    ref_q = _norm_rope_ref(x[:, :4], w[0], 1e-6, table, pos, interleaved)
+    ref_k = _norm_rope_ref(x[:, 4:6], w[1], 1e-6, table, pos, interleaved)
+    assert np.isnan(ref_k).any() and (ref_k == 0).any()
+    _equal_q(to_np(q), ref_q)
+    want_k = ref_k.astype(np.float32).astype(np.float16)
+    assert np.array_equal(to_np(k), want_k, equal_nan=True)
+    cache = q4.paged_kv_alloc(1, 16, 2, 128, 32)
+    slots = to_gpu(np.arange(5, dtype=np.int32))
+    q2 = q4.qk_norm_rope_append(g[:, :4], g[:, 4:6], g[:, 6:], *rest, cache, slots, to_gpu(w[0]), to_gpu(w[1]), 1e-6,
+                                interleaved)
+    assert np.array_equal(to_np(q2), to_np(q), equal_nan=True)
+    for got, rows in zip(q4.paged_kv_dequant(cache, slots), (want_k, x[:, 6:])):
+        bad = ~np.isfinite(rows.reshape(5, 2, 4, 32)).all(-1)
+        want = oracle.paged.store(np.where(np.repeat(bad, 32, -1), np.float16(0), rows), 32)[2].astype(np.float16)
+        want[np.repeat(bad, 32, -1)] = np.nan
+        assert bad.any() and not bad.all()
+        assert np.array_equal(to_np(got), want, equal_nan=True)
+    assert torch.isfinite(q4.paged_kv_dequant(cache, slots)[0][[0, 4]]).all()

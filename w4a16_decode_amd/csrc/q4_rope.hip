@@ -27,10 +27,11 @@
 namespace q4 {
 namespace {
 
-// 1 / sqrt(v): v_rsq_f64 (about 26 bits) and one Newton step.
+// 1 / sqrt(v): v_rsq_f64 (about 26 bits) and one Newton step; 0 for infinity (where the step
+// would make infinity * 0).
 __device__ __forceinline__ double inv_sqrt(double v) {
   const double y = __builtin_amdgcn_rsq(v);
-  return __builtin_fma(0.5 * y, __builtin_fma(-v * y, y, 1.0), y);
+  return v < __builtin_inf() ? __builtin_fma(0.5 * y, __builtin_fma(-v * y, y, 1.0), y) : y;
 }
 
 // v plus the value of another lane of the same 16, picked by a DPP control (no LDS).
