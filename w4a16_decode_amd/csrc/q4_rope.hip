@@ -135,7 +135,7 @@ __device__ __forceinline__ half8_t partners(half8_t x, const Turn& t, bool inter
 // q: norm and rotation in float32, with the weights already in c and s:
 // (x (w c) + y (w' s)) / rms. About 55 instructions for 8 channels a lane.
 template <int D>
-__device__ __forceinline__ half8_t q_row(half8_t x, half8_t y, bool norm, float eps, const Turn& t) {
+__device__ __forceinline__ half8_t q_row(half8_t x, half8_t y, bool norm, float eps, const Turn& t, bool rotate) {
   float r = 1.0f;
   if (norm) {
     float sum = 0.0f;
@@ -149,7 +149,8 @@ __device__ __forceinline__ half8_t q_row(half8_t x, half8_t y, bool norm, float 
   half8_t out;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float v = __builtin_fmaf((float)y[e], t.s[e], (float)x[e] * t.c[e]);
+    float v = (float)x[e] * t.c[e];
+    if (rotate) v = __builtin_fmaf((float)y[e], t.s[e], v);  // else y is x, and infinity * 0 a NaN
     out[e] = (_Float16)(v * r);
   }
   return out;
@@ -326,9 +327,9 @@ __global__ __launch_bounds__(256, 6) void rope_kernel(RopeArgs a, int segs, int 
     for (int i = 0; i < kAhead; ++i) {
       if (u + i >= last) break;
       const half8_t x = as_half8(raw[i]);
-      half8_t y{};  // no rotation: sines of 0 meet zeros, as behind rot_dim
+      half8_t y = x;
       if (rotate) y = partners(x, t, a.interleaved);
-      store(a.q_out, a.q_out_stride, (u + i) * RPW + sub, a.q_heads, q_row<D>(x, y, a.q_weight != nullptr, a.eps, t));
+      store(a.q_out, a.q_out_stride, (u + i) * RPW + sub, a.q_heads, q_row<D>(x, y, a.q_weight != nullptr, a.eps, t, rotate));
       raw[i] = next[i];
     }
   }
