@@ -343,3 +343,18 @@ def test_infinities_under_a_norm(q4, rot, interleaved):
         assert bad.any() and not bad.all()
         assert np.array_equal(to_np(got), want, equal_nan=True)
     assert torch.isfinite(q4.paged_kv_dequant(cache, slots)[0][[0, 4]]).all()
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_infinite_weight_behind_the_rotation(q4, interleaved):
+    """An infinite norm weight of a channel that is not turned gives that channel infinities only."""
+    x = np.random.default_rng(5).standard_normal((3, 4, 128)).astype(np.float16)
+    w = np.ones(128, np.float16)
+    w[100] = np.inf
+    pos, table = np.array([1, 2, 3], np.int32), _table(8, 64)
+    g = to_gpu(x)
+    q, k = q4.qk_norm_rope(g[:, :2], g[:, 2:], to_gpu(pos), to_gpu(table), to_gpu(w), to_gpu(w), 1e-6, interleaved)
+    ref = _norm_rope_ref(x, w, 1e-6, table, pos, interleaved)
+    assert np.isinf(ref[..., 100]).all() and np.isfinite(np.delete(ref, 100, -1)).all()
+    _equal_q(to_np(q), ref[:, :2])
+    assert np.array_equal(to_np(k), ref[:, 2:].astype(np.float32).astype(np.float16))

@@ -100,7 +100,8 @@ __device__ __forceinline__ void load_turn(const RopeArgs& a, int64_t token, int 
   }
 }
 
-// A norm's weights for a lane's channels and for its rotation partner's.
+// A norm's weights for a lane's channels and for its rotation partner's (zeros where there is no
+// partner: an infinite weight must not meet its sine of 0).
 struct Weights {
   half8_t own, other;
 };
@@ -110,12 +111,18 @@ __device__ __forceinline__ uint4 swap_pairs(uint4 r) {
   return make_uint4(r.x >> 16 | r.x << 16, r.y >> 16 | r.y << 16, r.z >> 16 | r.z << 16, r.w >> 16 | r.w << 16);
 }
 
+__device__ __forceinline__ uint4 masked(uint4 r, bool keep) {
+  const uint32_t m = keep ? 0xFFFFFFFFu : 0u;
+  return make_uint4(r.x & m, r.y & m, r.z & m, r.w & m);
+}
+
 template <int D>
-__device__ __forceinline__ Weights load_weights(const void* w, int lane, int partner, bool interleaved) {
+__device__ __forceinline__ Weights load_weights(const void* w, int lane, const Turn& t, bool interleaved) {
   constexpr int LPH = D / 8;
   const uint4* p = static_cast<const uint4*>(w);
   const uint4 own = p[lane & (LPH - 1)];
-  return Weights{as_half8(own), as_half8(interleaved ? swap_pairs(own) : p[partner & (LPH - 1)])};
+  const uint4 other = interleaved ? swap_pairs(own) : p[t.partner & (LPH - 1)];
+  return Weights{as_half8(own), as_half8(masked(other, t.turn))};
 }
 
 // The rotation partners of a lane's 8 channels; zeros where there is no rotation (the
@@ -128,8 +135,7 @@ __device__ __forceinline__ half8_t partners(half8_t x, const Turn& t, bool inter
     r = make_uint4(__shfl(r.x, t.partner, 64), __shfl(r.y, t.partner, 64), __shfl(r.z, t.partner, 64),
                    __shfl(r.w, t.partner, 64));
   }
-  const uint32_t keep = t.turn ? 0xFFFFFFFFu : 0u;
-  return as_half8(make_uint4(r.x & keep, r.y & keep, r.z & keep, r.w & keep));
+  return as_half8(masked(r, t.turn));
 }
 
 // q: norm and rotation in float32, with the weights already in c and s:
@@ -290,7 +296,7 @@ __global__ __launch_bounds__(256, 6) void rope_kernel(RopeArgs a, int segs, int 
 
   if (u0 < nk) {
     Weights w{};
-    if (a.k_weight) w = load_weights<D>(a.k_weight, lane, t.partner, a.interleaved);
+    if (a.k_weight) w = load_weights<D>(a.k_weight, lane, t, a.interleaved);
     for (int u = u0; u < min(u1, nk); ++u) {
       const int head = u * RPW + sub;
       const half8_t x = as_half8(fetch(a.k, a.k_stride, head, a.kv_heads));
@@ -310,7 +316,7 @@ __global__ __launch_bounds__(256, 6) void rope_kernel(RopeArgs a, int segs, int 
   }
   if (u1 <= q0) return;
   if (a.q_weight) {
-    const Weights w = load_weights<D>(a.q_weight, lane, t.partner, a.interleaved);
+    const Weights w = load_weights<D>(a.q_weight, lane, t, a.interleaved);
 #pragma unroll
     for (int e = 0; e < 8; ++e) t.c[e] *= (float)w.own[e], t.s[e] *= (float)w.other[e];
   }
