@@ -161,3 +161,12 @@ def test_scale_limits(lib):
                                              None, 0, None)
     assert f(2.5e38) == 2 and f(-2.5e38) == 2 and f(float("nan")) == 2
     assert f(1.9e38) == 1 and f(-1.9e38) == 1 and f(0.0) == 1                          # q is NULL
+
+
+def test_rope_table_needs_a_gpu():
+    """A table is filled on a GPU: a host device is refused before any launch."""
+    from w4a16_decode_amd import rope_table
+
+    for device in ("cpu", "meta"):
+        with pytest.raises(ValueError, match="GPU"):
+            rope_table(4, 64, device=device)

@@ -107,6 +107,8 @@ def rope_table(positions: int, rot_dim: int, theta: float = 10000.0, device="cud
     if rot_dim <= 0 or rot_dim % 2 or positions < 0:
         raise ValueError("positions must be >= 0 and rot_dim a positive multiple of 16")
     table = torch.empty((positions, rot_dim // 2, 2), dtype=torch.float32, device=device)
+    if not table.is_cuda:
+        raise ValueError(f"device must be a GPU (got {table.device}); libq4 has no CPU path")
     call(_lib.load().q4_rope_table, table.get_device(), positions, rot_dim, theta, table.data_ptr())
     return table
 
