@@ -170,3 +170,23 @@ def test_rope_table_needs_a_gpu():
     for device in ("cpu", "meta"):
         with pytest.raises(ValueError, match="GPU"):
             rope_table(4, 64, device=device)
+
+
+def test_copies_of_a_cache_drop_what_calls_keep(monkeypatch):
+    """What a cache keeps for its calls (addresses in a C structure) stays behind in copies and pickles."""
+    import copy
+    import pickle
+
+    import torch
+
+    from w4a16_decode_amd import PagedKVCache4
+
+    monkeypatch.setattr(PagedKVCache4, "_check", lambda self: None)
+    codes, scales = torch.zeros((2, 1, 1024), dtype=torch.uint8), torch.zeros((2, 1, 16), dtype=torch.float16)
+    cache = PagedKVCache4(codes, scales, codes.clone(), scales.clone(), 16, 128, 128)
+    cache._c()
+    assert cache._struct is not None
+    for other in (copy.copy(cache), copy.deepcopy(cache), pickle.loads(pickle.dumps(cache))):
+        assert other._struct is None and other.pages == 2 and other.page_size == 16
+        assert torch.equal(other.k_codes, codes) and other._c()[0][0] == other.k_codes.data_ptr()
+    assert cache._struct is not None

@@ -358,3 +358,27 @@ def test_infinite_weight_behind_the_rotation(q4, interleaved):
     assert np.isinf(ref[..., 100]).all() and np.isfinite(np.delete(ref, 100, -1)).all()
     _equal_q(to_np(q), ref[:, :2])
     assert np.array_equal(to_np(k), ref[:, 2:].astype(np.float32).astype(np.float16))
+
+
+def test_copies_and_pickles_of_a_used_cache(q4):
+    """A cache that has been used copies and pickles as an unused one does, and the copies work."""
+    import copy
+    import io
+    import pickle
+
+    import torch
+
+    cache = q4.paged_kv_alloc(3, 16, 2, 128, 64)
+    k = torch.randn((5, 2, 128), device="cuda").half()
+    slots = torch.tensor([0, 40, 17, 3, 22], dtype=torch.int32, device="cuda")
+    q4.paged_kv_append(k, k, cache, slots)
+    want = q4.paged_kv_dequant(cache, slots)
+    deep = copy.deepcopy(cache)
+    file = io.BytesIO()
+    torch.save(cache, file)
+    file.seek(0)
+    for other in (copy.copy(cache), deep, pickle.loads(pickle.dumps(cache)), torch.load(file, weights_only=False)):
+        assert all(torch.equal(a, b) for a, b in zip(q4.paged_kv_dequant(other, slots), want))
+    assert deep.k_codes.data_ptr() != cache.k_codes.data_ptr()
+    q4.paged_kv_append(-k, -k, deep, slots)
+    assert all(torch.equal(a, b) for a, b in zip(q4.paged_kv_dequant(cache, slots), want))

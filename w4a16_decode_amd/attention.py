@@ -60,6 +60,10 @@ class PagedKVCache4:
     def nbytes(self) -> int:
         return 2 * (self.k_codes.numel() + 2 * self.k_scales.numel())
 
+    def __getstate__(self) -> dict:
+        """Fields for a copy or a pickle: without the C structure, which holds this cache's addresses."""
+        return {**self.__dict__, "_struct": None}
+
     def _check(self) -> None:
         """The buffers have the layout's types and sizes."""
         torch = torch_()
