@@ -421,3 +421,29 @@ def test_many_rows_cut_captured(q4):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want), i
+
+
+def _quiet_channels(b, g, large):
+    """K with codes of zero in half the channels, where q is large and of one sign: the scores come from the
+    other half, small next to what q adds up to."""
+    r = np.random.default_rng(61)
+    loud = np.arange(b.d) % 4 < 2
+    b.q = np.where(loud, large + r.standard_normal(b.q.shape), 0.5 * r.standard_normal(b.q.shape)).astype(np.float16)
+    for n, k16 in enumerate(b.k16):
+        k16[:, :, loud] *= np.float16(2.0 ** -12)
+        b.k[n] = oracle.paged.store(k16, g)[2]
+        assert not b.k[n][:, :, loud].any()
+        b.put(n, k16, b.v16[n])
+
+
+@pytest.mark.parametrize("d,g", [(64, 64), (64, 32), (128, 128), (128, 64), (128, 32), (256, 128), (256, 32)])
+@pytest.mark.parametrize("form", [16, 32, 128])
+def test_scores_small_next_to_q(q4, form, d, g):
+    """Scores that are small next to the sum of q, in tiles of 16, 32 and 128 rows: codes must enter the
+    products exactly, without an offset that is taken off again."""
+    hq, hkv, lens, news = {16: (8, 1, [4, 64, 2000], [1, 1, 1]), 32: (8, 1, [4, 64, 2000], [3, 3, 3]),
+                           128: (64, 32, [200, 264, 2000, 199], [200, 200, 160, 199])}[form]
+    for large in (3.0, 60.0, 1000.0):
+        b = Batch(q4, lens, news, hq, hkv, d, g, 32, seed=d + g)
+        _quiet_channels(b, g, large)
+        say("quiet channels", form, d, g, large, "worst share of the bound", b.check(b.run(), heads=[0, 7]))

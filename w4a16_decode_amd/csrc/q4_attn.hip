@@ -73,25 +73,16 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2, a), __builtin_bit_cast(us2, b)));
 }
 
-// Eight codes of the K operand, biased: fields of a dword are moved to bits 2..5 and 6..9
-// of the half-words, where OR with 256.0h and 16.0h makes 256 + n and 16 + n: two shifts
-// and four v_and_or_b32 for eight codes, no subtraction. The biases times the query's
-// channels (264 = 256 + 8 on elements 0, 1, 4, 5, 24 on the others) are the start value of
-// the dot product's accumulator instead.
-struct KRegs {
-  uint32_t m2, m6, b2, b6;
-  __device__ __forceinline__ static KRegs make() {
-    return KRegs{vreg_const(0x003C003Cu), vreg_const(0x03C003C0u), vreg_const(0x5C005C00u), vreg_const(0x4C004C00u)};
-  }
-};
-
-__device__ __forceinline__ half8_t k_operand(uint32_t w, const KRegs& k) {
-  const uint32_t a = w << 2, b = w >> 6;
-  const half2_t p0 = as_half2((a & k.m2) | k.b2), p1 = as_half2((a & k.m6) | k.b6);
-  const half2_t p2 = as_half2((b & k.m2) | k.b2), p3 = as_half2((b & k.m6) | k.b6);
-  const half4_t lo = __builtin_shufflevector(p0, p1, 0, 1, 2, 3);
-  const half4_t hi = __builtin_shufflevector(p2, p3, 0, 1, 2, 3);
-  return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+// Eight codes of the K operand, exact: a score then rounds relative to its own terms. (Codes that keep
+// an offset, taken off again through the accumulator's start value, are three instructions
+// shorter: 63.8 us against 64.7 for 48 rows over 8K contexts. But the accumulator then rounds relative to
+// the offset times the sum of q, and scores small next to that moved the output by up to 7
+// times its other errors. The start values' registers were worth as much: 43.4 -> 41.6 us for eight
+// sequences of 5 rows.)
+__device__ __forceinline__ half8_t k_operand(uint32_t w, const DequantRegs& k) {
+  const half2_t lo_bias = {(_Float16)-1032.0f, (_Float16)-1032.0f};
+  const half2_t hi_bias = {(_Float16)-72.0f, (_Float16)-72.0f};
+  return dequant8r(w, k, lo_bias, hi_bias);
 }
 
 // Eight codes of the V operand: four tokens of each of two tiles. HI picks the channel
@@ -447,7 +438,6 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
   const int col = lane & 15, c4 = lane >> 4;
   const float scale = a.scale * 1.4426950408889634f;
   const DequantRegs dq = DequantRegs::make();
-  const KRegs kr = KRegs::make();
   const int tpp = a.cache.page_size / kTokTile;
   constexpr int kStride = 8;  // tiles from one step of a wavefront to the next
   const int stride_block = kStride / tpp, stride_rem = kStride - stride_block * tpp;
@@ -463,7 +453,6 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
 
     const int row = pc.r0 + col;
     half8_t q[KB];
-    float bias[GC];  // -(264 * sum of q over elements 0, 1, 4, 5 + 24 * the others), per scale group
     int pos;         // position of the lane's row: its own last visible key; -1: no row
     {
       const int i = min(row, w.rows - 1) / w.share, hs = min(row, w.rows - 1) - i * w.share;
@@ -532,9 +521,9 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int g = 0; g < GC; ++g) {
-          float4_t part = {bias[g], bias[g], bias[g], bias[g]};
+          float4_t part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int b = g * BPG; b < (g + 1) * BPG; ++b) part = mfma(k_operand(st.t[j].k[b], kr), q[b], part);
+          for (int b = g * BPG; b < (g + 1) * BPG; ++b) part = mfma(k_operand(st.t[j].k[b], dq), q[b], part);
           const half4_t kh = __builtin_bit_cast(half4_t, st.t[j].ks[g]);
 #pragma unroll
           for (int i = 0; i < 4; ++i)  // one v_fma_mix
@@ -656,18 +645,6 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
       fetch_pages();
 #pragma unroll
       for (int i = 0; i + 1 < C::kStages; ++i) load(ring[i]);
-#pragma unroll
-      for (int g = 0; g < GC; ++g) {
-        float s2 = 0.0f, s6 = 0.0f;
-#pragma unroll
-        for (int b = g * BPG; b < (g + 1) * BPG; ++b)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) (e & 2 ? s6 : s2) += (float)q[b][e];
-        float sum = 264.0f * s2 + 24.0f * s6;
-        sum += __shfl_xor(sum, 16, 64);
-        sum += __shfl_xor(sum, 32, 64);
-        bias[g] = -sum;
-      }
       for (int t0 = t_own; t0 < t_last;) {
 #pragma unroll
         for (int i = 0; i < C::kStages; ++i) {
@@ -750,7 +727,6 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_
   __shared__ float2 ml[4][32];
   const float scale = a.scale * 1.4426950408889634f;
   const DequantRegs dq = DequantRegs::make();
-  const KRegs kr = KRegs::make();
   VRegs vr;
   vr.mask = lane & 16 ? 0x00F000F0u : 0x000F000Fu;   // 64 + n, or 1024 + n
   vr.magic = lane & 16 ? 0x54005400u : 0x64006400u;
@@ -772,25 +748,13 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_
     const int row = r0 + col;
     half8_t q[2 * KB];
     int pos;  // position of the lane's row: its own last visible key; -1: no row
-    float16_t start = {};  // what a dot product starts at: see k_operand
     {
       const int i = min(row, w.rows - 1) / w.share, hs = min(row, w.rows - 1) - i * w.share;
       pos = row < w.rows ? w.len - w.nq + i : -1;
       const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.first + i) * a.q_stride +
                             (int64_t)(w.head * w.share + hs) * D + 8 * c;
-      float s2 = 0.0f, s6 = 0.0f;
 #pragma unroll
-      for (int b = 0; b < 2 * KB; ++b) {
-        q[b] = as_half8(*reinterpret_cast<const uint4*>(src + 16 * b));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) (e & 2 ? s6 : s2) += (float)q[b][e];
-      }
-      if (GC == 1) {
-        const float own = -(264.0f * s2 + 24.0f * s6);
-        const float both = own + __shfl_xor(own, 32, 64);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) start[e] = both;
-      }
+      for (int b = 0; b < 2 * KB; ++b) q[b] = as_half8(*reinterpret_cast<const uint4*>(src + 16 * b));
     }
     // base: m + E. A score more than `limit` above it makes m rise; a row that has seen no key
     // yet has base 0 and limit -infinity, and its first key sets m.
@@ -875,17 +839,11 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_
       float s[16];
 #pragma unroll
       for (int g = 0; g < GC; ++g) {
-        float16_t part = start;
+        float16_t part = {};
 #pragma unroll
         for (int b = g * BPG; b < (g + 1) * BPG; ++b)
 #pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const half2_t lo_bias = {(_Float16)-1032.0f, (_Float16)-1032.0f};
-            const half2_t hi_bias = {(_Float16)-72.0f, (_Float16)-72.0f};
-            // one group a head: biased codes against `start`; more: exact codes
-            const half8_t k = GC == 1 ? k_operand(kw[u][b], kr) : dequant8r(kw[u][b], dq, lo_bias, hi_bias);
-            part = mfma32(k, q[2 * b + u], part);
-          }
+          for (int u = 0; u < 2; ++u) part = mfma32(k_operand(kw[u][b], dq), q[2 * b + u], part);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const half4_t kh = __builtin_bit_cast(half4_t, ks[i >> 3][g][(i >> 2) & 1]);
@@ -1203,13 +1161,11 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
           to[2 * 16] = v_codes4(raw[j][b], hi);
         }
     } else {
-      const half2_t lo_bias = {(_Float16)-1032.0f, (_Float16)-1032.0f};
-      const half2_t hi_bias = {(_Float16)-72.0f, (_Float16)-72.0f};
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int b = 0; b < KB; ++b)
-          lds.k[pair][2 * b + (c4 >> 1)][r16 + 16 * j + 32 * (c4 & 1)] = dequant8r(raw[j][b], dq, lo_bias, hi_bias);
+          lds.k[pair][2 * b + (c4 >> 1)][r16 + 16 * j + 32 * (c4 & 1)] = k_operand(raw[j][b], dq);
     }
     // what no row sees may hold anything: 0 * NaN must not arise
     const int key = raw_t0 + 32 * pair + (lane & 31);
