@@ -125,10 +125,11 @@ q4_status q4_paged_kv_dequant(const q4_paged_kv* cache, const int32_t* slots, in
  *   max_q and max_kv bound the rows and the length of every sequence; they size the
  *   launch and the workspace, so a captured graph serves any lengths up to them.
  * A row that sees no key (an empty sequence, a row ahead of its sequence's start) is
- * zero. Rows of no sequence are left as they were. Lengths, offsets and rows beyond
- * the bounds are cut to them, and the keys of a page number outside [0, pages) count as
- * hidden, so no contents of these arrays lead outside the buffers. q . k and the
- * softmax are held in float32, the weights rounded to float16 with the V scale in
+ * zero; one whose scores are all -infinity, or one of them +infinity (infinities in q,
+ * scores beyond float32), is NaN, as its softmax is. Rows of no sequence are left as
+ * they were. Lengths, offsets and rows beyond the bounds are cut to them, and the keys
+ * of a page number outside [0, pages) count as hidden, so no contents of these arrays
+ * lead outside the buffers. q . k and the softmax are held in float32, the weights rounded to float16 with the V scale in
  * them before they meet the codes, out rounded once. The result does not depend on
  * timing: partial results of a split context are joined in a fixed order. Where a
  * context is split depends on the bounds, on the other sequences' lengths and on the

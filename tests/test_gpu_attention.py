@@ -447,3 +447,40 @@ def test_scores_small_next_to_q(q4, form, d, g):
         b = Batch(q4, lens, news, hq, hkv, d, g, 32, seed=d + g)
         _quiet_channels(b, g, large)
         say("quiet channels", form, d, g, large, "worst share of the bound", b.check(b.run(), heads=[0, 7]))
+
+
+@pytest.mark.parametrize("d,g", [(64, 64), (64, 32), (128, 128), (128, 64), (128, 32), (256, 128), (256, 32)])
+@pytest.mark.parametrize("sign", [-1, 1])
+def test_infinite_scores(q4, sign, d, g):
+    """Every key of a row at a score of -infinity (or +infinity): the softmax is NaN, not the zero of a
+    row that sees nothing, and the other rows are as without it; a finite score outweighs -infinity."""
+    for hq, hkv, lens, news in ((8, 1, [40, 900, 3], [1, 1, 1]), (8, 1, [40, 900, 4], [3, 3, 4]),
+                                (64, 32, [200, 264, 900, 199], [200, 200, 160, 199])):
+        b = Batch(q4, lens, news, hq, hkv, d, g, 16, seed=d + g)
+        for n, k16 in enumerate(b.k16):
+            k16[:, :, 5] = np.float16(8.0)                    # codes above zero there
+            b.put(n, k16, b.v16[n])
+            b.k[n] = oracle.paged.store(k16, g)[2]
+            assert (b.k[n][:, :, 5] > 0).all()
+        clean = to_np(b.run())
+        hit = np.array([int(b.offsets[1]) - 1, int(b.offsets[2]) - 1])
+        b.q[hit, 1, 5] = sign * np.inf
+        got = to_np(b.run())
+        assert np.isnan(got[hit, 1]).all(), (hq, lens, got[hit, 1])
+        got[hit, 1] = clean[hit, 1] = 0
+        # rows of one tile raise their maxima together, so another row's may be raised elsewhere: its weights
+        # move by a float16 step, 2^-10, at most, and the rounding of the mean by another
+        assert np.abs(got.astype(np.float64) - clean).max() <= 2.0 ** -9 * max(np.abs(v).max() for v in b.v)
+    if sign < 0:
+        b = Batch(q4, [900], [1], 8, 1, d, g, 16, seed=3)
+        scale = -1e38
+        b.q[:] = 1.0
+        k16 = np.full(b.k16[0].shape, 8.0, np.float16)        # q . k = 8 d: the scores overflow to -infinity
+        k16[700:] = 0                                        # and 0 here
+        b.put(0, k16, b.v16[0])
+        got = to_np(b.run(scale=scale)).astype(np.float64)
+        want = b.v[0][700:, 0].mean(axis=0)
+        assert np.abs(got[0] - want).max() <= 2.0 ** -9 * np.abs(b.v[0]).max()
+        k16[:] = 8.0
+        b.put(0, k16, b.v16[0])
+        assert np.isnan(to_np(b.run(scale=scale))).all()

@@ -75,7 +75,7 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 
 // Eight codes of the K operand, exact: a score then rounds relative to its own terms. (Codes that keep
 // an offset, taken off again through the accumulator's start value, are three instructions
-// shorter: 63.8 us against 64.7 for 48 rows over 8K contexts. But the accumulator then rounds relative to
+// shorter: 63.8 us against 65.7 for 48 rows over 8K contexts. But the accumulator then rounds relative to
 // the offset times the sum of q, and scores small next to that moved the output by up to 7
 // times its other errors. The start values' registers were worth as much: 43.4 -> 41.6 us for eight
 // sequences of 5 rows.)
@@ -187,9 +187,11 @@ struct Walk {
   int tile, block, in_page;  // tile of the sequence, its page table entry, tile of the page
 };
 
-// Float16 row from sums.
+// Float16 row from sums: zeros where the row saw no key (sum 0). A part of a row that saw keys at scores of
+// -infinity only carries a sum below 0, at the lowest base: any other key outweighs it, and where
+// there is none the row is NaN, as its softmax is.
 __device__ __forceinline__ uint2 to_row(float4_t o, float sum) {
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : __builtin_nanf("");
   half4_t h;
 #pragma unroll
   for (int e = 0; e < 4; ++e) h[e] = (_Float16)(o[e] * inv);
@@ -453,7 +455,7 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
 
     const int row = pc.r0 + col;
     half8_t q[KB];
-    int pos;         // position of the lane's row: its own last visible key; -1: no row
+    int pos;  // position of the lane's row: its own last visible key; -1: no row
     {
       const int i = min(row, w.rows - 1) / w.share, hs = min(row, w.rows - 1) - i * w.share;
       pos = row < w.rows ? w.len - w.nq + i : -1;
@@ -465,6 +467,7 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
     // base: m + E. A score more than `limit` above it makes m rise; a row that has seen no key
     // yet has base 0 and limit -infinity, and its first key sets m.
     float base = 0.0f, limit = -__builtin_inff(), l = 0.0f;
+    bool low = false;  // keys seen at -infinity while no score was above it
     float4_t acc[2 * KB];
 #pragma unroll
     for (int b = 0; b < 2 * KB; ++b) acc[b] = float4_t{0.f, 0.f, 0.f, 0.f};
@@ -591,7 +594,7 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
       }
       // a score far above its row's held maximum?
       float mx = fmaxf(max3(max3(s[0], s[1], s[2]), s[3], s[4]), max3(s[5], s[6], s[7]));
-      if (__any(mx > limit)) {
+      if (__any(mx >= limit)) {
         mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
         mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
         if (mx > -__builtin_inff()) {
@@ -605,6 +608,8 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
           for (int c = 0; c < 2 * KB; ++c) acc[c] *= alpha;
 #pragma unroll
           for (int e = 0; e < 8; ++e) s[e] -= up;
+        } else if (limit == -__builtin_inff()) {
+          low |= hidden != 0xFFu;
         }
       }
       // weights, to float16 with the V scale in them
@@ -654,6 +659,7 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
         }
       }
     }
+    if (low && limit == -__builtin_inff()) l -= 1.0f;
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
     if (limit == -__builtin_inff()) base = kLowest;
@@ -759,6 +765,7 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_
     // base: m + E. A score more than `limit` above it makes m rise; a row that has seen no key
     // yet has base 0 and limit -infinity, and its first key sets m.
     float base = 0.0f, limit = -__builtin_inff(), l = 0.0f;
+    bool low = false;  // keys seen at -infinity while no score was above it
     float16_t acc[KB];
 #pragma unroll
     for (int b = 0; b < KB; ++b) acc[b] = float16_t{};
@@ -924,7 +931,7 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_
 #pragma unroll
       for (int i = 3; i < 15; i += 2) mx = max3(mx, s[i], s[i + 1]);
       mx = fmaxf(mx, s[15]);
-      if (__any(mx > limit)) {
+      if (__any(mx >= limit)) {
         mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
         if (mx > -__builtin_inff()) {
           const bool first = limit == -__builtin_inff();
@@ -937,6 +944,8 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_
           for (int b = 0; b < KB; ++b) acc[b] *= alpha;
 #pragma unroll
           for (int i = 0; i < 16; ++i) s[i] -= up;
+        } else if (limit == -__builtin_inff()) {
+          low |= hidden != 0xFFFFu;
         }
       }
 #pragma unroll
@@ -977,6 +986,7 @@ __global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_
       walk();
       for (int t0 = t_own; t0 < t_last; t0 += kStride * kTokTile) step(t0);
     }
+    if (low && limit == -__builtin_inff()) l -= 1.0f;
     l += __shfl_xor(l, 32, 64);
     if (limit == -__builtin_inff()) base = kLowest;
 
@@ -1081,6 +1091,7 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
   // base: m + E. A score more than `limit` above it makes m rise; a row that has seen no key
   // yet has base 0 and limit -infinity, and its first key sets m.
   float base = 0.0f, limit = -__builtin_inff(), l = 0.0f;
+  bool low = false;  // keys seen at -infinity while no score was above it
   float16_t acc[KB];
 #pragma unroll
   for (int b = 0; b < KB; ++b) acc[b] = float16_t{};
@@ -1244,7 +1255,7 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
 #pragma unroll
       for (int i = 3; i < 15; i += 2) mx = max3(mx, s[i], s[i + 1]);
       mx = fmaxf(mx, s[15]);
-      if (__any(mx > limit)) {
+      if (__any(mx >= limit)) {
         mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
         if (mx > -__builtin_inff()) {
           const bool first = limit == -__builtin_inff();
@@ -1257,6 +1268,8 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
           for (int b = 0; b < KB; ++b) acc[b] *= alpha;
 #pragma unroll
           for (int i = 0; i < 16; ++i) s[i] -= up;
+        } else if (limit == -__builtin_inff()) {
+          low |= hidden != 0xFFFFu;
         }
       }
 #pragma unroll
@@ -1305,6 +1318,7 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
       lds_barrier();
     }
   }
+  if (low && limit == -__builtin_inff()) l -= 1.0f;
   l += __shfl_xor(l, 32, 64);
   if (row >= w.rows) return;
   if (cut) {
