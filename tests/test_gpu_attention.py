@@ -484,3 +484,32 @@ def test_infinite_scores(q4, sign, d, g):
         k16[:] = 8.0
         b.put(0, k16, b.v16[0])
         assert np.isnan(to_np(b.run(scale=scale))).all()
+
+
+def test_offsets_cut_to_the_bounds(q4):
+    """Descending offsets, offsets outside the rows and more rows than max_q: the rows that the cut bounds
+    leave, with every form of the launch; rows of no sequence and what lies behind `out` keep their contents."""
+    import torch
+
+    for hq, hkv, tokens, max_q, max_kv in ((8, 2, 200, 2, 48), (8, 2, 200, 2, 900), (16, 2, 200, 9, 900), (64, 32, 420, 200, 900)):
+        mid, last = (3, 5) if tokens == 200 else (20, 150)
+        mid, last = min(mid, max_q), min(mid, max_q) + min(last - mid, max_q)
+        lens = [70, 600, 333, 900, 10]
+        news = [0, mid, last - mid, max_q, 0]
+        b = Batch(q4, lens, news, hq, hkv, 128, 128, 16, seed=71, extra_rows=tokens - last - max_q)
+        raw = to_gpu(np.array([50, -3, mid, last, 2 ** 31 - 1, 7], np.int32))
+        big = torch.full((tokens + 40, hq, 128), 5.0, dtype=torch.float16, device="cuda")
+        q4.paged_attention(to_gpu(b.q), b.cache, to_gpu(b.table), raw, to_gpu(np.array(lens, np.int32)), max_q, max_kv,
+                           out=big[:tokens])
+        b.lens = [min(n, max_kv) for n in lens]
+        b.k, b.v = ([t[:max_kv] for t in kv] for kv in (b.k, b.v))
+        say("offsets", hq, max_q, max_kv, "worst share of the bound", b.check(big[:tokens], heads=[0, hq - 1]))
+        assert bool((big[last + max_q:] == 5.0).all())
+
+
+def test_subnormal_queries(q4):
+    """Queries among float16's subnormals keep their value in the matrix products."""
+    for hq, hkv, lens, news in ((8, 2, [300, 33], [1, 1]), (16, 2, [300, 33], [5, 3]),
+                                (64, 32, [264, 200, 199, 193], [199, 200, 199, 193])):
+        b = Batch(q4, lens, news, hq, hkv, 128, 128, 16, seed=81, spread=2.0 ** -17)
+        b.check(b.run(scale=2.0 ** 13), scale=2.0 ** 13, heads=[0, hq - 1])

@@ -167,3 +167,38 @@ def test_infinite_adapter_values(q4, rank):
         assert y[r, 7] == np.inf and y[r, 9] == -np.inf
         assert np.isfinite(np.delete(y[r], [7, 9])).all()
     assert (y[2] == np.inf).all()
+
+
+def test_two_calls_at_once(q4):
+    """Calls on two streams at the same time, eager and captured, each with its own workspace: the bits
+    that each gives alone."""
+    import torch
+
+    calls = []
+    for B, N, K, rank, seed in ((3, 2048, 2048, 16, 1), (40, 1037, 1024, 32, 2)):
+        qw = q4.quantize_pack(to_gpu(synth.weight(N, K, seed=seed)), 128)
+        adapters = q4.LoraAdapters(*(to_gpu(t) for t in _adapters(4, rank, N, K, seed)))
+        calls.append((to_gpu(synth.activation(B, K, seed=seed)), qw, adapters, to_gpu(_ids(B, 4, "mixed", seed))))
+    want = [q4.gemm_lora(*c) for c in calls]
+    streams, graphs, outs = [torch.cuda.Stream() for _ in calls], [], []
+    torch.cuda.synchronize()
+    for c in calls:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(q4.gemm_lora(*c))
+        graphs.append(graph)
+    for i in range(10):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for s, graph in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want)), i
+        got = []
+        for s, c in zip(streams, calls):
+            with torch.cuda.stream(s):
+                got.append(q4.gemm_lora(*c))
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(got, want)), i

@@ -382,3 +382,16 @@ def test_copies_and_pickles_of_a_used_cache(q4):
     assert deep.k_codes.data_ptr() != cache.k_codes.data_ptr()
     q4.paged_kv_append(-k, -k, deep, slots)
     assert all(torch.equal(a, b) for a, b in zip(q4.paged_kv_dequant(cache, slots), want))
+
+
+def test_norm_of_subnormal_rows(q4):
+    """Rows among float16's subnormals (all below 2^-14) keep their mean square."""
+    r = np.random.default_rng(9)
+    x = (r.standard_normal((4, 3, 128)) * 2.0 ** -17).astype(np.float16)
+    w = np.ones(128, np.float16)
+    g = to_gpu(x)
+    q, k = q4.qk_norm_rope(g[:, :2], g[:, 2:], None, None, to_gpu(w), to_gpu(w), 1e-14)
+    ref = _norm_rope_ref(x, w, np.float64(np.float32(1e-14)), None, None, False)
+    assert np.abs(ref).max() > 1
+    _equal_q(to_np(q), ref[:, :2])
+    assert _same_bits(to_np(k), ref[:, 2:].astype(np.float32).astype(np.float16))
