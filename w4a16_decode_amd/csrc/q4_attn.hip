@@ -411,7 +411,8 @@ struct Attn {
   static constexpr int BPG = KB / GC;  // of them per scale group
   // Steps of 32 keys a wavefront has in registers (one computed, the other in flight; three and
   // four stages were 3 us slower at 48 x 8K keys), and wavefronts per SIMD the registers are
-  // budgeted for (three with two stages spill at 128 channels: 68 -> 86 us).
+  // budgeted for (three with two stages spill at 128 channels: 68 -> 86 us). What is spilled with these
+  // budgets: 2 registers at 64 channels in two groups, 7 at 256 in eight.
   static constexpr int kStages = 2;
   static constexpr int kWavesSimd = D == 64 ? 3 : D == 128 ? 2 : 1;
 
@@ -702,10 +703,12 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
 //
 // The four wavefronts of a workgroup share 32 rows and split the keys. V is loaded at the start
 // of its step and K of the next one behind the scores, so about half a step covers each: the
-// registers left (K, V, 64 of output, 64 of q at 128 channels) hold no whole second step. Built
-// where the operands fit in registers: with 256 channels, or four scale groups, this form
-// spills (40 rows over 8K keys, 256 channels in groups of 64: 330 us, 78 with 16-row tiles).
-// Eight sequences of 5 rows over 8K keys, 64 heads over 8, 128 channels: 45.5 us.
+// registers left (K, V, 64 of output, 64 of q at 128 channels) hold no whole second step. All
+// instances have the registers of two wavefronts a SIMD: none is spilled at 64 channels (28 and 69
+// with three wavefronts: 37.6 and 58.9 us, now 34.6 and 39.2, for eight sequences of 5 rows over 8K keys,
+// 64 heads over 8, groups of 64 and 32), 2 at 128 channels in one group (42 us), 41 in two (49 us). With 256
+// channels, or four scale groups, it spills far more and is not built (256 channels in groups of 64: 330 us,
+// 74 with 16-row tiles).
 typedef float float16_t __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ float16_t mfma32(half8_t a, half8_t b, float16_t c) {
@@ -724,7 +727,7 @@ __device__ __forceinline__ half4_t v_codes4(uint32_t w, const VRegs& k) {
 }
 
 template <int D, int GC>
-__global__ __launch_bounds__(256, (D == 64 ? 3 : D == 128 ? 2 : 1)) void attn32_kernel(AttnArgs a, int tiles) {
+__global__ __launch_bounds__(256, 2) void attn32_kernel(AttnArgs a, int tiles) {
   constexpr int KB = D / 32, BPG = KB / GC;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -1056,7 +1059,9 @@ __device__ __forceinline__ int rows_job(const AttnArgs& a, unsigned job, int til
 // Workgroups that fill the chip a whole number of times (a.whole of them) take a job each. The
 // a.tail jobs behind would leave most of it idle for as long as one job takes; CUT cuts the keys
 // of each into pieces, which a second kernel joins (four 509-token chunks, 1024 jobs on 768
-// places: 626 -> 512 us; 1.5 us slower where nothing is cut, hence two instances).
+// places: 626 -> 512 us; 1.5 us slower where nothing is cut, hence two instances). At 128 channels in two
+// groups three wavefronts a SIMD spill 7 to 10 registers and are faster all the same (four chunks of 384
+// tokens over 8K: 455 us, 474 with two); 256 channels in eight groups spill 26 to 31.
 template <int D, int GC, bool CUT>
 __global__ __launch_bounds__(256, (D == 256 ? 1 : D == 128 && (GC == 2 || (CUT && GC == 1)) ? 3 : 2))
 void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {

@@ -137,8 +137,8 @@ struct AttnArgs {
 };
 
 // Whether tiles of 32 rows whose wavefronts split the keys are built: 256 channels, or four
-// scale groups a head, do not fit the registers next to them (five rows of each of eight
-// sequences over 8K keys at 256 channels, groups of 64: 330 us with spills).
+// scale groups a head, leave them too few registers (five rows of each of eight
+// sequences over 8K keys at 256 channels, groups of 64: 330 us with spills, 74 with 16-row tiles).
 constexpr bool has_attn32(int head_dim, int groups) { return head_dim <= 128 && groups <= 2; }
 // Workgroups of the kernel for rows_group that the current device holds at once.
 int attention_resident(int head_dim, int group, int rows_group);
