@@ -120,20 +120,26 @@ q4_status q4_paged_kv_dequant(const q4_paged_kv* cache, const int32_t* slots, in
  * be shared between sequences.
  *   q: float16 [tokens][q_heads][head_dim], q_stride elements from token to token;
  *   out: the same shape, contiguous, 8-byte aligned, overlapping no input; scale: within
- *   +-2e38 (0 and negative ones too); block_table: int32 [seqs]
- *   [max_blocks]; q_offsets: int32 [seqs + 1], ascending; kv_lens: int32 [seqs].
+ *   +-2e38 (0 and negative ones too), and within float32 times log2(e) and any K scale;
+ *   block_table: int32 [seqs][max_blocks]; q_offsets: int32 [seqs + 1], ascending;
+ *   kv_lens: int32 [seqs].
  *   max_q and max_kv bound the rows and the length of every sequence; they size the
- *   launch and the workspace, so a captured graph serves any lengths up to them.
+ *   launch and the workspace, so a captured graph serves any lengths up to them. They
+ *   also pick one form of the kernel for the whole call: beside long chunks a single
+ *   token's context is read by one workgroup per KV head, several times slower than
+ *   among single tokens, so long chunks are better given a call of their own.
  * A row that sees no key (an empty sequence, a row ahead of its sequence's start) is
  * zero; one whose scores are all -infinity, or one of them +infinity (infinities in q,
  * scores beyond float32), is NaN, as its softmax is. Rows of no sequence are left as
  * they were. Lengths, offsets and rows beyond the bounds are cut to them, and the keys
  * of a page number outside [0, pages) count as hidden, so no contents of these arrays
- * lead outside the buffers. q . k and the softmax are held in float32, the weights rounded to float16 with the V scale in
- * them before they meet the codes, out rounded once. The result does not depend on
- * timing: partial results of a split context are joined in a fixed order. Where a
- * context is split depends on the bounds, on the other sequences' lengths and on the
- * device's size, so a row's last bits may differ between batches it is part of.
+ * lead outside the buffers. q . k is taken with the exact codes and held in float32, as
+ * the softmax is; the weights are rounded to float16 with the V scale in them before they
+ * meet the codes (11 bits down to 2^-26 of the largest product of weight and V scale, in
+ * steps of 2^-36 of it below), out is rounded once. The result does not depend on timing:
+ * partial results of a split context are joined in a fixed order. Where a context is
+ * split depends on the bounds, on the other sequences' lengths and on the device's
+ * size, so a row's last bits may differ between batches it is part of.
  * `workspace` (16-byte aligned) must hold q4_paged_attention_workspace_bytes() bytes
  * on the device that the call runs on, taken there with the call's own bounds (NULL
  * when that is 0, else Q4_ERR_WORKSPACE); contents as q4_gemm's. seqs, heads and max_q

@@ -28,6 +28,8 @@ size_t q4_workspace_bytes_lora(int64_t B, int64_t out, int64_t in, int32_t group
  *   scaling: float32 [adapters] (alpha / rank, say); ids: int32 [B], the adapter of each
  *   row; one outside [0, adapters), -1 say, is a row without an adapter, whose result
  *   is q4_gemm's. Rows may come in any order.
+ * The weights are q4_gemm's and q4_gemm_asym's; act-order and INT8 weights have no form
+ * with adapters.
  * rank is a multiple of 8 in [8, 128]. A_a x[b] is summed and kept in float32, the
  * adapter's part added to the product's float32 sum and the whole rounded once to
  * float16. Deterministic: sums are taken in a fixed order. adapters = 0 is the plain

@@ -228,7 +228,9 @@ def paged_attention(q, cache: PagedKVCache4, block_table, q_offsets, kv_lens, ma
     q: float16 [tokens, q_heads, head_dim], sequence n's rows q_offsets[n] ..
     q_offsets[n + 1] - 1 being the last of its kv_lens[n] tokens (k and v appended
     before); block_table: int32 [seqs, max_blocks], the page of each page_size tokens;
-    max_q, max_kv: bounds of the rows and the length of any sequence. scale defaults to
+    max_q, max_kv: bounds of the rows and the length of any sequence (one form of the kernel
+    serves the whole call: long chunks beside single tokens are faster in a call of their
+    own). `out` must not overlap an input. scale defaults to
     1 / sqrt(head_dim); window > 0 hides keys more than window - 1 positions back. Returns
     float16 [tokens, q_heads, head_dim]; rows of no sequence keep what `out` held (an
     `out` made here holds anything there)."""

@@ -32,11 +32,14 @@
 // the third each wavefront has rows of its own, and only the jobs of the last, partly
 // filled round of the chip are cut.
 //
-// What bounds it. Few rows: the cache's bytes, read once (48 rows over 8K contexts of 8 heads
-// at 128 channels, 276 MB, in 64 us: 4.3 TB/s, a copy's read + write rate is 4.8). Many rows:
-// the matrix products and, beside them on the same issue ports, the softmax's vector work:
-// four 509-token chunks in contexts of up to 8190 tokens, 64 heads over 8, 430 GFLOP, in 511 to
-// 526 us, 16 of them in 1420 us: 820 to 870 TFLOP/s (an 8192^3 library product in float16: 1148).
+// What bounds it. Few rows: vector work between the loads (16.6 instructions a product: conversion,
+// scales, softmax) and the join's launch: 48 rows over 8K contexts of 8 heads at 128 channels, 276 MB,
+// in 63 to 66 us, 4.2 to 4.4 TB/s, where a plain read of as many bytes takes 40 us. Many rows:
+// the matrix products and, beside them on the same issue ports, the vector work of the softmax and the
+// conversion: four 509-token chunks in contexts of up to 8190 tokens, 64 heads over 8, 430 GFLOP, in 512
+// to 541 us, 16 of them in 1420 us: 800 to 870 TFLOP/s (an 8192^3 library product in float16: 1148).
+// Calls that mix long chunks with single tokens: one form serves the whole call (pick_attn), and in 128-row
+// workgroups a single token's context is walked by one workgroup a KV head.
 //
 // Range of the weights. P = p * vs is rounded to float16 before the product (half a
 // step, 2^-11 of each weight; its errors are independent and average over the keys).

@@ -112,13 +112,14 @@ q4_status check_attn(int64_t seqs, int64_t tokens, int64_t max_q, int64_t max_kv
   return Q4_OK;
 }
 
-// Launch shape (q4_attn.hip), from the bounds alone; the rows are those that a KV head's new
-// tokens of one sequence have.
+// Launch shape (q4_attn.hip), from the bounds alone and one for all sequences of the call (a 512-token
+// chunk and 47 single tokens over 8K contexts: 995 us together, 327 in two calls); the rows are those
+// that a KV head's new tokens of one sequence have.
 //   up to 16: the 16-row kernel (one tile holds them all);
 //   more: 128 a workgroup where those workgroups are two or more a CU, so that nothing has to
 //     be cut but the last round (sixteen 509-token chunks of 64 heads over 8: 870 TFLOP/s, 32-row
 //     tiles 760);
-//   else 32-row tiles (8 sequences of 5 tokens over 8K: 45 us; 128-row workgroups would leave
+//   else 32-row tiles (8 sequences of 5 tokens over 8K: 42 us; 128-row workgroups would leave
 //     three quarters of the chip idle), or 16-row ones where the 32-row kernel is not built.
 // The 16- and 32-row kernels take equal shares of all the work, cut anywhere (48 rows over
 // unequal 8K contexts 77 -> 68 us against a fixed number of cuts); where the keys of a row are

@@ -14,11 +14,12 @@
 // Bound: every head is read once and written once. 8191 tokens of 64 + 8 heads of 128, both
 // normed: 302 MB in 63 to 65 us, 4.7 TB/s, the rate of a large copy. The append is bound by its
 // arithmetic and by V's scattered bytes (16 tokens share a dword's neighbours): 4097 tokens
-// of 32 + 8 + 8 heads, k in float64, 23.5 us, 3.8 TB/s; few tokens by the launch: 3.4 us.
+// of 32 + 8 + 8 heads, k in float64, 23.5 us, 3.8 TB/s; few tokens by the launch: 3.4 us. An append alone
+// moves half that rate (393280 tokens of 8 heads in 850 us, 2.04 GB): V's bytes, and no load ahead.
 //
-// Rounding: x * w is exact in float32 (11 + 11 significant bits). q continues in
-// float32; k, whose value next decides a 4-bit code, in float64, so that a code
-// differs from the exact one only where the value lies within ~1e-15 of a border.
+// Rounding: q takes x * (w c) and y * (w s) in float32, a handful of roundings of 2^-24 before the
+// one to float16. k, whose value next decides a 4-bit code, is float64 arithmetic on exact products x * w,
+// rounded to float32 and that to float16 (k_row): off by half a float16 step and 2^-24 at most.
 #include <algorithm>
 
 #include "q4_paged.h"
@@ -162,10 +163,10 @@ __device__ __forceinline__ half8_t q_row(half8_t x, half8_t y, bool norm, float 
   return out;
 }
 
-// k: the same in float64, rounded to float32 and that to float16, as a float64 array converts:
-// a program that keeps its own float64 k gets these bits. (Off by half a float16 step and 2^-24
-// of the value at most; rounding once instead differs on ties of the second rounding, one
-// value in 16000, and through them in one code of 10 million.)
+// k: the same in float64, rounded to float32 and that to float16, as torch converts float64: a
+// torch program that keeps its own float64 k gets these bits. (Off by half a float16 step and 2^-24
+// of the value at most; rounding once instead, as numpy does, differs on ties of the second
+// rounding, one value in 16000, and through them in one code of 10 million.)
 template <int D>
 __device__ __forceinline__ half8_t k_row(half8_t x, half8_t y, bool norm, const Weights& w, float eps, const Turn& t,
                                          bool rotate) {

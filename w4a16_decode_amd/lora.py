@@ -33,7 +33,8 @@ def workspace_bytes_lora(batch: int, out_features: int, in_features: int, group:
 
 def gemm_lora(x, qw: QuantizedWeight, adapters: LoraAdapters, ids, out=None, workspace=None):
     """q4_gemm_lora: gemm plus scaling[i] * B_i (A_i x[b]) with i = ids[b] (int32 [B]; an id
-    outside the adapters, -1 say, is a row without one)."""
+    outside the adapters, -1 say, is a row without one). For QuantizedWeight; act-order and
+    INT8 weights have no form with adapters."""
     torch = torch_()
     N, K, g = qw.out_features, qw.in_features, qw.group
     a, b, s = adapters.a, adapters.b, adapters.scaling
