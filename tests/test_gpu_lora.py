@@ -202,3 +202,25 @@ def test_two_calls_at_once(q4):
                 got.append(q4.gemm_lora(*c))
         torch.cuda.synchronize()
         assert all(torch.equal(o, w) for o, w in zip(got, want)), i
+
+
+def test_adapters_far_apart(q4):
+    """Adapters whose offsets pass 32 bits (8.6 GB of A and of B): the same bits as from a short list."""
+    import torch
+
+    n, rank, N, K = 2050, 128, 8192, 8192
+    say("adapters far apart")
+    a = torch.zeros((n, rank, K), dtype=torch.float16, device="cuda")
+    b = torch.zeros((n, N, rank), dtype=torch.float16, device="cuda")
+    s = torch.ones(n, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    used = [0, 1030, n - 1]
+    for i in used:
+        a[i] = torch.randn((rank, K), generator=g, device="cuda") / 90
+        b[i] = torch.randn((N, rank), generator=g, device="cuda") / 10
+    qw = q4.quantize_pack(to_gpu(synth.weight(N, K, seed=3)), 128)
+    x = to_gpu(synth.activation(5, K, seed=4))
+    far = q4.gemm_lora(x, qw, q4.LoraAdapters(a, b, s), torch.tensor([n - 1, 0, 1030, -1, n - 1], dtype=torch.int32, device="cuda"))
+    near = q4.gemm_lora(x, qw, q4.LoraAdapters(a[used].contiguous(), b[used].contiguous(), s[:3].contiguous()),
+                        torch.tensor([2, 0, 1, -1, 2], dtype=torch.int32, device="cuda"))
+    assert torch.equal(far, near) and not torch.equal(far, q4.gemm(x, qw))

@@ -395,3 +395,34 @@ def test_norm_of_subnormal_rows(q4):
     assert np.abs(ref).max() > 1
     _equal_q(to_np(q), ref[:, :2])
     assert _same_bits(to_np(k), ref[:, 2:].astype(np.float32).astype(np.float16))
+
+
+def test_far_slots_and_rows(q4):
+    """Slots, rows and tokens whose offsets pass 32 bits: a cache of 8 GiB of codes for K and as many for
+    V, rows 2^30 elements apart; the same bits as near ones."""
+    import torch
+
+    say("far slots and rows")
+    pages, page, heads, d = (1 << 18) + 64, 64, 8, 128
+    far = q4.paged_kv_alloc(pages, page, heads, d, 128)
+    near = q4.paged_kv_alloc(4, page, heads, d, 128)
+    n, hq = 150, 16
+    r = np.random.default_rng(11)
+    k, v = (to_gpu(r.standard_normal((n, heads, d)).astype(np.float16)) for _ in range(2))
+    t = np.arange(n)
+    table = np.array([[pages - 1, pages - 7, pages // 2]], np.int32)
+    slots = [to_gpu((tab[0][t // page] * page + t % page).astype(np.int32)) for tab in (table, np.array([[2, 0, 3]]))]
+    for cache, s in zip((far, near), slots):
+        q4.paged_kv_append(k, v, cache, s)
+    for a, b in zip(q4.paged_kv_dequant(far, slots[0]), q4.paged_kv_dequant(near, slots[1])):
+        assert torch.equal(a, b) and bool(a.any())
+    rest = (to_gpu(np.array([0, 3], np.int32)), to_gpu(np.array([n], np.int32)), 3, n)
+    q = to_gpu(r.standard_normal((3, hq, d)).astype(np.float16))
+    want = q4.paged_attention(q, near, to_gpu(np.array([[2, 0, 3]], np.int32)), *rest)
+    wide = torch.zeros((2 << 30) + hq * d, dtype=torch.float16, device="cuda").as_strided((3, hq, d), (1 << 30, d, 1))
+    wide.copy_(q)
+    assert torch.equal(q4.paged_attention(wide, far, to_gpu(table), *rest), want)
+    pos, turn = to_gpu(np.array([5, 6, 7], np.int32)), q4.rope_table(16, d)
+    a, _ = q4.qk_norm_rope(q, k[:3], pos, turn)
+    b, _ = q4.qk_norm_rope(wide, k[:3], pos, turn, q_out=wide)
+    assert torch.equal(a, b)
