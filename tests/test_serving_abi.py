@@ -1,0 +1,109 @@
+"""Refusals of the serving loop's entry points (no GPU: every call returns from the host
+checks), and the oracle's plan and choice of tokens against hand-computed ones."""
+
+import math
+
+import numpy as np
+import pytest
+
+import oracle
+from w4a16_decode_amd import _lib
+
+FAKE = 0x100000  # a 16-byte-aligned non-NULL address that is never dereferenced
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return _lib.load()
+
+
+def test_plan_refusals(lib):
+    def f(lens=FAKE, new=FAKE, reset=None, starts=None, seqs=3, tokens=5, page=16, pages=9, table=FAKE, blocks=4,
+          free=FAKE, count=FAKE, off=FAKE, pos=FAKE, slots=FAKE, lens_out=FAKE, count_out=FAKE, lacking=FAKE, ws=None,
+          size=0):
+        return lib.q4_paged_plan(lens, new, reset, starts, seqs, tokens, page, pages, table, blocks, free, count, off, pos,
+                                 slots, lens_out, count_out, lacking, ws, size, None)
+
+    assert f(seqs=-1) == 2 and f(seqs=65537) == 2 and f(tokens=-1) == 2 and f(tokens=1 << 30) == 2
+    assert f(page=8) == 2 and f(page=0) == 2 and f(page=-16) == 2
+    assert f(pages=0) == 2 and f(pages=1 << 27) == 2                      # 2^31 slots
+    assert f(blocks=-1) == 2 and f(blocks=(1 << 26) + 1) == 2             # above 2^30 tokens a sequence
+    for name in ("lens", "table", "off", "pos", "slots", "lens_out", "lacking", "count", "count_out"):
+        assert f(**{name: None}) == 1, name
+        assert f(**{name: FAKE + 2}) == 4, name
+    for name in ("new", "reset", "starts", "free"):
+        assert f(**{name: FAKE + 1}) == 4, name
+    need = lib.q4_paged_plan_workspace_bytes(3, 100000)
+    assert need > 0 and lib.q4_paged_plan_workspace_bytes(3, 5) == 0
+    assert f(tokens=100000) == 6 and f(tokens=100000, ws=FAKE, size=need - 1) == 6
+    assert f(tokens=100000, ws=FAKE + 4, size=need) == 4
+    assert lib.q4_paged_plan_workspace_bytes(-1, 5) == 0 and lib.q4_paged_plan_workspace_bytes(3, -5) == 0
+
+
+def test_sample_refusals(lib):
+    def f(x=FAKE, dtype=0, stride=100, rows=3, vocab=100, u=FAKE, t=None, k=None, p=None, m=None, out=FAKE, probs=None):
+        need = lib.q4_sample_workspace_bytes(rows, vocab)
+        return lib.q4_sample(x, dtype, stride, rows, vocab, u, t, k, p, m, out, probs, FAKE, need, None)
+
+    assert f(dtype=3) == 5 and f(dtype=-1) == 5
+    assert f(rows=-1) == 2 and f(rows=1 << 22) == 2 and f(vocab=0) == 2 and f(vocab=(1 << 20) + 1) == 2
+    assert f(stride=99) == 2 and f(stride=1 << 40) == 2 and f(stride=0) == 2
+    assert f(rows=0, x=None, u=None, out=None) == 0
+    assert f(x=None) == 1 and f(u=None) == 1 and f(out=None) == 1
+    assert f(x=FAKE + 1) == 4 and f(x=FAKE + 2, dtype=2) == 4
+    for name in ("u", "t", "k", "p", "m", "out", "probs"):
+        assert f(**{name: FAKE + 2}) == 4, name
+    assert lib.q4_sample_workspace_bytes(-1, 5) == 0 and lib.q4_sample_workspace_bytes(5, 0) == 0
+
+
+def test_wrappers_refuse_host_tensors():
+    import torch
+
+    import w4a16_decode_amd as q4
+
+    i = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        q4.paged_plan(i, None, torch.zeros(2, 3, dtype=torch.int32), 16, 2, pages=4)
+    with pytest.raises(ValueError):
+        q4.paged_plan(i, None, i, 16, 2, pages=4)
+    with pytest.raises(ValueError):
+        q4.sample(torch.zeros(2, 10), torch.zeros(2))
+    with pytest.raises(TypeError):
+        q4.sample(np.zeros((2, 10)), torch.zeros(2))
+    with pytest.raises(ValueError):
+        q4.page_pool(0)
+
+
+def test_oracle_plan():
+    """Two sequences of 3 and 16 tokens on pages 5 and 6; the second needs a page, the stack's top is 7."""
+    table = np.array([[5, -1, -1], [6, -1, -1]])
+    free = np.array([9, 8, 7, 0])
+    off, pos, slots, lens, tab, stack, count, lacking = oracle.serving.plan([3, 16], [2, 1], table, 16, 4, 10, free, 3,
+                                                                           starts=[0, 100])
+    assert off.tolist() == [0, 2, 3] and pos.tolist() == [3, 4, 116, 0]
+    assert slots.tolist() == [5 * 16 + 3, 5 * 16 + 4, 7 * 16, -1]
+    assert lens.tolist() == [5, 17] and tab.tolist() == [[5, -1, -1], [6, 7, -1]]
+    assert count == 2 and lacking == 0 and stack.tolist() == free.tolist()
+    # the first ends: its page 5 is pushed behind 7 and is the next one popped
+    off, pos, slots, lens, tab, stack, count, lacking = oracle.serving.plan([3, 16], [0, 1], table, 16, 1, 10, free, 3,
+                                                                           reset=[1, 0])
+    assert stack.tolist() == [9, 8, 7, 5] and tab[1].tolist() == [6, 5, -1] and lens.tolist() == [0, 17] and count == 3
+    # one page for 40 tokens: 16 are stored, two pages lack
+    off, pos, slots, lens, tab, stack, count, lacking = oracle.serving.plan([0], [40], np.array([[-1, -1]]), 16, 40, 10,
+                                                                           free, 1)
+    assert lens.tolist() == [16] and lacking == 2 and count == 0 and (slots[16:] == -1).all() and slots[15] == 159
+
+
+def test_oracle_sample():
+    """w = 1, 2, 4, 1 (logits ln 1, ln 2, ln 4, ln 1)."""
+    x = np.log([1.0, 2.0, 4.0, 1.0])
+    f = oracle.serving.sample
+    assert [f(x, u)[0] for u in (0.0, 0.124, 0.126, 0.374, 0.376, 0.874, 0.876, 0.999)] == [0, 0, 1, 1, 2, 2, 3, 3]
+    assert math.isclose(f(x, 0.5)[1], 0.5) and f(x, 0.5, temperature=0.0) == (2, 1.0)
+    assert [f(x, u, top_k=3)[0] for u in (0.0, 0.15, 0.99)] == [0, 1, 2]       # of the equal ones the first stays
+    assert [f(x, u, top_p=0.5)[0] for u in (0.0, 0.99)] == [2, 2]              # 4 of 8 is enough
+    assert [f(x, u, top_p=0.51)[0] for u in (0.3, 0.4)] == [1, 2]
+    assert [f(x, u, min_p=0.4)[0] for u in (0.3, 0.4)] == [1, 2]
+    assert math.isclose(f(x, 0.9, temperature=0.5)[1], 16 / 22)
+    assert f(np.array([-np.inf, np.nan]), 0.5) == (-1, 0.0)
+    assert f(np.array([1.0, np.inf, 2.0, np.inf]), 0.6) == (3, 0.5)

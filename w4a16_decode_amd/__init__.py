@@ -59,6 +59,14 @@ from .ops import (  # noqa: F401
     workspace_bytes,
     workspace_bytes_perm,
 )
+from .serving import (  # noqa: F401
+    BatchPlan,
+    PagePool,
+    page_pool,
+    paged_plan,
+    sample,
+    sample_workspace_bytes,
+)
 
 __all__ = [
     "Q4Error", "QuantizedWeight", "quantize_pack", "quantize_pack_into", "quantize_pack_clip", "quantize_pack_clip_into", "gemm", "gemm_noalloc", "gemm_config", "to_canonical",
@@ -69,5 +77,6 @@ __all__ = [
     "LoraAdapters", "gemm_lora", "workspace_bytes_lora",
     "KVCache4", "kv_cache_alloc", "kv_quantize_pack", "kv_dequant",
     "PagedKVCache4", "paged_kv_alloc", "paged_kv_append", "paged_kv_dequant", "rope_table", "qk_norm_rope",
-    "qk_norm_rope_append", "paged_attention", "paged_attention_workspace_bytes", "read_probe", "rtn_check",
+    "qk_norm_rope_append", "paged_attention", "paged_attention_workspace_bytes",
+    "PagePool", "page_pool", "BatchPlan", "paged_plan", "sample", "sample_workspace_bytes", "read_probe", "rtn_check",
 ]

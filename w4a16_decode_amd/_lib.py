@@ -65,6 +65,11 @@ SIGNATURES = {
     "q4_workspace_bytes_lora": (_SZ, [_I64, _I64, _I64, _I32, _I32]),
     "q4_gemm_lora": (ctypes.c_int, [_P, _I64, _P, _P, _P, _I64, _I64, _I32, _P, _P, _P, _I64, _I32, _P, _P, _P, _SZ,
                                     _P]),
+    "q4_paged_plan_workspace_bytes": (_SZ, [_I64, _I64]),
+    "q4_paged_plan": (ctypes.c_int, [_P, _P, _P, _P, _I64, _I64, _I32, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                     _SZ, _P]),
+    "q4_sample_workspace_bytes": (_SZ, [_I64, _I64]),
+    "q4_sample": (ctypes.c_int, [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "q8_packed_bytes": (_SZ, [_I64, _I64]),
     "q8_scales_count": (_SZ, [_I64]),
     "q8_workspace_bytes": (_SZ, [_I64, _I64, _I64]),

@@ -142,6 +142,47 @@ struct AttnArgs {
 constexpr bool has_attn32(int head_dim, int groups) { return head_dim <= 128 && groups <= 2; }
 // Workgroups of the kernel for rows_group that the current device holds at once.
 int attention_resident(int head_dim, int group, int rows_group);
+// The plan of a batch (include/q4_serve.h).
+struct PlanArgs {
+  const int32_t* kv_lens;
+  const int32_t* new_lens;  // NULL: one each
+  const int32_t* reset;     // NULL: none
+  const int32_t* starts;    // NULL: 0
+  int seqs, tokens, page_size, pages, max_blocks;
+  int32_t* block_table;
+  int32_t* free_pages;  // NULL: no stack
+  const int32_t* free_count;
+  int32_t* q_offsets;
+  int32_t* positions;
+  int32_t* slots;
+  int32_t* kv_lens_out;
+  int32_t* free_count_out;
+  int32_t* lacking;
+  int32_t* seq_info;  // two launches: int32 [seqs][2], length and place of the first new page, and the stack's depth
+};
+
+// Whether one workgroup writes the rows too.
+constexpr bool plan_one_launch(int64_t seqs, int64_t tokens) { return seqs <= 1024 && tokens <= 2048; }
+hipError_t launch_plan(const PlanArgs& a, hipStream_t stream);
+
+// One token of each row of logits (include/q4_serve.h).
+struct SampleArgs {
+  const void* logits;
+  int dtype;
+  int64_t stride;
+  int rows, vocab;
+  const float* uniforms;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int32_t* tokens;
+  float* probs;
+  int shift;  // fractional bits of the weights
+};
+
+hipError_t launch_sample(const SampleArgs& a, hipStream_t stream);
+
 // Adapters beside a product (include/q4_lora.h). phase 0: A x into t; phase 1: y from the
 // product's partial sums and B t.
 struct LoraArgs {
