@@ -152,6 +152,33 @@ q4_status q4_paged_attention(const void* q, int64_t q_stride, const q4_paged_kv*
                              int64_t tokens, int64_t max_q, int64_t max_kv, int32_t q_heads, float scale,
                              int64_t window, void* out, void* workspace, size_t workspace_bytes, void* stream);
 
+/* Attention of requests that share long prefixes (a system prompt, a document), each prefix
+ * stored once and read once for all rows behind it: q4_paged_attention, without a window, of
+ * sequences whose first keys are their group's prefix. Sequences group_offsets[g] ..
+ * group_offsets[g + 1] - 1 (int32 [groups + 1], ascending) are group g's; token t <
+ * prefix_lens[g] (int32 [groups]) of its prefix lies in page prefix_table[g][t / page_size]
+ * (int32 [groups][max_prefix_blocks]). Every row of the group sees all of them, and its own
+ * sequence's keys as q4_paged_attention has them: kv_lens, block_table and max_kv count the
+ * keys behind the prefix only. A sequence of no group has no prefix. A prefix need not end
+ * where a page does; the rotation of the keys behind it counts from its length (starts of
+ * q4_paged_plan).
+ * max_group_q and max_prefix bound the rows of a group's sequences together and the prefixes'
+ * lengths; rows of a group beyond max_group_q are taken as having no prefix, longer prefixes
+ * are cut. With few rows behind a short prefix a plain call whose block tables begin with the
+ * prefix's pages may be as fast. Everything else, rows that see no key, infinities and what
+ * results depend on among it, is q4_paged_attention's. groups * heads * max_group_q and
+ * tokens * q_heads >= 2^26 are refused as seqs * heads * max_q is. */
+size_t q4_paged_attention_shared_workspace_bytes(int64_t seqs, int64_t groups, int64_t tokens, int64_t max_q,
+                                                 int64_t max_kv, int64_t max_group_q, int64_t max_prefix,
+                                                 int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t group);
+q4_status q4_paged_attention_shared(const void* q, int64_t q_stride, const q4_paged_kv* cache,
+                                    const int32_t* prefix_table, int64_t max_prefix_blocks,
+                                    const int32_t* prefix_lens, const int32_t* group_offsets, int64_t groups,
+                                    const int32_t* block_table, int64_t max_blocks, const int32_t* q_offsets,
+                                    const int32_t* kv_lens, int64_t seqs, int64_t tokens, int64_t max_q,
+                                    int64_t max_kv, int64_t max_group_q, int64_t max_prefix, int32_t q_heads,
+                                    float scale, void* out, void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -86,3 +86,28 @@ def attention(q, k, v, lens, offsets, scale: float, window: int = 0) -> np.ndarr
                 p = np.exp(z - z.max())
                 out[i, h] = (p / p.sum()) @ vh
     return out
+
+
+def attention_shared(q, prefix_k, prefix_v, group_offsets, k, v, lens, offsets, scale: float) -> np.ndarray:
+    """attention() of sequences behind shared prefixes: rows of sequences group_offsets[g] ..
+    group_offsets[g + 1] - 1 see all of prefix_k[g], prefix_v[g] (float64 [tokens, kv_heads, d]) and
+    then their own keys."""
+    q = np.asarray(q).astype(np.float64)
+    out = np.full(q.shape, np.nan)
+    for n, length in enumerate(lens):
+        first, last = offsets[n], offsets[n + 1]
+        mine = [g for g in range(len(prefix_k)) if group_offsets[g] <= n < group_offsets[g + 1]]
+        for i in range(first, last):
+            own = max(0, length - (last - first) + (i - first) + 1)
+            for h in range(q.shape[1]):
+                share = q.shape[1] // k[n].shape[1]
+                parts = [(prefix_k[g][:, h // share], prefix_v[g][:, h // share]) for g in mine]
+                parts.append((k[n][:own, h // share], v[n][:own, h // share]))
+                kh, vh = (np.concatenate([p[j] for p in parts]) for j in range(2))
+                if len(kh) == 0:
+                    out[i, h] = 0.0
+                    continue
+                z = kh @ q[i, h] * scale
+                p = np.exp(z - z.max())
+                out[i, h] = (p / p.sum()) @ vh
+    return out

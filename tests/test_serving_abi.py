@@ -107,3 +107,46 @@ def test_oracle_sample():
     assert math.isclose(f(x, 0.9, temperature=0.5)[1], 16 / 22)
     assert f(np.array([-np.inf, np.nan]), 0.5) == (-1, 0.0)
     assert f(np.array([1.0, np.inf, 2.0, np.inf]), 0.6) == (3, 0.5)
+
+
+def test_shared_attention_refusals(lib):
+    import ctypes
+
+    def cache(**kw):
+        d = dict(codes=FAKE, scales=FAKE, pages=4, page_size=32, kv_heads=2, head_dim=128, group=128)
+        d.update(kw)
+        return ctypes.byref(_lib.PagedKV(d["codes"], d["scales"], d["codes"], d["scales"], d["pages"], d["page_size"],
+                                         d["kv_heads"], d["head_dim"], d["group"]))
+
+    def f(q=FAKE, qs=512, c=None, ptab=FAKE, pblocks=4, plens=FAKE, goff=FAKE, groups=2, tab=FAKE, blocks=4, off=FAKE,
+          lens=FAKE, seqs=3, tokens=3, max_q=1, max_kv=100, max_gq=3, max_prefix=100, hq=4, scale=0.1, out=FAKE, ws=FAKE,
+          size=1 << 40):
+        return lib.q4_paged_attention_shared(q, qs, cache() if c is None else c, ptab, pblocks, plens, goff, groups, tab,
+                                             blocks, off, lens, seqs, tokens, max_q, max_kv, max_gq, max_prefix, hq, scale,
+                                             out, ws, size, None)
+
+    for name in ("q", "ptab", "plens", "goff", "tab", "off", "lens", "out"):
+        assert f(**{name: None}) == 1, name
+        assert f(**{name: FAKE + 2}) == 4, name
+    assert f(c=cache(codes=None)) == 1 and f(c=cache(page_size=8)) == 2 and f(c=cache(group=16)) == 3
+    for name in ("pblocks", "groups", "blocks", "seqs", "tokens", "max_q", "max_kv", "max_gq", "max_prefix"):
+        assert f(**{name: -1}) == 2 and f(**{name: 1 << 30}) == 2, name
+    assert f(hq=3) == 2 and f(hq=0) == 2 and f(qs=504) == 2 and f(qs=516) == 4
+    assert f(scale=2.1e38) == 2 and f(scale=float("nan")) == 2
+    assert f(tokens=1 << 24, max_gq=1) == 2                                # 2^26 rows
+    assert f(groups=1 << 22, max_gq=1 << 12, tokens=1 << 12) == 2          # too many jobs
+    assert f(ws=None) == 6 and f(size=16) == 6 and f(ws=FAKE + 8) == 4
+    assert f(seqs=0) == 0 and f(tokens=0) == 0 and f(max_q=0) == 0
+    w = lib.q4_paged_attention_shared_workspace_bytes
+    assert w(3, 2, 3, 1, 100, 3, 100, 4, 2, 128, 128) >= 3 * 4 * 130 * 4
+    assert w(3, 0, 3, 1, 100, 3, 100, 4, 2, 128, 128) == 0 and w(3, -1, 3, 1, 100, 3, 100, 4, 2, 128, 128) == 0
+    assert w(3, 2, 3, 1, 100, 3, 100, 4, 2, 96, 32) == 0 and w(3, 2, 3, 1, 100, 3, 100, 3, 2, 128, 128) == 0
+
+
+def test_oracle_shared_attention():
+    """One row, prefix of one key, one key of its own: equal scores average the two; no key is zero."""
+    q = np.zeros((3, 1, 2))
+    pk, pv = [np.ones((1, 1, 2))], [np.full((1, 1, 2), 4.0)]
+    k, v = [np.ones((1, 1, 2)), np.ones((0, 1, 2))], [np.full((1, 1, 2), 2.0), np.ones((0, 1, 2))]
+    out = oracle.paged.attention_shared(q, pk, pv, [0, 1], k, v, [1, 0], [0, 2, 3], 1.0)
+    assert out[:, 0].tolist() == [[4, 4], [3, 3], [0, 0]]                   # row 0 lies ahead of its sequence's start

@@ -12,6 +12,8 @@ fallback: without the built library or a GPU the calls raise.
 from .attention import (  # noqa: F401
     PagedKVCache4,
     paged_attention,
+    paged_attention_shared,
+    paged_attention_shared_workspace_bytes,
     paged_attention_workspace_bytes,
     paged_kv_alloc,
     paged_kv_append,
@@ -78,5 +80,6 @@ __all__ = [
     "KVCache4", "kv_cache_alloc", "kv_quantize_pack", "kv_dequant",
     "PagedKVCache4", "paged_kv_alloc", "paged_kv_append", "paged_kv_dequant", "rope_table", "qk_norm_rope",
     "qk_norm_rope_append", "paged_attention", "paged_attention_workspace_bytes",
+    "paged_attention_shared", "paged_attention_shared_workspace_bytes",
     "PagePool", "page_pool", "BatchPlan", "paged_plan", "sample", "sample_workspace_bytes", "read_probe", "rtn_check",
 ]

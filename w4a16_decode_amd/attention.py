@@ -262,3 +262,57 @@ def paged_attention(q, cache: PagedKVCache4, block_table, q_offsets, kv_lens, ma
     call(lib.q4_paged_attention, dev, q.data_ptr(), qs, ref, tab, blocks, off, lens, seqs, n, max_q, max_kv, hq,
           d ** -0.5 if scale is None else scale, window, to, ws, size)
     return out
+
+
+def paged_attention_shared_workspace_bytes(seqs: int, groups: int, tokens: int, max_q: int, max_kv: int, max_group_q: int,
+                                           max_prefix: int, q_heads: int, kv_heads: int, head_dim: int,
+                                           group: int) -> int:
+    return int(_lib.load().q4_paged_attention_shared_workspace_bytes(seqs, groups, tokens, max_q, max_kv, max_group_q,
+                                                                     max_prefix, q_heads, kv_heads, head_dim, group))
+
+
+def paged_attention_shared(q, cache: PagedKVCache4, prefix_table, prefix_lens, group_offsets, block_table, q_offsets,
+                           kv_lens, max_q: int, max_kv: int, max_group_q: int, max_prefix: int,
+                           scale: float | None = None, out=None, workspace=None):
+    """q4_paged_attention_shared: paged_attention, without a window, of sequences that share prefixes.
+
+    Sequences group_offsets[g] .. group_offsets[g + 1] - 1 (int32 [groups + 1], ascending) see
+    the prefix_lens[g] tokens in the pages prefix_table[g] (int32 [groups, max_prefix_blocks])
+    and then their own: block_table, kv_lens and max_kv count what lies behind the prefix.
+    max_group_q, max_prefix: bounds of the rows of a group's sequences together and of the
+    prefixes' lengths. The rest as in paged_attention."""
+    torch = torch_()
+    n, hq, d, qs, dev = _rows(q, "q")
+    _, _, ref, heads, cdev = cache._c()
+    if d != cache.head_dim:
+        raise ValueError(f"q must have the cache's head_dim {cache.head_dim}")
+    on_device("the cache", cdev, dev)
+    if block_table.dim() != 2 or prefix_table.dim() != 2:
+        raise ValueError("block_table must be [seqs, max_blocks] and prefix_table [groups, max_prefix_blocks]")
+    i32 = torch.int32
+    seqs, blocks = shape = block_table.shape
+    tab = array(block_table, "block_table", i32, shape, dev)
+    off = array(q_offsets, "q_offsets", i32, (seqs + 1,), dev)
+    lens = array(kv_lens, "kv_lens", i32, (seqs,), dev)
+    groups, prefix_blocks = shape = prefix_table.shape
+    ptab = array(prefix_table, "prefix_table", i32, shape, dev)
+    plens = array(prefix_lens, "prefix_lens", i32, (groups,), dev)
+    goff = array(group_offsets, "group_offsets", i32, (groups + 1,), dev)
+    if out is None:
+        out = torch.empty((n, hq, d), dtype=torch.float16, device=device(dev))
+        to = out.data_ptr()
+    else:
+        to = array(out, "out", torch.float16, (n, hq, d), dev)
+    lib = _lib.load()
+    cur = enter(dev)  # the split, and with it the workspace, depends on the device
+    try:
+        need = lib.q4_paged_attention_shared_workspace_bytes(seqs, groups, n, max_q, max_kv, max_group_q, max_prefix, hq,
+                                                             heads, d, cache.group)
+    finally:
+        if cur != dev:
+            torch.cuda.set_device(cur)
+    ws, size = _workspace(q, need, workspace)
+    call(lib.q4_paged_attention_shared, dev, q.data_ptr(), qs, ref, ptab, prefix_blocks, plens, goff, groups, tab, blocks,
+         off, lens, seqs, n, max_q, max_kv, max_group_q, max_prefix, hq, d ** -0.5 if scale is None else scale, to, ws,
+         size)
+    return out

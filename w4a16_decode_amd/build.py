@@ -24,8 +24,8 @@ ROOT = os.path.dirname(HERE)
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libq4.so")
 SOURCES = ["q4_api.cpp", "q4_attn_api.cpp", "q4_lora_api.cpp", "q4_serve_api.cpp", "q4_quant.hip",
-           "q4_gemm.hip", "q4_kv.hip", "q4_rope.hip", "q4_attn.hip", "q4_lora.hip", "q4_plan.hip",
-           "q4_sample.hip", "q4_probe.hip"]
+           "q4_gemm.hip", "q4_kv.hip", "q4_rope.hip", "q4_attn.hip", "q4_attn_shared.hip", "q4_lora.hip",
+           "q4_plan.hip", "q4_sample.hip", "q4_probe.hip"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops: no v_pk_*_f32 (float2 arithmetic is issued as scalar VALU ops).

@@ -158,6 +158,86 @@ size_t attn_workspace(const q4::AttnArgs& a, int32_t head_dim) {
   return attn_parts(a) * (head_dim + 2) * 4 + (size_t)a.shares * 32;
 }
 
+// The checks of an attention call and its arguments with the launch shape; *any: whether there is something
+// to launch.
+q4_status attn_args(const void* q, int64_t q_stride, const q4_paged_kv* cache, const int32_t* block_table,
+                    int64_t max_blocks, const int32_t* q_offsets, const int32_t* kv_lens, int64_t seqs, int64_t tokens,
+                    int64_t max_q, int64_t max_kv, int32_t q_heads, float scale, int64_t window, void* out,
+                    q4::AttnArgs* to, bool* any) {
+  q4::AttnArgs& a = *to;
+  q4_status st = check_paged(cache, &a.cache);
+  if (st != Q4_OK) return st;
+  if ((st = check_attn(seqs, tokens, max_q, max_kv, q_heads, a.cache.kv_heads, window)) != Q4_OK) return st;
+  if (max_blocks < 0 || max_blocks >= kMaxDim)
+    return fail(Q4_ERR_SHAPE, "max_blocks=%lld out of range", (long long)max_blocks);
+  // times log2(e) it has to stay finite
+  if (!(scale > -2.0e38f && scale < 2.0e38f)) return fail(Q4_ERR_SHAPE, "scale must be within +-2e38");
+  *any = seqs > 0 && tokens > 0 && max_q > 0;
+  if (!*any) return Q4_OK;
+  if ((st = check_rows("q", q, q_stride, q_heads, a.cache.head_dim)) != Q4_OK) return st;
+  if (!q_offsets || !kv_lens || !out || (!block_table && max_blocks > 0 && max_kv > 0))
+    return fail(Q4_ERR_NULL, "block_table, q_offsets, kv_lens, out must be non-NULL");
+  if (!aligned(out, 8) || !aligned(block_table, 4) || !aligned(q_offsets, 4) || !aligned(kv_lens, 4))
+    return fail(Q4_ERR_ALIGN, "out needs 8-byte, block_table, q_offsets and kv_lens 4-byte alignment");
+  a.q = q, a.q_stride = q_stride, a.block_table = block_table, a.max_blocks = (int)max_blocks;
+  a.q_offsets = q_offsets, a.kv_lens = kv_lens, a.seqs = (int)seqs, a.tokens = (int)tokens;
+  a.max_q = (int)std::min(max_q, tokens), a.max_kv = (int)max_kv, a.q_heads = q_heads;
+  a.scale = scale, a.window = (int)window, a.out = out;
+  return pick_attn(seqs, tokens, max_q, max_kv, q_heads, a.cache.kv_heads, a.cache.head_dim, a.cache.group, window, &a);
+}
+
+q4_status check_workspace(const void* workspace, size_t bytes, size_t need, const char* from) {
+  if (!workspace || bytes < need)
+    return fail(Q4_ERR_WORKSPACE, "this call needs %zu bytes of workspace (%s), got %zu", need, from,
+                workspace ? bytes : (size_t)0);
+  if (!aligned(workspace, 16)) return fail(Q4_ERR_ALIGN, "workspace needs 16-byte alignment");
+  return Q4_OK;
+}
+
+void place_parts(q4::AttnArgs* a, void* workspace) {
+  const size_t parts = attn_parts(*a);
+  a->part_o = static_cast<float*>(workspace);
+  a->part_ml = a->part_o + parts * a->cache.head_dim;
+  a->cuts = reinterpret_cast<int32_t*>(a->part_ml + 2 * parts);
+}
+
+// Shared prefixes: sizes beyond those of check_attn.
+q4_status check_prefix(int64_t groups, int64_t tokens, int64_t max_group_q, int64_t max_prefix, int32_t q_heads,
+                       int32_t kv_heads) {
+  if (groups < 0 || max_group_q < 0 || max_prefix < 0 || groups >= kMaxDim || max_group_q >= kMaxDim ||
+      max_prefix >= kMaxDim)
+    return fail(Q4_ERR_SHAPE, "groups=%lld, max_group_q=%lld, max_prefix=%lld out of range", (long long)groups,
+                (long long)max_group_q, (long long)max_prefix);
+  if (tokens * q_heads > 4 * kMaxGroups256)  // a wavefront a row joins the prefix's pieces
+    return fail(Q4_ERR_SHAPE, "tokens * q_heads = %lld: too many rows for one call", (long long)(tokens * q_heads));
+  return check_attn(groups, tokens, max_group_q, max_prefix, q_heads, kv_heads, 0);
+}
+bool has_prefix(int64_t groups, int64_t tokens, int64_t max_group_q, int64_t max_prefix) {
+  return groups > 0 && tokens > 0 && max_group_q > 0 && max_prefix > 0;
+}
+
+// Launch shape over the prefixes: 128 rows a workgroup, the keys of every job cut into as many pieces
+// as fill the chip, of 256 keys or more by the bound.
+q4_status pick_prefix(int64_t groups, int64_t tokens, int64_t max_group_q, int64_t max_prefix, int32_t q_heads,
+                      int32_t kv_heads, int32_t head_dim, int32_t group, q4::AttnArgs* p) {
+  const int64_t rows = std::min(max_group_q, tokens) * (q_heads / kv_heads);
+  const int64_t jobs = (rows + 127) / 128 * kv_heads * groups;
+  const int64_t slots = q4::prefix_attention_resident(head_dim, group);
+  const int64_t pieces = std::max<int64_t>(1, std::min(slots / jobs, (max_prefix + 255) / 256));
+  if (jobs * pieces > kMaxGroups256) return fail(Q4_ERR_SHAPE, "groups * heads * max_group_q too large for one call");
+  p->rows_group = 128, p->shares = 0, p->whole = 0, p->tail = (int)jobs, p->pieces = (int)pieces;
+  return Q4_OK;
+}
+
+// What each row starts from behind its prefix; then the partial results, whose place the two steps share.
+size_t start_bytes(int64_t tokens, int32_t q_heads, int32_t head_dim) {
+  return (size_t)q4::round_up(tokens * q_heads * (head_dim + 2) * 4, 256);
+}
+size_t shared_workspace(const q4::AttnArgs& a, const q4::AttnArgs& p, int64_t tokens, int32_t q_heads,
+                        int32_t head_dim) {
+  return start_bytes(tokens, q_heads, head_dim) + std::max(attn_workspace(a, head_dim), attn_workspace(p, head_dim));
+}
+
 }  // namespace
 
 extern "C" {
@@ -253,36 +333,82 @@ q4_status q4_paged_attention(const void* q, int64_t q_stride, const q4_paged_kv*
                              int64_t tokens, int64_t max_q, int64_t max_kv, int32_t q_heads, float scale,
                              int64_t window, void* out, void* workspace, size_t workspace_bytes, void* stream) {
   q4::AttnArgs a{};
-  q4_status st = check_paged(cache, &a.cache);
+  bool any = false;
+  q4_status st = attn_args(q, q_stride, cache, block_table, max_blocks, q_offsets, kv_lens, seqs, tokens, max_q, max_kv,
+                           q_heads, scale, window, out, &a, &any);
   if (st != Q4_OK) return st;
-  if ((st = check_attn(seqs, tokens, max_q, max_kv, q_heads, a.cache.kv_heads, window)) != Q4_OK) return st;
-  if (max_blocks < 0 || max_blocks >= kMaxDim)
-    return fail(Q4_ERR_SHAPE, "max_blocks=%lld out of range", (long long)max_blocks);
-  // times log2(e) it has to stay finite
-  if (!(scale > -2.0e38f && scale < 2.0e38f)) return fail(Q4_ERR_SHAPE, "scale must be within +-2e38");
-  if (seqs == 0 || tokens == 0 || max_q == 0) return ok();
-  if ((st = check_rows("q", q, q_stride, q_heads, a.cache.head_dim)) != Q4_OK) return st;
-  if (!q_offsets || !kv_lens || !out || (!block_table && max_blocks > 0 && max_kv > 0))
-    return fail(Q4_ERR_NULL, "block_table, q_offsets, kv_lens, out must be non-NULL");
-  if (!aligned(out, 8) || !aligned(block_table, 4) || !aligned(q_offsets, 4) || !aligned(kv_lens, 4))
-    return fail(Q4_ERR_ALIGN, "out needs 8-byte, block_table, q_offsets and kv_lens 4-byte alignment");
-  a.q = q, a.q_stride = q_stride, a.block_table = block_table, a.max_blocks = (int)max_blocks;
-  a.q_offsets = q_offsets, a.kv_lens = kv_lens, a.seqs = (int)seqs, a.tokens = (int)tokens;
-  a.max_q = (int)std::min(max_q, tokens), a.max_kv = (int)max_kv, a.q_heads = q_heads;
-  a.scale = scale, a.window = (int)window, a.out = out;
-  st = pick_attn(seqs, tokens, max_q, max_kv, q_heads, a.cache.kv_heads, a.cache.head_dim, a.cache.group, window, &a);
-  if (st != Q4_OK) return st;
+  if (!any) return ok();
   if (a.shares > 0 || a.tail > 0) {
-    const size_t parts = attn_parts(a), need = attn_workspace(a, a.cache.head_dim);
-    if (!workspace || workspace_bytes < need)
-      return fail(Q4_ERR_WORKSPACE, "this call needs %zu bytes of workspace (q4_paged_attention_workspace_bytes), got %zu",
-                  need, workspace ? workspace_bytes : (size_t)0);
-    if (!aligned(workspace, 16)) return fail(Q4_ERR_ALIGN, "workspace needs 16-byte alignment");
-    a.part_o = static_cast<float*>(workspace);
-    a.part_ml = a.part_o + parts * a.cache.head_dim;
-    a.cuts = reinterpret_cast<int32_t*>(a.part_ml + 2 * parts);
+    const size_t need = attn_workspace(a, a.cache.head_dim);
+    if ((st = check_workspace(workspace, workspace_bytes, need, "q4_paged_attention_workspace_bytes")) != Q4_OK) return st;
+    place_parts(&a, workspace);
   }
   return hip_status(q4::launch_attention(a, static_cast<hipStream_t>(stream)), "attention launch");
+}
+
+size_t q4_paged_attention_shared_workspace_bytes(int64_t seqs, int64_t groups, int64_t tokens, int64_t max_q,
+                                                 int64_t max_kv, int64_t max_group_q, int64_t max_prefix,
+                                                 int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t group) {
+  if (check_attn(seqs, tokens, max_q, max_kv, q_heads, kv_heads, 0) != Q4_OK) return 0;
+  if (check_prefix(groups, tokens, max_group_q, max_prefix, q_heads, kv_heads) != Q4_OK) return 0;
+  if (check_paged_dims(1, 16, kv_heads, head_dim, group) != Q4_OK) return 0;
+  q4::AttnArgs a{}, p{};
+  if (pick_attn(seqs, tokens, max_q, max_kv, q_heads, kv_heads, head_dim, group, 0, &a) != Q4_OK) return 0;
+  if (!has_prefix(groups, tokens, max_group_q, max_prefix)) return attn_workspace(a, head_dim);
+  if (pick_prefix(groups, tokens, max_group_q, max_prefix, q_heads, kv_heads, head_dim, group, &p) != Q4_OK) return 0;
+  return shared_workspace(a, p, tokens, q_heads, head_dim);
+}
+
+q4_status q4_paged_attention_shared(const void* q, int64_t q_stride, const q4_paged_kv* cache,
+                                    const int32_t* prefix_table, int64_t max_prefix_blocks,
+                                    const int32_t* prefix_lens, const int32_t* group_offsets, int64_t groups,
+                                    const int32_t* block_table, int64_t max_blocks, const int32_t* q_offsets,
+                                    const int32_t* kv_lens, int64_t seqs, int64_t tokens, int64_t max_q,
+                                    int64_t max_kv, int64_t max_group_q, int64_t max_prefix, int32_t q_heads,
+                                    float scale, void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  q4::AttnArgs a{};
+  bool any = false;
+  q4_status st = attn_args(q, q_stride, cache, block_table, max_blocks, q_offsets, kv_lens, seqs, tokens, max_q, max_kv,
+                           q_heads, scale, 0, out, &a, &any);
+  if (st != Q4_OK) return st;
+  if ((st = check_prefix(groups, tokens, max_group_q, max_prefix, q_heads, a.cache.kv_heads)) != Q4_OK) return st;
+  if (max_prefix_blocks < 0 || max_prefix_blocks >= kMaxDim)
+    return fail(Q4_ERR_SHAPE, "max_prefix_blocks=%lld out of range", (long long)max_prefix_blocks);
+  if (!any) return ok();
+  const bool prefix = has_prefix(groups, tokens, max_group_q, max_prefix);
+  q4::AttnArgs p = a;
+  size_t need = attn_workspace(a, a.cache.head_dim);
+  if (prefix) {
+    if (!prefix_lens || !group_offsets || (!prefix_table && max_prefix_blocks > 0))
+      return fail(Q4_ERR_NULL, "prefix_table, prefix_lens, group_offsets must be non-NULL");
+    if (!aligned(prefix_table, 4) || !aligned(prefix_lens, 4) || !aligned(group_offsets, 4))
+      return fail(Q4_ERR_ALIGN, "prefix_table, prefix_lens and group_offsets need 4-byte alignment");
+    p.block_table = prefix_table, p.max_blocks = (int)max_prefix_blocks, p.kv_lens = prefix_lens;
+    p.group_offsets = group_offsets, p.members = a.seqs, p.seqs = (int)groups;
+    p.max_q = (int)std::min(max_group_q, tokens), p.max_kv = (int)max_prefix;
+    st = pick_prefix(groups, tokens, max_group_q, max_prefix, q_heads, a.cache.kv_heads, a.cache.head_dim,
+                     a.cache.group, &p);
+    if (st != Q4_OK) return st;
+    need = shared_workspace(a, p, tokens, q_heads, a.cache.head_dim);
+  }
+  if (need > 0) {
+    st = check_workspace(workspace, workspace_bytes, need, "q4_paged_attention_shared_workspace_bytes");
+    if (st != Q4_OK) return st;
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (!prefix) {
+    place_parts(&a, workspace);
+    return hip_status(q4::launch_attention(a, s), "attention launch");
+  }
+  // the rows' starts, then the partial results of one step after the other
+  unsigned char* parts = static_cast<unsigned char*>(workspace) + start_bytes(tokens, q_heads, a.cache.head_dim);
+  p.init_o = a.init_o = static_cast<float*>(workspace);
+  p.init_ml = a.init_ml = a.init_o + tokens * q_heads * a.cache.head_dim;
+  place_parts(&p, parts);
+  place_parts(&a, parts);
+  hipError_t e = q4::launch_prefix_attention(p, s);
+  if (e == hipSuccess) e = q4::launch_behind_attention(a, s);
+  return hip_status(e, "attention with shared prefixes launch");
 }
 
 }  // extern "C"

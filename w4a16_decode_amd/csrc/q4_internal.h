@@ -134,6 +134,13 @@ struct AttnArgs {
   float* part_o;   // partial results: float32 [shares][2][rows_group] or [pieces][tail][128], [head_dim]
   float* part_ml;  // and as many [2]: what exponents are relative to, sum
   int32_t* cuts;   // shares > 0: int32 [shares][8], the job a share begins and does not end
+  // shared prefixes: the sequences are groups, group g's members group_offsets[g] .. [g + 1] - 1 of `members`
+  const int32_t* group_offsets;
+  int members;
+  // what rows behind a prefix start from: float32 [tokens][q_heads][head_dim] and [tokens][q_heads][2], the
+  // logarithm (base 2) of the sum of weights and 1 (0: no prefix, below 0: one of scores of -infinity only)
+  float* init_o;
+  float* init_ml;
 };
 
 // Whether tiles of 32 rows whose wavefronts split the keys are built: 256 channels, or four
@@ -203,6 +210,11 @@ struct LoraArgs {
 int lora_splits(int K);  // slices of the channel range of A x
 hipError_t launch_lora(const LoraArgs& a, hipStream_t stream);
 hipError_t launch_attention(const AttnArgs& a, hipStream_t stream);
+// Attention over shared prefixes into init_o and init_ml (rows_group 128, all jobs cut into `pieces`), and
+// over the keys behind them from there.
+hipError_t launch_prefix_attention(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_behind_attention(const AttnArgs& a, hipStream_t stream);
+int prefix_attention_resident(int head_dim, int group);
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
 hipError_t launch_paged_dequant(const PagedArgs& c, const int32_t* slots, int64_t tokens, void* k_out, void* v_out,
                                 hipStream_t stream);
