@@ -78,7 +78,8 @@ q4_status q4_paged_plan(const int32_t* kv_lens, const int32_t* new_lens, const i
  * ceil(log2(vocab))) of the largest a step (2^-45 for 131072 tokens), so that sums are exact
  * in any order and the choice is that of 64-bit arithmetic but where u * total or a cut
  * comes within about 1e-12 of a border; a token whose weight rounds to 0 is never drawn.
- * Deterministic. vocab <= 2^20, rows < 2^22. `workspace` (16-byte aligned) must hold
+ * Deterministic. vocab <= 2^20, rows < 2^22, rows *
+ * ceil(vocab / 4096) < 2^24 (Q4_ERR_SHAPE). `workspace` (16-byte aligned) must hold
  * q4_sample_workspace_bytes() bytes (NULL when that is 0). */
 typedef enum { Q4_F16 = 0, Q4_BF16 = 1, Q4_F32 = 2 } q4_dtype;
 

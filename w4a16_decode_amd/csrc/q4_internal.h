@@ -185,9 +185,19 @@ struct SampleArgs {
   const float* min_p;
   int32_t* tokens;
   float* probs;
-  int shift;  // fractional bits of the weights
+  int shift;   // fractional bits of the weights
+  int chunks;  // of kSampleChunk logits, a row
+  // workspace
+  float* tops;                   // [rows][chunks]: largest logits
+  unsigned long long* bins;      // [rows][kSampleBins]: weights or tokens by bin; NULL without top-k and top-p
+  unsigned long long* sums;      // [rows][chunks]: weights before the cut's bin
+  unsigned long long* cut_sums;  // [rows][2]: the sum before the cut's first bin, and the one it is to reach
+  int4* cuts;                    // [rows]: the cut's first and last bin
+  int32_t* counts;               // [rows][chunks]: tokens in those bins
+  uint16_t* list;                // [rows][chunks][kSampleChunk]: which
 };
 
+constexpr int kSampleChunk = 4096, kSampleBins = 1024, kSampleMaxChunks = 256;
 hipError_t launch_sample(const SampleArgs& a, hipStream_t stream);
 
 // Adapters beside a product (include/q4_lora.h). phase 0: A x into t; phase 1: y from the

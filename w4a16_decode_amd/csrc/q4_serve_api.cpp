@@ -1,6 +1,7 @@
 // C ABI front end of the serving loop's calls (include/q4_serve.h): argument validation on
 // the host, before any HIP call.
 #include <algorithm>
+#include <type_traits>
 
 #include <hip/hip_runtime.h>
 
@@ -23,6 +24,32 @@ int weight_shift(int64_t vocab) {
   int bits = 0;
   while ((int64_t(1) << bits) < vocab) ++bits;
   return std::min(50, 62 - bits);
+}
+
+int64_t sample_chunks(int64_t vocab) { return (vocab + q4::kSampleChunk - 1) / q4::kSampleChunk; }
+
+q4_status check_sample(int64_t rows, int64_t vocab) {
+  if (rows < 0 || rows >= kMaxRows || vocab <= 0 || vocab > kMaxVocab || rows * sample_chunks(vocab) > q4::kMaxGroups256)
+    return fail(Q4_ERR_SHAPE, "rows=%lld, vocab=%lld out of range", (long long)rows, (long long)vocab);
+  return Q4_OK;
+}
+
+// The workspace's parts, from `base` on (NULL: their size alone), the widest elements first.
+size_t place_sample(q4::SampleArgs* a, unsigned char* base) {
+  const size_t rows = a->rows, all = rows * a->chunks;
+  size_t at = 0;
+  auto part = [&](auto** p, size_t n) {
+    *p = reinterpret_cast<std::remove_reference_t<decltype(*p)>>(base + at);
+    at += (n * sizeof(**p) + 15) / 16 * 16;
+  };
+  part(&a->cuts, rows);
+  part(&a->bins, rows * q4::kSampleBins);
+  part(&a->sums, all);
+  part(&a->cut_sums, 2 * rows);
+  part(&a->tops, all);
+  part(&a->counts, all);
+  part(&a->list, all * q4::kSampleChunk);
+  return at;
 }
 
 }  // namespace
@@ -73,7 +100,12 @@ q4_status q4_paged_plan(const int32_t* kv_lens, const int32_t* new_lens, const i
   return hip_status(q4::launch_plan(a, static_cast<hipStream_t>(stream)), "plan launch");
 }
 
-size_t q4_sample_workspace_bytes(int64_t rows, int64_t vocab) { return 0; }
+size_t q4_sample_workspace_bytes(int64_t rows, int64_t vocab) {
+  if (check_sample(rows, vocab) != Q4_OK) return 0;
+  q4::SampleArgs a{};
+  a.rows = (int)rows, a.chunks = (int)sample_chunks(vocab);
+  return place_sample(&a, nullptr);
+}
 
 q4_status q4_sample(const void* logits, int32_t dtype, int64_t stride, int64_t rows, int64_t vocab,
                     const float* uniforms, const float* temperature, const int32_t* top_k, const float* top_p,
@@ -81,8 +113,8 @@ q4_status q4_sample(const void* logits, int32_t dtype, int64_t stride, int64_t r
                     void* stream) {
   if (dtype != Q4_F16 && dtype != Q4_BF16 && dtype != Q4_F32)
     return fail(Q4_ERR_UNSUPPORTED, "dtype=%d: logits are float16, bfloat16 or float32", (int)dtype);
-  if (rows < 0 || rows >= kMaxRows || vocab <= 0 || vocab > kMaxVocab)
-    return fail(Q4_ERR_SHAPE, "rows=%lld, vocab=%lld out of range", (long long)rows, (long long)vocab);
+  q4_status st = check_sample(rows, vocab);
+  if (st != Q4_OK) return st;
   if (rows > 1 && (stride < vocab || stride >= (int64_t(1) << 40)))
     return fail(Q4_ERR_SHAPE, "stride %lld is not in [vocab, 2^40)", (long long)stride);
   if (rows == 0) return ok();
@@ -95,6 +127,13 @@ q4_status q4_sample(const void* logits, int32_t dtype, int64_t stride, int64_t r
   a.rows = (int)rows, a.vocab = (int)vocab;
   a.uniforms = uniforms, a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p;
   a.tokens = tokens, a.probs = probs, a.shift = weight_shift(vocab);
+  a.chunks = (int)sample_chunks(vocab);
+  const size_t need = place_sample(&a, static_cast<unsigned char*>(workspace));
+  if (!workspace || workspace_bytes < need)
+    return fail(Q4_ERR_WORKSPACE, "this shape needs %zu bytes of workspace (q4_sample_workspace_bytes), got %zu", need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (!aligned(workspace, 16)) return fail(Q4_ERR_ALIGN, "workspace needs 16-byte alignment");
+  if (!top_k && !top_p) a.bins = nullptr;
   return hip_status(q4::launch_sample(a, static_cast<hipStream_t>(stream)), "sample launch");
 }
 
