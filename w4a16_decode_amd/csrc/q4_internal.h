@@ -186,7 +186,7 @@ struct SampleArgs {
   int32_t* tokens;
   float* probs;
   int shift;   // fractional bits of the weights
-  int chunks;  // of kSampleChunk logits, a row
+  int chunks;  // of kSampleChunk logits, a row; 0: a workgroup takes a whole row
   // workspace
   float* tops;                   // [rows][chunks]: largest logits
   unsigned long long* bins;      // [rows][kSampleBins]: weights or tokens by bin; NULL without top-k and top-p
@@ -197,7 +197,7 @@ struct SampleArgs {
   uint16_t* list;                // [rows][chunks][kSampleChunk]: which
 };
 
-constexpr int kSampleChunk = 4096, kSampleBins = 1024, kSampleMaxChunks = 256;
+constexpr int kSampleChunk = 4096, kSampleBins = 1024, kSampleMaxChunks = 256, kSampleWhole = 32768;
 hipError_t launch_sample(const SampleArgs& a, hipStream_t stream);
 
 // Adapters beside a product (include/q4_lora.h). phase 0: A x into t; phase 1: y from the

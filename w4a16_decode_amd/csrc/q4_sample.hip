@@ -1,21 +1,24 @@
 // The next tokens from rows of logits (include/q4_serve.h).
 //
 // Weights are whole numbers: w_i = rint(2^shift exp((l_i - m) / T)) in 64 bits, a row's sum below
-// 2^63. Their sums are exact, so any split of a row over workgroups and any order of additions
-// (atomics among them) give the same cuts and the same token.
+// 2^63. Their sums are exact, so any split of a row over threads and workgroups and any order of
+// additions (atomics among them) give the same cuts and the same token.
 //
-// A row is split into chunks of 4096 logits, a workgroup each. Four launches, each a pass over
-// what the one before left (the last three read the logits from the caches):
+// Cuts. The sums of a row's weights (top-p) or tokens (top-k) by the weight's logarithm, 1024 bins,
+// say which bin a cut falls into; only the tokens of that bin are listed and ranked. Ranks go by
+// key = (descending logit, ascending index) in 64 bits, without ties: digit by digit from the
+// first one that differs, sums over the tokens that share the digits found so far by their next
+// one. With top-k and top-p both, top-p's total is that of the tokens top-k left, so the list
+// holds all tokens down to top-k's bin.
+//
+// A workgroup a row, in one launch, holds up to 32768 logits in registers. Longer rows are split into
+// chunks of 4096 logits, a workgroup each, in four launches, each a pass over what the one before
+// left (the last three read the logits from the caches):
 //   tops    the chunks' largest logits;
-//   bins    the row's weights (top-p) or tokens (top-k) by the weight's logarithm, 1024 bins: the
-//           bin that a cut falls into follows from their sums alone. Left out without cuts;
-//   sums    per chunk the sum of the weights before that bin, and a list of the tokens in it;
+//   bins    the sums by bin. Left out without top-k and top-p;
+//   sums    per chunk the sum of the weights before the cut's bin, and the list;
 //   choose  a workgroup a row: the cut inside the bin, the chunk that the draw falls into, and
 //           the token in it.
-// Cuts inside a bin go by rank, key = (descending logit, ascending index) in 64 bits, without
-// ties: digit by digit from the first one that differs, sums over the tokens that share the digits
-// found so far by their next one. With top-k and top-p both, top-p's total is that of
-// the tokens top-k left, so the list holds all tokens down to top-k's bin.
 #include "q4_device.h"
 #include "q4_internal.h"
 
@@ -24,11 +27,82 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kChunk = kSampleChunk, kThreads = 256, kGroups = kChunk / kThreads / 4;
-constexpr int kChoose = 512;                  // threads of the last launch
-constexpr int kHeld = 8;                      // listed tokens one of its threads holds
-constexpr int kBins = kSampleBins, kDigits = 256;
+constexpr int kChunk = kSampleChunk, kThreads = 256, kRun = kChunk / kThreads;
+constexpr int kChoose = 512;   // threads of the last launch
+constexpr int kWhole = 1024;   // threads of the launch that takes whole rows
+constexpr int kList = 4096;    // listed tokens that a workgroup holds in registers
+constexpr int kBins = kSampleBins, kDigits = 256, kRounds = 8;
 
+// ---- across the wavefront -----------------------------------------------------------
+// Sums and maxima through DPP: rows of 16 lanes by shifts of 1, 2, 4, 8, then lane 15 of a row and
+// lane 31 passed on (about 8 cycles a step; through the LDS crossbar it is over 60).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp(uint32_t old, uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)v, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ u64 plus_dpp(u64 v) {
+  return v + ((u64)dpp<CTRL, ROWS>(0, (uint32_t)(v >> 32)) << 32 | dpp<CTRL, ROWS>(0, (uint32_t)v));
+}
+__device__ __forceinline__ u64 wave_scan(u64 v) {  // inclusive
+  v = plus_dpp<0x111, 0xF>(v);
+  v = plus_dpp<0x112, 0xF>(v);
+  v = plus_dpp<0x114, 0xF>(v);
+  v = plus_dpp<0x118, 0xF>(v);
+  v = plus_dpp<0x142, 0xA>(v);
+  return plus_dpp<0x143, 0xC>(v);
+}
+__device__ __forceinline__ u64 lane_of(u64 v, int lane) {
+  return (u64)(uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane) << 32 |
+         (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float max_dpp(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  return fmaxf(v, __builtin_bit_cast(float, dpp<CTRL, ROWS>(b, b)));
+}
+__device__ __forceinline__ float wave_max(float v) {  // in every lane
+  v = max_dpp<0x111, 0xF>(v);
+  v = max_dpp<0x112, 0xF>(v);
+  v = max_dpp<0x114, 0xF>(v);
+  v = max_dpp<0x118, 0xF>(v);
+  v = max_dpp<0x142, 0xA>(v);
+  v = max_dpp<0x143, 0xC>(v);
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 63));
+}
+__device__ __forceinline__ uint32_t wave_or(uint32_t v) {  // in lane 63
+  v |= dpp<0x111, 0xF>(0, v);
+  v |= dpp<0x112, 0xF>(0, v);
+  v |= dpp<0x114, 0xF>(0, v);
+  v |= dpp<0x118, 0xF>(0, v);
+  v |= dpp<0x142, 0xA>(0, v);
+  return v | dpp<0x143, 0xC>(0, v);
+}
+
+// ---- across the workgroup: each call has its own LDS, so one barrier is enough ------------
+template <int N>
+struct Scan {
+  u64 wave[N / kWave];
+};
+// Sum of the values of the threads before this one; *total: of all.
+template <int N>
+__device__ __forceinline__ u64 block_scan(u64 v, Scan<N>& s, u64* total) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const u64 incl = wave_scan(v);
+  if (lane == kWave - 1) s.wave[wave] = incl;
+  __syncthreads();
+  u64 before = incl - v, all = 0;
+#pragma unroll
+  for (int w = 0; w < N / kWave; ++w) {
+    const u64 x = s.wave[w];
+    if (w < wave) before += x;
+    all += x;
+  }
+  *total = all;
+  return before;
+}
+
+// ---- logits ------------------------------------------------------------------------
 __device__ __forceinline__ float clean(float v) {  // no NaN, one zero
   return v == v ? v + 0.0f : -__builtin_inff();
 }
@@ -41,24 +115,28 @@ __device__ __forceinline__ float load_one(const void* p, int64_t i) {
   return clean(static_cast<const float*>(p)[i]);
 }
 
-// Logits i .. i + 3 (rows may start at any element: the loads promise no more); -infinity behind the end.
-template <int DT>
-__device__ __forceinline__ void load_four(const void* p, int i, int vocab, float (&v)[4]) {
-  if (i + 4 <= vocab) {
-    if constexpr (DT == 2) {
-      float4_t x;
-      __builtin_memcpy(&x, static_cast<const float*>(p) + i, 16);
+// Logits i .. i + N - 1 (rows may start at any element: the loads promise no more); -infinity behind the end.
+template <int DT, int N>
+__device__ __forceinline__ void load_run(const void* p, int i, int vocab, float (&v)[N]) {
+  if (i + N <= vocab) {
+    constexpr int kPiece = DT == 2 || N == 4 ? 4 : 8;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = clean(x[e]);
-    } else {
-      uint16_t x[4];
-      __builtin_memcpy(x, static_cast<const uint16_t*>(p) + i, 8);
+    for (int j = 0; j < N; j += kPiece) {
+      if constexpr (DT == 2) {
+        float4_t x;
+        __builtin_memcpy(&x, static_cast<const float*>(p) + i + j, 16);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = clean(DT == 1 ? bf16(x[e]) : (float)__builtin_bit_cast(_Float16, x[e]));
+        for (int e = 0; e < 4; ++e) v[j + e] = clean(x[e]);
+      } else {
+        uint16_t x[kPiece];
+        __builtin_memcpy(x, static_cast<const uint16_t*>(p) + i + j, 2 * kPiece);
+#pragma unroll
+        for (int e = 0; e < kPiece; ++e) v[j + e] = clean(DT == 1 ? bf16(x[e]) : (float)__builtin_bit_cast(_Float16, x[e]));
+      }
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = i + e < vocab ? load_one<DT>(p, i + e) : -__builtin_inff();
+    for (int e = 0; e < N; ++e) v[e] = i + e < vocab ? load_one<DT>(p, i + e) : -__builtin_inff();
   }
 }
 
@@ -71,7 +149,9 @@ __device__ __forceinline__ u64 rank_key(float v, int i) {
   const uint32_t u = __builtin_bit_cast(uint32_t, v);
   return (u64)~(u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u)) << 32 | (uint32_t)i;
 }
+constexpr int kIndexBits = 20;  // of a key
 
+// ---- weights ------------------------------------------------------------------------
 // A row's settings. Greedy (temperature <= 0): only the largest logits have weight, and the draw is 0.
 struct Row {
   float top;     // largest logit
@@ -82,6 +162,7 @@ struct Row {
   bool cut_p, greedy;
   double p;
   u64 w_min;  // smallest weight that min-p leaves
+  __device__ __forceinline__ bool cuts() const { return k > 0 || cut_p; }
 };
 
 __device__ __forceinline__ Row row_settings(const SampleArgs& a, int row, float top) {
@@ -97,20 +178,20 @@ __device__ __forceinline__ Row row_settings(const SampleArgs& a, int row, float 
   r.p = a.top_p ? (double)a.top_p[row] : 1.0;
   r.cut_p = !r.greedy && r.p < 1.0;
   const double pm = a.min_p ? (double)a.min_p[row] : 0.0;
-  r.w_min = pm > 0.0 ? (u64)ceil(ldexp(pm < 1.0 ? pm : 1.0, a.shift)) : 1;
+  r.w_min = pm > 0.0 ? (u64)ceil(ldexp(pm < 1.0 ? pm : 1.0, a.shift)) : 0;
   return r;
 }
 
-// log2 of the weight; below -1 (or NaN, where an infinity met a zero): no weight.
+// log2 of the weight; up to -1 (or NaN, where an infinity met a zero): no weight.
 __device__ __forceinline__ double exponent(const Row& r, float v) {
   return v == r.top ? r.shift : __builtin_fma((double)v - (double)r.top, r.slope, r.shift);
 }
+__device__ __forceinline__ bool has_weight(double z) { return z > -1.0; }
 
-// rint(2^z), -1 <= z <= 50: with k = rint(256 z), 2^(k / 256) from the table and 2^(z - k / 256) by its
-// series to the fourth power, whose next term is below 2^-54; the whole is within 2^-50 of
-// itself before the rounding.
+// rint(2^z), 1 or more, for -1 < z <= 50: with k = rint(256 z), 2^(k / 256) from the table and
+// 2^(z - k / 256) by its series to the fourth power, whose next term is below 2^-54; the whole is
+// within 2^-50 of itself before the rounding.
 __device__ __forceinline__ u64 weight_of(double z, const double* table) {
-  if (!(z >= -1.0)) return 0;
   constexpr double kMagic = 26388279066624.0;  // 1.5 * 2^44: the sum's last bit is 1/256
   const double m = z + kMagic;
   const int k = (int)(uint32_t)__builtin_bit_cast(u64, m);
@@ -120,108 +201,19 @@ __device__ __forceinline__ u64 weight_of(double z, const double* table) {
   s = __builtin_fma(x, s, 1.0);
   s = __builtin_fma(x, s, 1.0);
   const double w = ldexp(table[k & 255] * s, k >> 8);
-  return __builtin_bit_cast(u64, w + 4503599627370496.0) & 0xFFFFFFFFFFFFFull;  // + 2^52: rounded to a whole number
+  // + 2^52: rounded to a whole number, which is in the low bits
+  const u64 n = __builtin_bit_cast(u64, w + 4503599627370496.0) & 0xFFFFFFFFFFFFFull;
+  return n > 0 ? n : 1;
+}
+template <int N>
+__device__ __forceinline__ void fill_table(double* table) {
+  if (N == 256 || threadIdx.x < 256) table[threadIdx.x] = exp2((double)threadIdx.x / 256);
 }
 __device__ __forceinline__ int bin_of(const Row& r, double z) {  // of a token with weight
   return min(kBins - 1, (int)((float)(r.shift - z) * r.bin_scale));
 }
 
-template <int N>
-struct Scan {
-  u64 wave[N / kWave];
-};
-
-// Sum of the values of the threads before this one; *total: of all.
-template <int N>
-__device__ __forceinline__ u64 block_scan(u64 v, Scan<N>& s, u64* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  u64 incl = v;
-#pragma unroll
-  for (int m = 1; m < kWave; m <<= 1) {
-    const u64 up = __shfl_up(incl, m, 64);
-    if (lane >= m) incl += up;
-  }
-  if (lane == kWave - 1) s.wave[wave] = incl;
-  __syncthreads();
-  u64 before = incl - v, all = 0;
-#pragma unroll
-  for (int w = 0; w < N / kWave; ++w) {
-    const u64 x = s.wave[w];
-    if (w < wave) before += x;
-    all += x;
-  }
-  __syncthreads();  // s may be written again
-  *total = all;
-  return before;
-}
-
-template <int N>
-__device__ __forceinline__ float block_max(float v, float* wave) {
-#pragma unroll
-  for (int m = 1; m < kWave; m <<= 1) v = fmaxf(v, __shfl_xor(v, m, 64));
-  if ((threadIdx.x & 63) == 0) wave[threadIdx.x >> 6] = v;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < N / kWave; ++w) v = fmaxf(v, wave[w]);
-  return v;
-}
-
-// Largest logit of a row from its chunks'.
-template <int N>
-__device__ __forceinline__ float row_top(const SampleArgs& a, int row, float* wave) {
-  float v = -__builtin_inff();
-  for (int c = threadIdx.x; c < a.chunks; c += N) v = fmaxf(v, a.tops[(int64_t)row * a.chunks + c]);
-  return block_max<N>(v, wave);
-}
-
-template <int DT>
-__global__ __launch_bounds__(kThreads) void tops_kernel(SampleArgs a) {
-  __shared__ float wave[kThreads / kWave];
-  const int row = (int)(blockIdx.x / (unsigned)a.chunks), chunk = (int)(blockIdx.x - (unsigned)row * a.chunks);
-  const void* p = row_of(a, row, DT);
-  float top = -__builtin_inff();
-#pragma unroll
-  for (int j = 0; j < kGroups; ++j) {
-    float v[4];
-    load_four<DT>(p, chunk * kChunk + (j * kThreads + (int)threadIdx.x) * 4, a.vocab, v);
-    top = fmaxf(fmaxf(fmaxf(top, v[0]), fmaxf(v[1], v[2])), v[3]);
-  }
-  top = block_max<kThreads>(top, wave);
-  if (threadIdx.x == 0) a.tops[blockIdx.x] = top;
-  // the row's bins, for the next launch
-  if (a.bins)
-    for (int b = chunk * kThreads + (int)threadIdx.x; b < kBins; b += a.chunks * kThreads)
-      a.bins[(int64_t)row * kBins + b] = 0;
-}
-
-template <int DT>
-__global__ __launch_bounds__(kThreads) void bins_kernel(SampleArgs a) {
-  __shared__ float wave[kThreads / kWave];
-  __shared__ double table[256];
-  __shared__ u64 bins[kBins];
-  const int row = (int)(blockIdx.x / (unsigned)a.chunks), chunk = (int)(blockIdx.x - (unsigned)row * a.chunks);
-  const void* p = row_of(a, row, DT);
-  float v[kGroups][4];
-#pragma unroll
-  for (int j = 0; j < kGroups; ++j)
-    load_four<DT>(p, chunk * kChunk + (j * kThreads + (int)threadIdx.x) * 4, a.vocab, v[j]);
-  table[threadIdx.x] = exp2((double)threadIdx.x / 256);
-  for (int b = threadIdx.x; b < kBins; b += kThreads) bins[b] = 0;
-  const Row r = row_settings(a, row, row_top<kThreads>(a, row, wave));  // (a barrier)
-  if (r.k == 0 && !r.cut_p) return;
-#pragma unroll
-  for (int j = 0; j < kGroups; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const double z = exponent(r, v[j][e]);
-      const u64 w = weight_of(z, table);
-      if (w > 0) atomicAdd(&bins[bin_of(r, z)], r.k > 0 ? 1 : w);
-    }
-  __syncthreads();
-  for (int b = threadIdx.x; b < kBins; b += kThreads)
-    if (bins[b] > 0) atomicAdd(a.bins + (int64_t)row * kBins + b, bins[b]);
-}
-
+// ---- cuts -----------------------------------------------------------------------------
 // Bins that a row's cuts need a closer look at: first .. last are listed, those before stay whole, and what
 // comes before `first` in the sum that the cut goes by.
 struct Cut {
@@ -230,21 +222,22 @@ struct Cut {
   u64 target;  // the cut goes after the token with which the sum reaches it; 0: nothing is cut
 };
 
+__device__ __forceinline__ u64 part_of(double p, u64 total) {
+  const double part = ceil(p * (double)total);
+  const u64 t = part >= 1.0 ? (u64)part : 1;
+  return t < total ? t : total;
+}
+
 template <int N>
-__device__ __forceinline__ Cut find_cut(const SampleArgs& a, const Row& r, int row, Scan<N>& s, u64* found) {
-  if (r.k == 0 && !r.cut_p) return Cut{kBins, -1, 0, 0};
+__device__ __forceinline__ Cut find_cut(const Row& r, const u64* bins, Scan<N>& s, u64* found) {
+  if (!r.cuts()) return Cut{kBins, -1, 0, 0};
   constexpr int kPer = kBins / N;
   u64 own[kPer], sum = 0, total;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) sum += own[i] = a.bins[(int64_t)row * kBins + threadIdx.x * kPer + i];
+  for (int i = 0; i < kPer; ++i) sum += own[i] = bins[threadIdx.x * kPer + i];
   u64 before = block_scan<N>(sum, s, &total);
-  u64 target = (u64)r.k;
-  if (r.k == 0) {
-    const double part = ceil(r.p * (double)total);
-    target = part >= 1.0 ? (u64)part : 1;
-  }
-  const bool all = r.k > 0 && target >= total;  // top-k leaves every token that has weight
-  target = target < total ? target : total;
+  const bool all = r.k > 0 && (u64)r.k >= total;  // top-k leaves every token that has weight
+  const u64 target = r.k > 0 ? (all ? total : (u64)r.k) : part_of(r.p, total);
   if (target > before && target <= before + sum) {
     int i = 0;
 #pragma unroll
@@ -261,224 +254,434 @@ __device__ __forceinline__ Cut find_cut(const SampleArgs& a, const Row& r, int r
   return all ? Cut{kBins, -1, 0, 0} : Cut{at, at, found[1], target};
 }
 
+struct Digits {
+  u64 sums[kRounds][kDigits];
+  uint32_t counts[kRounds][kDigits];
+  u64 key;
+  uint32_t differ;
+};
+
+// Smallest key up to which the listed tokens with keys <= last add up to `target` or more
+// (1 <= target <= their total). each(f): f(key, weight) for this thread's; ONES: a token counts 1.
+template <int N, bool ONES, typename Each>
+__device__ __forceinline__ u64 select_key(const Row& r, u64 last, u64 target, Digits& s, Each each) {
+  const int lane = threadIdx.x & 63;
+  __syncthreads();  // an earlier cut has been read
+  for (int i = threadIdx.x; i < kRounds * kDigits; i += N) {
+    (&s.sums[0][0])[i] = 0;
+    (&s.counts[0][0])[i] = 0;
+  }
+  if (threadIdx.x == 0) s.differ = 0;
+  __syncthreads();
+  // the first digit that differs, from the largest logit's key
+  const uint32_t first = (uint32_t)(rank_key(r.top, 0) >> 32);
+  uint32_t differ = 0;
+  each([&](u64 key, u64) __attribute__((always_inline)) { differ |= key <= last ? (uint32_t)(key >> 32) ^ first : 0; });
+  differ = wave_or(differ);
+  if (lane == kWave - 1 && differ) atomicOr(&s.differ, differ);
+  __syncthreads();
+  differ = s.differ;
+  int bit = differ ? 64 - __builtin_clz(differ) : kIndexBits;  // digits from this bit down
+  u64 prefix = bit < 64 ? ((u64)first << 32) >> bit << bit : 0, before = 0;
+  for (int round = 0; bit > 0; ++round) {
+    // a digit does not reach from the logit into the index
+    const int floor = bit > 32 ? 32 : 0, width = min(bit - floor, 8), at = bit - width;
+    each([&](u64 key, u64 w) __attribute__((always_inline)) {
+      if (key > last || (bit < 64 && (key ^ prefix) >> bit != 0)) return;
+      const int d = (int)(key >> at) & ((1 << width) - 1);
+      if (!ONES) atomicAdd(&s.sums[round][d], w);
+      atomicAdd(&s.counts[round][d], 1u);
+    });
+    __syncthreads();
+    // every wavefront for itself: four digits a lane
+    u64 own[4], sum = 0;
+    uint32_t count[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      count[i] = s.counts[round][4 * lane + i];
+      sum += own[i] = ONES ? (u64)count[i] : s.sums[round][4 * lane + i];
+    }
+    u64 upto = before + wave_scan(sum) - sum;
+    const bool here = target > upto && target <= upto + sum;
+    int digit = 4 * lane;
+    uint32_t n = count[0];
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (here && digit == 4 * lane + i && target > upto + own[i]) upto += own[i], ++digit, n = count[i + 1];
+    const int l = __builtin_ctzll(__ballot(here));
+    prefix |= (u64)(uint32_t)__builtin_amdgcn_readlane(digit, l) << at;
+    before = lane_of(upto, l);
+    bit = at == 32 ? kIndexBits : at;
+    if (bit == 0 || at == 0) break;
+    if (__builtin_amdgcn_readlane((int)n, l) == 1) {  // the token itself
+      each([&](u64 key, u64) __attribute__((always_inline)) {
+        if (key <= last && (key ^ prefix) >> at == 0) s.key = key;
+      });
+      __syncthreads();
+      return s.key;
+    }
+  }
+  return prefix;
+}
+
+// Key of the last token that top-k and top-p leave of the listed ones. kept(key, w): each that min-p leaves too.
+template <int N, typename Each, typename Kept>
+__device__ __forceinline__ u64 cut_list(const Row& r, const Cut& cut, Digits& s, Scan<N>& scan, Each each, Kept kept) {
+  u64 last = ~0ull;
+  if (r.k > 0 && cut.target > 0) last = select_key<N, true>(r, last, cut.target - cut.before, s, each);
+  if (r.cut_p) {
+    u64 target = cut.target - cut.before;
+    if (r.k > 0) {
+      u64 sum = 0, total;
+      each([&](u64 key, u64 w) __attribute__((always_inline)) { sum += key <= last ? w : 0; });
+      block_scan<N>(sum, scan, &total);
+      target = part_of(r.p, total);
+    }
+    last = select_key<N, false>(r, last, target, s, each);
+  }
+  each([&](u64 key, u64 w) __attribute__((always_inline)) {
+    if (key <= last && w >= r.w_min) kept(key, w);
+  });
+  return last;
+}
+
+// The same with the listed tokens token_at(0) .. token_at(count - 1): in registers, or where they are too
+// many read again each time.
+template <int N, int DT, typename TokenAt, typename Kept>
+__device__ __forceinline__ u64 cut_tokens(const Row& r, const void* p, const Cut& cut, int count, const double* table,
+                                          Digits& s, Scan<N>& scan, TokenAt token_at, Kept kept) {
+  constexpr int kHeld = kList / N;
+  auto look = [&](int n, u64* key, u64* w) __attribute__((always_inline)) {
+    const int token = token_at(n);
+    const float v = load_one<DT>(p, token);
+    *key = rank_key(v, token);
+    *w = weight_of(exponent(r, v), table);
+  };
+  if (count <= N) {
+    u64 key = 0, w = 0;
+    const bool any = (int)threadIdx.x < count;
+    if (any) look(threadIdx.x, &key, &w);
+    return cut_list<N>(r, cut, s, scan, [&](auto f) __attribute__((always_inline)) { if (any) f(key, w); }, kept);
+  }
+  if (count <= kList) {
+    u64 keys[kHeld], weights[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i * N + (int)threadIdx.x < count) look(i * N + threadIdx.x, &keys[i], &weights[i]);
+    return cut_list<N>(r, cut, s, scan, [&](auto f) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < kHeld; ++i)
+        if (i * N + (int)threadIdx.x < count) f(keys[i], weights[i]);
+    }, kept);
+  }
+  return cut_list<N>(r, cut, s, scan, [&](auto f) __attribute__((always_inline)) {
+    for (int n = threadIdx.x; n < count; n += N) {
+      u64 key, w;
+      look(n, &key, &w);
+      f(key, w);
+    }
+  }, kept);
+}
+
+// Weight of a token that the cuts left, else 0.
+__device__ __forceinline__ u64 kept_weight(const Row& r, const Cut& cut, u64 last, float v, int i, const double* table) {
+  const double z = exponent(r, v);
+  if (!has_weight(z)) return 0;
+  if (cut.last >= 0) {
+    const int bin = bin_of(r, z);
+    if (bin > cut.last || (bin >= cut.first && rank_key(v, i) > last)) return 0;
+  }
+  const u64 w = weight_of(z, table);
+  return w >= r.w_min ? w : 0;
+}
+
+__device__ __forceinline__ u64 draw_of(const SampleArgs& a, const Row& r, int row, u64 total) {
+  const double u = r.greedy ? 0.0 : (double)a.uniforms[row];
+  const double at = u > 0.0 ? floor(u * (double)total) : 0.0;
+  const u64 draw = at < 9.2e18 ? (u64)at : total;
+  return draw < total ? draw : total - 1;
+}
+
+// The token of this thread's run i0 .. that the draw falls into, `upto` being the sum before the run.
+template <int DT, int N, typename Weight>
+__device__ __forceinline__ void write_token(const SampleArgs& a, const Row& r, int row, const void* p, int i0,
+                                            Weight weight, u64 upto, u64 draw, u64 total) {
+  int i = 0;
+#pragma unroll
+  for (int j = 0; j < N - 1; ++j) {
+    upto += weight(j);
+    i += draw >= upto;
+  }
+  a.tokens[row] = i0 + i;
+  if (a.probs)
+    a.probs[row] = r.greedy ? 1.0f
+                            : (float)(exp2(exponent(r, load_one<DT>(p, i0 + i)) - r.shift) / ldexp((double)total, -a.shift));
+}
+
+__device__ __forceinline__ void write_none(const SampleArgs& a, int row) {
+  if (threadIdx.x != 0) return;
+  a.tokens[row] = -1;
+  if (a.probs) a.probs[row] = 0.0f;
+}
+
+// What is computed of v behind this is computed anew: keeping a whole run's exponents or weights from one
+// pass to the next would take more registers than there are.
+template <int N>
+__device__ __forceinline__ void again(float (&v)[N]) {
+#pragma unroll
+  for (int e = 0; e < N; ++e) asm volatile("" : "+v"(v[e]));
+}
+
+// Between every four of a run's tokens: the scheduler else overlaps so many that registers spill.
+__device__ __forceinline__ void apart(int e) {
+  if (e % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+}
+
+// ---- whole rows ------------------------------------------------------------------------
+struct WholeLds {
+  Scan<kWhole> scan[4];
+  float wave[kWhole / kWave];
+  double table[256];
+  u64 bins[kBins];
+  u64 found[2];
+  Digits digits;
+  int listed;
+  uint16_t list[kList];
+};
+
+template <int DT, int E>
+__global__ __launch_bounds__(kWhole) void whole_kernel(SampleArgs a) {
+  __shared__ WholeLds s;
+  const int row = blockIdx.x;
+  const void* p = row_of(a, row, DT);
+  const int i0 = (int)threadIdx.x * E;
+  float v[E];
+  load_run<DT>(p, i0, a.vocab, v);
+  fill_table<kWhole>(s.table);
+  s.bins[threadIdx.x] = 0;
+  if (threadIdx.x == 0) s.listed = 0;
+  float top = v[0];
+#pragma unroll
+  for (int e = 1; e < E; ++e) top = fmaxf(top, v[e]);
+  top = wave_max(top);
+  if ((threadIdx.x & 63) == 0) s.wave[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWhole / kWave; ++w) top = fmaxf(top, s.wave[w]);
+  if (top == -__builtin_inff()) return write_none(a, row);
+  const Row r = row_settings(a, row, top);
+  Cut cut{kBins, -1, 0, 0};
+  u64 last = ~0ull;
+  if (r.cuts()) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const double z = exponent(r, v[e]);
+      if (has_weight(z)) atomicAdd(&s.bins[bin_of(r, z)], r.k > 0 ? 1 : weight_of(z, s.table));
+      apart(e);
+    }
+    __syncthreads();
+    cut = find_cut<kWhole>(r, s.bins, s.scan[0], s.found);
+    if (cut.last >= 0) {
+      again(v);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const double z = exponent(r, v[e]);
+        const int bin = has_weight(z) ? bin_of(r, z) : kBins;
+        if (bin >= cut.first && bin <= cut.last) {
+          const int at = atomicAdd(&s.listed, 1);
+          if (at < kList) s.list[at] = (uint16_t)(i0 + e);
+        }
+        apart(e);
+      }
+      __syncthreads();
+      const int count = s.listed;
+      if (count <= kList) {
+        last = cut_tokens<kWhole, DT>(r, p, cut, count, s.table, s.digits, s.scan[1],
+                                      [&](int n) __attribute__((always_inline)) { return (int)s.list[n]; },
+                                      [](u64, u64) {});
+      } else {  // too many to list: all logits again, from the caches
+        last = cut_list<kWhole>(r, cut, s.digits, s.scan[1], [&](auto f) __attribute__((always_inline)) {
+          for (int i = threadIdx.x; i < a.vocab; i += kWhole) {
+            const float x = load_one<DT>(p, i);
+            const double z = exponent(r, x);
+            if (!has_weight(z)) continue;
+            const int bin = bin_of(r, z);
+            if (bin >= cut.first && bin <= cut.last) f(rank_key(x, i), weight_of(z, s.table));
+          }
+        }, [](u64, u64) {});
+      }
+    }
+  }
+  again(v);
+  u64 sum = 0, total;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    sum += kept_weight(r, cut, last, v[e], i0 + e, s.table);
+    apart(e);
+  }
+  const u64 upto = block_scan<kWhole>(sum, s.scan[2], &total);
+  const u64 draw = draw_of(a, r, row, total);
+  if (draw >= upto && draw < upto + sum) {
+    again(v);
+    write_token<DT, E>(a, r, row, p, i0, [&](int e) __attribute__((always_inline)) {
+      apart(e);
+      return kept_weight(r, cut, last, v[e], i0 + e, s.table);
+    }, upto, draw, total);
+  }
+}
+
+// ---- rows in chunks ----------------------------------------------------------------------
+// Largest logit of a row from its chunks', every wavefront for itself.
+__device__ __forceinline__ float row_top(const SampleArgs& a, int row) {
+  float v = -__builtin_inff();
+#pragma unroll
+  for (int j = 0; j < kSampleMaxChunks / kWave; ++j) {
+    const int c = j * kWave + (int)(threadIdx.x & 63);
+    if (c < a.chunks) v = fmaxf(v, a.tops[(int64_t)row * a.chunks + c]);
+  }
+  return wave_max(v);
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void tops_kernel(SampleArgs a) {
+  __shared__ float wave[kThreads / kWave];
+  const int row = (int)(blockIdx.x / (unsigned)a.chunks), chunk = (int)(blockIdx.x - (unsigned)row * a.chunks);
+  float v[kRun];
+  load_run<DT>(row_of(a, row, DT), chunk * kChunk + (int)threadIdx.x * kRun, a.vocab, v);
+  // the row's bins, for the next launch
+  if (a.bins)
+    for (int b = chunk * kThreads + (int)threadIdx.x; b < kBins; b += a.chunks * kThreads)
+      a.bins[(int64_t)row * kBins + b] = 0;
+  float top = v[0];
+#pragma unroll
+  for (int e = 1; e < kRun; ++e) top = fmaxf(top, v[e]);
+  top = wave_max(top);
+  if ((threadIdx.x & 63) == 0) wave[threadIdx.x >> 6] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kThreads / kWave; ++w) top = fmaxf(top, wave[w]);
+  if (threadIdx.x == 0) a.tops[blockIdx.x] = top;
+}
+
+template <int DT>
+__global__ __launch_bounds__(kThreads) void bins_kernel(SampleArgs a) {
+  __shared__ double table[256];
+  __shared__ u64 bins[kBins];
+  const int row = (int)(blockIdx.x / (unsigned)a.chunks), chunk = (int)(blockIdx.x - (unsigned)row * a.chunks);
+  float v[kRun];
+  load_run<DT>(row_of(a, row, DT), chunk * kChunk + (int)threadIdx.x * kRun, a.vocab, v);
+  const Row r = row_settings(a, row, row_top(a, row));
+  if (!r.cuts()) return;
+  fill_table<kThreads>(table);
+#pragma unroll
+  for (int b = 0; b < kBins / kThreads; ++b) bins[b * kThreads + threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < kRun; ++e) {
+    const double z = exponent(r, v[e]);
+    if (has_weight(z)) atomicAdd(&bins[bin_of(r, z)], r.k > 0 ? 1 : weight_of(z, table));
+  }
+  __syncthreads();
+#pragma unroll
+  for (int b = 0; b < kBins / kThreads; ++b) {
+    const u64 n = bins[b * kThreads + threadIdx.x];
+    if (n > 0) atomicAdd(a.bins + (int64_t)row * kBins + b * kThreads + threadIdx.x, n);
+  }
+}
+
 template <int DT>
 __global__ __launch_bounds__(kThreads) void sums_kernel(SampleArgs a) {
-  __shared__ float wave[kThreads / kWave];
   __shared__ double table[256];
-  __shared__ Scan<kThreads> scan;
+  __shared__ Scan<kThreads> scan[2];
   __shared__ u64 found[2];
   __shared__ int listed;
   const int row = (int)(blockIdx.x / (unsigned)a.chunks), chunk = (int)(blockIdx.x - (unsigned)row * a.chunks);
-  const void* p = row_of(a, row, DT);
-  float v[kGroups][4];
-#pragma unroll
-  for (int j = 0; j < kGroups; ++j)
-    load_four<DT>(p, chunk * kChunk + (j * kThreads + (int)threadIdx.x) * 4, a.vocab, v[j]);
-  table[threadIdx.x] = exp2((double)threadIdx.x / 256);
+  float v[kRun];
+  load_run<DT>(row_of(a, row, DT), chunk * kChunk + (int)threadIdx.x * kRun, a.vocab, v);
+  fill_table<kThreads>(table);
   if (threadIdx.x == 0) listed = 0;
-  const Row r = row_settings(a, row, row_top<kThreads>(a, row, wave));  // (a barrier)
-  const Cut cut = find_cut<kThreads>(a, r, row, scan, found);
+  const Row r = row_settings(a, row, row_top(a, row));
+  const Cut cut = find_cut<kThreads>(r, a.bins ? a.bins + (int64_t)row * kBins : nullptr, scan[0], found);
+  __syncthreads();
   u64 sum = 0;
 #pragma unroll
-  for (int j = 0; j < kGroups; ++j)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const double z = exponent(r, v[j][e]);
+  for (int e = 0; e < kRun; ++e) {
+    const double z = exponent(r, v[e]);
+    if (!has_weight(z)) continue;
+    const int bin = cut.last < 0 ? -1 : bin_of(r, z);
+    if (bin > cut.last) continue;
+    if (bin < cut.first) {
       const u64 w = weight_of(z, table);
-      if (w == 0) continue;
-      const int bin = cut.last < 0 ? 0 : bin_of(r, z);
-      if (bin < cut.first)
-        sum += w >= r.w_min ? w : 0;
-      else if (bin <= cut.last)
-        a.list[(int64_t)blockIdx.x * kChunk + atomicAdd(&listed, 1)] =
-            (uint16_t)((j * kThreads + (int)threadIdx.x) * 4 + e);
+      sum += w >= r.w_min ? w : 0;
+    } else {
+      a.list[(int64_t)blockIdx.x * kChunk + atomicAdd(&listed, 1)] = (uint16_t)((int)threadIdx.x * kRun + e);
     }
+  }
   u64 total;
-  block_scan<kThreads>(sum, scan, &total);
+  block_scan<kThreads>(sum, scan[1], &total);  // (and `listed` is whole)
   if (threadIdx.x == 0) {
     a.sums[blockIdx.x] = total;
     a.counts[blockIdx.x] = listed;
-    if (chunk == 0) a.cuts[row] = make_int4(cut.first, cut.last, 0, 0);
     if (chunk == 0) {
+      a.cuts[row] = make_int4(cut.first, cut.last, 0, 0);
       a.cut_sums[2 * row] = cut.before;
       a.cut_sums[2 * row + 1] = cut.target;
     }
   }
 }
 
-struct Chosen {
-  Scan<kChoose> scan;
+struct ChooseLds {
+  Scan<kChoose> scan[4];
   double table[256];
-  float wave[kChoose / kWave];
-  u64 sums[kDigits];
-  uint32_t counts[kDigits];
   u64 chunk_sums[kSampleMaxChunks];
   int starts[kSampleMaxChunks + 1];
-  u64 found[4];
-  u64 bits[2];
+  u64 found[2];
+  Digits digits;
 };
-
-// Smallest key up to which the listed tokens with keys <= last add up to `target` or more
-// (1 <= target <= their total). each(f): f(key, weight) for this thread's; ONES: a token counts 1.
-template <bool ONES, typename Each>
-__device__ __forceinline__ u64 select_key(u64 last, u64 target, Chosen& s, Each each) {
-  __syncthreads();  // bits and found of an earlier cut have been read
-  // the digits that differ
-  if (threadIdx.x == 0) s.bits[0] = ~0ull, s.bits[1] = 0;
-  __syncthreads();
-  u64 low = ~0ull, high = 0;
-  each([&](u64 key, u64) __attribute__((always_inline)) {
-    if (key > last) return;
-    low = key < low ? key : low;
-    high = key > high ? key : high;
-  });
-#pragma unroll
-  for (int m = 1; m < kWave; m <<= 1) {
-    const u64 l = __shfl_xor(low, m, 64), h = __shfl_xor(high, m, 64);
-    low = l < low ? l : low;
-    high = h > high ? h : high;
-  }
-  if ((threadIdx.x & 63) == 0) {
-    atomicMin(&s.bits[0], low);
-    atomicMax(&s.bits[1], high);
-  }
-  __syncthreads();
-  low = s.bits[0], high = s.bits[1];
-  if (low == high) return low;
-  int bit = 64 - __builtin_clzll(low ^ high);  // digits from this bit down
-  u64 prefix = bit < 64 ? low >> bit << bit : 0, before = 0;
-  while (bit > 0) {
-    const int width = bit < 8 ? bit : 8, at = bit - width;
-    if (threadIdx.x < kDigits) s.sums[threadIdx.x] = 0, s.counts[threadIdx.x] = 0;
-    __syncthreads();
-    each([&](u64 key, u64 w) __attribute__((always_inline)) {
-      if (key > last || (bit < 64 && (key ^ prefix) >> bit != 0)) return;
-      const int d = (int)(key >> at) & ((1 << width) - 1);
-      if (!ONES) atomicAdd(&s.sums[d], w);
-      atomicAdd(&s.counts[d], 1u);
-    });
-    __syncthreads();
-    u64 total;
-    const u64 own = threadIdx.x < kDigits ? ONES ? (u64)s.counts[threadIdx.x] : s.sums[threadIdx.x] : 0;
-    const u64 sum = before + block_scan<kChoose>(own, s.scan, &total);
-    if (target > sum && target <= sum + own) {
-      s.found[0] = threadIdx.x;
-      s.found[1] = sum;
-      s.found[2] = s.counts[threadIdx.x];
-    }
-    __syncthreads();
-    prefix |= s.found[0] << at;
-    before = s.found[1];
-    bit = at;
-    const bool one = s.found[2] == 1;
-    __syncthreads();
-    if (one && bit > 0) {  // the token itself
-      each([&](u64 key, u64) __attribute__((always_inline)) {
-        if (key <= last && (key ^ prefix) >> bit == 0) s.found[3] = key;
-      });
-      __syncthreads();
-      return s.found[3];
-    }
-  }
-  return prefix;
-}
 
 template <int DT>
 __global__ __launch_bounds__(kChoose) void choose_kernel(SampleArgs a) {
-  __shared__ Chosen s;
+  static_assert(kSampleMaxChunks <= kChoose, "a thread a chunk");
+  __shared__ ChooseLds s;
   const int row = blockIdx.x;
   const void* p = row_of(a, row, DT);
   const int64_t first_chunk = (int64_t)row * a.chunks;
-  const int4 cut_bins = a.cuts[row];
-  const u64 cut_before = a.cut_sums[2 * row], cut_target = a.cut_sums[2 * row + 1];
-  if (threadIdx.x < 256) s.table[threadIdx.x] = exp2((double)threadIdx.x / 256);
-  const Row r = row_settings(a, row, row_top<kChoose>(a, row, s.wave));
-  if (r.top == -__builtin_inff()) {
-    if (threadIdx.x == 0) {
-      a.tokens[row] = -1;
-      if (a.probs) a.probs[row] = 0.0f;
-    }
-    return;
-  }
-  // places of the chunks' tokens in one list
-  static_assert(kSampleMaxChunks <= kChoose, "a thread a chunk");
   const bool mine = (int)threadIdx.x < a.chunks;
+  const int own_listed = mine ? a.counts[first_chunk + threadIdx.x] : 0;
+  const u64 own_sum = mine ? a.sums[first_chunk + threadIdx.x] : 0;
+  const int4 bins = a.cuts[row];
+  const Cut cut{bins.x, bins.y, a.cut_sums[2 * row], a.cut_sums[2 * row + 1]};
+  fill_table<kChoose>(s.table);
+  const Row r = row_settings(a, row, row_top(a, row));
+  if (r.top == -__builtin_inff()) return write_none(a, row);
+  // places of the chunks' tokens in one list
   u64 listed;
-  const u64 start = block_scan<kChoose>(mine ? (u64)a.counts[first_chunk + threadIdx.x] : 0, s.scan, &listed);
+  const u64 start = block_scan<kChoose>((u64)own_listed, s.scan[0], &listed);
   if (mine) {
     s.starts[threadIdx.x] = (int)start;
-    s.chunk_sums[threadIdx.x] = a.sums[first_chunk + threadIdx.x];
+    s.chunk_sums[threadIdx.x] = own_sum;
   }
-  if (threadIdx.x == 0) s.starts[a.chunks] = (int)listed;
   __syncthreads();
-  const int count = (int)listed;
-
   u64 last = ~0ull;  // key of the last token that top-k and top-p leave
-  if (count > 0) {
-    auto token_at = [&](int i) __attribute__((always_inline)) {
-      int lo = 0, hi = a.chunks;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (s.starts[mid] <= i) lo = mid; else hi = mid;
-      }
-      return lo * kChunk + (int)a.list[(first_chunk + lo) * kChunk + (i - s.starts[lo])];
-    };
-    auto cut = [&](auto each) __attribute__((always_inline)) {
-      if (r.k > 0 && cut_target > 0) last = select_key<true>(last, cut_target - cut_before, s, each);
-      if (r.cut_p) {
-        u64 target = cut_target - cut_before;
-        if (r.k > 0) {
-          u64 sum = 0, total;
-          each([&](u64 key, u64 w) __attribute__((always_inline)) { sum += key <= last ? w : 0; });
-          block_scan<kChoose>(sum, s.scan, &total);
-          const double part = ceil(r.p * (double)total);
-          target = part >= 1.0 ? (u64)part : 1;
-          target = target < total ? target : total;
-        }
-        last = select_key<false>(last, target, s, each);
-      }
-      each([&](u64 key, u64 w) __attribute__((always_inline)) {
-        if (key <= last && w >= r.w_min) atomicAdd(&s.chunk_sums[(uint32_t)key / kChunk], w);
-      });
-    };
-    if (count <= kChoose * kHeld) {
-      u64 keys[kHeld], weights[kHeld];
-#pragma unroll
-      for (int i = 0; i < kHeld; ++i) {
-        keys[i] = ~0ull, weights[i] = 0;
-        const int n = i * kChoose + (int)threadIdx.x;
-        if (n < count) {
-          const int token = token_at(n);
-          const float v = load_one<DT>(p, token);
-          keys[i] = rank_key(v, token);
-          weights[i] = weight_of(exponent(r, v), s.table);
-        }
-      }
-      cut([&](auto f) __attribute__((always_inline)) {
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i)
-          if (i * kChoose + (int)threadIdx.x < count) f(keys[i], weights[i]);
-      });
-    } else {
-      cut([&](auto f) __attribute__((always_inline)) {
-        for (int n = threadIdx.x; n < count; n += kChoose) {
-          const int token = token_at(n);
-          const float v = load_one<DT>(p, token);
-          f(rank_key(v, token), weight_of(exponent(r, v), s.table));
-        }
-      });
-    }
+  if (listed > 0) {
+    last = cut_tokens<kChoose, DT>(
+        r, p, cut, (int)listed, s.table, s.digits, s.scan[1],
+        [&](int n) __attribute__((always_inline)) {
+          int lo = 0, hi = a.chunks;
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s.starts[mid] <= n) lo = mid; else hi = mid;
+          }
+          return lo * kChunk + (int)a.list[(first_chunk + lo) * kChunk + (n - s.starts[lo])];
+        },
+        [&](u64 key, u64 w) __attribute__((always_inline)) { atomicAdd(&s.chunk_sums[(uint32_t)key / kChunk], w); });
     __syncthreads();
   }
-
   // the chunk that the draw falls into, and the token
-  u64 total;
+  u64 total, all;
   const u64 own = mine ? s.chunk_sums[threadIdx.x] : 0;
-  const u64 before = block_scan<kChoose>(own, s.scan, &total);
-  const double u = r.greedy ? 0.0 : (double)a.uniforms[row];
-  const double at = u > 0.0 ? floor(u * (double)total) : 0.0;
-  u64 draw = at < 9.2e18 ? (u64)at : total;
-  draw = draw < total ? draw : total - 1;
+  const u64 before = block_scan<kChoose>(own, s.scan[2], &total);
+  u64 draw = draw_of(a, r, row, total);
   if (draw >= before && draw < before + own) {
     s.found[0] = threadIdx.x;
     s.found[1] = draw - before;
@@ -488,47 +691,33 @@ __global__ __launch_bounds__(kChoose) void choose_kernel(SampleArgs a) {
   draw = s.found[1];
   constexpr int kPer = kChunk / kChoose;
   const int i0 = chunk * kChunk + (int)threadIdx.x * kPer;
-  u64 w[kPer], sum = 0, all;
+  float v[kPer];
+  load_run<DT>(p, i0, a.vocab, v);
+  u64 w[kPer], sum = 0;
 #pragma unroll
-  for (int j = 0; j < kPer; j += 4) {
-    float v[4];
-    load_four<DT>(p, i0 + j, a.vocab, v);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const double z = exponent(r, v[e]);
-      u64 x = weight_of(z, s.table);
-      if (x < r.w_min) x = 0;
-      if (x > 0 && cut_bins.y >= 0) {
-        const int bin = bin_of(r, z);
-        if (bin > cut_bins.y || (bin >= cut_bins.x && rank_key(v[e], i0 + j + e) > last)) x = 0;
-      }
-      w[j + e] = x;
-      sum += x;
-    }
-  }
-  u64 upto = block_scan<kChoose>(sum, s.scan, &all);
-  if (draw >= upto && draw < upto + sum) {
-    int i = 0;
-#pragma unroll
-    for (; i < kPer - 1; ++i) {
-      upto += w[i];
-      if (draw < upto) break;
-    }
-    a.tokens[row] = i0 + i;
-    if (a.probs)
-      a.probs[row] = r.greedy ? 1.0f
-                              : (float)(exp2(exponent(r, load_one<DT>(p, i0 + i)) - r.shift) /
-                                        ldexp((double)total, -a.shift));
-  }
+  for (int e = 0; e < kPer; ++e) sum += w[e] = kept_weight(r, cut, last, v[e], i0 + e, s.table);
+  const u64 upto = block_scan<kChoose>(sum, s.scan[3], &all);
+  if (draw >= upto && draw < upto + sum)
+    write_token<DT, kPer>(a, r, row, p, i0, [&](int e) __attribute__((always_inline)) { return w[e]; }, upto, draw, total);
 }
 
 template <int DT>
 hipError_t launch_t(const SampleArgs& a, hipStream_t stream) {
+  const dim3 rows((unsigned)a.rows);
+  if (a.chunks == 0) {
+    if (a.vocab <= 4 * kWhole)
+      hipLaunchKernelGGL((whole_kernel<DT, 4>), rows, dim3(kWhole), 0, stream, a);
+    else if (a.vocab <= 16 * kWhole)
+      hipLaunchKernelGGL((whole_kernel<DT, 16>), rows, dim3(kWhole), 0, stream, a);
+    else
+      hipLaunchKernelGGL((whole_kernel<DT, 32>), rows, dim3(kWhole), 0, stream, a);
+    return hipGetLastError();
+  }
   const dim3 grid((unsigned)(a.rows * (int64_t)a.chunks)), block(kThreads);
   hipLaunchKernelGGL((tops_kernel<DT>), grid, block, 0, stream, a);
   if (a.bins) hipLaunchKernelGGL((bins_kernel<DT>), grid, block, 0, stream, a);
   hipLaunchKernelGGL((sums_kernel<DT>), grid, block, 0, stream, a);
-  hipLaunchKernelGGL((choose_kernel<DT>), dim3((unsigned)a.rows), dim3(kChoose), 0, stream, a);
+  hipLaunchKernelGGL((choose_kernel<DT>), rows, dim3(kChoose), 0, stream, a);
   return hipGetLastError();
 }
 

@@ -26,7 +26,10 @@ int weight_shift(int64_t vocab) {
   return std::min(50, 62 - bits);
 }
 
-int64_t sample_chunks(int64_t vocab) { return (vocab + q4::kSampleChunk - 1) / q4::kSampleChunk; }
+// Chunks of a row; 0: a workgroup takes the whole row.
+int64_t sample_chunks(int64_t vocab) {
+  return vocab <= q4::kSampleWhole ? 0 : (vocab + q4::kSampleChunk - 1) / q4::kSampleChunk;
+}
 
 q4_status check_sample(int64_t rows, int64_t vocab) {
   if (rows < 0 || rows >= kMaxRows || vocab <= 0 || vocab > kMaxVocab || rows * sample_chunks(vocab) > q4::kMaxGroups256)
@@ -38,6 +41,7 @@ q4_status check_sample(int64_t rows, int64_t vocab) {
 size_t place_sample(q4::SampleArgs* a, unsigned char* base) {
   const size_t rows = a->rows, all = rows * a->chunks;
   size_t at = 0;
+  if (a->chunks == 0) return 0;
   auto part = [&](auto** p, size_t n) {
     *p = reinterpret_cast<std::remove_reference_t<decltype(*p)>>(base + at);
     at += (n * sizeof(**p) + 15) / 16 * 16;
@@ -129,10 +133,10 @@ q4_status q4_sample(const void* logits, int32_t dtype, int64_t stride, int64_t r
   a.tokens = tokens, a.probs = probs, a.shift = weight_shift(vocab);
   a.chunks = (int)sample_chunks(vocab);
   const size_t need = place_sample(&a, static_cast<unsigned char*>(workspace));
-  if (!workspace || workspace_bytes < need)
+  if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(Q4_ERR_WORKSPACE, "this shape needs %zu bytes of workspace (q4_sample_workspace_bytes), got %zu", need,
                 workspace ? workspace_bytes : (size_t)0);
-  if (!aligned(workspace, 16)) return fail(Q4_ERR_ALIGN, "workspace needs 16-byte alignment");
+  if (need > 0 && !aligned(workspace, 16)) return fail(Q4_ERR_ALIGN, "workspace needs 16-byte alignment");
   if (!top_k && !top_p) a.bins = nullptr;
   return hip_status(q4::launch_sample(a, static_cast<hipStream_t>(stream)), "sample launch");
 }
