@@ -154,11 +154,12 @@ constexpr int kIndexBits = 20;  // of a key
 // ---- weights ------------------------------------------------------------------------
 // A row's settings. Greedy (temperature <= 0): only the largest logits have weight, and the draw is 0.
 struct Row {
-  float top;     // largest logit
-  double slope;  // log2(e) / temperature
+  double top;    // largest logit
+  double slope;  // log2(e) / temperature; greedy: so steep that nothing below the largest has weight
   double shift;
   float bin_scale;
   int k;  // 0: no top-k
+  bool infinite;  // the largest logit is: those count as 0, all others as -infinity
   bool cut_p, greedy;
   double p;
   u64 w_min;  // smallest weight that min-p leaves
@@ -167,10 +168,11 @@ struct Row {
 
 __device__ __forceinline__ Row row_settings(const SampleArgs& a, int row, float top) {
   Row r;
-  r.top = top;
+  r.infinite = top == __builtin_inff();
+  r.top = r.infinite ? 0.0 : (double)top;
   const float t = a.temperature ? a.temperature[row] : 1.0f;
   r.greedy = !(t > 0.0f);
-  r.slope = r.greedy ? __builtin_inf() : 1.4426950408889634 / (double)t;
+  r.slope = r.greedy ? 1e300 : 1.4426950408889634 / (double)t;
   r.shift = (double)a.shift;
   r.bin_scale = (float)kBins / (float)(a.shift + 2);
   r.k = a.top_k ? a.top_k[row] : 0;
@@ -182,17 +184,29 @@ __device__ __forceinline__ Row row_settings(const SampleArgs& a, int row, float 
   return r;
 }
 
-// log2 of the weight; up to -1 (or NaN, where an infinity met a zero): no weight.
+// A logit as the row counts it.
+__device__ __forceinline__ float settle(const Row& r, float v) {
+  return !r.infinite ? v : v == __builtin_inff() ? 0.0f : -__builtin_inff();
+}
+template <int N>
+__device__ __forceinline__ void settle_all(const Row& r, float (&v)[N]) {
+  if (!r.infinite) return;
+#pragma unroll
+  for (int e = 0; e < N; ++e) v[e] = settle(r, v[e]);
+}
+
+// log2 of the weight. (NaN where -infinity meets a slope of 0: it has no weight either.)
 __device__ __forceinline__ double exponent(const Row& r, float v) {
-  return v == r.top ? r.shift : __builtin_fma((double)v - (double)r.top, r.slope, r.shift);
+  return __builtin_fma((double)v - r.top, r.slope, r.shift);
 }
 __device__ __forceinline__ bool has_weight(double z) { return z > -1.0; }
 
-// rint(2^z), 1 or more, for -1 < z <= 50: with k = rint(256 z), 2^(k / 256) from the table and
+// rint(2^z), z <= 50, 0 for no weight: with k = rint(256 z), 2^(k / 256) from the table and
 // 2^(z - k / 256) by its series to the fourth power, whose next term is below 2^-54; the whole is
 // within 2^-50 of itself before the rounding.
 __device__ __forceinline__ u64 weight_of(double z, const double* table) {
   constexpr double kMagic = 26388279066624.0;  // 1.5 * 2^44: the sum's last bit is 1/256
+  z = __builtin_fmax(z, -2.0);
   const double m = z + kMagic;
   const int k = (int)(uint32_t)__builtin_bit_cast(u64, m);
   const double x = (z - (m - kMagic)) * 0.6931471805599453;
@@ -202,8 +216,7 @@ __device__ __forceinline__ u64 weight_of(double z, const double* table) {
   s = __builtin_fma(x, s, 1.0);
   const double w = ldexp(table[k & 255] * s, k >> 8);
   // + 2^52: rounded to a whole number, which is in the low bits
-  const u64 n = __builtin_bit_cast(u64, w + 4503599627370496.0) & 0xFFFFFFFFFFFFFull;
-  return n > 0 ? n : 1;
+  return __builtin_bit_cast(u64, w + 4503599627370496.0) & 0xFFFFFFFFFFFFFull;
 }
 template <int N>
 __device__ __forceinline__ void fill_table(double* table) {
@@ -274,7 +287,7 @@ __device__ __forceinline__ u64 select_key(const Row& r, u64 last, u64 target, Di
   if (threadIdx.x == 0) s.differ = 0;
   __syncthreads();
   // the first digit that differs, from the largest logit's key
-  const uint32_t first = (uint32_t)(rank_key(r.top, 0) >> 32);
+  const uint32_t first = (uint32_t)(rank_key((float)r.top, 0) >> 32);
   uint32_t differ = 0;
   each([&](u64 key, u64) __attribute__((always_inline)) { differ |= key <= last ? (uint32_t)(key >> 32) ^ first : 0; });
   differ = wave_or(differ);
@@ -353,7 +366,7 @@ __device__ __forceinline__ u64 cut_tokens(const Row& r, const void* p, const Cut
   constexpr int kHeld = kList / N;
   auto look = [&](int n, u64* key, u64* w) __attribute__((always_inline)) {
     const int token = token_at(n);
-    const float v = load_one<DT>(p, token);
+    const float v = settle(r, load_one<DT>(p, token));
     *key = rank_key(v, token);
     *w = weight_of(exponent(r, v), table);
   };
@@ -386,8 +399,8 @@ __device__ __forceinline__ u64 cut_tokens(const Row& r, const void* p, const Cut
 // Weight of a token that the cuts left, else 0.
 __device__ __forceinline__ u64 kept_weight(const Row& r, const Cut& cut, u64 last, float v, int i, const double* table) {
   const double z = exponent(r, v);
-  if (!has_weight(z)) return 0;
   if (cut.last >= 0) {
+    if (!has_weight(z)) return 0;
     const int bin = bin_of(r, z);
     if (bin > cut.last || (bin >= cut.first && rank_key(v, i) > last)) return 0;
   }
@@ -402,20 +415,20 @@ __device__ __forceinline__ u64 draw_of(const SampleArgs& a, const Row& r, int ro
   return draw < total ? draw : total - 1;
 }
 
-// The token of this thread's run i0 .. that the draw falls into, `upto` being the sum before the run.
-template <int DT, int N, typename Weight>
-__device__ __forceinline__ void write_token(const SampleArgs& a, const Row& r, int row, const void* p, int i0,
+// The token of this thread's run v, i0 .., that the draw falls into, `upto` being the sum before the run.
+template <int N, typename Weight>
+__device__ __forceinline__ void write_token(const SampleArgs& a, const Row& r, int row, int i0, const float (&v)[N],
                                             Weight weight, u64 upto, u64 draw, u64 total) {
   int i = 0;
+  float x = v[0];
 #pragma unroll
   for (int j = 0; j < N - 1; ++j) {
     upto += weight(j);
-    i += draw >= upto;
+    if (draw >= upto) i = j + 1, x = v[j + 1];
   }
   a.tokens[row] = i0 + i;
   if (a.probs)
-    a.probs[row] = r.greedy ? 1.0f
-                            : (float)(exp2(exponent(r, load_one<DT>(p, i0 + i)) - r.shift) / ldexp((double)total, -a.shift));
+    a.probs[row] = r.greedy ? 1.0f : (float)(exp2(exponent(r, x) - r.shift) / ldexp((double)total, -a.shift));
 }
 
 __device__ __forceinline__ void write_none(const SampleArgs& a, int row) {
@@ -443,6 +456,7 @@ struct WholeLds {
   float wave[kWhole / kWave];
   double table[256];
   u64 bins[kBins];
+  uint32_t counts[kBins];
   u64 found[2];
   Digits digits;
   int listed;
@@ -459,6 +473,7 @@ __global__ __launch_bounds__(kWhole) void whole_kernel(SampleArgs a) {
   load_run<DT>(p, i0, a.vocab, v);
   fill_table<kWhole>(s.table);
   s.bins[threadIdx.x] = 0;
+  s.counts[threadIdx.x] = 0;
   if (threadIdx.x == 0) s.listed = 0;
   float top = v[0];
 #pragma unroll
@@ -470,16 +485,28 @@ __global__ __launch_bounds__(kWhole) void whole_kernel(SampleArgs a) {
   for (int w = 0; w < kWhole / kWave; ++w) top = fmaxf(top, s.wave[w]);
   if (top == -__builtin_inff()) return write_none(a, row);
   const Row r = row_settings(a, row, top);
+  settle_all(r, v);
   Cut cut{kBins, -1, 0, 0};
   u64 last = ~0ull;
   if (r.cuts()) {
+    if (r.k > 0) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const double z = exponent(r, v[e]);
-      if (has_weight(z)) atomicAdd(&s.bins[bin_of(r, z)], r.k > 0 ? 1 : weight_of(z, s.table));
-      apart(e);
+      for (int e = 0; e < E; ++e) {
+        const double z = exponent(r, v[e]);
+        if (has_weight(z)) atomicAdd(&s.counts[bin_of(r, z)], 1u);
+        apart(e);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const double z = exponent(r, v[e]);
+        if (has_weight(z)) atomicAdd(&s.bins[bin_of(r, z)], weight_of(z, s.table));
+        apart(e);
+      }
     }
     __syncthreads();
+    if (r.k > 0) s.bins[threadIdx.x] = s.counts[threadIdx.x];  // read by this thread alone
+
     cut = find_cut<kWhole>(r, s.bins, s.scan[0], s.found);
     if (cut.last >= 0) {
       again(v);
@@ -502,7 +529,7 @@ __global__ __launch_bounds__(kWhole) void whole_kernel(SampleArgs a) {
       } else {  // too many to list: all logits again, from the caches
         last = cut_list<kWhole>(r, cut, s.digits, s.scan[1], [&](auto f) __attribute__((always_inline)) {
           for (int i = threadIdx.x; i < a.vocab; i += kWhole) {
-            const float x = load_one<DT>(p, i);
+            const float x = settle(r, load_one<DT>(p, i));
             const double z = exponent(r, x);
             if (!has_weight(z)) continue;
             const int bin = bin_of(r, z);
@@ -513,19 +540,35 @@ __global__ __launch_bounds__(kWhole) void whole_kernel(SampleArgs a) {
     }
   }
   again(v);
-  u64 sum = 0, total;
+  constexpr int kParts = E / 4;
+  u64 part[kParts], sum = 0, total;  // every four tokens' weights
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    sum += kept_weight(r, cut, last, v[e], i0 + e, s.table);
-    apart(e);
+  for (int j = 0; j < kParts; ++j) {
+    part[j] = 0;
+#pragma unroll
+    for (int e = 4 * j; e < 4 * j + 4; ++e) part[j] += kept_weight(r, cut, last, v[e], i0 + e, s.table);
+    sum += part[j];
+    __builtin_amdgcn_sched_barrier(0);
   }
-  const u64 upto = block_scan<kWhole>(sum, s.scan[2], &total);
+  u64 upto = block_scan<kWhole>(sum, s.scan[2], &total);
   const u64 draw = draw_of(a, r, row, total);
   if (draw >= upto && draw < upto + sum) {
-    again(v);
-    write_token<DT, E>(a, r, row, p, i0, [&](int e) __attribute__((always_inline)) {
-      apart(e);
-      return kept_weight(r, cut, last, v[e], i0 + e, s.table);
+    int at = 0;
+    float x[4] = {v[0], v[1], v[2], v[3]};
+    bool past = true;
+#pragma unroll
+    for (int j = 0; j + 1 < kParts; ++j) {
+      past = past && draw >= upto + part[j];
+      if (past) {
+        upto += part[j];
+        at = 4 * j + 4;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = v[4 * j + 4 + e];
+      }
+    }
+    again(x);
+    write_token(a, r, row, i0 + at, x, [&](int e) __attribute__((always_inline)) {
+      return kept_weight(r, cut, last, x[e], i0 + at + e, s.table);
     }, upto, draw, total);
   }
 }
@@ -572,19 +615,30 @@ __global__ __launch_bounds__(kThreads) void bins_kernel(SampleArgs a) {
   load_run<DT>(row_of(a, row, DT), chunk * kChunk + (int)threadIdx.x * kRun, a.vocab, v);
   const Row r = row_settings(a, row, row_top(a, row));
   if (!r.cuts()) return;
+  settle_all(r, v);
   fill_table<kThreads>(table);
 #pragma unroll
   for (int b = 0; b < kBins / kThreads; ++b) bins[b * kThreads + threadIdx.x] = 0;
   __syncthreads();
+  uint32_t* counts = reinterpret_cast<uint32_t*>(bins);
+  if (r.k > 0) {
 #pragma unroll
-  for (int e = 0; e < kRun; ++e) {
-    const double z = exponent(r, v[e]);
-    if (has_weight(z)) atomicAdd(&bins[bin_of(r, z)], r.k > 0 ? 1 : weight_of(z, table));
+    for (int e = 0; e < kRun; ++e) {
+      const double z = exponent(r, v[e]);
+      if (has_weight(z)) atomicAdd(&counts[bin_of(r, z)], 1u);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < kRun; ++e) {
+      const double z = exponent(r, v[e]);
+      if (has_weight(z)) atomicAdd(&bins[bin_of(r, z)], weight_of(z, table));
+    }
   }
   __syncthreads();
 #pragma unroll
   for (int b = 0; b < kBins / kThreads; ++b) {
-    const u64 n = bins[b * kThreads + threadIdx.x];
+    const int i = b * kThreads + threadIdx.x;
+    const u64 n = r.k > 0 ? (u64)counts[i] : bins[i];
     if (n > 0) atomicAdd(a.bins + (int64_t)row * kBins + b * kThreads + threadIdx.x, n);
   }
 }
@@ -601,15 +655,18 @@ __global__ __launch_bounds__(kThreads) void sums_kernel(SampleArgs a) {
   fill_table<kThreads>(table);
   if (threadIdx.x == 0) listed = 0;
   const Row r = row_settings(a, row, row_top(a, row));
+  settle_all(r, v);
   const Cut cut = find_cut<kThreads>(r, a.bins ? a.bins + (int64_t)row * kBins : nullptr, scan[0], found);
   __syncthreads();
   u64 sum = 0;
 #pragma unroll
   for (int e = 0; e < kRun; ++e) {
     const double z = exponent(r, v[e]);
-    if (!has_weight(z)) continue;
-    const int bin = cut.last < 0 ? -1 : bin_of(r, z);
-    if (bin > cut.last) continue;
+    int bin = -1;
+    if (cut.last >= 0) {
+      bin = has_weight(z) ? bin_of(r, z) : kBins;
+      if (bin > cut.last) continue;
+    }
     if (bin < cut.first) {
       const u64 w = weight_of(z, table);
       sum += w >= r.w_min ? w : 0;
@@ -653,7 +710,7 @@ __global__ __launch_bounds__(kChoose) void choose_kernel(SampleArgs a) {
   const Cut cut{bins.x, bins.y, a.cut_sums[2 * row], a.cut_sums[2 * row + 1]};
   fill_table<kChoose>(s.table);
   const Row r = row_settings(a, row, row_top(a, row));
-  if (r.top == -__builtin_inff()) return write_none(a, row);
+  if (r.top == -__builtin_inf()) return write_none(a, row);
   // places of the chunks' tokens in one list
   u64 listed;
   const u64 start = block_scan<kChoose>((u64)own_listed, s.scan[0], &listed);
@@ -693,12 +750,13 @@ __global__ __launch_bounds__(kChoose) void choose_kernel(SampleArgs a) {
   const int i0 = chunk * kChunk + (int)threadIdx.x * kPer;
   float v[kPer];
   load_run<DT>(p, i0, a.vocab, v);
+  settle_all(r, v);
   u64 w[kPer], sum = 0;
 #pragma unroll
   for (int e = 0; e < kPer; ++e) sum += w[e] = kept_weight(r, cut, last, v[e], i0 + e, s.table);
   const u64 upto = block_scan<kChoose>(sum, s.scan[3], &all);
   if (draw >= upto && draw < upto + sum)
-    write_token<DT, kPer>(a, r, row, p, i0, [&](int e) __attribute__((always_inline)) { return w[e]; }, upto, draw, total);
+    write_token(a, r, row, i0, v, [&](int e) __attribute__((always_inline)) { return w[e]; }, upto, draw, total);
 }
 
 template <int DT>
