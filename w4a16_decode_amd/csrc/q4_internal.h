@@ -194,7 +194,7 @@ struct SampleArgs {
   unsigned long long* cut_sums;  // [rows][2]: the sum before the cut's first bin, and the one it is to reach
   int4* cuts;                    // [rows]: the cut's first and last bin
   int32_t* counts;               // [rows][chunks]: tokens in those bins
-  uint16_t* list;                // [rows][chunks][kSampleChunk]: which
+  uint2* list;                   // [rows][chunks][kSampleChunk]: which, and their logits
 };
 
 constexpr int kSampleChunk = 4096, kSampleBins = 1024, kSampleMaxChunks = 256, kSampleWhole = 32768;

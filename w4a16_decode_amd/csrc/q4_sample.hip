@@ -241,13 +241,14 @@ __device__ __forceinline__ u64 part_of(double p, u64 total) {
   return t < total ? t : total;
 }
 
+// own: this thread's bins, the threadIdx.x-th kBins / N.
 template <int N>
-__device__ __forceinline__ Cut find_cut(const Row& r, const u64* bins, Scan<N>& s, u64* found) {
+__device__ __forceinline__ Cut find_cut(const Row& r, const u64 (&own)[kBins / N], Scan<N>& s, u64* found) {
   if (!r.cuts()) return Cut{kBins, -1, 0, 0};
   constexpr int kPer = kBins / N;
-  u64 own[kPer], sum = 0, total;
+  u64 sum = 0, total;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) sum += own[i] = bins[threadIdx.x * kPer + i];
+  for (int i = 0; i < kPer; ++i) sum += own[i];
   u64 before = block_scan<N>(sum, s, &total);
   const bool all = r.k > 0 && (u64)r.k >= total;  // top-k leaves every token that has weight
   const u64 target = r.k > 0 ? (all ? total : (u64)r.k) : part_of(r.p, total);
@@ -271,31 +272,38 @@ struct Digits {
   u64 sums[kRounds][kDigits];
   uint32_t counts[kRounds][kDigits];
   u64 key;
-  uint32_t differ;
+  uint32_t ones, zeros;  // bits that some key has set, and clear
 };
 
 // Smallest key up to which the listed tokens with keys <= last add up to `target` or more
 // (1 <= target <= their total). each(f): f(key, weight) for this thread's; ONES: a token counts 1.
 template <int N, bool ONES, typename Each>
-__device__ __forceinline__ u64 select_key(const Row& r, u64 last, u64 target, Digits& s, Each each) {
+__device__ __forceinline__ u64 select_key(u64 last, u64 target, Digits& s, Each each) {
   const int lane = threadIdx.x & 63;
   __syncthreads();  // an earlier cut has been read
   for (int i = threadIdx.x; i < kRounds * kDigits; i += N) {
     (&s.sums[0][0])[i] = 0;
     (&s.counts[0][0])[i] = 0;
   }
-  if (threadIdx.x == 0) s.differ = 0;
+  if (threadIdx.x == 0) s.ones = s.zeros = 0;
   __syncthreads();
-  // the first digit that differs, from the largest logit's key
-  const uint32_t first = (uint32_t)(rank_key((float)r.top, 0) >> 32);
-  uint32_t differ = 0;
-  each([&](u64 key, u64) __attribute__((always_inline)) { differ |= key <= last ? (uint32_t)(key >> 32) ^ first : 0; });
-  differ = wave_or(differ);
-  if (lane == kWave - 1 && differ) atomicOr(&s.differ, differ);
+  // the first bit that differs
+  uint32_t ones = 0, zeros = 0;
+  each([&](u64 key, u64) __attribute__((always_inline)) {
+    if (key > last) return;
+    ones |= (uint32_t)(key >> 32);
+    zeros |= ~(uint32_t)(key >> 32);
+  });
+  ones = wave_or(ones), zeros = wave_or(zeros);
+  if (lane == kWave - 1 && (ones | zeros)) {
+    atomicOr(&s.ones, ones);
+    atomicOr(&s.zeros, zeros);
+  }
   __syncthreads();
-  differ = s.differ;
+  ones = s.ones;
+  const uint32_t differ = ones & s.zeros;
   int bit = differ ? 64 - __builtin_clz(differ) : kIndexBits;  // digits from this bit down
-  u64 prefix = bit < 64 ? ((u64)first << 32) >> bit << bit : 0, before = 0;
+  u64 prefix = bit < 64 ? ((u64)ones << 32) >> bit << bit : 0, before = 0;
   for (int round = 0; bit > 0; ++round) {
     // a digit does not reach from the logit into the index
     const int floor = bit > 32 ? 32 : 0, width = min(bit - floor, 8), at = bit - width;
@@ -337,11 +345,65 @@ __device__ __forceinline__ u64 select_key(const Row& r, u64 last, u64 target, Di
   return prefix;
 }
 
+// Few listed tokens: every one counts those ranked up to it and adds their weights, N / kFew threads a
+// token, which answers both cuts at once.
+constexpr int kFew = 128;
+struct Few {
+  u64 keys[kFew], weights[kFew];
+  u64 upto[kFew];    // weights up to the token
+  uint32_t rank[kFew];
+  u64 total, key_k, key_p;
+};
+template <int N>
+__device__ __forceinline__ u64 cut_few(const Row& r, const Cut& cut, int count, u64 key, u64 w, Few& s) {
+  const int i = (int)threadIdx.x % kFew;
+  if (threadIdx.x < kFew) {
+    const bool any = (int)threadIdx.x < count;
+    s.keys[i] = any ? key : ~0ull, s.weights[i] = any ? w : 0;
+    s.upto[i] = 0, s.rank[i] = 0;
+  }
+  if (threadIdx.x == 0) s.key_k = s.key_p = ~0ull;
+  __syncthreads();
+  constexpr int kShare = kFew / (N / kFew);
+  const int j0 = (int)threadIdx.x / kFew * kShare;
+  const u64 mine = s.keys[i];
+  if (j0 < count) {
+    u64 upto = 0;
+    uint32_t rank = 0;
+#pragma unroll 4
+    for (int j = j0; j < j0 + kShare; ++j) {
+      const bool before = s.keys[j] <= mine;
+      upto += before ? s.weights[j] : 0;
+      rank += before;
+    }
+    atomicAdd(&s.upto[i], upto);
+    atomicAdd(&s.rank[i], rank);
+  }
+  __syncthreads();
+  const bool any = (int)threadIdx.x < count;
+  const u64 upto = any ? s.upto[i] : 0;
+  const uint32_t rank = any ? s.rank[i] : 0;
+  const u64 leave = r.k > 0 && cut.target > 0 ? cut.target - cut.before : (u64)count;  // by rank
+  u64 last = ~0ull;
+  if (r.k > 0) {
+    if (any && rank == leave) s.key_k = mine, s.total = upto;
+    __syncthreads();
+    last = s.key_k;
+  }
+  if (r.cut_p) {
+    const u64 target = r.k > 0 ? part_of(r.p, s.total) : cut.target - cut.before;
+    if (any && upto >= target && upto - w < target) s.key_p = mine;
+    __syncthreads();
+    last = s.key_p < last ? s.key_p : last;
+  }
+  return last;
+}
+
 // Key of the last token that top-k and top-p leave of the listed ones. kept(key, w): each that min-p leaves too.
 template <int N, typename Each, typename Kept>
 __device__ __forceinline__ u64 cut_list(const Row& r, const Cut& cut, Digits& s, Scan<N>& scan, Each each, Kept kept) {
   u64 last = ~0ull;
-  if (r.k > 0 && cut.target > 0) last = select_key<N, true>(r, last, cut.target - cut.before, s, each);
+  if (r.k > 0 && cut.target > 0) last = select_key<N, true>(last, cut.target - cut.before, s, each);
   if (r.cut_p) {
     u64 target = cut.target - cut.before;
     if (r.k > 0) {
@@ -350,7 +412,7 @@ __device__ __forceinline__ u64 cut_list(const Row& r, const Cut& cut, Digits& s,
       block_scan<N>(sum, scan, &total);
       target = part_of(r.p, total);
     }
-    last = select_key<N, false>(r, last, target, s, each);
+    last = select_key<N, false>(last, target, s, each);
   }
   each([&](u64 key, u64 w) __attribute__((always_inline)) {
     if (key <= last && w >= r.w_min) kept(key, w);
@@ -360,13 +422,13 @@ __device__ __forceinline__ u64 cut_list(const Row& r, const Cut& cut, Digits& s,
 
 // The same with the listed tokens token_at(0) .. token_at(count - 1): in registers, or where they are too
 // many read again each time.
-template <int N, int DT, typename TokenAt, typename Kept>
-__device__ __forceinline__ u64 cut_tokens(const Row& r, const void* p, const Cut& cut, int count, const double* table,
-                                          Digits& s, Scan<N>& scan, TokenAt token_at, Kept kept) {
+template <int N, typename TokenAt, typename Kept>
+__device__ __forceinline__ u64 cut_tokens(const Row& r, const Cut& cut, int count, const double* table, Digits& s,
+                                          Few& few, Scan<N>& scan, TokenAt token_at, Kept kept) {
   constexpr int kHeld = kList / N;
   auto look = [&](int n, u64* key, u64* w) __attribute__((always_inline)) {
-    const int token = token_at(n);
-    const float v = settle(r, load_one<DT>(p, token));
+    float v;
+    const int token = token_at(n, &v);
     *key = rank_key(v, token);
     *w = weight_of(exponent(r, v), table);
   };
@@ -374,6 +436,11 @@ __device__ __forceinline__ u64 cut_tokens(const Row& r, const void* p, const Cut
     u64 key = 0, w = 0;
     const bool any = (int)threadIdx.x < count;
     if (any) look(threadIdx.x, &key, &w);
+    if (count <= kFew) {
+      const u64 last = cut_few<N>(r, cut, count, key, w, few);
+      if (any && key <= last && w >= r.w_min) kept(key, w);
+      return last;
+    }
     return cut_list<N>(r, cut, s, scan, [&](auto f) __attribute__((always_inline)) { if (any) f(key, w); }, kept);
   }
   if (count <= kList) {
@@ -459,8 +526,9 @@ struct WholeLds {
   uint32_t counts[kBins];
   u64 found[2];
   Digits digits;
+  Few few;
   int listed;
-  uint16_t list[kList];
+  uint2 list[kList];  // token and logit
 };
 
 template <int DT, int E>
@@ -505,9 +573,8 @@ __global__ __launch_bounds__(kWhole) void whole_kernel(SampleArgs a) {
       }
     }
     __syncthreads();
-    if (r.k > 0) s.bins[threadIdx.x] = s.counts[threadIdx.x];  // read by this thread alone
-
-    cut = find_cut<kWhole>(r, s.bins, s.scan[0], s.found);
+    const u64 own[1] = {r.k > 0 ? (u64)s.counts[threadIdx.x] : s.bins[threadIdx.x]};
+    cut = find_cut<kWhole>(r, own, s.scan[0], s.found);
     if (cut.last >= 0) {
       again(v);
 #pragma unroll
@@ -516,16 +583,20 @@ __global__ __launch_bounds__(kWhole) void whole_kernel(SampleArgs a) {
         const int bin = has_weight(z) ? bin_of(r, z) : kBins;
         if (bin >= cut.first && bin <= cut.last) {
           const int at = atomicAdd(&s.listed, 1);
-          if (at < kList) s.list[at] = (uint16_t)(i0 + e);
+          if (at < kList) s.list[at] = make_uint2(i0 + e, __builtin_bit_cast(uint32_t, v[e]));
         }
         apart(e);
       }
       __syncthreads();
       const int count = s.listed;
       if (count <= kList) {
-        last = cut_tokens<kWhole, DT>(r, p, cut, count, s.table, s.digits, s.scan[1],
-                                      [&](int n) __attribute__((always_inline)) { return (int)s.list[n]; },
-                                      [](u64, u64) {});
+        last = cut_tokens<kWhole>(r, cut, count, s.table, s.digits, s.few, s.scan[1],
+                                  [&](int n, float* x) __attribute__((always_inline)) {
+                                    const uint2 l = s.list[n];
+                                    *x = __builtin_bit_cast(float, l.y);
+                                    return (int)l.x;
+                                  },
+                                  [](u64, u64) {});
       } else {  // too many to list: all logits again, from the caches
         last = cut_list<kWhole>(r, cut, s.digits, s.scan[1], [&](auto f) __attribute__((always_inline)) {
           for (int i = threadIdx.x; i < a.vocab; i += kWhole) {
@@ -652,11 +723,18 @@ __global__ __launch_bounds__(kThreads) void sums_kernel(SampleArgs a) {
   const int row = (int)(blockIdx.x / (unsigned)a.chunks), chunk = (int)(blockIdx.x - (unsigned)row * a.chunks);
   float v[kRun];
   load_run<DT>(row_of(a, row, DT), chunk * kChunk + (int)threadIdx.x * kRun, a.vocab, v);
+  u64 own[kBins / kThreads] = {};
+  if (a.bins) {
+    const ulonglong2* from = reinterpret_cast<const ulonglong2*>(a.bins + (int64_t)row * kBins) + 2 * threadIdx.x;
+    const ulonglong2 lo = from[0], hi = from[1];
+    static_assert(kBins / kThreads == 4, "two loads of two");
+    own[0] = lo.x, own[1] = lo.y, own[2] = hi.x, own[3] = hi.y;
+  }
   fill_table<kThreads>(table);
   if (threadIdx.x == 0) listed = 0;
   const Row r = row_settings(a, row, row_top(a, row));
   settle_all(r, v);
-  const Cut cut = find_cut<kThreads>(r, a.bins ? a.bins + (int64_t)row * kBins : nullptr, scan[0], found);
+  const Cut cut = find_cut<kThreads>(r, own, scan[0], found);
   __syncthreads();
   u64 sum = 0;
 #pragma unroll
@@ -671,7 +749,8 @@ __global__ __launch_bounds__(kThreads) void sums_kernel(SampleArgs a) {
       const u64 w = weight_of(z, table);
       sum += w >= r.w_min ? w : 0;
     } else {
-      a.list[(int64_t)blockIdx.x * kChunk + atomicAdd(&listed, 1)] = (uint16_t)((int)threadIdx.x * kRun + e);
+      a.list[(int64_t)blockIdx.x * kChunk + atomicAdd(&listed, 1)] =
+          make_uint2(chunk * kChunk + (int)threadIdx.x * kRun + e, __builtin_bit_cast(uint32_t, v[e]));
     }
   }
   u64 total;
@@ -694,6 +773,7 @@ struct ChooseLds {
   int starts[kSampleMaxChunks + 1];
   u64 found[2];
   Digits digits;
+  Few few;
 };
 
 template <int DT>
@@ -721,15 +801,17 @@ __global__ __launch_bounds__(kChoose) void choose_kernel(SampleArgs a) {
   __syncthreads();
   u64 last = ~0ull;  // key of the last token that top-k and top-p leave
   if (listed > 0) {
-    last = cut_tokens<kChoose, DT>(
-        r, p, cut, (int)listed, s.table, s.digits, s.scan[1],
-        [&](int n) __attribute__((always_inline)) {
+    last = cut_tokens<kChoose>(
+        r, cut, (int)listed, s.table, s.digits, s.few, s.scan[1],
+        [&](int n, float* x) __attribute__((always_inline)) {
           int lo = 0, hi = a.chunks;
           while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (s.starts[mid] <= n) lo = mid; else hi = mid;
           }
-          return lo * kChunk + (int)a.list[(first_chunk + lo) * kChunk + (n - s.starts[lo])];
+          const uint2 l = a.list[(first_chunk + lo) * kChunk + (n - s.starts[lo])];
+          *x = __builtin_bit_cast(float, l.y);
+          return (int)l.x;
         },
         [&](u64 key, u64 w) __attribute__((always_inline)) { atomicAdd(&s.chunk_sums[(uint32_t)key / kChunk], w); });
     __syncthreads();
