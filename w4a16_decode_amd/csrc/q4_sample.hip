@@ -332,8 +332,14 @@ __device__ __forceinline__ u64 select_key(u64 last, u64 target, Digits& s, Each 
     const int l = __builtin_ctzll(__ballot(here));
     prefix |= (u64)(uint32_t)__builtin_amdgcn_readlane(digit, l) << at;
     before = lane_of(upto, l);
-    bit = at == 32 ? kIndexBits : at;
-    if (bit == 0 || at == 0) break;
+    if (at == 0) break;
+    bit = at;
+    if (at >= 32) {  // down to the next bit in which any two logits differ, or to the index
+      const uint32_t below = differ & ((1u << (at - 32)) - 1);
+      bit = below ? 64 - __builtin_clz(below) : kIndexBits;
+      const uint32_t same = ((1u << (at - 32)) - 1) & ~(below ? (1u << (bit - 32)) - 1 : 0);
+      prefix |= (u64)(ones & same) << 32;
+    }
     if (__builtin_amdgcn_readlane((int)n, l) == 1) {  // the token itself
       each([&](u64 key, u64) __attribute__((always_inline)) {
         if (key <= last && (key ^ prefix) >> at == 0) s.key = key;
@@ -445,13 +451,18 @@ __device__ __forceinline__ u64 cut_tokens(const Row& r, const Cut& cut, int coun
   }
   if (count <= kList) {
     u64 keys[kHeld], weights[kHeld];
+    float v[kHeld];
+    int token[kHeld];
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)  // all loads, then what is computed of them
+      if (i * N < count) token[i] = token_at(min(i * N + (int)threadIdx.x, count - 1), &v[i]);
 #pragma unroll
     for (int i = 0; i < kHeld; ++i)
-      if (i * N + (int)threadIdx.x < count) look(i * N + threadIdx.x, &keys[i], &weights[i]);
+      if (i * N < count) keys[i] = rank_key(v[i], token[i]), weights[i] = weight_of(exponent(r, v[i]), table);
     return cut_list<N>(r, cut, s, scan, [&](auto f) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < kHeld; ++i)
-        if (i * N + (int)threadIdx.x < count) f(keys[i], weights[i]);
+        if (i * N < count && i * N + (int)threadIdx.x < count) f(keys[i], weights[i]);
     }, kept);
   }
   return cut_list<N>(r, cut, s, scan, [&](auto f) __attribute__((always_inline)) {
