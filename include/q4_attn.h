@@ -166,8 +166,8 @@ q4_status q4_paged_attention(const void* q, int64_t q_stride, const q4_paged_kv*
  * lengths; rows of a group beyond max_group_q are taken as having no prefix, longer prefixes
  * are cut. With few rows behind a short prefix a plain call whose block tables begin with the
  * prefix's pages may be as fast. Everything else, rows that see no key, infinities and what
- * results depend on among it, is q4_paged_attention's. groups * heads * max_group_q and
- * tokens * q_heads >= 2^26 are refused as seqs * heads * max_q is. */
+ * results depend on among it, is q4_paged_attention's. groups * heads * max_group_q
+ * is refused as seqs * heads * max_q is. */
 size_t q4_paged_attention_shared_workspace_bytes(int64_t seqs, int64_t groups, int64_t tokens, int64_t max_q,
                                                  int64_t max_kv, int64_t max_group_q, int64_t max_prefix,
                                                  int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t group);

@@ -133,7 +133,6 @@ def test_shared_attention_refusals(lib):
         assert f(**{name: -1}) == 2 and f(**{name: 1 << 30}) == 2, name
     assert f(hq=3) == 2 and f(hq=0) == 2 and f(qs=504) == 2 and f(qs=516) == 4
     assert f(scale=2.1e38) == 2 and f(scale=float("nan")) == 2
-    assert f(tokens=1 << 24, max_gq=1) == 2                                # 2^26 rows
     assert f(groups=1 << 22, max_gq=1 << 12, tokens=1 << 12) == 2          # too many jobs
     assert f(ws=None) == 6 and f(size=16) == 6 and f(ws=FAKE + 8) == 4
     assert f(seqs=0) == 0 and f(tokens=0) == 0 and f(max_q=0) == 0

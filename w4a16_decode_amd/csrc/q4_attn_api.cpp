@@ -208,34 +208,34 @@ q4_status check_prefix(int64_t groups, int64_t tokens, int64_t max_group_q, int6
       max_prefix >= kMaxDim)
     return fail(Q4_ERR_SHAPE, "groups=%lld, max_group_q=%lld, max_prefix=%lld out of range", (long long)groups,
                 (long long)max_group_q, (long long)max_prefix);
-  if (tokens * q_heads > 4 * kMaxGroups256)  // a wavefront a row joins the prefix's pieces
-    return fail(Q4_ERR_SHAPE, "tokens * q_heads = %lld: too many rows for one call", (long long)(tokens * q_heads));
   return check_attn(groups, tokens, max_group_q, max_prefix, q_heads, kv_heads, 0);
 }
 bool has_prefix(int64_t groups, int64_t tokens, int64_t max_group_q, int64_t max_prefix) {
   return groups > 0 && tokens > 0 && max_group_q > 0 && max_prefix > 0;
 }
 
-// Launch shape over the prefixes: 128 rows a workgroup, the keys of every job cut into as many pieces
-// as fill the chip, of 256 keys or more by the bound.
+// Launch shape over the prefixes: tiles of 16, 32 or 128 rows, the keys of every job cut into as many pieces
+// as fill the chip, each of a tile kernel's least by the bound.
 q4_status pick_prefix(int64_t groups, int64_t tokens, int64_t max_group_q, int64_t max_prefix, int32_t q_heads,
                       int32_t kv_heads, int32_t head_dim, int32_t group, q4::AttnArgs* p) {
   const int64_t rows = std::min(max_group_q, tokens) * (q_heads / kv_heads);
-  const int64_t jobs = (rows + 127) / 128 * kv_heads * groups;
-  const int64_t slots = q4::prefix_attention_resident(head_dim, group);
-  const int64_t pieces = std::max<int64_t>(1, std::min(slots / jobs, (max_prefix + 255) / 256));
+  p->rows_group = rows <= 16 ? 16 : rows > 64 ? 128 : q4::has_attn32(head_dim, head_dim / group) ? 32 : 16;
+  const int64_t tiles = (rows + p->rows_group - 1) / p->rows_group, jobs = tiles * kv_heads * groups;
+  const int64_t slots = q4::prefix_attention_resident(head_dim, group, p->rows_group);
+  const int64_t least = p->rows_group == 128 ? 256 : 128;
+  const int64_t pieces = std::max<int64_t>(1, std::min(slots / jobs, (max_prefix + least - 1) / least));
   if (jobs * pieces > kMaxGroups256) return fail(Q4_ERR_SHAPE, "groups * heads * max_group_q too large for one call");
-  p->rows_group = 128, p->shares = 0, p->whole = 0, p->tail = (int)jobs, p->pieces = (int)pieces;
+  p->shares = 0, p->whole = 0, p->tail = (int)jobs, p->pieces = (int)pieces;
+  p->prefix_pieces = (int)pieces, p->prefix_rows = (int)(tiles * p->rows_group);
   return Q4_OK;
 }
 
-// What each row starts from behind its prefix; then the partial results, whose place the two steps share.
-size_t start_bytes(int64_t tokens, int32_t q_heads, int32_t head_dim) {
-  return (size_t)q4::round_up(tokens * q_heads * (head_dim + 2) * 4, 256);
+// Partial results over the prefixes; those over the keys behind them follow.
+size_t prefix_parts(const q4::AttnArgs& p, int64_t groups, int32_t kv_heads) {
+  return (size_t)p.prefix_pieces * groups * kv_heads * p.prefix_rows;
 }
-size_t shared_workspace(const q4::AttnArgs& a, const q4::AttnArgs& p, int64_t tokens, int32_t q_heads,
-                        int32_t head_dim) {
-  return start_bytes(tokens, q_heads, head_dim) + std::max(attn_workspace(a, head_dim), attn_workspace(p, head_dim));
+size_t prefix_bytes(const q4::AttnArgs& p, int64_t groups, int32_t kv_heads, int32_t head_dim) {
+  return (size_t)q4::round_up(prefix_parts(p, groups, kv_heads) * (head_dim + 2) * 4, 256);
 }
 
 }  // namespace
@@ -356,7 +356,7 @@ size_t q4_paged_attention_shared_workspace_bytes(int64_t seqs, int64_t groups, i
   if (pick_attn(seqs, tokens, max_q, max_kv, q_heads, kv_heads, head_dim, group, 0, &a) != Q4_OK) return 0;
   if (!has_prefix(groups, tokens, max_group_q, max_prefix)) return attn_workspace(a, head_dim);
   if (pick_prefix(groups, tokens, max_group_q, max_prefix, q_heads, kv_heads, head_dim, group, &p) != Q4_OK) return 0;
-  return shared_workspace(a, p, tokens, q_heads, head_dim);
+  return prefix_bytes(p, groups, kv_heads, head_dim) + attn_workspace(a, head_dim);
 }
 
 q4_status q4_paged_attention_shared(const void* q, int64_t q_stride, const q4_paged_kv* cache,
@@ -389,7 +389,7 @@ q4_status q4_paged_attention_shared(const void* q, int64_t q_stride, const q4_pa
     st = pick_prefix(groups, tokens, max_group_q, max_prefix, q_heads, a.cache.kv_heads, a.cache.head_dim,
                      a.cache.group, &p);
     if (st != Q4_OK) return st;
-    need = shared_workspace(a, p, tokens, q_heads, a.cache.head_dim);
+    need += prefix_bytes(p, groups, a.cache.kv_heads, a.cache.head_dim);
   }
   if (need > 0) {
     st = check_workspace(workspace, workspace_bytes, need, "q4_paged_attention_shared_workspace_bytes");
@@ -400,12 +400,11 @@ q4_status q4_paged_attention_shared(const void* q, int64_t q_stride, const q4_pa
     place_parts(&a, workspace);
     return hip_status(q4::launch_attention(a, s), "attention launch");
   }
-  // the rows' starts, then the partial results of one step after the other
-  unsigned char* parts = static_cast<unsigned char*>(workspace) + start_bytes(tokens, q_heads, a.cache.head_dim);
-  p.init_o = a.init_o = static_cast<float*>(workspace);
-  p.init_ml = a.init_ml = a.init_o + tokens * q_heads * a.cache.head_dim;
-  place_parts(&p, parts);
-  place_parts(&a, parts);
+  p.part_o = static_cast<float*>(workspace);
+  p.part_ml = p.part_o + prefix_parts(p, groups, a.cache.kv_heads) * a.cache.head_dim;
+  a.prefix_o = p.part_o, a.prefix_ml = p.part_ml, a.prefix_pieces = p.prefix_pieces, a.prefix_rows = p.prefix_rows;
+  a.group_offsets = group_offsets, a.groups = (int)groups, a.max_group_q = p.max_q;
+  place_parts(&a, static_cast<unsigned char*>(workspace) + prefix_bytes(p, groups, a.cache.kv_heads, a.cache.head_dim));
   hipError_t e = q4::launch_prefix_attention(p, s);
   if (e == hipSuccess) e = q4::launch_behind_attention(a, s);
   return hip_status(e, "attention with shared prefixes launch");

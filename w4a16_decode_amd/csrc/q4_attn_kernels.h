@@ -156,7 +156,7 @@ __device__ __forceinline__ ScalarInts scalar_ints(const int32_t* p) { return (Sc
 
 // What a launch is for: all keys of its sequences; the prefix that groups of sequences share (its
 // "sequences" are the groups, their rows those of all members, and every row sees every key), left
-// as partial results; or the keys behind a prefix, whose result each row starts from.
+// as partial results; or the keys behind a prefix, where each row starts from those.
 enum AttnMode { kPlain, kPrefix, kBehind };
 
 // What a workgroup works on.
@@ -232,21 +232,61 @@ __device__ __forceinline__ uint2* out_at(const AttnArgs& a, const Job& w, int ro
   return reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + r * D + ch);
 }
 
-// The state that a row behind a prefix starts from: the prefix's output o and the logarithm m of
-// its sum of weights as maximum. (At most log2 of the prefix's keys above its largest score: that many
-// of the weights' 26 binades.) `any` false: the row has no prefix.
-struct Start {
-  const float* o;
-  float m;
-  bool any, low;  // low: the prefix's scores were all -infinity
-};
-__device__ __forceinline__ Start start_of(const AttnArgs& a, const Job& w, int row) {
-  const int i = row / w.share, hs = row - i * w.share;
-  const int64_t r = (int64_t)(w.first + i) * a.q_heads + w.head * w.share + hs;
-  const float2 ml = *reinterpret_cast<const float2*>(a.init_ml + 2 * r);
-  return Start{a.init_o + r * a.cache.head_dim, ml.x, !(ml.y <= 0.0f), ml.y < 0.0f};
+// Partial results over the prefixes: [pieces][groups][kv_heads][prefix_rows], a group's rows for a KV head
+// padded to whole tiles.
+__device__ __forceinline__ int64_t prefix_row(const AttnArgs& a, int groups, int piece, int group, int head, int row) {
+  return (((int64_t)piece * groups + group) * a.cache.kv_heads + head) * a.prefix_rows + row;
 }
-constexpr float kStartScale = 18446744073709551616.0f;  // 2^64: weights relative to E = -64
+
+// Those that a job's rows start from: group (below 0: none), the first row of the group's tokens and their number.
+struct Before {
+  int group, first, tokens;
+};
+__device__ __forceinline__ Before before_of(const AttnArgs& a, int seq) {
+  const int lane = threadIdx.x & 63;
+  for (int base = 0; base < a.groups; base += kWave) {
+    int begin = 0, end = 0;
+    if (base + lane < a.groups) {
+      begin = min(max(a.group_offsets[base + lane], 0), a.seqs);
+      end = min(max(a.group_offsets[base + lane + 1], begin), a.seqs);
+    }
+    const uint64_t in = __ballot(seq >= begin && seq < end);
+    if (in) {
+      const int at = __builtin_ctzll(in);
+      const int b0 = __builtin_amdgcn_readlane(begin, at), b1 = __builtin_amdgcn_readlane(end, at);
+      const int first = min(max(scalar_ints(a.q_offsets)[b0], 0), a.tokens);
+      const int last = min(max(scalar_ints(a.q_offsets)[b1], first), a.tokens);
+      return Before{base + at, first, min(last - first, a.max_group_q)};
+    }
+  }
+  return Before{-1, 0, 0};
+}
+
+// A row's start: pieces piece0, piece0 + step, ... of its prefix, added up in order: base, limit and sum of a
+// row that has seen keys, add(o, f) a piece's output times f. m + E of the prefix is taken as m here, E as 0.
+template <typename Add>
+__device__ __forceinline__ void start_row(const AttnArgs& a, const Job& w, const Before& p, int row, int piece0, int step,
+                                          float* base, float* limit, float* sum, bool* low, Add add) {
+  const int i = row / w.share, token = w.first + i - p.first;
+  if (p.group < 0 || token < 0 || token >= p.tokens) return;
+  const int64_t at = prefix_row(a, a.groups, piece0, p.group, w.head, token * w.share + row - i * w.share);
+  const int64_t stride = step * (int64_t)a.groups * a.cache.kv_heads * a.prefix_rows;
+  const float2* ml = reinterpret_cast<const float2*>(a.prefix_ml) + at;
+  const float* o = a.prefix_o + at * a.cache.head_dim;
+  float top = kLowest, l = 0.0f;
+#pragma unroll 4
+  for (int n = piece0; n < a.prefix_pieces; n += step, ml += stride) top = fmaxf(top, ml->x);
+  ml = reinterpret_cast<const float2*>(a.prefix_ml) + at;
+#pragma unroll 2
+  for (int n = piece0; n < a.prefix_pieces; n += step, ml += stride, o += stride * a.cache.head_dim) {
+    const float2 v = *ml;
+    const float f = exp2_fast(v.x - top);
+    l = __builtin_fmaf(v.y, f, l);
+    add(o, f);
+  }
+  *low = l < 0.0f;
+  if (!(l <= 0.0f)) *base = top, *limit = kSlack, *sum = l;
+}
 
 // ---------------------------------------------------------------------------------
 // Work shares. Where the wavefronts of a workgroup split the keys, a job (RG rows of a sequence
@@ -355,7 +395,7 @@ struct Shares {
   }
 
   __device__ __forceinline__ bool begin(const AttnArgs& a, int rg, int lane) {
-    whole = a.shares == 0;
+    whole = a.shares == 0;  // (also over prefixes)
     if (whole) {
       at = blockIdx.x;
       return true;
@@ -389,18 +429,33 @@ struct Shares {
     return true;
   }
 
+  template <int MODE = kPlain>
   __device__ __forceinline__ bool next(const AttnArgs& a, int rg, int lane, int tiles, Piece* p) {
-    if (whole) {
+    if (MODE == kPrefix || whole) {
       if (at < 0) return false;
-      const unsigned j = (unsigned)at, heads = (unsigned)a.cache.kv_heads;
+      unsigned j = (unsigned)at;
+      const unsigned heads = (unsigned)a.cache.kv_heads;
       at = -1;
+      int piece = 0;
+      if constexpr (MODE == kPrefix) {  // row tiles of the same keys next to each other
+        const unsigned tile = j % (unsigned)tiles, line = j / (unsigned)tiles;
+        piece = uniform((int)(line % (unsigned)a.prefix_pieces));
+        const unsigned group_head = line / (unsigned)a.prefix_pieces;
+        j = (group_head / heads * (unsigned)tiles + tile) * heads + group_head % heads;
+      }
       const int group = uniform((int)(j / heads));
       const int seq = uniform((int)((unsigned)group / (unsigned)tiles));
-      if (!make_job(a, seq, (int)j - group * (int)heads, &p->w)) return false;
+      if (!make_job<MODE>(a, seq, (int)j - group * (int)heads, &p->w)) return false;
       p->r0 = (group - seq * tiles) * rg;
       p->key0 = 0;
       p->key1 = -1;
       p->slot = -1;
+      if constexpr (MODE == kPrefix) {  // its units, cut evenly
+        const int units = (p->w.len + kUnit - 1) / kUnit, next = piece + 1;
+        p->key0 = uniform((int)((int64_t)units * piece / a.prefix_pieces)) * kUnit;
+        if (next < a.prefix_pieces) p->key1 = uniform((int)((int64_t)units * next / a.prefix_pieces)) * kUnit;
+        p->slot = piece;
+      }
       return p->r0 < p->w.rows;
     }
     if (at >= end) return false;
@@ -435,9 +490,16 @@ struct Shares {
 };
 
 // Channels ch .. ch + 3 of a piece's row r0 + local: the output, or the piece's slot.
-template <int D, int RG>
+template <int D, int RG, int MODE = kPlain>
 __device__ __forceinline__ void store_piece(const AttnArgs& a, const Piece& p, int local, int ch, float4_t o, float sum,
                                             float base) {
+  if constexpr (MODE == kPrefix) {
+    if (p.r0 + local >= p.w.rows) return;
+    const int64_t at = prefix_row(a, a.seqs, p.slot, p.w.seq, p.w.head, p.r0 + local);
+    *reinterpret_cast<float4_t*>(a.part_o + at * D + ch) = o;
+    if (ch == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(base, sum);
+    return;
+  }
   if (p.slot < 0) {
     if (p.r0 + local < p.w.rows) *out_at<D>(a, p.w, p.r0 + local, ch) = to_row(o, sum);
     return;
@@ -491,7 +553,7 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
   bool more = uniform(shares.begin(a, 16, lane));
   for (bool again = false; more; again = true) {
     Piece next_piece;
-    if (!uniform(shares.next(a, 16, lane, tiles, &next_piece))) break;
+    if (!uniform(shares.next<MODE>(a, 16, lane, tiles, &next_piece))) break;
     pc = uniform_piece(next_piece);
     if (again) __syncthreads();  // buf of the piece before has been read
     const Job& w = pc.w;
@@ -501,7 +563,7 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
     int pos;  // position of the lane's row: its own last visible key; -1: no row
     {
       const int i = min(row, w.rows - 1) / w.share, hs = min(row, w.rows - 1) - i * w.share;
-      pos = row < w.rows ? w.len - w.nq + i : -1;
+      pos = row < w.rows ? MODE == kPrefix ? w.len - 1 : w.len - w.nq + i : -1;
       const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.first + i) * a.q_stride +
                             (int64_t)(w.head * w.share + hs) * D + 8 * c4;
 #pragma unroll
@@ -514,26 +576,23 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
     float4_t acc[2 * KB];
 #pragma unroll
     for (int b = 0; b < 2 * KB; ++b) acc[b] = float4_t{0.f, 0.f, 0.f, 0.f};
+    float exp_v = MODE == kBehind ? 0.0f : -64.0f;  // E (wave-uniform)
     if constexpr (MODE == kBehind) {
-      if (wave == 0 && pc.slot != 0) {
-        const Start st = start_of(a, w, min(row, w.rows - 1));
-        low = st.low;
-        if (st.any) {
-          base = st.m - 64.0f;
-          limit = kSlack + 64.0f;
-          l = c4 == 0 ? kStartScale : 0.0f;
+      // a quarter of the prefix's pieces each
+      if (pc.slot != 0)
+        start_row(a, w, before_of(a, w.seq), min(row, w.rows - 1), wave, 4, &base, &limit, &l, &low,
+                  [&](const float* o, float f) __attribute__((always_inline)) {
 #pragma unroll
-          for (int b = 0; b < 2 * KB; ++b)
-            acc[b] = *reinterpret_cast<const float4_t*>(st.o + 16 * b + 4 * c4) * kStartScale;
-        }
-      }
+                    for (int b = 0; b < 2 * KB; ++b)
+                      acc[b] += *reinterpret_cast<const float4_t*>(o + 16 * b + 4 * c4) * f;
+                  });
+      if (c4 != 0) l = 0.0f;
     }
 
-    const Span sp = span_of(a, w, pc.r0, 16);
+    const Span sp = span_of<MODE>(a, w, pc.r0, 16);
     const int t_first = max(pc.key0, sp.first);
     const int t_last = pc.key1 < 0 ? sp.last : min(sp.last, pc.key1);
     const ScalarInts table = scalar_ints(a.block_table + (int64_t)w.seq * a.max_blocks);
-    float exp_v = -64.0f;  // E (wave-uniform)
     uint32_t cap_v = 0;    // largest V scale that E covers, as float16 bits
 
     const int last_tile = max(t_last - 1, 0) / kTokTile;
@@ -738,7 +797,7 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
       float4_t o = buf[0][c][lane] * f[0];
 #pragma unroll
       for (int v = 1; v < 4; ++v) o += buf[v][c][lane] * f[v];
-      store_piece<D, 16>(a, pc, col, 16 * c + 4 * c4, o, sum, top);
+      store_piece<D, 16, MODE>(a, pc, col, 16 * c + 4 * c4, o, sum, top);
     }
   }
   shares.finish(a, pc);
@@ -782,23 +841,22 @@ __device__ __forceinline__ half4_t v_codes4(uint32_t w, const VRegs& k) {
   return __builtin_shufflevector(a, b, 0, 1, 2, 3);
 }
 
-// A row's start in the layout of the 32-row kernels (kStartScale above).
+// A row's start in the layout of the 32-row kernels.
 template <int KB>
-__device__ __forceinline__ void start32(const Start& st, int c, float* base, float* limit, float* l, bool* low,
-                                        float16_t (&acc)[KB]) {
-  *low = st.low;
-  if (!st.any) return;
-  *base = st.m - 64.0f;
-  *limit = kSlack + 64.0f;
-  *l = c == 0 ? kStartScale : 0.0f;
+__device__ __forceinline__ void start32(const AttnArgs& a, const Job& w, int row, int piece0, int step, int c, float* base,
+                                        float* limit, float* l, bool* low, float16_t (&acc)[KB]) {
+  start_row(a, w, before_of(a, w.seq), min(row, w.rows - 1), piece0, step, base, limit, l, low,
+            [&](const float* o, float f) __attribute__((always_inline)) {
 #pragma unroll
-  for (int b = 0; b < KB; ++b)
+              for (int b = 0; b < KB; ++b)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float4_t o = *reinterpret_cast<const float4_t*>(st.o + 32 * b + 8 * u + 4 * c) * kStartScale;
+                for (int u = 0; u < 4; ++u) {
+                  const float4_t x = *reinterpret_cast<const float4_t*>(o + 32 * b + 8 * u + 4 * c) * f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[b][4 * u + e] = o[e];
-    }
+                  for (int e = 0; e < 4; ++e) acc[b][4 * u + e] += x[e];
+                }
+            });
+  if (c != 0) *l = 0.0f;
 }
 
 template <int D, int GC, int MODE = kPlain>
@@ -823,7 +881,7 @@ __global__ __launch_bounds__(256, 2) void attn32_kernel(AttnArgs a, int tiles) {
   bool more = uniform(shares.begin(a, 32, lane));
   for (bool again = false; more; again = true) {
     Piece next_piece;
-    if (!uniform(shares.next(a, 32, lane, tiles, &next_piece))) break;
+    if (!uniform(shares.next<MODE>(a, 32, lane, tiles, &next_piece))) break;
     pc = uniform_piece(next_piece);
     if (again) __syncthreads();  // buf of the piece before has been read
     const Job& w = pc.w;
@@ -834,7 +892,7 @@ __global__ __launch_bounds__(256, 2) void attn32_kernel(AttnArgs a, int tiles) {
     int pos;  // position of the lane's row: its own last visible key; -1: no row
     {
       const int i = min(row, w.rows - 1) / w.share, hs = min(row, w.rows - 1) - i * w.share;
-      pos = row < w.rows ? w.len - w.nq + i : -1;
+      pos = row < w.rows ? MODE == kPrefix ? w.len - 1 : w.len - w.nq + i : -1;
       const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.first + i) * a.q_stride +
                             (int64_t)(w.head * w.share + hs) * D + 8 * c;
 #pragma unroll
@@ -847,14 +905,14 @@ __global__ __launch_bounds__(256, 2) void attn32_kernel(AttnArgs a, int tiles) {
     float16_t acc[KB];
 #pragma unroll
     for (int b = 0; b < KB; ++b) acc[b] = float16_t{};
+    float exp_v = MODE == kBehind ? 0.0f : -64.0f;  // E (wave-uniform)
     if constexpr (MODE == kBehind) {
-      if (wave == 0 && pc.slot != 0) start32<KB>(start_of(a, w, min(row, w.rows - 1)), c, &base, &limit, &l, &low, acc);
+      if (pc.slot != 0) start32<KB>(a, w, row, wave, 4, c, &base, &limit, &l, &low, acc);
     }
 
-    const Span sp = span_of(a, w, r0, 32);
+    const Span sp = span_of<MODE>(a, w, r0, 32);
     const int t_own = max(pc.key0, sp.first) + kStep * wave;
     const int t_last = pc.key1 < 0 ? sp.last : min(sp.last, pc.key1);
-    float exp_v = -64.0f;  // E (wave-uniform)
     uint32_t cap_v = 0;    // largest V scale that E covers, as float16 bits
 
     const ScalarInts table = scalar_ints(a.block_table + (int64_t)w.seq * a.max_blocks);
@@ -1090,7 +1148,7 @@ __global__ __launch_bounds__(256, 2) void attn32_kernel(AttnArgs a, int tiles) {
         sum = __builtin_fmaf(ml[v][col].y, f, sum);
         o += buf[v][wave][lane] * f;
       }
-      store_piece<D, 32>(a, pc, col, 32 * b + 8 * wave + 4 * c, o, sum, top);
+      store_piece<D, 32, MODE>(a, pc, col, 32 * b + 8 * wave + 4 * c, o, sum, top);
     }
   }
   shares.finish(a, pc);
@@ -1179,8 +1237,9 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
   float16_t acc[KB];
 #pragma unroll
   for (int b = 0; b < KB; ++b) acc[b] = float16_t{};
+  float exp_v = MODE == kBehind ? 0.0f : -64.0f;  // E (wave-uniform)
   if constexpr (MODE == kBehind) {
-    if (piece == 0) start32<KB>(start_of(a, w, min(row, w.rows - 1)), c, &base, &limit, &l, &low, acc);
+    if (piece == 0) start32<KB>(a, w, row, 0, 1, c, &base, &limit, &l, &low, acc);
   }
 
   const Span all = span_of<MODE>(a, w, g0, kGroup);                   // the workgroup's keys
@@ -1194,7 +1253,6 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
     t_first += kKeys * b0;
   }
   const float scale = a.scale * 1.4426950408889634f;
-  float exp_v = -64.0f;  // E (wave-uniform)
   int cap_v = 0;         // largest V scale that E covers, as float16 bits
 
   // --- producer: one pair of tiles of K (wavefronts 0, 1) or of V (2, 3) every 64 keys
@@ -1409,7 +1467,8 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
   l += __shfl_xor(l, 32, 64);
   if (row >= w.rows) return;
   if (cut) {
-    const int64_t slot = (int64_t)behind * kGroup + 32 * wave + col;
+    const int64_t slot = MODE == kPrefix ? prefix_row(a, a.seqs, piece, w.seq, w.head, row)
+                                         : (int64_t)behind * kGroup + 32 * wave + col;
 #pragma unroll
     for (int b = 0; b < KB; ++b)
 #pragma unroll

@@ -134,13 +134,13 @@ struct AttnArgs {
   float* part_o;   // partial results: float32 [shares][2][rows_group] or [pieces][tail][128], [head_dim]
   float* part_ml;  // and as many [2]: what exponents are relative to, sum
   int32_t* cuts;   // shares > 0: int32 [shares][8], the job a share begins and does not end
-  // shared prefixes: the sequences are groups, group g's members group_offsets[g] .. [g + 1] - 1 of `members`
+  // Shared prefixes. Over them the sequences are the groups, group g's members group_offsets[g] .. [g + 1] - 1 of
+  // `members`; behind them the rows start from the partial results in prefix_o and prefix_ml.
   const int32_t* group_offsets;
-  int members;
-  // what rows behind a prefix start from: float32 [tokens][q_heads][head_dim] and [tokens][q_heads][2], the
-  // logarithm (base 2) of the sum of weights and 1 (0: no prefix, below 0: one of scores of -infinity only)
-  float* init_o;
-  float* init_ml;
+  int members, groups, max_group_q;
+  int prefix_pieces, prefix_rows;  // pieces of a prefix's keys; rows of a group for a KV head, in whole tiles
+  const float* prefix_o;           // float32 [prefix_pieces][groups][kv_heads][prefix_rows][head_dim]
+  const float* prefix_ml;          // and [2]: what exponents are relative to, sum
 };
 
 // Whether tiles of 32 rows whose wavefronts split the keys are built: 256 channels, or four
@@ -220,11 +220,10 @@ struct LoraArgs {
 int lora_splits(int K);  // slices of the channel range of A x
 hipError_t launch_lora(const LoraArgs& a, hipStream_t stream);
 hipError_t launch_attention(const AttnArgs& a, hipStream_t stream);
-// Attention over shared prefixes into init_o and init_ml (rows_group 128, all jobs cut into `pieces`), and
-// over the keys behind them from there.
+// Attention over shared prefixes into part_o and part_ml, and over the keys behind them from there.
 hipError_t launch_prefix_attention(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_behind_attention(const AttnArgs& a, hipStream_t stream);
-int prefix_attention_resident(int head_dim, int group);
+int prefix_attention_resident(int head_dim, int group, int rows_group);
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
 hipError_t launch_paged_dequant(const PagedArgs& c, const int32_t* slots, int64_t tokens, void* k_out, void* v_out,
                                 hipStream_t stream);
