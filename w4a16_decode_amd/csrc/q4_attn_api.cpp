@@ -214,28 +214,53 @@ bool has_prefix(int64_t groups, int64_t tokens, int64_t max_group_q, int64_t max
   return groups > 0 && tokens > 0 && max_group_q > 0 && max_prefix > 0;
 }
 
-// Launch shape over the prefixes: tiles of 16, 32 or 128 rows, the keys of every job cut into as many pieces
-// as fill the chip, each of a tile kernel's least by the bound.
-q4_status pick_prefix(int64_t groups, int64_t tokens, int64_t max_group_q, int64_t max_prefix, int32_t q_heads,
-                      int32_t kv_heads, int32_t head_dim, int32_t group, q4::AttnArgs* p) {
-  const int64_t rows = std::min(max_group_q, tokens) * (q_heads / kv_heads);
-  p->rows_group = rows <= 16 ? 16 : rows > 64 ? 128 : q4::has_attn32(head_dim, head_dim / group) ? 32 : 16;
-  const int64_t tiles = (rows + p->rows_group - 1) / p->rows_group, jobs = tiles * kv_heads * groups;
-  const int64_t slots = q4::prefix_attention_resident(head_dim, group, p->rows_group);
-  const int64_t least = p->rows_group == 128 ? 256 : 128;
-  const int64_t pieces = std::max<int64_t>(1, std::min(slots / jobs, (max_prefix + least - 1) / least));
-  if (jobs * pieces > kMaxGroups256) return fail(Q4_ERR_SHAPE, "groups * heads * max_group_q too large for one call");
-  p->shares = 0, p->whole = 0, p->tail = (int)jobs, p->pieces = (int)pieces;
-  p->prefix_pieces = (int)pieces, p->prefix_rows = (int)(tiles * p->rows_group);
+// Launch shape of an attention call with shared prefixes, whose own keys' shape pick_attn has picked already.
+// Up to 256 rows of a group a KV head (and 16 of a sequence): one launch of 16-row tiles over prefixes and
+// own keys, cut into pieces of equal length until they are one round of the chip, then a join.
+// Else 128-row workgroups over the prefixes, cut until they fill the chip, and the rows behind them start from
+// those pieces.
+constexpr int64_t kMaxPieces = 64;
+q4_status pick_shared(int64_t groups, int64_t max_group_q, int64_t max_prefix, q4::AttnArgs* a) {
+  const int heads = a->cache.kv_heads, share = a->q_heads / heads, d = a->cache.head_dim, g = a->cache.group;
+  a->groups = (int)groups, a->max_group_q = (int)std::min<int64_t>(max_group_q, a->tokens), a->max_prefix = (int)max_prefix;
+  const int64_t rows = (int64_t)a->max_group_q * share, own_rows = (int64_t)a->max_q * share;
+  if (rows <= 256) {
+    a->rows_group = 16, a->shares = 0, a->whole = 0, a->tail = 0, a->pieces = 0;
+    const int64_t jobs = (rows + 15) / 16 * heads * groups, own = (own_rows + 15) / 16 * heads * a->seqs;
+    const int64_t slots = q4::prefix_attention_resident(d, g, 16);
+    auto pieces = [](int64_t keys, int64_t units) { return std::max<int64_t>(1, (keys + 128 * units - 1) / (128 * units)); };
+    int64_t lo = (std::max<int64_t>(max_prefix, a->max_kv) + 128 * kMaxPieces - 1) / (128 * kMaxPieces);
+    int64_t hi = std::max<int64_t>(max_prefix, a->max_kv) / 128 + 1;  // units of 128 keys a piece
+    lo = std::max<int64_t>(lo, 1);
+    while (lo < hi) {
+      const int64_t mid = (lo + hi) / 2;
+      if (jobs * pieces(max_prefix, mid) + own * pieces(a->max_kv, mid) <= slots) hi = mid; else lo = mid + 1;
+    }
+    a->prefix_pieces = (int)pieces(max_prefix, lo), a->own_pieces = (int)pieces(a->max_kv, lo);
+    a->prefix_rows = (int)((rows + 15) / 16 * 16);
+    if (jobs * a->prefix_pieces + own * a->own_pieces > kMaxGroups256 || own > kMaxGroups256 / 2)
+      return fail(Q4_ERR_SHAPE, "groups * heads * max_group_q too large for one call");
+    return Q4_OK;
+  }
+  a->own_pieces = 0;
+  const int64_t jobs = (rows + 127) / 128 * heads * groups;
+  const int64_t slots = q4::prefix_attention_resident(d, g, 128);
+  const int64_t pieces = std::max<int64_t>(1, std::min(slots / jobs, (max_prefix + 255) / 256));
+  if (jobs * pieces > kMaxGroups256 / 2) return fail(Q4_ERR_SHAPE, "groups * heads * max_group_q too large for one call");
+  a->prefix_pieces = (int)pieces, a->prefix_rows = (int)((rows + 127) / 128 * 128);
   return Q4_OK;
 }
 
 // Partial results over the prefixes; those over the keys behind them follow.
-size_t prefix_parts(const q4::AttnArgs& p, int64_t groups, int32_t kv_heads) {
-  return (size_t)p.prefix_pieces * groups * kv_heads * p.prefix_rows;
+size_t prefix_parts(const q4::AttnArgs& a) {
+  return (size_t)a.prefix_pieces * a.groups * a.cache.kv_heads * a.prefix_rows;
 }
-size_t prefix_bytes(const q4::AttnArgs& p, int64_t groups, int32_t kv_heads, int32_t head_dim) {
-  return (size_t)q4::round_up(prefix_parts(p, groups, kv_heads) * (head_dim + 2) * 4, 256);
+size_t prefix_bytes(const q4::AttnArgs& a) {
+  return (size_t)q4::round_up(prefix_parts(a) * (a.cache.head_dim + 2) * 4, 256);
+}
+size_t shared_workspace(const q4::AttnArgs& a) {
+  const size_t own = (size_t)a.own_pieces * a.tokens * a.q_heads * (a.cache.head_dim + 2) * 4;
+  return prefix_bytes(a) + (a.own_pieces > 0 ? own : attn_workspace(a, a.cache.head_dim));
 }
 
 }  // namespace
@@ -352,11 +377,14 @@ size_t q4_paged_attention_shared_workspace_bytes(int64_t seqs, int64_t groups, i
   if (check_attn(seqs, tokens, max_q, max_kv, q_heads, kv_heads, 0) != Q4_OK) return 0;
   if (check_prefix(groups, tokens, max_group_q, max_prefix, q_heads, kv_heads) != Q4_OK) return 0;
   if (check_paged_dims(1, 16, kv_heads, head_dim, group) != Q4_OK) return 0;
-  q4::AttnArgs a{}, p{};
+  q4::AttnArgs a{};
+  a.cache.kv_heads = kv_heads, a.cache.head_dim = head_dim, a.cache.group = group;
+  a.seqs = (int)seqs, a.tokens = (int)tokens, a.max_q = (int)std::min(max_q, tokens), a.max_kv = (int)max_kv;
+  a.q_heads = q_heads;
   if (pick_attn(seqs, tokens, max_q, max_kv, q_heads, kv_heads, head_dim, group, 0, &a) != Q4_OK) return 0;
-  if (!has_prefix(groups, tokens, max_group_q, max_prefix)) return attn_workspace(a, head_dim);
-  if (pick_prefix(groups, tokens, max_group_q, max_prefix, q_heads, kv_heads, head_dim, group, &p) != Q4_OK) return 0;
-  return prefix_bytes(p, groups, kv_heads, head_dim) + attn_workspace(a, head_dim);
+  if (seqs == 0 || max_q == 0 || !has_prefix(groups, tokens, max_group_q, max_prefix)) return attn_workspace(a, head_dim);
+  if (pick_shared(groups, max_group_q, max_prefix, &a) != Q4_OK) return 0;
+  return shared_workspace(a);
 }
 
 q4_status q4_paged_attention_shared(const void* q, int64_t q_stride, const q4_paged_kv* cache,
@@ -376,20 +404,16 @@ q4_status q4_paged_attention_shared(const void* q, int64_t q_stride, const q4_pa
     return fail(Q4_ERR_SHAPE, "max_prefix_blocks=%lld out of range", (long long)max_prefix_blocks);
   if (!any) return ok();
   const bool prefix = has_prefix(groups, tokens, max_group_q, max_prefix);
-  q4::AttnArgs p = a;
   size_t need = attn_workspace(a, a.cache.head_dim);
   if (prefix) {
     if (!prefix_lens || !group_offsets || (!prefix_table && max_prefix_blocks > 0))
       return fail(Q4_ERR_NULL, "prefix_table, prefix_lens, group_offsets must be non-NULL");
     if (!aligned(prefix_table, 4) || !aligned(prefix_lens, 4) || !aligned(group_offsets, 4))
       return fail(Q4_ERR_ALIGN, "prefix_table, prefix_lens and group_offsets need 4-byte alignment");
-    p.block_table = prefix_table, p.max_blocks = (int)max_prefix_blocks, p.kv_lens = prefix_lens;
-    p.group_offsets = group_offsets, p.members = a.seqs, p.seqs = (int)groups;
-    p.max_q = (int)std::min(max_group_q, tokens), p.max_kv = (int)max_prefix;
-    st = pick_prefix(groups, tokens, max_group_q, max_prefix, q_heads, a.cache.kv_heads, a.cache.head_dim,
-                     a.cache.group, &p);
-    if (st != Q4_OK) return st;
-    need += prefix_bytes(p, groups, a.cache.kv_heads, a.cache.head_dim);
+    a.prefix_table = prefix_table, a.prefix_blocks = (int)max_prefix_blocks, a.prefix_lens = prefix_lens;
+    a.group_offsets = group_offsets;
+    if ((st = pick_shared(groups, max_group_q, max_prefix, &a)) != Q4_OK) return st;
+    need = shared_workspace(a);
   }
   if (need > 0) {
     st = check_workspace(workspace, workspace_bytes, need, "q4_paged_attention_shared_workspace_bytes");
@@ -400,11 +424,17 @@ q4_status q4_paged_attention_shared(const void* q, int64_t q_stride, const q4_pa
     place_parts(&a, workspace);
     return hip_status(q4::launch_attention(a, s), "attention launch");
   }
-  p.part_o = static_cast<float*>(workspace);
-  p.part_ml = p.part_o + prefix_parts(p, groups, a.cache.kv_heads) * a.cache.head_dim;
-  a.prefix_o = p.part_o, a.prefix_ml = p.part_ml, a.prefix_pieces = p.prefix_pieces, a.prefix_rows = p.prefix_rows;
-  a.group_offsets = group_offsets, a.groups = (int)groups, a.max_group_q = p.max_q;
-  place_parts(&a, static_cast<unsigned char*>(workspace) + prefix_bytes(p, groups, a.cache.kv_heads, a.cache.head_dim));
+  a.prefix_o = static_cast<float*>(workspace);
+  a.prefix_ml = a.prefix_o + prefix_parts(a) * a.cache.head_dim;
+  void* behind = static_cast<unsigned char*>(workspace) + prefix_bytes(a);
+  if (a.own_pieces > 0) {
+    a.part_o = static_cast<float*>(behind);
+    a.part_ml = a.part_o + (size_t)a.own_pieces * a.tokens * a.q_heads * a.cache.head_dim;
+    return hip_status(q4::launch_both_attention(a, s), "attention with shared prefixes launch");
+  }
+  place_parts(&a, behind);
+  q4::AttnArgs p = a;  // over the prefixes every job is cut
+  p.shares = 0, p.whole = 0, p.pieces = a.prefix_pieces, p.tail = a.prefix_rows / 128 * a.cache.kv_heads * a.groups;
   hipError_t e = q4::launch_prefix_attention(p, s);
   if (e == hipSuccess) e = q4::launch_behind_attention(a, s);
   return hip_status(e, "attention with shared prefixes launch");

@@ -154,10 +154,11 @@ __device__ __forceinline__ void load_tile(Tile<D, GC>& t, const PagedArgs& c, in
 typedef const __attribute__((address_space(4))) int32_t* ScalarInts;
 __device__ __forceinline__ ScalarInts scalar_ints(const int32_t* p) { return (ScalarInts)(uintptr_t)p; }
 
-// What a launch is for: all keys of its sequences; the prefix that groups of sequences share (its
-// "sequences" are the groups, their rows those of all members, and every row sees every key), left
-// as partial results; or the keys behind a prefix, where each row starts from those.
-enum AttnMode { kPlain, kPrefix, kBehind };
+// What a launch is for: all keys of its sequences; the prefix that groups of sequences share (a job's
+// "sequence" is a group, its rows those of all members, and every row sees every key), left as
+// partial results; the keys behind a prefix, where each row starts from those; or prefixes and the keys
+// behind them next to each other, all left as partial results.
+enum AttnMode { kPlain, kPrefix, kBehind, kBoth };
 
 // What a workgroup works on.
 struct Job {
@@ -165,22 +166,22 @@ struct Job {
   int seq, head, share;
 };
 
-template <int MODE = kPlain>
-__device__ __forceinline__ bool make_job(const AttnArgs& a, int seq, int head, Job* w) {
+// over: over a prefix, `seq` being the group.
+__device__ __forceinline__ bool make_job(const AttnArgs& a, int seq, int head, Job* w, bool over = false) {
   // kept inside what the arguments promise
   w->seq = seq;
   w->head = head;
   w->share = __builtin_amdgcn_readfirstlane(a.q_heads / a.cache.kv_heads);
   const ScalarInts offsets = scalar_ints(a.q_offsets);
   int begin = seq, end = seq + 1;
-  if constexpr (MODE == kPrefix) {
+  if (over) {
     const ScalarInts groups = scalar_ints(a.group_offsets);
-    begin = min(max(groups[seq], 0), a.members);
-    end = min(max(groups[seq + 1], begin), a.members);
+    begin = min(max(groups[seq], 0), a.seqs);
+    end = min(max(groups[seq + 1], begin), a.seqs);
   }
   w->first = min(max(offsets[begin], 0), a.tokens);
-  w->nq = min(min(max(offsets[end], w->first), a.tokens) - w->first, a.max_q);
-  w->len = min(max(scalar_ints(a.kv_lens)[seq], 0), a.max_kv);
+  w->nq = min(min(max(offsets[end], w->first), a.tokens) - w->first, over ? a.max_group_q : a.max_q);
+  w->len = min(max(scalar_ints(over ? a.prefix_lens : a.kv_lens)[seq], 0), over ? a.max_prefix : a.max_kv);
   w->rows = w->nq * w->share;
   return w->rows > 0;
 }
@@ -190,10 +191,9 @@ struct Span {
   int pos_lo, pos_hi, window, first, last;
 };
 
-template <int MODE = kPlain>
-__device__ __forceinline__ Span span_of(const AttnArgs& a, const Job& w, int r0, int n) {
+__device__ __forceinline__ Span span_of(const AttnArgs& a, const Job& w, int r0, int n, bool over = false) {
   Span s;
-  if constexpr (MODE == kPrefix) {
+  if (over) {
     s.pos_lo = s.pos_hi = w.len - 1;
     s.last = w.len;
     s.window = s.last + 1;
@@ -234,8 +234,8 @@ __device__ __forceinline__ uint2* out_at(const AttnArgs& a, const Job& w, int ro
 
 // Partial results over the prefixes: [pieces][groups][kv_heads][prefix_rows], a group's rows for a KV head
 // padded to whole tiles.
-__device__ __forceinline__ int64_t prefix_row(const AttnArgs& a, int groups, int piece, int group, int head, int row) {
-  return (((int64_t)piece * groups + group) * a.cache.kv_heads + head) * a.prefix_rows + row;
+__device__ __forceinline__ int64_t prefix_row(const AttnArgs& a, int piece, int group, int head, int row) {
+  return (((int64_t)piece * a.groups + group) * a.cache.kv_heads + head) * a.prefix_rows + row;
 }
 
 // Those that a job's rows start from: group (below 0: none), the first row of the group's tokens and their number.
@@ -269,7 +269,7 @@ __device__ __forceinline__ void start_row(const AttnArgs& a, const Job& w, const
                                           float* base, float* limit, float* sum, bool* low, Add add) {
   const int i = row / w.share, token = w.first + i - p.first;
   if (p.group < 0 || token < 0 || token >= p.tokens) return;
-  const int64_t at = prefix_row(a, a.groups, piece0, p.group, w.head, token * w.share + row - i * w.share);
+  const int64_t at = prefix_row(a, piece0, p.group, w.head, token * w.share + row - i * w.share);
   const int64_t stride = step * (int64_t)a.groups * a.cache.kv_heads * a.prefix_rows;
   const float2* ml = reinterpret_cast<const float2*>(a.prefix_ml) + at;
   const float* o = a.prefix_o + at * a.cache.head_dim;
@@ -371,13 +371,14 @@ __device__ __forceinline__ int64_t shares_of(const AttnArgs& a, int64_t total) {
 struct Piece {
   Job w;
   int r0, key0, key1, slot;
+  bool over;  // of a prefix
 };
 
 // `p` with every field in scalar registers.
 __device__ __forceinline__ Piece uniform_piece(const Piece& p) {
   return Piece{Job{uniform(p.w.first), uniform(p.w.rows), uniform(p.w.len), uniform(p.w.nq), uniform(p.w.seq),
                    uniform(p.w.head), uniform(p.w.share)},
-               uniform(p.r0), uniform(p.key0), uniform(p.key1), uniform(p.slot)};
+               uniform(p.r0), uniform(p.key0), uniform(p.key1), uniform(p.slot), (bool)uniform(p.over)};
 }
 
 struct Shares {
@@ -394,8 +395,9 @@ struct Shares {
     seq_end = before + (int64_t)s.tiles * a.cache.kv_heads * s.units;
   }
 
+  template <int MODE = kPlain>
   __device__ __forceinline__ bool begin(const AttnArgs& a, int rg, int lane) {
-    whole = a.shares == 0;  // (also over prefixes)
+    whole = MODE == kBoth || a.shares == 0;
     if (whole) {
       at = blockIdx.x;
       return true;
@@ -429,33 +431,43 @@ struct Shares {
     return true;
   }
 
+  // kBoth: pieces of the prefixes, then pieces of the sequences' own keys, row tiles of the same keys next to
+  // each other.
+  __device__ __forceinline__ bool next_of_both(const AttnArgs& a, int rg, int tiles, Piece* p) {
+    if (at < 0) return false;
+    const unsigned heads = (unsigned)a.cache.kv_heads;
+    const unsigned over_tiles = (unsigned)(a.prefix_rows / rg);
+    const unsigned over = over_tiles * heads * (unsigned)a.groups * (unsigned)a.prefix_pieces;
+    p->over = (unsigned)at < over;
+    const unsigned j = (unsigned)at - (p->over ? 0 : over), across = p->over ? over_tiles : (unsigned)tiles;
+    const unsigned pieces = (unsigned)(p->over ? a.prefix_pieces : a.own_pieces);
+    at = -1;
+    const unsigned line = j / across, seq_head = line / pieces, seq = seq_head / heads;
+    const int piece = uniform((int)(line % pieces));
+    if (!make_job(a, uniform((int)seq), uniform((int)(seq_head - seq * heads)), &p->w, p->over)) return false;
+    p->r0 = uniform((int)(j % across)) * rg;
+    const int units = (p->w.len + kUnit - 1) / kUnit;
+    p->key0 = uniform((int)((int64_t)units * piece / (int)pieces)) * kUnit;
+    p->key1 = piece + 1 == (int)pieces ? -1 : uniform((int)((int64_t)units * (piece + 1) / (int)pieces)) * kUnit;
+    p->slot = piece;
+    return p->r0 < p->w.rows;
+  }
+
   template <int MODE = kPlain>
   __device__ __forceinline__ bool next(const AttnArgs& a, int rg, int lane, int tiles, Piece* p) {
-    if (MODE == kPrefix || whole) {
+    if constexpr (MODE == kBoth) return next_of_both(a, rg, tiles, p);
+    p->over = false;
+    if (whole) {
       if (at < 0) return false;
-      unsigned j = (unsigned)at;
-      const unsigned heads = (unsigned)a.cache.kv_heads;
+      const unsigned j = (unsigned)at, heads = (unsigned)a.cache.kv_heads;
       at = -1;
-      int piece = 0;
-      if constexpr (MODE == kPrefix) {  // row tiles of the same keys next to each other
-        const unsigned tile = j % (unsigned)tiles, line = j / (unsigned)tiles;
-        piece = uniform((int)(line % (unsigned)a.prefix_pieces));
-        const unsigned group_head = line / (unsigned)a.prefix_pieces;
-        j = (group_head / heads * (unsigned)tiles + tile) * heads + group_head % heads;
-      }
       const int group = uniform((int)(j / heads));
       const int seq = uniform((int)((unsigned)group / (unsigned)tiles));
-      if (!make_job<MODE>(a, seq, (int)j - group * (int)heads, &p->w)) return false;
+      if (!make_job(a, seq, (int)j - group * (int)heads, &p->w)) return false;
       p->r0 = (group - seq * tiles) * rg;
       p->key0 = 0;
       p->key1 = -1;
       p->slot = -1;
-      if constexpr (MODE == kPrefix) {  // its units, cut evenly
-        const int units = (p->w.len + kUnit - 1) / kUnit, next = piece + 1;
-        p->key0 = uniform((int)((int64_t)units * piece / a.prefix_pieces)) * kUnit;
-        if (next < a.prefix_pieces) p->key1 = uniform((int)((int64_t)units * next / a.prefix_pieces)) * kUnit;
-        p->slot = piece;
-      }
       return p->r0 < p->w.rows;
     }
     if (at >= end) return false;
@@ -493,11 +505,14 @@ struct Shares {
 template <int D, int RG, int MODE = kPlain>
 __device__ __forceinline__ void store_piece(const AttnArgs& a, const Piece& p, int local, int ch, float4_t o, float sum,
                                             float base) {
-  if constexpr (MODE == kPrefix) {
-    if (p.r0 + local >= p.w.rows) return;
-    const int64_t at = prefix_row(a, a.seqs, p.slot, p.w.seq, p.w.head, p.r0 + local);
-    *reinterpret_cast<float4_t*>(a.part_o + at * D + ch) = o;
-    if (ch == 0) *reinterpret_cast<float2*>(a.part_ml + 2 * at) = make_float2(base, sum);
+  if constexpr (MODE == kBoth) {
+    const int row = p.r0 + local, i = row / p.w.share;
+    if (row >= p.w.rows) return;
+    const int64_t at = p.over ? prefix_row(a, p.slot, p.w.seq, p.w.head, row)
+                              : ((int64_t)p.slot * a.tokens + p.w.first + i) * a.q_heads + p.w.head * p.w.share +
+                                    row - i * p.w.share;
+    *reinterpret_cast<float4_t*>((p.over ? a.prefix_o : a.part_o) + at * D + ch) = o;
+    if (ch == 0) *reinterpret_cast<float2*>((p.over ? a.prefix_ml : a.part_ml) + 2 * at) = make_float2(base, sum);
     return;
   }
   if (p.slot < 0) {
@@ -550,20 +565,21 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
   const int stride_block = kStride / tpp, stride_rem = kStride - stride_block * tpp;
   Shares shares;
   Piece pc{};
-  bool more = uniform(shares.begin(a, 16, lane));
+  bool more = uniform(shares.begin<MODE>(a, 16, lane));
   for (bool again = false; more; again = true) {
     Piece next_piece;
     if (!uniform(shares.next<MODE>(a, 16, lane, tiles, &next_piece))) break;
     pc = uniform_piece(next_piece);
     if (again) __syncthreads();  // buf of the piece before has been read
     const Job& w = pc.w;
+    const bool over = MODE == kBoth && pc.over;
 
     const int row = pc.r0 + col;
     half8_t q[KB];
     int pos;  // position of the lane's row: its own last visible key; -1: no row
     {
       const int i = min(row, w.rows - 1) / w.share, hs = min(row, w.rows - 1) - i * w.share;
-      pos = row < w.rows ? MODE == kPrefix ? w.len - 1 : w.len - w.nq + i : -1;
+      pos = row < w.rows ? over ? w.len - 1 : w.len - w.nq + i : -1;
       const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.first + i) * a.q_stride +
                             (int64_t)(w.head * w.share + hs) * D + 8 * c4;
 #pragma unroll
@@ -589,10 +605,11 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
       if (c4 != 0) l = 0.0f;
     }
 
-    const Span sp = span_of<MODE>(a, w, pc.r0, 16);
+    const Span sp = span_of(a, w, pc.r0, 16, over);
     const int t_first = max(pc.key0, sp.first);
     const int t_last = pc.key1 < 0 ? sp.last : min(sp.last, pc.key1);
-    const ScalarInts table = scalar_ints(a.block_table + (int64_t)w.seq * a.max_blocks);
+    const int blocks = over ? a.prefix_blocks : a.max_blocks;
+    const ScalarInts table = scalar_ints((over ? a.prefix_table : a.block_table) + (int64_t)w.seq * blocks);
     uint32_t cap_v = 0;    // largest V scale that E covers, as float16 bits
 
     const int last_tile = max(t_last - 1, 0) / kTokTile;
@@ -607,8 +624,8 @@ __global__ __launch_bounds__(256, (Attn<D, GC>::kWavesSimd)) void attn16_kernel(
       in_page2 = wraps ? 0 : next.in_page + 1;
       const int b2 = next.block + (wraps ? 1 : 0);
       // entries behind the last key's are not read
-      page[0] = next.tile <= last_tile && next.block < a.max_blocks ? table[next.block] : -1;
-      page[1] = next.tile + 1 <= last_tile && b2 < a.max_blocks ? table[b2] : -1;
+      page[0] = next.tile <= last_tile && next.block < blocks ? table[next.block] : -1;
+      page[1] = next.tile + 1 <= last_tile && b2 < blocks ? table[b2] : -1;
     };
     // Loads of the step at `next`, which then moves on. A tile behind the last key or of a
     // page outside the cache is read from page 0 and masked.
@@ -881,7 +898,7 @@ __global__ __launch_bounds__(256, 2) void attn32_kernel(AttnArgs a, int tiles) {
   bool more = uniform(shares.begin(a, 32, lane));
   for (bool again = false; more; again = true) {
     Piece next_piece;
-    if (!uniform(shares.next<MODE>(a, 32, lane, tiles, &next_piece))) break;
+    if (!uniform(shares.next(a, 32, lane, tiles, &next_piece))) break;
     pc = uniform_piece(next_piece);
     if (again) __syncthreads();  // buf of the piece before has been read
     const Job& w = pc.w;
@@ -892,7 +909,7 @@ __global__ __launch_bounds__(256, 2) void attn32_kernel(AttnArgs a, int tiles) {
     int pos;  // position of the lane's row: its own last visible key; -1: no row
     {
       const int i = min(row, w.rows - 1) / w.share, hs = min(row, w.rows - 1) - i * w.share;
-      pos = row < w.rows ? MODE == kPrefix ? w.len - 1 : w.len - w.nq + i : -1;
+      pos = row < w.rows ? w.len - w.nq + i : -1;
       const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.first + i) * a.q_stride +
                             (int64_t)(w.head * w.share + hs) * D + 8 * c;
 #pragma unroll
@@ -910,7 +927,7 @@ __global__ __launch_bounds__(256, 2) void attn32_kernel(AttnArgs a, int tiles) {
       if (pc.slot != 0) start32<KB>(a, w, row, wave, 4, c, &base, &limit, &l, &low, acc);
     }
 
-    const Span sp = span_of<MODE>(a, w, r0, 32);
+    const Span sp = span_of(a, w, r0, 32);
     const int t_own = max(pc.key0, sp.first) + kStep * wave;
     const int t_last = pc.key1 < 0 ? sp.last : min(sp.last, pc.key1);
     uint32_t cap_v = 0;    // largest V scale that E covers, as float16 bits
@@ -1148,7 +1165,7 @@ __global__ __launch_bounds__(256, 2) void attn32_kernel(AttnArgs a, int tiles) {
         sum = __builtin_fmaf(ml[v][col].y, f, sum);
         o += buf[v][wave][lane] * f;
       }
-      store_piece<D, 32, MODE>(a, pc, col, 32 * b + 8 * wave + 4 * c, o, sum, top);
+      store_piece<D, 32>(a, pc, col, 32 * b + 8 * wave + 4 * c, o, sum, top);
     }
   }
   shares.finish(a, pc);
@@ -1188,7 +1205,7 @@ __device__ __forceinline__ int rows_job(const AttnArgs& a, unsigned job, int til
   }
   const int tile = tiles - 1 - uniform((int)at), heads = a.cache.kv_heads;
   const int seq = uniform((int)(group / (unsigned)heads));
-  const bool any = make_job<MODE>(a, seq, uniform((int)group) - seq * heads, w);
+  const bool any = make_job(a, seq, uniform((int)group) - seq * heads, w, MODE == kPrefix);
   return any && 128 * tile < w->rows ? tile : -1;
 }
 
@@ -1199,15 +1216,24 @@ __device__ __forceinline__ int rows_job(const AttnArgs& a, unsigned job, int til
 // places: 626 -> 512 us; 1.5 us slower where nothing is cut, hence two instances). At 128 channels in two
 // groups three wavefronts a SIMD spill 7 to 10 registers and are faster all the same (four chunks of 384
 // tokens over 8K: 455 us, 474 with two); 256 channels in eight groups spill 26 to 31.
-template <int D, int GC, bool CUT, int MODE = kPlain>
-__global__ __launch_bounds__(256, (D == 256 ? 1 : D == 128 && (GC == 2 || (CUT && GC == 1)) ? 3 : 2))
+//
+// HALVES: over prefixes, where everything is cut and each piece leaves 4 (D + 2) bytes a row to write and to read
+// again, eight wavefronts take a piece, four the even 64 keys and four the odd ones, and add up in
+// LDS: a third of the partial results of three workgroups on the CU. Each half has two LDS buffers and
+// one barrier a step; the two wavefronts of a SIMD are of different halves, and one converts before it
+// multiplies, the other behind it.
+template <int D, int GC, bool CUT, int MODE = kPlain, bool HALVES = false>
+__global__ __launch_bounds__(HALVES ? 512 : 256,
+                             (HALVES ? D == 64 ? 4 : 2 : D == 256 ? 1 : D == 128 && (GC == 2 || (CUT && GC == 1)) ? 3 : 2))
 void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
   using S = Shared<D, GC>;
-  constexpr int KB = S::KB, BPG = KB / GC, kKeys = S::kKeys;
+  constexpr int KB = S::KB, BPG = KB / GC, kKeys = S::kKeys, kApart = HALVES ? 2 * kKeys : kKeys;
   extern __shared__ __align__(16) unsigned char smem[];
-  S& lds = *reinterpret_cast<S*>(smem);
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = HALVES ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) : 0;
+  const int wave = __builtin_amdgcn_readfirstlane((threadIdx.x >> 6) - 4 * half);
+  S* from = reinterpret_cast<S*>(smem) + 2 * half;  // what is multiplied now
+  S* into = HALVES ? from + 1 : from;               // what is converted
   const int col = lane & 31, c = lane >> 5;
   constexpr int kGroup = 128;
   const bool cut = CUT && blockIdx.x >= (unsigned)a.whole;  // one piece of a job's keys
@@ -1242,13 +1268,13 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
     if (piece == 0) start32<KB>(a, w, row, 0, 1, c, &base, &limit, &l, &low, acc);
   }
 
-  const Span all = span_of<MODE>(a, w, g0, kGroup);                   // the workgroup's keys
-  const Span own = span_of<MODE>(a, w, min(r0, w.rows - 1), 32);      // those of this wavefront's rows
+  const Span all = span_of(a, w, g0, kGroup, MODE == kPrefix);                // the workgroup's keys
+  const Span own = span_of(a, w, min(r0, w.rows - 1), 32, MODE == kPrefix);   // those of this wavefront's rows
   int t_first = all.first, t_last = all.last;
   if (cut) {
-    const int blocks = (max(t_last - t_first, 0) + kKeys - 1) / kKeys;
-    const int b0 = uniform((int)((int64_t)blocks * piece / a.pieces));
-    const int b1 = uniform((int)((int64_t)blocks * (piece + 1) / a.pieces));
+    const int steps = (max(t_last - t_first, 0) + kKeys - 1) / kKeys;
+    const int b0 = uniform((int)((int64_t)steps * piece / a.pieces));
+    const int b1 = uniform((int)((int64_t)steps * (piece + 1) / a.pieces));
     t_last = min(t_last, t_first + kKeys * b1);
     t_first += kKeys * b0;
   }
@@ -1261,26 +1287,29 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
   const int pair = wave & 1;
   const uint32_t* codes = static_cast<const uint32_t*>(is_v ? a.cache.v_codes : a.cache.k_codes);
   const uint16_t* scales = static_cast<const uint16_t*>(is_v ? a.cache.v_scales : a.cache.k_scales);
-  const ScalarInts table = scalar_ints(a.block_table + (int64_t)w.seq * a.max_blocks);
+  constexpr bool kOver = MODE == kPrefix;
+  const int blocks = kOver ? a.prefix_blocks : a.max_blocks;
+  const ScalarInts table = scalar_ints((kOver ? a.prefix_table : a.block_table) + (int64_t)w.seq * blocks);
   const int tpp = a.cache.page_size / kTokTile;
-  const int stride_block = 4 / tpp, stride_rem = 4 - stride_block * tpp;
+  constexpr int kTilesApart = kApart / kTokTile;
+  const int stride_block = kTilesApart / tpp, stride_rem = kTilesApart - stride_block * tpp;
   const int last_tile = max(t_last - 1, 0) / kTokTile;
   Walk next;
-  next.tile = t_first / kTokTile + 2 * pair;
+  next.tile = t_first / kTokTile + 4 * half + 2 * pair;
   next.block = next.tile / tpp;
   next.in_page = next.tile - next.block * tpp;
   uint32_t raw[2][KB];  // codes of the 64 keys after those in LDS
   uint16_t raw_s[GC];   // scale of key lane % 32
   bool raw_there[2];
-  int raw_t0 = t_first;
+  int raw_t0 = t_first + kKeys * half;
   int page[2], in_page2;
   int top_v = 0;  // largest V scale this wavefront has converted
   auto fetch_pages = [&]() __attribute__((always_inline)) {
     const bool wraps = next.in_page + 1 == tpp;
     in_page2 = wraps ? 0 : next.in_page + 1;
     const int b2 = next.block + (wraps ? 1 : 0);
-    page[0] = next.tile <= last_tile && next.block < a.max_blocks ? table[next.block] : -1;
-    page[1] = next.tile + 1 <= last_tile && b2 < a.max_blocks ? table[b2] : -1;
+    page[0] = next.tile <= last_tile && next.block < blocks ? table[next.block] : -1;
+    page[1] = next.tile + 1 <= last_tile && b2 < blocks ? table[b2] : -1;
   };
   auto load = [&]() __attribute__((always_inline)) {
     int64_t tile[2];
@@ -1294,7 +1323,7 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
     const uint16_t* sc = scales + ((lane & 16) ? tile[1] : tile[0]) * (GC * kTokTile) + (lane & 15);
 #pragma unroll
     for (int g = 0; g < GC; ++g) raw_s[g] = sc[g * kTokTile];
-    next.tile += 4;
+    next.tile += kTilesApart;
     next.block += stride_block;
     next.in_page += stride_rem;
     if (next.in_page >= tpp) {
@@ -1312,7 +1341,7 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int b = 0; b < KB; ++b) {
-          half4_t* to = reinterpret_cast<half4_t*>(&lds.v[pair][j][b][r16 + 32 * (c4 & 1)]) + (c4 >> 1);
+          half4_t* to = reinterpret_cast<half4_t*>(&into->v[pair][j][b][r16 + 32 * (c4 & 1)]) + (c4 >> 1);
           to[0] = v_codes4(raw[j][b], lo);
           to[2 * 16] = v_codes4(raw[j][b], hi);
         }
@@ -1321,7 +1350,7 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int b = 0; b < KB; ++b)
-          lds.k[pair][2 * b + (c4 >> 1)][r16 + 16 * j + 32 * (c4 & 1)] = k_operand(raw[j][b], dq);
+          into->k[pair][2 * b + (c4 >> 1)][r16 + 16 * j + 32 * (c4 & 1)] = k_operand(raw[j][b], dq);
     }
     // what no row sees may hold anything: 0 * NaN must not arise
     const int key = raw_t0 + 32 * pair + (lane & 31);
@@ -1331,7 +1360,7 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
     for (int g = 0; g < GC; ++g) {
       const uint32_t bits = seen ? raw_s[g] : 0u;
       const float f = (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
-      if (lane < 32) (is_v ? lds.vs : lds.ks)[g][32 * pair + lane] = is_v ? f : f * scale;
+      if (lane < 32) (is_v ? into->vs : into->ks)[g][32 * pair + lane] = is_v ? f : f * scale;
       top = max(top, bits < 0x7C00u ? (int)bits : 0);
     }
     if (is_v) {
@@ -1340,15 +1369,15 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
         for (int i = 1; i < 32; i <<= 1) top = max(top, __shfl_xor(top, i, 64));
         top_v = max(top_v, __builtin_amdgcn_readfirstlane(top));
       }
-      if (lane == 0) lds.vmax[pair] = top_v;
+      if (lane == 0) into->vmax[pair] = top_v;
     } else if (lane < 2) {
-      lds.there[2 * pair + lane] = lane ? raw_there[1] : raw_there[0];
+      into->there[2 * pair + lane] = lane ? raw_there[1] : raw_there[0];
     }
-    raw_t0 += kKeys;
+    raw_t0 += kApart;
   };
 
   auto compute = [&](int t0) __attribute__((always_inline)) {
-    const int vmax = __builtin_amdgcn_readfirstlane(max(lds.vmax[0], lds.vmax[1]));
+    const int vmax = __builtin_amdgcn_readfirstlane(max(from->vmax[0], from->vmax[1]));
     if (vmax > cap_v) {
       cap_v = vmax | 0x3FF;  // up to the end of its binade
       const float up = (float)(cap_v >> 10) - 14.0f - kHeadroom - exp_v, alpha = exp2_fast(-up);
@@ -1365,8 +1394,8 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
     for (int h = 0; h < 2; ++h) {
       const int th = t0 + kStep * h;
       if (th > own.pos_hi || th + kStep <= own.first) continue;  // none of these rows sees any (uniform)
-      const bool there0 = __builtin_amdgcn_readfirstlane(lds.there[2 * h]);
-      const bool there1 = __builtin_amdgcn_readfirstlane(lds.there[2 * h + 1]);
+      const bool there0 = __builtin_amdgcn_readfirstlane(from->there[2 * h]);
+      const bool there1 = __builtin_amdgcn_readfirstlane(from->there[2 * h + 1]);
       const bool edge =
           th + kStep > own.pos_lo + 1 || th <= own.pos_hi - own.window || th + kStep > t_last || !there0 || !there1;
 
@@ -1376,10 +1405,10 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
       for (int g = 0; g < GC; ++g) {
         float16_t part = {};
 #pragma unroll
-        for (int b = 2 * g * BPG; b < 2 * (g + 1) * BPG; ++b) part = mfma32(lds.k[h][b][lane], q[b], part);
+        for (int b = 2 * g * BPG; b < 2 * (g + 1) * BPG; ++b) part = mfma32(from->k[h][b][lane], q[b], part);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const float4_t ks = *reinterpret_cast<const float4_t*>(&lds.ks[g][32 * h + 8 * u + 4 * c]);
+          const float4_t ks = *reinterpret_cast<const float4_t*>(&from->ks[g][32 * h + 8 * u + 4 * c]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) s[4 * u + i] = __builtin_fmaf(part[4 * u + i], ks[i], g == 0 ? -base : s[4 * u + i]);
         }
@@ -1430,7 +1459,7 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
         for (int g = 0; g < GC; ++g)
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const float4_t vs = *reinterpret_cast<const float4_t*>(&lds.vs[g][32 * h + 16 * j + 8 * u + 4 * c]);
+            const float4_t vs = *reinterpret_cast<const float4_t*>(&from->vs[g][32 * h + 16 * j + 8 * u + 4 * c]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) p[g][4 * u + i] = (_Float16)(s[8 * j + 4 * u + i] * vs[i]);
           }
@@ -1443,7 +1472,7 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
               if (hidden >> (8 * j + i) & 1u) p[g][i] = (_Float16)0.0f;
         }
 #pragma unroll
-        for (int b = 0; b < KB; ++b) acc[b] = mfma32(lds.v[h][j][b][lane], p[b / BPG], acc[b]);
+        for (int b = 0; b < KB; ++b) acc[b] = mfma32(from->v[h][j][b][lane], p[b / BPG], acc[b]);
       }
     }
   };
@@ -1451,32 +1480,82 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
   if (t_first < t_last) {
     fetch_pages();
     load();
+    if constexpr (HALVES) into = from;
     convert();
     load();
     lds_barrier();
-    for (int t0 = t_first;;) {
-      if (!idle) compute(t0);
-      if ((t0 += kKeys) >= t_last) break;
-      lds_barrier();  // all have read these keys
-      convert();
-      load();
-      lds_barrier();
+    if constexpr (HALVES) {
+      for (int t0 = t_first;; from = into) {
+        into = reinterpret_cast<S*>(smem) + 2 * half + (from == reinterpret_cast<S*>(smem) + 2 * half);
+        const bool more = t0 + kApart < t_last;
+        if (more && half == 0) {
+          convert();
+          load();
+        }
+        if (!idle && t0 + kKeys * half < t_last) compute(t0 + kKeys * half);
+        if (!more) break;
+        if (half == 1) {
+          convert();
+          load();
+        }
+        t0 += kApart;
+        lds_barrier();
+      }
+    } else {
+      for (int t0 = t_first;;) {
+        if (!idle) compute(t0);
+        if ((t0 += kKeys) >= t_last) break;
+        lds_barrier();  // all have read these keys
+        convert();
+        load();
+        lds_barrier();
+      }
     }
   }
   if (low && limit == -__builtin_inff()) l -= 1.0f;
   l += __shfl_xor(l, 32, 64);
+  if constexpr (HALVES) {
+    // the odd keys' part through LDS
+    if (limit == -__builtin_inff()) base = kLowest;
+    limit = 0.0f;
+    float4_t* parts = reinterpret_cast<float4_t*>(smem) + wave * (4 * KB * kWave) + lane;
+    float2* ml = reinterpret_cast<float2*>(smem + 4 * (4 * KB * kWave) * sizeof(float4_t)) + 32 * wave + col;
+    lds_barrier();  // all have read the last keys
+    if (half == 1) {
+#pragma unroll
+      for (int b = 0; b < KB; ++b)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          parts[(4 * b + u) * kWave] = float4_t{acc[b][4 * u], acc[b][4 * u + 1], acc[b][4 * u + 2], acc[b][4 * u + 3]};
+      if (c == 0) *ml = make_float2(base, l);
+    }
+    lds_barrier();
+    if (half == 1) return;
+    const float2 other = *ml;
+    const float top = fmaxf(base, other.x), f0 = exp2_fast(base - top), f1 = exp2_fast(other.x - top);
+    base = top;
+    l = l * f0 + other.y * f1;
+#pragma unroll
+    for (int b = 0; b < KB; ++b)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float4_t x = parts[(4 * b + u) * kWave];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[b][4 * u + e] = acc[b][4 * u + e] * f0 + x[e] * f1;
+      }
+  }
   if (row >= w.rows) return;
   if (cut) {
-    const int64_t slot = MODE == kPrefix ? prefix_row(a, a.seqs, piece, w.seq, w.head, row)
+    const int64_t slot = MODE == kPrefix ? prefix_row(a, piece, w.seq, w.head, row)
                                          : (int64_t)behind * kGroup + 32 * wave + col;
 #pragma unroll
     for (int b = 0; b < KB; ++b)
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        *reinterpret_cast<float4_t*>(a.part_o + slot * D + 32 * b + 8 * u + 4 * c) =
+        *reinterpret_cast<float4_t*>((MODE == kPrefix ? a.prefix_o : a.part_o) + slot * D + 32 * b + 8 * u + 4 * c) =
             float4_t{acc[b][4 * u], acc[b][4 * u + 1], acc[b][4 * u + 2], acc[b][4 * u + 3]};
     if (c == 0)
-      *reinterpret_cast<float2*>(a.part_ml + 2 * slot) = make_float2(limit == -__builtin_inff() ? kLowest : base, l);
+      *reinterpret_cast<float2*>((MODE == kPrefix ? a.prefix_ml : a.part_ml) + 2 * slot) = make_float2(limit == -__builtin_inff() ? kLowest : base, l);
     return;
   }
 #pragma unroll
@@ -1515,6 +1594,58 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, const Job& w, int ro
     for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], m, 64);
   }
   if (g == 0) *out_at<D>(a, w, row, ch) = to_row(o, sum);
+}
+
+// kBoth: rows of a job (a tile of 16 rows of a sequence and KV head) from the pieces of their prefix and of
+// their own keys, added up in order; a wavefront a row.
+constexpr int kJoinBoth = 512;
+template <int D>
+__global__ __launch_bounds__(kJoinBoth) void attn_join_both_kernel(AttnArgs a, int tiles) {
+  constexpr int LPR = D / 4, G = kWave / LPR;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int g = lane / LPR, ch = 4 * (lane % LPR);
+  const unsigned heads = (unsigned)a.cache.kv_heads, line = blockIdx.x / (unsigned)tiles, seq = line / heads;
+  Job w;
+  if (!make_job(a, uniform((int)seq), uniform((int)(line - seq * heads)), &w)) return;
+  const int r0 = uniform((int)(blockIdx.x - line * tiles)) * 16;
+  if (r0 + wave >= w.rows) return;
+  const Before p = before_of(a, w.seq);
+  for (int row = r0 + wave; row < min(r0 + 16, w.rows); row += kJoinBoth / kWave) {
+    const int i = row / w.share, hs = row - i * w.share, token = w.first + i - p.first;
+    const int over = p.group >= 0 && token >= 0 && token < p.tokens ? a.prefix_pieces : 0;
+    const int64_t over_at = prefix_row(a, 0, max(p.group, 0), w.head, token * w.share + hs);
+    const int64_t over_step = (int64_t)a.groups * a.cache.kv_heads * a.prefix_rows;
+    const int64_t own_at = (int64_t)(w.first + i) * a.q_heads + w.head * w.share + hs;
+    const int64_t own_step = (int64_t)a.tokens * a.q_heads;
+    const int n = over + a.own_pieces;
+    auto ml = [&](int j) __attribute__((always_inline)) {
+      return *reinterpret_cast<const float2*>(j < over ? a.prefix_ml + 2 * (over_at + j * over_step)
+                                                       : a.part_ml + 2 * (own_at + (j - over) * own_step));
+    };
+    float top = kLowest, sum = 0.0f;
+    float4_t o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int j = g; j < n; j += G) top = fmaxf(top, ml(j).x);
+#pragma unroll
+    for (int m = LPR; m < kWave; m <<= 1) top = fmaxf(top, __shfl_xor(top, m, 64));
+#pragma unroll 4
+    for (int j = g; j < n; j += G) {
+      const float2 v = ml(j);
+      const float f = exp2_fast(v.x - top);
+      sum = __builtin_fmaf(v.y, f, sum);
+      o += *reinterpret_cast<const float4_t*>((j < over ? a.prefix_o + (over_at + j * over_step) * D
+                                                        : a.part_o + (own_at + (j - over) * own_step) * D) +
+                                              ch) *
+           f;
+    }
+#pragma unroll
+    for (int m = LPR; m < kWave; m <<= 1) {
+      sum += __shfl_xor(sum, m, 64);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], m, 64);
+    }
+    if (g == 0) *out_at<D>(a, w, row, ch) = to_row(o, sum);
+  }
 }
 
 // The job that share blockIdx.x / (rg / 4) begins and does not end.

@@ -14,34 +14,40 @@
 namespace q4 {
 namespace {
 
+// Whether eight wavefronts take a piece (HALVES): 256 channels would leave them too few registers.
+constexpr bool halves(int head_dim) { return head_dim <= 128; }
+template <int D, int GC>
+constexpr size_t prefix_lds() {
+  return (halves(D) ? 4 : 1) * sizeof(Shared<D, GC>);
+}
+
 template <int D, int GC>
 hipError_t prefix_t(const AttnArgs& a, hipStream_t stream) {
-  const int tiles = a.prefix_rows / a.rows_group;
-  const int64_t lines = (int64_t)a.cache.kv_heads * a.seqs;
-  const dim3 grid((unsigned)(tiles * lines * a.prefix_pieces));
-  if (a.rows_group == 128) {
-    const int swizzle = lines % 8 == 0 && tiles > 1;
-    hipLaunchKernelGGL((attn_rows_kernel<D, GC, true, kPrefix>), grid, dim3(256), sizeof(Shared<D, GC>), stream, a, tiles,
-                       swizzle);
-  } else if (a.rows_group == 32) {
-    if constexpr (has_attn32(D, GC))
-      hipLaunchKernelGGL((attn32_kernel<D, GC, kPrefix>), grid, dim3(256), 0, stream, a, tiles);
-  } else {
-    hipLaunchKernelGGL((attn16_kernel<D, GC, false, kPrefix>), grid, dim3(256), 0, stream, a, tiles);
-  }
+  const int tiles = a.prefix_rows / 128;
+  const int swizzle = (int64_t)a.cache.kv_heads * a.groups % 8 == 0 && tiles > 1;
+  hipLaunchKernelGGL((attn_rows_kernel<D, GC, true, kPrefix, halves(D)>), dim3((unsigned)(a.tail * a.pieces)),
+                     dim3(halves(D) ? 512 : 256), (prefix_lds<D, GC>()), stream, a, tiles, swizzle);
+  return hipGetLastError();
+}
+
+template <int D, int GC>
+hipError_t both_t(const AttnArgs& a, hipStream_t stream) {
+  const int64_t rows = (int64_t)a.max_q * (a.q_heads / a.cache.kv_heads);
+  const int tiles = (int)((rows + 15) / 16);
+  const int64_t over = (int64_t)a.prefix_rows / 16 * a.cache.kv_heads * a.groups * a.prefix_pieces;
+  const int64_t own = (int64_t)tiles * a.cache.kv_heads * a.seqs;
+  hipLaunchKernelGGL((attn16_kernel<D, GC, false, kBoth>), dim3((unsigned)(over + own * a.own_pieces)), dim3(256), 0,
+                     stream, a, tiles);
+  hipLaunchKernelGGL(attn_join_both_kernel<D>, dim3((unsigned)own), dim3(kJoinBoth), 0, stream, a, tiles);
   return hipGetLastError();
 }
 
 template <int D, int GC>
 int prefix_resident_t(int rows_group) {
-  if (rows_group == 128)
-    return resident_per_cu(reinterpret_cast<const void*>(&attn_rows_kernel<D, GC, true, kPrefix>), 256,
-                           sizeof(Shared<D, GC>)) *
-           device_cu_count_cached();
-  if constexpr (has_attn32(D, GC)) {
-    if (rows_group == 32) return resident_grid(reinterpret_cast<const void*>(&attn32_kernel<D, GC, kPrefix>), 256);
-  }
-  return resident_grid(reinterpret_cast<const void*>(&attn16_kernel<D, GC, false, kPrefix>), 256);
+  if (rows_group == 16) return resident_grid(reinterpret_cast<const void*>(&attn16_kernel<D, GC, false, kBoth>), 256);
+  return resident_per_cu(reinterpret_cast<const void*>(&attn_rows_kernel<D, GC, true, kPrefix, halves(D)>),
+                         halves(D) ? 512 : 256, prefix_lds<D, GC>()) *
+         device_cu_count_cached();
 }
 
 }  // namespace
@@ -54,6 +60,12 @@ int prefix_attention_resident(int head_dim, int group, int rows_group) {
 
 hipError_t launch_prefix_attention(const AttnArgs& a, hipStream_t stream) {
 #define Q4_CALL(D, GC) prefix_t<D, GC>(a, stream)
+  Q4_ATTN_DISPATCH(a.cache.head_dim, a.cache.group, Q4_CALL)
+#undef Q4_CALL
+}
+
+hipError_t launch_both_attention(const AttnArgs& a, hipStream_t stream) {
+#define Q4_CALL(D, GC) both_t<D, GC>(a, stream)
   Q4_ATTN_DISPATCH(a.cache.head_dim, a.cache.group, Q4_CALL)
 #undef Q4_CALL
 }

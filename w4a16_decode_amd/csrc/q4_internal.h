@@ -134,13 +134,15 @@ struct AttnArgs {
   float* part_o;   // partial results: float32 [shares][2][rows_group] or [pieces][tail][128], [head_dim]
   float* part_ml;  // and as many [2]: what exponents are relative to, sum
   int32_t* cuts;   // shares > 0: int32 [shares][8], the job a share begins and does not end
-  // Shared prefixes. Over them the sequences are the groups, group g's members group_offsets[g] .. [g + 1] - 1 of
-  // `members`; behind them the rows start from the partial results in prefix_o and prefix_ml.
+  // Shared prefixes: sequences group_offsets[g] .. [g + 1] - 1 are group g's.
   const int32_t* group_offsets;
-  int members, groups, max_group_q;
+  const int32_t* prefix_table;  // [groups][prefix_blocks]
+  const int32_t* prefix_lens;   // [groups]
+  int groups, prefix_blocks, max_group_q, max_prefix;
   int prefix_pieces, prefix_rows;  // pieces of a prefix's keys; rows of a group for a KV head, in whole tiles
-  const float* prefix_o;           // float32 [prefix_pieces][groups][kv_heads][prefix_rows][head_dim]
-  const float* prefix_ml;          // and [2]: what exponents are relative to, sum
+  int own_pieces;                  // pieces of a sequence's own keys, where they are left as partial results too
+  float* prefix_o;                 // float32 [prefix_pieces][groups][kv_heads][prefix_rows][head_dim]
+  float* prefix_ml;                // and [2]: what exponents are relative to, sum
 };
 
 // Whether tiles of 32 rows whose wavefronts split the keys are built: 256 channels, or four
@@ -220,9 +222,12 @@ struct LoraArgs {
 int lora_splits(int K);  // slices of the channel range of A x
 hipError_t launch_lora(const LoraArgs& a, hipStream_t stream);
 hipError_t launch_attention(const AttnArgs& a, hipStream_t stream);
-// Attention over shared prefixes into part_o and part_ml, and over the keys behind them from there.
+// Attention over shared prefixes into prefix_o and prefix_ml, and over the keys behind them from there; both as
+// partial results in one launch (part_o: [own_pieces][tokens][q_heads]) and their join.
 hipError_t launch_prefix_attention(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_behind_attention(const AttnArgs& a, hipStream_t stream);
+hipError_t launch_both_attention(const AttnArgs& a, hipStream_t stream);
+// Workgroups over prefixes, of rows_group 128 or (in one launch with the rest) 16, that the device holds at once.
 int prefix_attention_resident(int head_dim, int group, int rows_group);
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
 hipError_t launch_paged_dequant(const PagedArgs& c, const int32_t* slots, int64_t tokens, void* k_out, void* v_out,
