@@ -215,10 +215,15 @@ bool has_prefix(int64_t groups, int64_t tokens, int64_t max_group_q, int64_t max
 }
 
 // Launch shape of an attention call with shared prefixes, whose own keys' shape pick_attn has picked already.
-// Up to 256 rows of a group a KV head (and 16 of a sequence): one launch of 16-row tiles over prefixes and
-// own keys, cut into pieces of equal length until they are one round of the chip, then a join.
-// Else 128-row workgroups over the prefixes, cut until they fill the chip, and the rows behind them start from
-// those pieces.
+//   Up to 256 rows of a group a KV head: one launch of 16-row tiles over prefixes and own keys, cut
+//     into pieces of equal length until they are one round of the chip, then a join (8 sequences
+//     behind 4000 keys, 64 heads over 8: 42 -> 20 us against prefixes first and own keys from there;
+//     of 256 rows behind 8000 keys 40 -> 33, of 512 57 -> 67). Counted are the tiles that the call's rows can
+//     fill at most, not those that the bounds allow: empty ones end at once (five groups of 41 rows in all,
+//     bound 26: 50 us when the bounds' were counted).
+//   More: 128-row workgroups over the prefixes, cut until they fill the chip, and the rows behind start
+//     from those pieces. There a workgroup takes all of a row's own keys up to 4096 (64 rows behind 8190
+//     keys, own keys up to 513: 75 us with equal shares of them and a join, 57 so; up to 2000: 90, 69).
 constexpr int64_t kMaxPieces = 64;
 q4_status pick_shared(int64_t groups, int64_t max_group_q, int64_t max_prefix, q4::AttnArgs* a) {
   const int heads = a->cache.kv_heads, share = a->q_heads / heads, d = a->cache.head_dim, g = a->cache.group;
@@ -226,7 +231,10 @@ q4_status pick_shared(int64_t groups, int64_t max_group_q, int64_t max_prefix, q
   const int64_t rows = (int64_t)a->max_group_q * share, own_rows = (int64_t)a->max_q * share;
   if (rows <= 256) {
     a->rows_group = 16, a->shares = 0, a->whole = 0, a->tail = 0, a->pieces = 0;
-    const int64_t jobs = (rows + 15) / 16 * heads * groups, own = (own_rows + 15) / 16 * heads * a->seqs;
+    const int64_t tiles = (rows + 15) / 16, own = (own_rows + 15) / 16 * heads * a->seqs;
+    const int64_t filled = (int64_t)a->tokens * share / 16;
+    const int64_t jobs = std::min(tiles * groups, filled + groups) * heads;
+    const int64_t own_jobs = std::min(own, (filled + a->seqs) * heads);
     const int64_t slots = q4::prefix_attention_resident(d, g, 16);
     auto pieces = [](int64_t keys, int64_t units) { return std::max<int64_t>(1, (keys + 128 * units - 1) / (128 * units)); };
     int64_t lo = (std::max<int64_t>(max_prefix, a->max_kv) + 128 * kMaxPieces - 1) / (128 * kMaxPieces);
@@ -234,15 +242,16 @@ q4_status pick_shared(int64_t groups, int64_t max_group_q, int64_t max_prefix, q
     lo = std::max<int64_t>(lo, 1);
     while (lo < hi) {
       const int64_t mid = (lo + hi) / 2;
-      if (jobs * pieces(max_prefix, mid) + own * pieces(a->max_kv, mid) <= slots) hi = mid; else lo = mid + 1;
+      if (jobs * pieces(max_prefix, mid) + own_jobs * pieces(a->max_kv, mid) <= slots) hi = mid; else lo = mid + 1;
     }
     a->prefix_pieces = (int)pieces(max_prefix, lo), a->own_pieces = (int)pieces(a->max_kv, lo);
-    a->prefix_rows = (int)((rows + 15) / 16 * 16);
-    if (jobs * a->prefix_pieces + own * a->own_pieces > kMaxGroups256 || own > kMaxGroups256 / 2)
+    a->prefix_rows = (int)(tiles * 16);
+    if (tiles * groups * heads * a->prefix_pieces + own * a->own_pieces > kMaxGroups256 || own > kMaxGroups256 / 2)
       return fail(Q4_ERR_SHAPE, "groups * heads * max_group_q too large for one call");
     return Q4_OK;
   }
   a->own_pieces = 0;
+  if (a->max_kv <= 4096) a->shares = 0;
   const int64_t jobs = (rows + 127) / 128 * heads * groups;
   const int64_t slots = q4::prefix_attention_resident(d, g, 128);
   const int64_t pieces = std::max<int64_t>(1, std::min(slots / jobs, (max_prefix + 255) / 256));
