@@ -162,8 +162,8 @@ q4_status q4_paged_attention(const void* q, int64_t q_stride, const q4_paged_kv*
  * keys behind the prefix only. A sequence of no group has no prefix. A prefix need not end
  * where a page does; the rotation of the keys behind it counts from its length (starts of
  * q4_paged_plan).
- * max_group_q and max_prefix bound the rows of a group's sequences together and the prefixes'
- * lengths; rows of a group beyond max_group_q are taken as having no prefix, longer prefixes
+ * max_group_q and max_prefix (with max_kv below 2^30) bound the rows of a group's sequences together
+ * and the prefixes' lengths; rows of a group beyond max_group_q are taken as having no prefix, longer prefixes
  * are cut. With few rows behind a short prefix a plain call whose block tables begin with the
  * prefix's pages may be as fast. Everything else, rows that see no key, infinities and what
  * results depend on among it, is q4_paged_attention's. groups * heads * max_group_q

@@ -92,7 +92,14 @@ class Shared:
         args.update(kw)
         return self.q4.paged_attention_shared(t.pop("q"), self.cache, **t, **args, scale=scale)
 
-    def check(self, got, scale=None, what=""):
+    def view(self, **fields):
+        """The same tensors with other groups, prefixes or values to compare with."""
+        other = Shared.__new__(Shared)
+        other.__dict__.update(self.__dict__, **fields)
+        return other
+
+    def check(self, got, scale=None, what="", only=None):
+        """`only`: a slice of the rows to look at."""
         s = self.d ** -0.5 if scale is None else scale
         got = to_np(got).astype(np.float64)
         rows = self.offsets[-1]
@@ -107,8 +114,11 @@ class Shared:
         rel = 2.0 ** -11 + 2 * (self.d / 32 + 8) * 2.0 ** -23 * z + 2 * (n / 32 + 32) * 2.0 ** -24
         rel += (4 + 3 * (1.45 * z + 64)) * 2.0 ** -24
         bound = rel * mag + 2.0 ** -11 * np.abs(ref) + 2.0 ** -25
-        err = np.abs(got[:rows] - ref)
-        assert np.all(np.isfinite(got[:rows])), what
+        got = got[:rows]
+        if only is not None:
+            got, ref, bound = got[only], ref[only], bound[only]
+        err = np.abs(got - ref)
+        assert np.all(np.isfinite(got)), what
         assert np.all(err <= bound), (what, (err / bound).max(), np.argwhere(err > bound)[:4])
         return (err / bound).max()
 
@@ -181,7 +191,8 @@ def test_without_prefix_is_paged_attention(q4):
     assert torch.equal(b.run(max_prefix=0), plain) and torch.equal(b.run(max_group_q=0), plain)
     got = b.run(prefix_table=i32(np.zeros((0, 2))), prefix_lens=i32([]), group_offsets=i32([0]))
     assert torch.equal(got, plain)
-    assert torch.equal(b.run(prefix_lens=i32([0])), plain) or torch.allclose(b.run(prefix_lens=i32([0])), plain, 2e-3, 1e-4)
+    none = np.zeros((0, 2, 128))
+    b.view(pk=[none], pv=[none]).check(b.run(prefix_lens=i32([0])))
     out = torch.full_like(plain, 3.0)
     assert b.run(q=to_gpu(b.q[:0]), out=out[:0]).numel() == 0 and bool((out == 3.0).all())
 
@@ -224,6 +235,42 @@ def test_rows_ahead_of_their_sequence(q4):
     assert np.all(to_np(got)[7:10] == 0) and np.any(to_np(got)[4:7] != 0)
 
 
+@pytest.mark.parametrize("d,g", [(64, 32), (128, 128), (128, 64), (256, 64)])
+@pytest.mark.parametrize("page", [16, 48])
+def test_rows_that_fill_tiles(q4, d, g, page):
+    """Sequences of 640 and more rows a KV head walk prefix and own keys as one line: lengths around its borders,
+    sequences outside groups, rows ahead of their start, rows beyond max_group_q, jobs whole and cut."""
+    import torch
+
+    prefix = [1, 63, 64, 65, 200, 0, 130]
+    sizes = [1, 1, 2, 1, 1, 1, 1]
+    lens = [30, 40, 17, 64, 100, 5, 3, 0, 70, 33]
+    news = [20, 40, 17, 9, 33, 16, 20, 4, 1, 12]
+    b = Shared(q4, sizes, prefix, lens, news, 32, 2, d, g, page, seed=d + page, lead=1, extra_rows=3)
+    out = torch.full((len(b.q), 32, d), 7.0, dtype=torch.float16, device="cuda")
+    say("  line", d, g, page, b.check(b.run(out=out)))
+    assert bool((out[b.offsets[-1]:] == 7.0).all())
+    say("  long bounds", b.check(b.run(max_kv=3000, max_prefix=3000, max_group_q=90, max_q=50)))
+    # rows of a group beyond the bound have no prefix: of group 2's, 9 and 33, those from the second's 17 - 9th on
+    none = np.zeros((0, 2, d))
+    alone = b.view(groups=np.arange(1, 10), prefix=prefix[:3] + [0] + prefix[3:], pk=b.pk[:3] + [none] + b.pk[3:],
+                   pv=b.pv[:3] + [none] + b.pv[3:])
+    got = b.run(max_group_q=17)
+    alone.check(got, only=slice(b.offsets[4] + 8, b.offsets[5]))
+    b.check(got, only=slice(b.offsets[3], b.offsets[4] + 8))
+    # a page of prefix and one of own keys outside the cache: their keys are hidden
+    ptable, table = b.ptable.copy(), b.table.copy()
+    ptable[4, 1], table[5, 0] = b.pages, -5
+    hole = b.view(pk=list(b.pk), pv=list(b.pv))
+    keep = np.array([t for t in range(200) if t // page != 1])
+    hole.pk[4], hole.pv[4] = b.pk[4][keep], b.pv[4][keep]
+    hole.check(b.run(prefix_table=i32(ptable)))
+    b.run(block_table=i32(table))
+    for groups in ([5, 0, 5, 1, 2, 3, 4, 9], [-3, 900, 2, 7, 7, 7, 8, 2 ** 31 - 1]):
+        b.run(group_offsets=i32(groups), prefix_lens=i32([2 ** 31 - 1, -1, 5, 900, 3, 2, 1]))
+    torch.cuda.synchronize()
+
+
 def test_bounds_and_bad_entries(q4):
     """Lengths cut to their bounds, rows beyond max_group_q without a prefix, pages outside the cache hidden,
     offsets that descend or lie outside."""
@@ -232,26 +279,19 @@ def test_bounds_and_bad_entries(q4):
     b = Shared(q4, [3, 2], [100, 64], [20, 30, 40, 50, 60], [1, 1, 1, 1, 1], 8, 2, 128, 128, 16, seed=11)
     full = to_np(b.run())
     # prefixes cut
-    cut = Shared.__new__(Shared)
-    cut.__dict__.update(b.__dict__)
-    cut.prefix, cut.pk, cut.pv = [48, 48], [t[:48] for t in b.pk], [t[:48] for t in b.pv]
-    cut.check(b.run(max_prefix=48))
+    b.view(prefix=[48, 48], pk=[t[:48] for t in b.pk], pv=[t[:48] for t in b.pv]).check(b.run(max_prefix=48))
     # the third member's row of group 0 lies beyond the bound
-    none = Shared.__new__(Shared)
-    none.__dict__.update(b.__dict__)
-    got = to_np(b.run(max_group_q=2))
-    plain = to_np(q4.paged_attention(to_gpu(b.q), b.cache, to_gpu(b.table), to_gpu(b.offsets), i32(b.lens), 1, 60))
-    assert np.allclose(got[2], plain[2], 2e-3, 1e-4) and np.array_equal(got[[0, 1, 3, 4]], full[[0, 1, 3, 4]])
-    # pages outside the cache: the keys of blocks 2 and 5 of the first prefix hidden
+    none = np.zeros((0, 2, 128))
+    got = b.run(max_group_q=2)
+    b.view(groups=np.array([0, 2, 3, 5]), prefix=[100, 0, 64], pk=[b.pk[0], none, b.pk[1]],
+           pv=[b.pv[0], none, b.pv[1]]).check(got)
+    # pages outside the cache: the keys of blocks 2 and 5 of the first prefix hidden, then all of them
     ptable = b.ptable.copy()
     ptable[0, 2], ptable[0, 5] = b.pages, -1
-    hole = Shared.__new__(Shared)
-    hole.__dict__.update(b.__dict__)
     keep = np.array([t for t in range(100) if t // 16 not in (2, 5)])
-    hole.pk, hole.pv = [b.pk[0][keep], b.pk[1]], [b.pv[0][keep], b.pv[1]]
-    hole.check(b.run(prefix_table=i32(ptable)))
-    hole.pk, hole.pv = [b.pk[0][:0], b.pk[1]], [b.pv[0][:0], b.pv[1]]
-    hole.check(b.run(prefix_table=i32(np.full_like(ptable, -7) * (np.arange(2) == 0)[:, None] + ptable * (np.arange(2) == 1)[:, None])))
+    b.view(pk=[b.pk[0][keep], b.pk[1]], pv=[b.pv[0][keep], b.pv[1]]).check(b.run(prefix_table=i32(ptable)))
+    ptable[0] = -7
+    b.view(pk=[none, b.pk[1]], pv=[none, b.pv[1]]).check(b.run(prefix_table=i32(ptable)))
     # garbage in the small arrays stays inside the buffers
     for groups in ([5, 0, 5], [-3, 900, 2], [0, 5, 3], [2 ** 31 - 1, -2 ** 31, 0]):
         for lens in ([100, 64], [-1, 2 ** 31 - 1], [2 ** 31 - 1, 7]):
@@ -287,7 +327,9 @@ def test_infinite_scores(q4):
                         own = v[1 + n][:40 - new + i + 1] if at_own is zero else v[0][:0]
                         seen = np.concatenate([v[0] if at_prefix is zero else v[0][:0], own])
                         want = np.mean(oracle.paged.store(np.ascontiguousarray(seen), 64)[2], axis=0)
-                        assert np.allclose(got[rows[n] + i], want, 2e-3, 2e-3), (sign, new, n, i)
+                        # equal weights, one half step of float16 in them and one in the result
+                        bound = 2.0 ** -10 * np.mean(np.abs(oracle.paged.store(np.ascontiguousarray(seen), 64)[2]), axis=0)
+                        assert np.all(np.abs(got[rows[n] + i] - want) <= bound + 2.0 ** -18), (sign, new, n, i)
 
 
 def test_not_finite_values(q4):

@@ -202,11 +202,11 @@ void place_parts(q4::AttnArgs* a, void* workspace) {
 }
 
 // Shared prefixes: sizes beyond those of check_attn.
-q4_status check_prefix(int64_t groups, int64_t tokens, int64_t max_group_q, int64_t max_prefix, int32_t q_heads,
-                       int32_t kv_heads) {
+q4_status check_prefix(int64_t groups, int64_t tokens, int64_t max_kv, int64_t max_group_q, int64_t max_prefix,
+                       int32_t q_heads, int32_t kv_heads) {
   if (groups < 0 || max_group_q < 0 || max_prefix < 0 || groups >= kMaxDim || max_group_q >= kMaxDim ||
-      max_prefix >= kMaxDim)
-    return fail(Q4_ERR_SHAPE, "groups=%lld, max_group_q=%lld, max_prefix=%lld out of range", (long long)groups,
+      max_prefix + max_kv >= kMaxDim)
+    return fail(Q4_ERR_SHAPE, "groups=%lld, max_group_q=%lld, max_prefix=%lld (and max_kv) out of range", (long long)groups,
                 (long long)max_group_q, (long long)max_prefix);
   return check_attn(groups, tokens, max_group_q, max_prefix, q_heads, kv_heads, 0);
 }
@@ -221,7 +221,10 @@ bool has_prefix(int64_t groups, int64_t tokens, int64_t max_group_q, int64_t max
 //     of 256 rows behind 8000 keys 40 -> 33, of 512 57 -> 67). Counted are the tiles that the call's rows can
 //     fill at most, not those that the bounds allow: empty ones end at once (five groups of 41 rows in all,
 //     bound 26: 50 us when the bounds' were counted).
-//   More: 128-row workgroups over the prefixes, cut until they fill the chip, and the rows behind start
+//   More, and 640 or more of a sequence: its rows fill tiles by themselves, so prefix and own keys are walked as
+//     one line of keys, 128 rows a workgroup; jobs that do not fill the chip a whole number of times are
+//     cut and joined (nine chunks of up to 251 rows behind 6001 keys: 552 us with the prefix first).
+//   Else: 128-row workgroups over the prefixes, cut until they fill the chip, and the rows behind start
 //     from those pieces. There a workgroup takes all of a row's own keys up to 4096 (64 rows behind 8190
 //     keys, own keys up to 513: 75 us with equal shares of them and a join, 57 so; up to 2000: 90, 69).
 constexpr int64_t kMaxPieces = 64;
@@ -251,6 +254,21 @@ q4_status pick_shared(int64_t groups, int64_t max_group_q, int64_t max_prefix, q
     return Q4_OK;
   }
   a->own_pieces = 0;
+  if (own_rows >= 640) {
+    const int64_t jobs = (own_rows + 127) / 128 * heads * a->seqs, slots = q4::line_attention_resident(d, g);
+    // of these the call's rows fill about so many; the last round's share of them is cut
+    const int64_t full = std::min(jobs, ((int64_t)a->tokens * share / 128 + (a->seqs + 1) / 2) * heads);
+    const int64_t rest = full % slots;
+    const int64_t pieces = rest > 0 ? std::min(slots / rest, (max_prefix + a->max_kv) / 512) : 0;
+    a->prefix_pieces = a->prefix_rows = 0;
+    a->rows_group = 128, a->shares = 0;
+    a->tail = pieces > 1 ? (int)std::min<int64_t>(rest * jobs / full, kMaxDim) : 0;
+    a->pieces = pieces > 1 ? (int)pieces : 0;
+    a->whole = (int)std::min(jobs - a->tail, kMaxDim);
+    if (jobs > kMaxGroups256 || a->tail * (int64_t)std::max(a->pieces, 32) > kMaxGroups256)
+      return fail(Q4_ERR_SHAPE, "seqs * heads * max_q too large for one call");
+    return Q4_OK;
+  }
   if (a->max_kv <= 4096) a->shares = 0;
   const int64_t jobs = (rows + 127) / 128 * heads * groups;
   const int64_t slots = q4::prefix_attention_resident(d, g, 128);
@@ -384,7 +402,7 @@ size_t q4_paged_attention_shared_workspace_bytes(int64_t seqs, int64_t groups, i
                                                  int64_t max_kv, int64_t max_group_q, int64_t max_prefix,
                                                  int32_t q_heads, int32_t kv_heads, int32_t head_dim, int32_t group) {
   if (check_attn(seqs, tokens, max_q, max_kv, q_heads, kv_heads, 0) != Q4_OK) return 0;
-  if (check_prefix(groups, tokens, max_group_q, max_prefix, q_heads, kv_heads) != Q4_OK) return 0;
+  if (check_prefix(groups, tokens, max_kv, max_group_q, max_prefix, q_heads, kv_heads) != Q4_OK) return 0;
   if (check_paged_dims(1, 16, kv_heads, head_dim, group) != Q4_OK) return 0;
   q4::AttnArgs a{};
   a.cache.kv_heads = kv_heads, a.cache.head_dim = head_dim, a.cache.group = group;
@@ -408,7 +426,7 @@ q4_status q4_paged_attention_shared(const void* q, int64_t q_stride, const q4_pa
   q4_status st = attn_args(q, q_stride, cache, block_table, max_blocks, q_offsets, kv_lens, seqs, tokens, max_q, max_kv,
                            q_heads, scale, 0, out, &a, &any);
   if (st != Q4_OK) return st;
-  if ((st = check_prefix(groups, tokens, max_group_q, max_prefix, q_heads, a.cache.kv_heads)) != Q4_OK) return st;
+  if ((st = check_prefix(groups, tokens, max_kv, max_group_q, max_prefix, q_heads, a.cache.kv_heads)) != Q4_OK) return st;
   if (max_prefix_blocks < 0 || max_prefix_blocks >= kMaxDim)
     return fail(Q4_ERR_SHAPE, "max_prefix_blocks=%lld out of range", (long long)max_prefix_blocks);
   if (!any) return ok();
@@ -442,6 +460,8 @@ q4_status q4_paged_attention_shared(const void* q, int64_t q_stride, const q4_pa
     return hip_status(q4::launch_both_attention(a, s), "attention with shared prefixes launch");
   }
   place_parts(&a, behind);
+  if (a.prefix_pieces == 0)
+    return hip_status(q4::launch_line_attention(a, s), "attention with shared prefixes launch");
   q4::AttnArgs p = a;  // over the prefixes every job is cut
   p.shares = 0, p.whole = 0, p.pieces = a.prefix_pieces, p.tail = a.prefix_rows / 128 * a.cache.kv_heads * a.groups;
   hipError_t e = q4::launch_prefix_attention(p, s);

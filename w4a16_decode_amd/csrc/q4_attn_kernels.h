@@ -156,9 +156,10 @@ __device__ __forceinline__ ScalarInts scalar_ints(const int32_t* p) { return (Sc
 
 // What a launch is for: all keys of its sequences; the prefix that groups of sequences share (a job's
 // "sequence" is a group, its rows those of all members, and every row sees every key), left as
-// partial results; the keys behind a prefix, where each row starts from those; or prefixes and the keys
-// behind them next to each other, all left as partial results.
-enum AttnMode { kPlain, kPrefix, kBehind, kBoth };
+// partial results; the keys behind a prefix, where each row starts from those; prefixes and the keys
+// behind them next to each other, all left as partial results; or each sequence's prefix and own keys as
+// one line of keys, where its own rows fill the tiles.
+enum AttnMode { kPlain, kPrefix, kBehind, kBoth, kLine };
 
 // What a workgroup works on.
 struct Job {
@@ -1244,13 +1245,28 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
   if (tile_q < 0) return;  // the whole workgroup; a wavefront without rows still converts
   const int g0 = tile_q * kGroup, r0 = g0 + 32 * wave;
   const bool idle = r0 >= w.rows;
+  int group_of = 0;
 
   const int row = r0 + col;
+  // kLine: keys [0, prefix) of the prefix, padded to whole steps, and the sequence's own from `lead` on
+  int prefix = 0, lead = 0;
+  bool sees = true;  // whether the lane's row sees the prefix
+  if constexpr (MODE == kLine) {
+    const Before p = before_of(a, w.seq);
+    if (p.group >= 0) {
+      prefix = min(max(scalar_ints(a.prefix_lens)[p.group], 0), a.max_prefix);
+      lead = (prefix + kKeys - 1) / kKeys * kKeys;
+      sees = w.first + min(row, w.rows - 1) / w.share - p.first < p.tokens;
+    }
+    group_of = max(p.group, 0);
+    w.len += lead;
+  }
   half8_t q[2 * KB];
   int pos;  // position of the lane's row: its own last visible key; -1: no row
   {
     const int i = min(row, w.rows - 1) / w.share, hs = min(row, w.rows - 1) - i * w.share;
     pos = row < w.rows ? MODE == kPrefix ? w.len - 1 : w.len - w.nq + i : -1;
+    if (MODE == kLine && row < w.rows) pos = max(pos, lead - 1);  // ahead of its sequence's start it sees the prefix
     const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(w.first + i) * a.q_stride +
                           (int64_t)(w.head * w.share + hs) * D + 8 * c;
 #pragma unroll
@@ -1268,8 +1284,17 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
     if (piece == 0) start32<KB>(a, w, row, 0, 1, c, &base, &limit, &l, &low, acc);
   }
 
-  const Span all = span_of(a, w, g0, kGroup, MODE == kPrefix);                // the workgroup's keys
-  const Span own = span_of(a, w, min(r0, w.rows - 1), 32, MODE == kPrefix);   // those of this wavefront's rows
+  Span all = span_of(a, w, g0, kGroup, MODE == kPrefix);                // the workgroup's keys
+  Span own = span_of(a, w, min(r0, w.rows - 1), 32, MODE == kPrefix);   // those of this wavefront's rows
+  bool part = false;  // not all of the wavefront's rows see the prefix
+  if constexpr (MODE == kLine) {
+    for (Span* s : {&all, &own}) {
+      s->first = 0;
+      s->pos_lo = max(s->pos_lo, lead - 1), s->pos_hi = max(s->pos_hi, lead - 1);
+      s->last = s->pos_hi + 1, s->window = s->last + 1;
+    }
+    part = !__all(sees);
+  }
   int t_first = all.first, t_last = all.last;
   if (cut) {
     const int steps = (max(t_last - t_first, 0) + kKeys - 1) / kKeys;
@@ -1288,16 +1313,25 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
   const uint32_t* codes = static_cast<const uint32_t*>(is_v ? a.cache.v_codes : a.cache.k_codes);
   const uint16_t* scales = static_cast<const uint16_t*>(is_v ? a.cache.v_scales : a.cache.k_scales);
   constexpr bool kOver = MODE == kPrefix;
-  const int blocks = kOver ? a.prefix_blocks : a.max_blocks;
-  const ScalarInts table = scalar_ints((kOver ? a.prefix_table : a.block_table) + (int64_t)w.seq * blocks);
+  int blocks = kOver ? a.prefix_blocks : a.max_blocks;
+  ScalarInts table = scalar_ints((kOver ? a.prefix_table : a.block_table) + (int64_t)w.seq * blocks);
   const int tpp = a.cache.page_size / kTokTile;
   constexpr int kTilesApart = kApart / kTokTile;
   const int stride_block = kTilesApart / tpp, stride_rem = kTilesApart - stride_block * tpp;
-  const int last_tile = max(t_last - 1, 0) / kTokTile;
+  int last_tile = max(t_last - 1, 0) / kTokTile;
   Walk next;
   next.tile = t_first / kTokTile + 4 * half + 2 * pair;
-  next.block = next.tile / tpp;
-  next.in_page = next.tile - next.block * tpp;
+  bool in_prefix = MODE == kLine && next.tile < lead / kTokTile;
+  {
+    const int tile = MODE == kLine && !in_prefix ? next.tile - lead / kTokTile : next.tile;
+    next.block = tile / tpp;
+    next.in_page = tile - next.block * tpp;
+  }
+  if (MODE == kLine && in_prefix) {
+    blocks = a.prefix_blocks;
+    table = scalar_ints(a.prefix_table + (int64_t)group_of * blocks);
+    last_tile = min(last_tile, max(prefix - 1, 0) / kTokTile);
+  }
   uint32_t raw[2][KB];  // codes of the 64 keys after those in LDS
   uint16_t raw_s[GC];   // scale of key lane % 32
   bool raw_there[2];
@@ -1330,6 +1364,15 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
       next.in_page -= tpp;
       ++next.block;
     }
+    if (MODE == kLine && in_prefix && next.tile >= lead / kTokTile) {  // on to the sequence's own
+      in_prefix = false;
+      blocks = a.max_blocks;
+      table = scalar_ints(a.block_table + (int64_t)w.seq * blocks);
+      last_tile = max(t_last - 1, 0) / kTokTile;
+      const int tile = next.tile - lead / kTokTile;
+      next.block = tile / tpp;
+      next.in_page = tile - next.block * tpp;
+    }
     fetch_pages();
   };
   auto convert = [&]() __attribute__((always_inline)) {
@@ -1354,7 +1397,8 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
     }
     // what no row sees may hold anything: 0 * NaN must not arise
     const int key = raw_t0 + 32 * pair + (lane & 31);
-    const bool seen = ((lane & 16) ? raw_there[1] : raw_there[0]) && key < t_last && key > all.pos_lo - all.window;
+    const bool seen = ((lane & 16) ? raw_there[1] : raw_there[0]) && key < t_last && key > all.pos_lo - all.window &&
+                      (MODE != kLine || key < prefix || key >= lead);
     int top = 0;
 #pragma unroll
     for (int g = 0; g < GC; ++g) {
@@ -1397,7 +1441,8 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
       const bool there0 = __builtin_amdgcn_readfirstlane(from->there[2 * h]);
       const bool there1 = __builtin_amdgcn_readfirstlane(from->there[2 * h + 1]);
       const bool edge =
-          th + kStep > own.pos_lo + 1 || th <= own.pos_hi - own.window || th + kStep > t_last || !there0 || !there1;
+          th + kStep > own.pos_lo + 1 || th <= own.pos_hi - own.window || th + kStep > t_last || !there0 || !there1 ||
+          (MODE == kLine && th < lead && (part || th + kStep > prefix));
 
       // scores, base 2, relative to m + E
       float s[16];
@@ -1418,7 +1463,8 @@ void attn_rows_kernel(AttnArgs a, int tiles, int swizzle) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int key = th + 8 * (i >> 2) + 4 * c + (i & 3);
-          if (!(i < 8 ? there0 : there1) || key >= t_last || key > pos || key <= pos - own.window) {
+          if (!(i < 8 ? there0 : there1) || key >= t_last || key > pos || key <= pos - own.window ||
+              (MODE == kLine && key < lead && (key >= prefix || !sees))) {
             s[i] = -__builtin_inff();
             hidden |= 1u << i;
           }

@@ -43,6 +43,25 @@ hipError_t both_t(const AttnArgs& a, hipStream_t stream) {
 }
 
 template <int D, int GC>
+hipError_t line_t(const AttnArgs& a, hipStream_t stream) {
+  const int64_t rows = (int64_t)a.max_q * (a.q_heads / a.cache.kv_heads);
+  const int tiles = (int)((rows + 127) / 128);
+  const int swizzle = (int64_t)a.cache.kv_heads * a.seqs % 8 == 0 && tiles > 1;
+  hipLaunchKernelGGL((attn_rows_kernel<D, GC, true, kLine>), dim3((unsigned)(a.whole + a.tail * a.pieces)), dim3(256),
+                     sizeof(Shared<D, GC>), stream, a, tiles, swizzle);
+  if (a.tail > 0)
+    hipLaunchKernelGGL(attn_join_rows_kernel<D>, dim3((unsigned)(a.tail * 32)), dim3(256), 0, stream, a, tiles, swizzle);
+  return hipGetLastError();
+}
+
+template <int D, int GC>
+int line_resident_t() {
+  return resident_per_cu(reinterpret_cast<const void*>(&attn_rows_kernel<D, GC, true, kLine>), 256,
+                         sizeof(Shared<D, GC>)) *
+         device_cu_count_cached();
+}
+
+template <int D, int GC>
 int prefix_resident_t(int rows_group) {
   if (rows_group == 16) return resident_grid(reinterpret_cast<const void*>(&attn16_kernel<D, GC, false, kBoth>), 256);
   return resident_per_cu(reinterpret_cast<const void*>(&attn_rows_kernel<D, GC, true, kPrefix, halves(D)>),
@@ -60,6 +79,18 @@ int prefix_attention_resident(int head_dim, int group, int rows_group) {
 
 hipError_t launch_prefix_attention(const AttnArgs& a, hipStream_t stream) {
 #define Q4_CALL(D, GC) prefix_t<D, GC>(a, stream)
+  Q4_ATTN_DISPATCH(a.cache.head_dim, a.cache.group, Q4_CALL)
+#undef Q4_CALL
+}
+
+int line_attention_resident(int head_dim, int group) {
+#define Q4_CALL(D, GC) line_resident_t<D, GC>()
+  Q4_ATTN_DISPATCH(head_dim, group, Q4_CALL)
+#undef Q4_CALL
+}
+
+hipError_t launch_line_attention(const AttnArgs& a, hipStream_t stream) {
+#define Q4_CALL(D, GC) line_t<D, GC>(a, stream)
   Q4_ATTN_DISPATCH(a.cache.head_dim, a.cache.group, Q4_CALL)
 #undef Q4_CALL
 }

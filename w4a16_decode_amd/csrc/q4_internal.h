@@ -227,6 +227,9 @@ hipError_t launch_attention(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_prefix_attention(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_behind_attention(const AttnArgs& a, hipStream_t stream);
 hipError_t launch_both_attention(const AttnArgs& a, hipStream_t stream);
+// Each sequence's prefix and own keys as one line of keys: whole jobs, then `tail` cut ones and their join.
+hipError_t launch_line_attention(const AttnArgs& a, hipStream_t stream);
+int line_attention_resident(int head_dim, int group);
 // Workgroups over prefixes, of rows_group 128 or (in one launch with the rest) 16, that the device holds at once.
 int prefix_attention_resident(int head_dim, int group, int rows_group);
 hipError_t launch_rope(const RopeArgs& a, hipStream_t stream);
