@@ -256,9 +256,11 @@ q4_status pick_shared(int64_t groups, int64_t max_group_q, int64_t max_prefix, q
   a->own_pieces = 0;
   if (own_rows >= 640) {
     const int64_t jobs = (own_rows + 127) / 128 * heads * a->seqs, slots = q4::line_attention_resident(d, g);
-    // of these the call's rows fill about so many; the last round's share of them is cut
+    // of these the call's rows fill about so many; the last round's share of them is cut, and a tenth of a round
+    // more, so that no whole job is left for it
     const int64_t full = std::min(jobs, ((int64_t)a->tokens * share / 128 + (a->seqs + 1) / 2) * heads);
-    const int64_t rest = full % slots;
+    int64_t rest = full % slots;
+    if (full > slots && rest > 0) rest = std::min(rest + slots / 10, slots);
     const int64_t pieces = rest > 0 ? std::min(slots / rest, (max_prefix + a->max_kv) / 512) : 0;
     a->prefix_pieces = a->prefix_rows = 0;
     a->rows_group = 128, a->shares = 0;
