@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass, field
+from functools import lru_cache
 
 from . import _lib
 from ._tensors import array, call, complain, device, enter, on_device, torch_
@@ -271,6 +272,16 @@ def paged_attention_shared_workspace_bytes(seqs: int, groups: int, tokens: int, 
                                                                      max_prefix, q_heads, kv_heads, head_dim, group))
 
 
+@lru_cache(maxsize=1024)  # of sizes alone; the split, and with it the workspace, depends on the device
+def _shared_workspace(dev: int, *sizes) -> int:
+    cur = enter(dev)
+    try:
+        return int(_lib.load().q4_paged_attention_shared_workspace_bytes(*sizes))
+    finally:
+        if cur != dev:
+            torch_().cuda.set_device(cur)
+
+
 def paged_attention_shared(q, cache: PagedKVCache4, prefix_table, prefix_lens, group_offsets, block_table, q_offsets,
                            kv_lens, max_q: int, max_kv: int, max_group_q: int, max_prefix: int,
                            scale: float | None = None, out=None, workspace=None):
@@ -303,16 +314,9 @@ def paged_attention_shared(q, cache: PagedKVCache4, prefix_table, prefix_lens, g
         to = out.data_ptr()
     else:
         to = array(out, "out", torch.float16, (n, hq, d), dev)
-    lib = _lib.load()
-    cur = enter(dev)  # the split, and with it the workspace, depends on the device
-    try:
-        need = lib.q4_paged_attention_shared_workspace_bytes(seqs, groups, n, max_q, max_kv, max_group_q, max_prefix, hq,
-                                                             heads, d, cache.group)
-    finally:
-        if cur != dev:
-            torch.cuda.set_device(cur)
+    need = _shared_workspace(dev, seqs, groups, n, max_q, max_kv, max_group_q, max_prefix, hq, heads, d, cache.group)
     ws, size = _workspace(q, need, workspace)
-    call(lib.q4_paged_attention_shared, dev, q.data_ptr(), qs, ref, ptab, prefix_blocks, plens, goff, groups, tab, blocks,
+    call(_lib.load().q4_paged_attention_shared, dev, q.data_ptr(), qs, ref, ptab, prefix_blocks, plens, goff, groups, tab, blocks,
          off, lens, seqs, n, max_q, max_kv, max_group_q, max_prefix, hq, d ** -0.5 if scale is None else scale, to, ws,
          size)
     return out

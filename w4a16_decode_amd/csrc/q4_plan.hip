@@ -18,18 +18,27 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 
-// Exclusive sums over the workgroup of two 64-bit numbers a thread, and the totals.
+// Exclusive sums over the workgroup of two 64-bit numbers a thread, and the totals. Each call has its own LDS.
 struct Pair64 {
   int64_t a, b;
 };
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t plus_dpp(int64_t v) {
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), CTRL, ROWS, 0xF, false);
+  return v + (int64_t)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo);
+}
+__device__ __forceinline__ int64_t wave_scan(int64_t v) {  // inclusive: rows of 16 lanes, then from row to row
+  v = plus_dpp<0x111, 0xF>(v);
+  v = plus_dpp<0x112, 0xF>(v);
+  v = plus_dpp<0x114, 0xF>(v);
+  v = plus_dpp<0x118, 0xF>(v);
+  v = plus_dpp<0x142, 0xA>(v);
+  return plus_dpp<0x143, 0xC>(v);
+}
 __device__ __forceinline__ Pair64 block_scan(Pair64 v, Pair64* wave_sums, Pair64* total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = (int)(blockDim.x >> 6);
-  Pair64 incl = v;
-#pragma unroll
-  for (int m = 1; m < kWave; m <<= 1) {
-    const int64_t a = __shfl_up((long long)incl.a, m, 64), b = __shfl_up((long long)incl.b, m, 64);
-    if (lane >= m) incl.a += a, incl.b += b;
-  }
+  const Pair64 incl{wave_scan(v.a), wave_scan(v.b)};
   if (lane == kWave - 1) wave_sums[wave] = incl;
   __syncthreads();
   Pair64 before{0, 0}, all{0, 0};
@@ -38,7 +47,6 @@ __device__ __forceinline__ Pair64 block_scan(Pair64 v, Pair64* wave_sums, Pair64
     if (w < wave) before.a += s.a, before.b += s.b;
     all.a += s.a, all.b += s.b;
   }
-  __syncthreads();  // wave_sums may be written again
   *total = all;
   return Pair64{before.a + incl.a - v.a, before.b + incl.b - v.b};
 }
@@ -83,7 +91,8 @@ __device__ __forceinline__ void plan_row(const PlanArgs& a, int row, int total, 
 // rows too (seqs <= kPlanThreads), else what the rows need is left in the workspace.
 template <bool FILL>
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
-  __shared__ Pair64 wave_sums[kPlanThreads / kWave];
+  __shared__ Pair64 wave_sums[2][kPlanThreads / kWave];
+  __shared__ int2 given[kPlanThreads];  // pages that a sequence gives back, and where to
   __shared__ int off_of[FILL ? kPlanThreads + 1 : 1];
   __shared__ PlanSeq seq_of[FILL ? kPlanThreads : 1];
   const int lane = threadIdx.x & 63;
@@ -99,23 +108,25 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
       int n = 0;
       if (s < a.seqs && a.reset[s] != 0) n = (min(max(a.kv_lens[s], 0), cap) + page - 1) / page;
       Pair64 total;
-      const int64_t at = avail + block_scan(Pair64{n, 0}, wave_sums, &total).a;
-      // a wavefront copies the pages of its own lanes' sequences, one sequence after the other
-      for (uint64_t left = __ballot(n > 0); left; left &= left - 1) {
-        const int l = __builtin_ctzll(left);
-        const int64_t to = __shfl((long long)at, l, 64);
-        const int count = __shfl(n, l, 64);
-        const int32_t* from = a.block_table + (int64_t)(s - lane + l) * a.max_blocks;
-        for (int i = lane; i < count; i += kWave)
-          if (to + i < a.pages) a.free_pages[to + i] = from[i];
+      const int64_t at = avail + block_scan(Pair64{n, 0}, wave_sums[0], &total).a;
+      if (total.a > 0) {
+        given[threadIdx.x] = make_int2(n, (int)(at < a.pages ? at : a.pages));
+        __syncthreads();
+        for (int i = (int)threadIdx.x >> 6; i < threads && base + i < a.seqs; i += threads >> 6) {  // a wavefront a sequence
+          const int2 g = given[i];
+          const int32_t* from = a.block_table + (int64_t)(base + i) * a.max_blocks;
+          for (int j = lane; j < g.x; j += kWave)
+            if (j < a.pages - g.y) a.free_pages[g.y + j] = from[j];
+        }
       }
+      __syncthreads();  // given and wave_sums may be written again
       avail += total.a;
     }
     avail = avail < a.pages ? avail : a.pages;
     __syncthreads();  // the stack is complete before pages are taken from it
   }
 
-  int64_t rows = 0, taken = 0, lacking = 0, granted_all = 0;
+  int64_t rows = 0, taken = 0, wanted = 0;
   for (int base = 0; base < a.seqs; base += threads) {
     const int s = base + (int)threadIdx.x;
     const bool there = s < a.seqs;
@@ -125,21 +136,19 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
       fresh = a.new_lens ? min(max(a.new_lens[s], 0), a.tokens) : 1;
     }
     Pair64 total;
-    const int64_t first = rows + block_scan(Pair64{there ? fresh : 0, 0}, wave_sums, &total).a;
+    const int64_t first = rows + block_scan(Pair64{there ? fresh : 0, 0}, wave_sums[0], &total).a;
     const int off = (int)(first < a.tokens ? first : a.tokens);
     const int end = (int)(first + fresh < a.tokens ? first + fresh : a.tokens);
     rows += total.a;
     const int have = (len + page - 1) / page;
     const int want = there ? (int)(((int64_t)len + (end - off) + page - 1) / page) : have;
     const int need = min(want, a.max_blocks) - have;  // have <= max_blocks
-    const Pair64 ex = block_scan(Pair64{need, 0}, wave_sums, &total);
+    const Pair64 ex = block_scan(Pair64{need, want - have}, wave_sums[1], &total);
     const int64_t place = taken + ex.a;
     taken += total.a;
+    wanted += total.b;
     int granted = need;
     if (a.free_pages) granted = (int)(avail - place < 0 ? 0 : avail - place < need ? avail - place : need);
-    block_scan(Pair64{want - have - granted, granted}, wave_sums, &total);
-    lacking += total.a;
-    granted_all += total.b;
     if (there) {
       const int64_t room = (int64_t)(have + granted) * page, full = (int64_t)len + (end - off);
       const PlanSeq mine{len, (int)place};
@@ -153,6 +162,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
       }
     }
   }
+  // pages go out in order until there are none
+  const int64_t granted_all = a.free_pages && avail < taken ? avail : taken, lacking = wanted - granted_all;
   const int total_rows = (int)(rows < a.tokens ? rows : a.tokens);
   if (threadIdx.x == 0) {
     a.q_offsets[a.seqs] = total_rows;

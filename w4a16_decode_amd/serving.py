@@ -33,7 +33,7 @@ def page_pool(pages: int, device="cuda") -> PagePool:
                     torch.full((1,), pages, dtype=torch.int32, device=device))
 
 
-@dataclass
+@dataclass(slots=True)
 class BatchPlan:
     """What q4_paged_plan writes, all int32 on the GPU."""
 
@@ -65,8 +65,9 @@ def paged_plan(kv_lens, new_lens, block_table, page_size: int, tokens: int, pool
     i32 = torch.int32
     tab = array(block_table, "block_table", i32, shape, dev)
     lens = array(kv_lens, "kv_lens", i32, (seqs,), dev)
-    new, start, rst = (0 if t is None else array(t, name, i32, (seqs,), dev)
-                       for t, name in ((new_lens, "new_lens"), (starts, "starts"), (reset, "reset")))
+    new = 0 if new_lens is None else array(new_lens, "new_lens", i32, (seqs,), dev)
+    start = 0 if starts is None else array(starts, "starts", i32, (seqs,), dev)
+    rst = 0 if reset is None else array(reset, "reset", i32, (seqs,), dev)
     stack = count = count_to = 0
     if pool is not None:
         if pages is not None:
@@ -74,28 +75,31 @@ def paged_plan(kv_lens, new_lens, block_table, page_size: int, tokens: int, pool
         pages = pool.pages.shape[0]
         stack = array(pool.pages, "pool.pages", i32, (pages,), dev)
         count = array(pool.count, "pool.count", i32, (1,), dev)
-        if free_count_out is None:
-            free_count_out = torch.empty(1, dtype=i32, device=device(dev))
-        count_to = array(free_count_out, "free_count_out", i32, (1,), dev)
+        if free_count_out is not None:
+            count_to = array(free_count_out, "free_count_out", i32, (1,), dev)
     elif pages is None:
         raise ValueError("without a pool, pages (of the cache) must be given")
     elif free_count_out is not None:
         raise ValueError("free_count_out goes with a pool")
-    if kv_lens_out is None:
-        kv_lens_out = torch.empty_like(kv_lens)
-    lens_to = array(kv_lens_out, "kv_lens_out", i32, (seqs,), dev)
+    lens_to = 0 if kv_lens_out is None else array(kv_lens_out, "kv_lens_out", i32, (seqs,), dev)
     if tokens < 0:
         raise ValueError("tokens must be >= 0")
-    # one allocation, the parts on 16-byte boundaries
-    n, row = (seqs + 4) // 4 * 4, (tokens + 3) // 4 * 4
-    buf = torch.empty(4 + n + 2 * row, dtype=i32, device=device(dev))
-    lacking, q_offsets = buf[:1], buf[4:5 + seqs]
-    positions, slots = buf[4 + n:4 + n + tokens], buf[4 + n + row:4 + n + row + tokens]
+    # one allocation for what is made here
+    buf = torch.empty(3 + 2 * (seqs + tokens), dtype=i32, device=device(dev))
+    lacking, count_new, lens_new, q_offsets, positions, slots = buf.split_with_sizes(
+        (1, 1, seqs, seqs + 1, tokens, tokens))
     at = buf.data_ptr()
+    if kv_lens_out is None:
+        kv_lens_out, lens_to = lens_new, at + 8
+    if pool is not None and free_count_out is None:
+        free_count_out, count_to = count_new, at + 4
+    offsets_to = at + 8 + 4 * seqs
+    positions_to = offsets_to + 4 + 4 * seqs
     lib = _lib.load()
-    ws, size = _workspace(block_table, lib.q4_paged_plan_workspace_bytes(seqs, tokens), workspace)
+    need = lib.q4_paged_plan_workspace_bytes(seqs, tokens)
+    ws, size = (None, 0) if need == 0 and workspace is None else _workspace(block_table, need, workspace)
     call(lib.q4_paged_plan, dev, lens, new, rst, start, seqs, tokens, page_size, pages, tab, blocks, stack, count,
-         at + 16, at + 4 * (4 + n), at + 4 * (4 + n + row), lens_to, count_to, at, ws, size)
+         offsets_to, positions_to, positions_to + 4 * tokens, lens_to, count_to, at, ws, size)
     return BatchPlan(q_offsets, positions, slots, kv_lens_out, free_count_out, lacking)
 
 
