@@ -157,7 +157,7 @@ struct Row {
   double top;    // largest logit
   double slope;  // log2(e) / temperature; greedy: so steep that nothing below the largest has weight
   double shift;
-  float bin_scale;
+  float bin_top, bin_slope;  // bins a step of the logit
   int k;  // 0: no top-k
   bool infinite;  // the largest logit is: those count as 0, all others as -infinity
   bool cut_p, greedy;
@@ -174,7 +174,8 @@ __device__ __forceinline__ Row row_settings(const SampleArgs& a, int row, float 
   r.greedy = !(t > 0.0f);
   r.slope = r.greedy ? 1e300 : 1.4426950408889634 / (double)t;
   r.shift = (double)a.shift;
-  r.bin_scale = (float)kBins / (float)(a.shift + 2);
+  r.bin_top = (float)r.top;
+  r.bin_slope = (float)__builtin_fmin(r.slope * kBins / (a.shift + 2), 1e38);
   r.k = a.top_k ? a.top_k[row] : 0;
   if (r.greedy || r.k < 0 || r.k >= a.vocab) r.k = 0;
   r.p = a.top_p ? (double)a.top_p[row] : 1.0;
@@ -199,7 +200,6 @@ __device__ __forceinline__ void settle_all(const Row& r, float (&v)[N]) {
 __device__ __forceinline__ double exponent(const Row& r, float v) {
   return __builtin_fma((double)v - r.top, r.slope, r.shift);
 }
-__device__ __forceinline__ bool has_weight(double z) { return z > -1.0; }
 
 // rint(2^z), z <= 50, 0 for no weight: with k = rint(256 z), 2^(k / 256) from the table and
 // 2^(z - k / 256) by its series to the fourth power, whose next term is below 2^-54; the whole is
@@ -222,8 +222,11 @@ template <int N>
 __device__ __forceinline__ void fill_table(double* table) {
   if (N == 256 || threadIdx.x < 256) table[threadIdx.x] = exp2((double)threadIdx.x / 256);
 }
-__device__ __forceinline__ int bin_of(const Row& r, double z) {  // of a token with weight
-  return min(kBins - 1, (int)((float)(r.shift - z) * r.bin_scale));
+// The weight's binades below the largest one's, shift + 2 of them in kBins bins. In float32, as all that is asked
+// of it is that it grows with the rank; tokens of the last bin have no weight.
+constexpr int kNoBin = kBins - 1;
+__device__ __forceinline__ int bin_of(const Row& r, float v) {
+  return (int)fminf((r.bin_top - v) * r.bin_slope, (float)kNoBin);
 }
 
 // ---- cuts -----------------------------------------------------------------------------
@@ -476,13 +479,11 @@ __device__ __forceinline__ u64 cut_tokens(const Row& r, const Cut& cut, int coun
 
 // Weight of a token that the cuts left, else 0.
 __device__ __forceinline__ u64 kept_weight(const Row& r, const Cut& cut, u64 last, float v, int i, const double* table) {
-  const double z = exponent(r, v);
   if (cut.last >= 0) {
-    if (!has_weight(z)) return 0;
-    const int bin = bin_of(r, z);
+    const int bin = bin_of(r, v);
     if (bin > cut.last || (bin >= cut.first && rank_key(v, i) > last)) return 0;
   }
-  const u64 w = weight_of(z, table);
+  const u64 w = weight_of(exponent(r, v), table);
   return w >= r.w_min ? w : 0;
 }
 
@@ -571,15 +572,14 @@ __global__ __launch_bounds__(kWhole) void whole_kernel(SampleArgs a) {
     if (r.k > 0) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const double z = exponent(r, v[e]);
-        if (has_weight(z)) atomicAdd(&s.counts[bin_of(r, z)], 1u);
-        apart(e);
+        const int bin = bin_of(r, v[e]);
+        if (bin < kNoBin) atomicAdd(&s.counts[bin], 1u);
       }
     } else {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const double z = exponent(r, v[e]);
-        if (has_weight(z)) atomicAdd(&s.bins[bin_of(r, z)], weight_of(z, s.table));
+        const int bin = bin_of(r, v[e]);
+        if (bin < kNoBin) atomicAdd(&s.bins[bin], weight_of(exponent(r, v[e]), s.table));
         apart(e);
       }
     }
@@ -590,13 +590,11 @@ __global__ __launch_bounds__(kWhole) void whole_kernel(SampleArgs a) {
       again(v);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        const double z = exponent(r, v[e]);
-        const int bin = has_weight(z) ? bin_of(r, z) : kBins;
+        const int bin = bin_of(r, v[e]);
         if (bin >= cut.first && bin <= cut.last) {
           const int at = atomicAdd(&s.listed, 1);
           if (at < kList) s.list[at] = make_uint2(i0 + e, __builtin_bit_cast(uint32_t, v[e]));
         }
-        apart(e);
       }
       __syncthreads();
       const int count = s.listed;
@@ -612,10 +610,8 @@ __global__ __launch_bounds__(kWhole) void whole_kernel(SampleArgs a) {
         last = cut_list<kWhole>(r, cut, s.digits, s.scan[1], [&](auto f) __attribute__((always_inline)) {
           for (int i = threadIdx.x; i < a.vocab; i += kWhole) {
             const float x = settle(r, load_one<DT>(p, i));
-            const double z = exponent(r, x);
-            if (!has_weight(z)) continue;
-            const int bin = bin_of(r, z);
-            if (bin >= cut.first && bin <= cut.last) f(rank_key(x, i), weight_of(z, s.table));
+            const int bin = bin_of(r, x);
+            if (bin >= cut.first && bin <= cut.last) f(rank_key(x, i), weight_of(exponent(r, x), s.table));
           }
         }, [](u64, u64) {});
       }
@@ -706,14 +702,14 @@ __global__ __launch_bounds__(kThreads) void bins_kernel(SampleArgs a) {
   if (r.k > 0) {
 #pragma unroll
     for (int e = 0; e < kRun; ++e) {
-      const double z = exponent(r, v[e]);
-      if (has_weight(z)) atomicAdd(&counts[bin_of(r, z)], 1u);
+      const int bin = bin_of(r, v[e]);
+      if (bin < kNoBin) atomicAdd(&counts[bin], 1u);
     }
   } else {
 #pragma unroll
     for (int e = 0; e < kRun; ++e) {
-      const double z = exponent(r, v[e]);
-      if (has_weight(z)) atomicAdd(&bins[bin_of(r, z)], weight_of(z, table));
+      const int bin = bin_of(r, v[e]);
+      if (bin < kNoBin) atomicAdd(&bins[bin], weight_of(exponent(r, v[e]), table));
     }
   }
   __syncthreads();
@@ -750,14 +746,13 @@ __global__ __launch_bounds__(kThreads) void sums_kernel(SampleArgs a) {
   u64 sum = 0;
 #pragma unroll
   for (int e = 0; e < kRun; ++e) {
-    const double z = exponent(r, v[e]);
     int bin = -1;
     if (cut.last >= 0) {
-      bin = has_weight(z) ? bin_of(r, z) : kBins;
+      bin = bin_of(r, v[e]);
       if (bin > cut.last) continue;
     }
     if (bin < cut.first) {
-      const u64 w = weight_of(z, table);
+      const u64 w = weight_of(exponent(r, v[e]), table);
       sum += w >= r.w_min ? w : 0;
     } else {
       a.list[(int64_t)blockIdx.x * kChunk + atomicAdd(&listed, 1)] =
