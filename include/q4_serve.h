@@ -57,8 +57,8 @@ q4_status q4_paged_plan(const int32_t* kv_lens, const int32_t* new_lens, const i
                         int32_t* lacking, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---- the next tokens -------------------------------------------------------------
- * One token of each row of logits [rows][vocab], rows `stride` elements apart, for a given
- * uniform random number u in [0, 1) a row. With m the row's largest logit:
+ * One token of each row of logits [rows][vocab], rows `stride` >= 0 elements apart (0: all
+ * draws from the same logits), for a given uniform random number u in [0, 1) a row. With m the row's largest logit:
  *   w_i = exp((l_i - m) / temperature), tokens ranked by logit, equal ones by index;
  *   top_k: the first k stay (k <= 0 or >= vocab: all);
  *   top_p: of those the shortest run of first ones whose w sum to top_p times theirs or

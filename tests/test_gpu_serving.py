@@ -326,9 +326,11 @@ def test_sample_strided_and_in_place_outputs(q4):
     assert a is out and b is probs and int((out == 77).sum()) < 9
     a, b = q4.sample(wide[:0], torch.rand(0, device="cuda"))
     assert a.shape == (0,) and b.shape == (0,)
-    one = torch.randn(1, 1000, device="cuda").expand(4, 1000)              # all rows the same memory
-    with pytest.raises(q4.Q4Error):
-        q4.sample(one, torch.rand(4, device="cuda"))
+    for n in (1000, 40001):
+        one = torch.randn(1, n, device="cuda").expand(5, n)                # several draws from the same logits
+        check_sample(q4, one, r.random(5), top_k=[0, 0, 9, 0, 3], top_p=[1.0, 0.9, 0.8, 0.1, 1.0])
+    over = torch.randn(5 * 900, device="cuda").as_strided((5, 1500), (700, 1))   # rows that overlap
+    check_sample(q4, over, r.random(5), top_p=[0.95] * 5)
 
 
 def test_sample_distribution(q4):

@@ -119,8 +119,8 @@ q4_status q4_sample(const void* logits, int32_t dtype, int64_t stride, int64_t r
     return fail(Q4_ERR_UNSUPPORTED, "dtype=%d: logits are float16, bfloat16 or float32", (int)dtype);
   q4_status st = check_sample(rows, vocab);
   if (st != Q4_OK) return st;
-  if (rows > 1 && (stride < vocab || stride >= (int64_t(1) << 40)))
-    return fail(Q4_ERR_SHAPE, "stride %lld is not in [vocab, 2^40)", (long long)stride);
+  if (rows > 1 && (stride < 0 || stride >= (int64_t(1) << 40)))
+    return fail(Q4_ERR_SHAPE, "stride %lld is not in [0, 2^40)", (long long)stride);
   if (rows == 0) return ok();
   if (!logits || !uniforms || !tokens) return fail(Q4_ERR_NULL, "logits, uniforms, tokens must be non-NULL");
   if (!aligned(logits, dtype == Q4_F32 ? 4 : 2) || !aligned(uniforms, 4) || !aligned(temperature, 4) ||

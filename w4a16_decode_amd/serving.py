@@ -115,7 +115,7 @@ def sample(logits, uniforms, temperature=None, top_k=None, top_p=None, min_p=Non
     """q4_sample: one token a row, (tokens int32 [rows], probs float32 [rows]).
 
     logits: float16, bfloat16 or float32 [rows, vocab], a row's elements contiguous, rows any
-    stride apart; uniforms: float32 [rows], random numbers in [0, 1); temperature, top_p,
+    stride apart (expanded ones too: several draws from the same logits); uniforms: float32 [rows], random numbers in [0, 1); temperature, top_p,
     min_p: float32 [rows], top_k: int32 [rows], each None where no row is to be cut by it
     (temperature: 1). A temperature <= 0 takes the largest logit. probs: the token's share
     of the tokens that the cuts left."""
