@@ -244,6 +244,7 @@ __device__ __forceinline__ u64 part_of(double p, u64 total) {
   return t < total ? t : total;
 }
 
+constexpr int kFew = 128;  // listed tokens that are ranked by counting
 // own: this thread's bins, the threadIdx.x-th kBins / N.
 template <int N>
 __device__ __forceinline__ Cut find_cut(const Row& r, const u64 (&own)[kBins / N], Scan<N>& s, u64* found) {
@@ -267,7 +268,7 @@ __device__ __forceinline__ Cut find_cut(const Row& r, const u64 (&own)[kBins / N
   }
   __syncthreads();
   const int at = (int)found[0];
-  if (r.k > 0 && r.cut_p) return Cut{0, at, 0, all ? 0 : target};
+  if (r.k > 0 && (r.cut_p || r.k <= kFew)) return Cut{0, at, 0, all ? 0 : target};
   return all ? Cut{kBins, -1, 0, 0} : Cut{at, at, found[1], target};
 }
 
@@ -354,14 +355,26 @@ __device__ __forceinline__ u64 select_key(u64 last, u64 target, Digits& s, Each 
   return prefix;
 }
 
+__device__ __forceinline__ u64 draw_of(const SampleArgs& a, const Row& r, int row, u64 total) {
+  const double u = r.greedy ? 0.0 : (double)a.uniforms[row];
+  const double at = u > 0.0 ? floor(u * (double)total) : 0.0;
+  const u64 draw = at < 9.2e18 ? (u64)at : total;
+  return draw < total ? draw : total - 1;
+}
+
+// The chosen token's share of the tokens that the cuts left, whose weights sum to `total`.
+__device__ __forceinline__ float share_of(const SampleArgs& a, const Row& r, float v, u64 total) {
+  return r.greedy ? 1.0f : (float)(exp2(exponent(r, v) - r.shift) / ldexp((double)total, -a.shift));
+}
+
 // Few listed tokens: every one counts those ranked up to it and adds their weights, N / kFew threads a
 // token, which answers both cuts at once.
-constexpr int kFew = 128;
 struct Few {
   u64 keys[kFew], weights[kFew];
   u64 upto[kFew];    // weights up to the token
   uint32_t rank[kFew];
   u64 total, key_k, key_p;
+  u64 drawn[kFew], all;  // weights that stayed: up to the token's index, of all
 };
 template <int N>
 __device__ __forceinline__ u64 cut_few(const Row& r, const Cut& cut, int count, u64 key, u64 w, Few& s) {
@@ -406,6 +419,39 @@ __device__ __forceinline__ u64 cut_few(const Row& r, const Cut& cut, int count, 
     last = s.key_p < last ? s.key_p : last;
   }
   return last;
+}
+
+// The token that the draw falls into where the cuts leave listed tokens only, `last` from cut_few: each adds up
+// the weights that stayed of those up to its index.
+template <int N>
+__device__ __forceinline__ void draw_few(const SampleArgs& a, const Row& r, int row, int count, u64 key, u64 w, float v,
+                                         u64 last, Few& s) {
+  const int i = (int)threadIdx.x % kFew;
+  const bool any = (int)threadIdx.x < count;
+  if (!any || key > last || w < r.w_min) w = 0;
+  if (threadIdx.x < kFew) s.weights[i] = w, s.drawn[i] = 0;
+  if (threadIdx.x == 0) s.all = 0;
+  __syncthreads();
+  constexpr int kShare = kFew / (N / kFew);
+  const int j0 = (int)threadIdx.x / kFew * kShare;
+  if (j0 < count) {
+    const uint32_t mine = (uint32_t)s.keys[i];
+    u64 upto = 0, all = 0;
+#pragma unroll 4
+    for (int j = j0; j < j0 + kShare; ++j) {
+      const u64 x = s.weights[j];
+      upto += (uint32_t)s.keys[j] <= mine ? x : 0;
+      all += x;
+    }
+    atomicAdd(&s.drawn[i], upto);
+    if (i == 0) atomicAdd(&s.all, all);
+  }
+  __syncthreads();
+  const u64 total = s.all, draw = draw_of(a, r, row, total);
+  if (any && draw < s.drawn[i] && draw >= s.drawn[i] - w) {
+    a.tokens[row] = (int)(uint32_t)key;
+    if (a.probs) a.probs[row] = share_of(a, r, v, total);
+  }
 }
 
 // Key of the last token that top-k and top-p leave of the listed ones. kept(key, w): each that min-p leaves too.
@@ -487,13 +533,6 @@ __device__ __forceinline__ u64 kept_weight(const Row& r, const Cut& cut, u64 las
   return w >= r.w_min ? w : 0;
 }
 
-__device__ __forceinline__ u64 draw_of(const SampleArgs& a, const Row& r, int row, u64 total) {
-  const double u = r.greedy ? 0.0 : (double)a.uniforms[row];
-  const double at = u > 0.0 ? floor(u * (double)total) : 0.0;
-  const u64 draw = at < 9.2e18 ? (u64)at : total;
-  return draw < total ? draw : total - 1;
-}
-
 // The token of this thread's run v, i0 .., that the draw falls into, `upto` being the sum before the run.
 template <int N, typename Weight>
 __device__ __forceinline__ void write_token(const SampleArgs& a, const Row& r, int row, int i0, const float (&v)[N],
@@ -506,8 +545,7 @@ __device__ __forceinline__ void write_token(const SampleArgs& a, const Row& r, i
     if (draw >= upto) i = j + 1, x = v[j + 1];
   }
   a.tokens[row] = i0 + i;
-  if (a.probs)
-    a.probs[row] = r.greedy ? 1.0f : (float)(exp2(exponent(r, x) - r.shift) / ldexp((double)total, -a.shift));
+  if (a.probs) a.probs[row] = share_of(a, r, x, total);
 }
 
 __device__ __forceinline__ void write_none(const SampleArgs& a, int row) {
@@ -806,19 +844,30 @@ __global__ __launch_bounds__(kChoose) void choose_kernel(SampleArgs a) {
   }
   __syncthreads();
   u64 last = ~0ull;  // key of the last token that top-k and top-p leave
+  auto token_at = [&](int n, float* x) __attribute__((always_inline)) {
+    int lo = 0, hi = a.chunks;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s.starts[mid] <= n) lo = mid; else hi = mid;
+    }
+    const uint2 l = a.list[(first_chunk + lo) * kChunk + (n - s.starts[lo])];
+    *x = __builtin_bit_cast(float, l.y);
+    return (int)l.x;
+  };
+  if (cut.first == 0 && listed <= kFew) {  // nothing but listed tokens, and few of them
+    u64 key = 0, w = 0;
+    float v = 0.0f;
+    if (threadIdx.x < listed) {
+      const int token = token_at(threadIdx.x, &v);
+      key = rank_key(v, token);
+      w = weight_of(exponent(r, v), s.table);
+    }
+    last = cut_few<kChoose>(r, cut, (int)listed, key, w, s.few);
+    return draw_few<kChoose>(a, r, row, (int)listed, key, w, v, last, s.few);
+  }
   if (listed > 0) {
     last = cut_tokens<kChoose>(
-        r, cut, (int)listed, s.table, s.digits, s.few, s.scan[1],
-        [&](int n, float* x) __attribute__((always_inline)) {
-          int lo = 0, hi = a.chunks;
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (s.starts[mid] <= n) lo = mid; else hi = mid;
-          }
-          const uint2 l = a.list[(first_chunk + lo) * kChunk + (n - s.starts[lo])];
-          *x = __builtin_bit_cast(float, l.y);
-          return (int)l.x;
-        },
+        r, cut, (int)listed, s.table, s.digits, s.few, s.scan[1], token_at,
         [&](u64 key, u64 w) __attribute__((always_inline)) { atomicAdd(&s.chunk_sums[(uint32_t)key / kChunk], w); });
     __syncthreads();
   }
