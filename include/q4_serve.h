@@ -80,7 +80,7 @@ q4_status q4_paged_plan(const int32_t* kv_lens, const int32_t* new_lens, const i
  * comes within about 1e-12 of a border; a token whose weight rounds to 0 is never drawn.
  * Deterministic. vocab <= 2^20, rows < 2^22, rows *
  * ceil(vocab / 4096) < 2^24 (Q4_ERR_SHAPE). `workspace` (16-byte aligned) must hold
- * q4_sample_workspace_bytes() bytes (NULL when that is 0). */
+ * q4_sample_workspace_bytes() bytes (NULL when that is 0), which serve fewer rows too. */
 typedef enum { Q4_F16 = 0, Q4_BF16 = 1, Q4_F32 = 2 } q4_dtype;
 
 size_t q4_sample_workspace_bytes(int64_t rows, int64_t vocab);

@@ -235,6 +235,19 @@ def test_sample_sizes(q4, dtype, vocab):
     check_sample(q4, x, r.random(rows))
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("vocab", [4096, 16385, 32000, 32767, 32768, 32769])
+def test_sample_many_rows(q4, dtype, vocab):
+    import torch
+
+    say("sample", dtype, vocab)
+    r = np.random.default_rng(vocab + 1)
+    rows = 33                                              # more than those that are split from 16385 logits on
+    x = to_gpu((r.standard_normal((rows, vocab)) * r.uniform(0.1, 6.0, (rows, 1))).astype(np.float32))
+    x = x.to(getattr(torch, dtype))
+    check_sample(q4, x, r.random(rows), **random_settings(r, rows, vocab))
+
+
 def test_sample_large(q4):
     """The largest vocabulary, and 128256 logits with every kind of cut."""
     import torch

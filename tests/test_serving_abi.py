@@ -53,6 +53,9 @@ def test_sample_refusals(lib):
     assert f(x=FAKE + 1) == 4 and f(x=FAKE + 2, dtype=2) == 4
     for name in ("u", "t", "k", "p", "m", "out", "probs"):
         assert f(**{name: FAKE + 2}) == 4, name
+    for vocab in (16384, 16385, 32768, 32769, 128256):     # a workspace serves fewer rows
+        sizes = [lib.q4_sample_workspace_bytes(rows, vocab) for rows in (0, 1, 31, 32, 33, 34, 500)]
+        assert sizes == sorted(sizes) and (sizes[-1] > 0) == (vocab > 16384), (vocab, sizes)
     assert lib.q4_sample_workspace_bytes(-1, 5) == 0 and lib.q4_sample_workspace_bytes(5, 0) == 0
 
 

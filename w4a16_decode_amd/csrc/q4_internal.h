@@ -199,7 +199,7 @@ struct SampleArgs {
   uint2* list;                   // [rows][chunks][kSampleChunk]: which, and their logits
 };
 
-constexpr int kSampleChunk = 4096, kSampleBins = 1024, kSampleMaxChunks = 256, kSampleWhole = 32768;
+constexpr int kSampleChunk = 4096, kSampleBins = 1024, kSampleMaxChunks = 256;
 hipError_t launch_sample(const SampleArgs& a, hipStream_t stream);
 
 // Adapters beside a product (include/q4_lora.h). phase 0: A x into t; phase 1: y from the

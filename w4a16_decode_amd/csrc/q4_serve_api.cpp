@@ -26,13 +26,19 @@ int weight_shift(int64_t vocab) {
   return std::min(50, 62 - bits);
 }
 
-// Chunks of a row; 0: a workgroup takes the whole row.
-int64_t sample_chunks(int64_t vocab) {
-  return vocab <= q4::kSampleWhole ? 0 : (vocab + q4::kSampleChunk - 1) / q4::kSampleChunk;
+// Chunks of a row; 0: a workgroup takes the whole row, in one launch instead of four. Up to 32768 logits fit
+// its registers, but from 16384 on few rows leave most of the chip idle meanwhile. In a graph, a whole
+// row / chunks, us: 16000 float16 logits, 1 row: softmax 8.1 / 12.7, top-p 16.9 / 22.5; 256 rows: 9.8 / 17.5,
+// 18.5 / 31.6. 32000 logits, 1 row: 12.9 / 13.0, 28.8 / 22.5; 17 rows: 13.3 / 13.7, 31.0 / 25.0; 64 rows: 13.6 / 14.9,
+// 30.8 / 27.4 (with top-k too: 17.6 / 20.8); 256 rows: 14.6 / 22.3, 31.5 / 44.5.
+constexpr int64_t kFewRows = 32;
+int64_t sample_chunks(int64_t rows, int64_t vocab) {
+  const bool whole = vocab <= 16384 || (vocab <= 32768 && rows > kFewRows);
+  return whole ? 0 : (vocab + q4::kSampleChunk - 1) / q4::kSampleChunk;
 }
 
 q4_status check_sample(int64_t rows, int64_t vocab) {
-  if (rows < 0 || rows >= kMaxRows || vocab <= 0 || vocab > kMaxVocab || rows * sample_chunks(vocab) > q4::kMaxGroups256)
+  if (rows < 0 || rows >= kMaxRows || vocab <= 0 || vocab > kMaxVocab || rows * sample_chunks(rows, vocab) > q4::kMaxGroups256)
     return fail(Q4_ERR_SHAPE, "rows=%lld, vocab=%lld out of range", (long long)rows, (long long)vocab);
   return Q4_OK;
 }
@@ -107,7 +113,9 @@ q4_status q4_paged_plan(const int32_t* kv_lens, const int32_t* new_lens, const i
 size_t q4_sample_workspace_bytes(int64_t rows, int64_t vocab) {
   if (check_sample(rows, vocab) != Q4_OK) return 0;
   q4::SampleArgs a{};
-  a.rows = (int)rows, a.chunks = (int)sample_chunks(vocab);
+  // what serves a number of rows serves fewer
+  const int64_t n = sample_chunks(rows, vocab) == 0 ? std::min(rows, kFewRows) : rows;
+  a.rows = (int)n, a.chunks = (int)sample_chunks(n, vocab);
   return place_sample(&a, nullptr);
 }
 
@@ -131,7 +139,7 @@ q4_status q4_sample(const void* logits, int32_t dtype, int64_t stride, int64_t r
   a.rows = (int)rows, a.vocab = (int)vocab;
   a.uniforms = uniforms, a.temperature = temperature, a.top_k = top_k, a.top_p = top_p, a.min_p = min_p;
   a.tokens = tokens, a.probs = probs, a.shift = weight_shift(vocab);
-  a.chunks = (int)sample_chunks(vocab);
+  a.chunks = (int)sample_chunks(rows, vocab);
   const size_t need = place_sample(&a, static_cast<unsigned char*>(workspace));
   if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(Q4_ERR_WORKSPACE, "this shape needs %zu bytes of workspace (q4_sample_workspace_bytes), got %zu", need,
