@@ -170,8 +170,14 @@ struct PlanArgs {
   int32_t* seq_info;  // two launches: int32 [seqs][2], length and place of the first new page, and the stack's depth
 };
 
-// Whether one workgroup writes the rows too.
-constexpr bool plan_one_launch(int64_t seqs, int64_t tokens) { return seqs <= 1024 && tokens <= 2048; }
+// 256 threads scan up to 256 sequences, else 1024 (48 tokens of as many sequences: 4.2 us in a graph, 5.8 with 1024
+// threads; 3904 of 61: 6.8, 8.2).
+constexpr int kPlanSmall = 256, kPlanThreads = 1024;
+// Whether that workgroup writes the rows too, in a graph, us, against two launches: 48 sequences, 48 rows 4.2 / 5.7;
+// 4, 2048 rows 8.0 / 6.0 (8, 1024 rows 6.0 in one); 1000, 1000 rows 7.2 / 10.1; 1000, 8000 rows 16.1 / 9.8.
+constexpr bool plan_one_launch(int64_t seqs, int64_t tokens) {
+  return seqs <= kPlanSmall ? tokens <= 1024 : seqs <= kPlanThreads && tokens <= 2048;
+}
 hipError_t launch_plan(const PlanArgs& a, hipStream_t stream);
 
 // One token of each row of logits (include/q4_serve.h).
