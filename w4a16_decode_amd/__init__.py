@@ -1,7 +1,7 @@
 """w4a16_decode_amd: INT4 group-wise RTN weight quantization and the fused
 W4A16 GEMV / skinny GEMM for AMD MI355X (gfx950), plus per-channel INT8
-weights with the W8A16 GEMV, and the attention side of a decoder layer on a paged
-INT4 KV cache.
+weights with the W8A16 GEMV, the attention side of a decoder layer on a paged
+INT4 KV cache, and the turn of a serving loop around it (batch plans, sampling).
 
 Every computation runs in the HIP kernels of ``libq4.so`` behind the C ABI
 declared under ``include/``; this package only marshals torch tensors (device
