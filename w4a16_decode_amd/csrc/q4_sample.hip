@@ -158,7 +158,6 @@ __device__ __forceinline__ u64 rank_key(float v, int i) {
   const uint32_t u = __builtin_bit_cast(uint32_t, v);
   return (u64)~(u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u)) << 32 | (uint32_t)i;
 }
-constexpr int kIndexBits = 20;  // of a key
 
 // ---- weights ------------------------------------------------------------------------
 // A row's settings. Greedy (temperature <= 0): only the largest logits have weight, and the draw is 0.
@@ -167,6 +166,7 @@ struct Row {
   double slope;  // log2(e) / temperature; greedy: so steep that nothing below the largest has weight
   double shift;
   float bin_top, bin_slope;  // bins a step of the logit
+  int index_bits;            // of a key
   int k;  // 0: no top-k
   bool infinite;  // the largest logit is: those count as 0, all others as -infinity
   bool cut_p, greedy;
@@ -185,6 +185,7 @@ __device__ __forceinline__ Row row_settings(const SampleArgs& a, int row, float 
   r.shift = (double)a.shift;
   r.bin_top = (float)r.top;
   r.bin_slope = (float)__builtin_fmin(r.slope * kBins / (a.shift + 2), 1e38);
+  r.index_bits = 32 - __builtin_clz((unsigned)(a.vocab - 1) | 1u);
   r.k = a.top_k ? a.top_k[row] : 0;
   if (r.greedy || r.k < 0 || r.k >= a.vocab) r.k = 0;
   r.p = a.top_p ? (double)a.top_p[row] : 1.0;
@@ -291,7 +292,7 @@ struct Digits {
 // Smallest key up to which the listed tokens with keys <= last add up to `target` or more
 // (1 <= target <= their total). each(f): f(key, weight) for this thread's; ONES: a token counts 1.
 template <int N, bool ONES, typename Each>
-__device__ __forceinline__ u64 select_key(u64 last, u64 target, Digits& s, Each each) {
+__device__ __forceinline__ u64 select_key(const Row& r, u64 last, u64 target, Digits& s, Each each) {
   const int lane = threadIdx.x & 63;
   __syncthreads();  // an earlier cut has been read
   for (int i = threadIdx.x; i < kRounds * kDigits; i += N) {
@@ -315,7 +316,7 @@ __device__ __forceinline__ u64 select_key(u64 last, u64 target, Digits& s, Each 
   __syncthreads();
   ones = s.ones;
   const uint32_t differ = ones & s.zeros;
-  int bit = differ ? 64 - __builtin_clz(differ) : kIndexBits;  // digits from this bit down
+  int bit = differ ? 64 - __builtin_clz(differ) : r.index_bits;  // digits from this bit down
   u64 prefix = bit < 64 ? ((u64)ones << 32) >> bit << bit : 0, before = 0;
   for (int round = 0; bit > 0; ++round) {
     // a digit does not reach from the logit into the index
@@ -349,7 +350,7 @@ __device__ __forceinline__ u64 select_key(u64 last, u64 target, Digits& s, Each 
     bit = at;
     if (at >= 32) {  // down to the next bit in which any two logits differ, or to the index
       const uint32_t below = differ & ((1u << (at - 32)) - 1);
-      bit = below ? 64 - __builtin_clz(below) : kIndexBits;
+      bit = below ? 64 - __builtin_clz(below) : r.index_bits;
       const uint32_t same = ((1u << (at - 32)) - 1) & ~(below ? (1u << (bit - 32)) - 1 : 0);
       prefix |= (u64)(ones & same) << 32;
     }
@@ -467,7 +468,7 @@ __device__ __forceinline__ void draw_few(const SampleArgs& a, const Row& r, int 
 template <int N, typename Each, typename Kept>
 __device__ __forceinline__ u64 cut_list(const Row& r, const Cut& cut, Digits& s, Scan<N>& scan, Each each, Kept kept) {
   u64 last = ~0ull;
-  if (r.k > 0 && cut.target > 0) last = select_key<N, true>(last, cut.target - cut.before, s, each);
+  if (r.k > 0 && cut.target > 0) last = select_key<N, true>(r, last, cut.target - cut.before, s, each);
   if (r.cut_p) {
     u64 target = cut.target - cut.before;
     if (r.k > 0) {
@@ -476,7 +477,7 @@ __device__ __forceinline__ u64 cut_list(const Row& r, const Cut& cut, Digits& s,
       block_scan<N>(sum, scan, &total);
       target = part_of(r.p, total);
     }
-    last = select_key<N, false>(last, target, s, each);
+    last = select_key<N, false>(r, last, target, s, each);
   }
   each([&](u64 key, u64 w) __attribute__((always_inline)) {
     if (key <= last && w >= r.w_min) kept(key, w);
