@@ -23,7 +23,7 @@
 //           the token in it.
 //
 // What bounds it: with few rows the chain of four launches (15 us of one greedy row in a graph, of 128256
-// logits; 18 with top-k, 24 to 26 with top-p alone, whose bin holds more tokens than are ranked at once). 64 rows
+// logits; 18 with top-k, 23 to 25 with top-p alone, whose bin holds more tokens than are ranked at once). 64 rows
 // of 128256 float32 logits (33 MB, 7 us at a large copy's rate) take 5.7 + 12.4 + 13.0 + 12.1 us: logits and bins are
 // waited for at the start of each pass, a weight's float64 arithmetic and its sum are 35 vector instructions a
 // logit, the bins' sums meet in the caches (without that 8.9 for 12.4), and the last launch runs on 64 CUs. 256
