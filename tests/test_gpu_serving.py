@@ -346,6 +346,51 @@ def test_sample_strided_and_in_place_outputs(q4):
     check_sample(q4, over, r.random(5), top_p=[0.95] * 5)
 
 
+def test_sample_rows_far_apart(q4):
+    """Rows whose offsets pass 32 bits, in bytes and in elements."""
+    import torch
+
+    r = np.random.default_rng(11)
+    apart = (1 << 31) + 17
+    for n in (3000, 40001):
+        memory = torch.empty(2 * apart + n, dtype=torch.float16, device="cuda")
+        x = memory.as_strided((3, n), (apart, 1))
+        x.copy_(2 * torch.randn(3, n, device="cuda"))
+        check_sample(q4, x, r.random(3), top_k=[0, 30, 0], top_p=[1.0, 0.9, 0.8])
+        del memory, x
+
+
+def test_workspaces(q4):
+    """A workspace holds anything on entry; more rows' serves fewer; one too small is refused."""
+    import torch
+
+    x, u = 2 * torch.randn(50, 20000, device="cuda"), torch.rand(50, device="cuda")
+    p, k = torch.full((50,), 0.9, device="cuda"), torch.full((50,), 300, dtype=torch.int32, device="cuda")
+    ws = torch.full((q4.sample_workspace_bytes(50, 20000),), 0xA5, dtype=torch.uint8, device="cuda")
+    want = q4.sample(x, u, None, k, p)
+    for rows in (50, 33, 32, 7):
+        for fill in (0xFF, 0x7F, 0):
+            ws.fill_(fill)
+            got = q4.sample(x[:rows], u[:rows], None, k[:rows], p[:rows], workspace=ws)
+            assert torch.equal(got[0], want[0][:rows]) and torch.equal(got[1], want[1][:rows])
+    with pytest.raises(q4.Q4Error):
+        q4.sample(x[:32], u[:32], workspace=ws[:1024])
+    seqs, new = 5, 500
+    lens = torch.tensor([0, 40, 16, 5, 300], dtype=torch.int32, device="cuda")
+    news = torch.full((seqs,), new, dtype=torch.int32, device="cuda")
+
+    def plan(**kw):
+        table = torch.arange(seqs * 60, dtype=torch.int32, device="cuda").view(seqs, 60)
+        return q4.paged_plan(lens, news, table, 16, seqs * new, pages=seqs * 60, **kw)
+
+    want = plan()
+    for fill in (-1, 2 ** 31 - 1, 0):
+        got = plan(workspace=torch.full((2 * seqs + 2,), fill, dtype=torch.int32, device="cuda"))
+        assert all(torch.equal(getattr(got, f), getattr(want, f)) for f in ("q_offsets", "positions", "slots", "kv_lens"))
+    with pytest.raises(q4.Q4Error):
+        plan(workspace=torch.zeros(2 * seqs + 1, dtype=torch.int32, device="cuda"))
+
+
 def test_sample_distribution(q4):
     """Equally spaced uniforms meet each token as often as its share says, to one draw."""
     import torch
