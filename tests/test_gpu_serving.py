@@ -309,6 +309,41 @@ def test_sample_masked_and_not_finite(q4):
     check_sample(q4, to_gpu(h), [0.5, 0.5])
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+@pytest.mark.parametrize("vocab", [300, 17000])
+def test_sample_spreads_beyond_float32(q4, dtype, vocab):
+    """Finite logits that lie further apart than float32 reaches have weight where the temperature is as large, or
+    infinite: every cut counts them."""
+    import torch
+
+    say("sample, spread logits", dtype, vocab)
+    inf = np.inf
+    r = np.random.default_rng(12)
+    top = float(torch.finfo(getattr(torch, dtype)).max)
+    x = np.full((10, vocab), -inf, np.float32)
+    x[0, [1, vocab - 1]] = [top, -top]
+    x[1, [1, vocab - 1]] = [-top, top]
+    x[2, ::3], x[2, 1::3] = top, -top
+    x[3, 5:9] = [top, -top, -top, 0.0]
+    x[4] = top * r.uniform(-1, 1, vocab)
+    x[5] = top * r.choice([-1.0, -0.5, 0.0, 0.5, 1.0], vocab)
+    x[6] = -top
+    x[6, 77] = top
+    x[7, 200:] = top * r.uniform(-1, 0, vocab - 200)
+    x[7, 3] = top
+    x[8] = 1e31 * r.standard_normal(vocab)
+    x[8, 9] = top
+    x[9, [2, 4]] = [inf, top]
+    x = to_gpu(x).to(getattr(torch, dtype))
+    u = np.array([0.95, 0.03, 0.61, 0.7, 0.33, 0.88, 0.52, 0.47, 0.99, 0.2])
+    for t in (inf, 3e38, 1e38, 2e37):
+        for settings in ({}, dict(top_k=[3] * 10), dict(top_k=[200] * 10), dict(top_p=[0.99] * 10), dict(top_p=[0.3] * 10),
+                         dict(min_p=[0.05] * 10), dict(top_k=[150] * 10, top_p=[0.8] * 10, min_p=[0.01] * 10)):
+            check_sample(q4, x, u, (t, settings), temperature=[t] * 10, **settings)
+    tokens, _ = check_sample(q4, x[:1], [0.95], temperature=[3e38], top_p=[0.99])
+    assert tokens[0] == vocab - 1
+
+
 def test_sample_settings_out_of_range(q4):
     r = np.random.default_rng(3)
     inf, nan = np.inf, np.nan

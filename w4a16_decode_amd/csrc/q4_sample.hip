@@ -165,7 +165,7 @@ struct Row {
   double top;    // largest logit
   double slope;  // log2(e) / temperature; greedy: so steep that nothing below the largest has weight
   double shift;
-  float bin_top, bin_slope;  // bins a step of the logit
+  float half_top, bin_slope;  // half the largest logit, bins a half step of the logit
   int index_bits;            // of a key
   int k;  // 0: no top-k
   bool infinite;  // the largest logit is: those count as 0, all others as -infinity
@@ -183,8 +183,8 @@ __device__ __forceinline__ Row row_settings(const SampleArgs& a, int row, float 
   r.greedy = !(t > 0.0f);
   r.slope = r.greedy ? 1e300 : 1.4426950408889634 / (double)t;
   r.shift = (double)a.shift;
-  r.bin_top = (float)r.top;
-  r.bin_slope = (float)__builtin_fmin(r.slope * kBins / (a.shift + 2), 1e38);
+  r.half_top = (float)r.top * 0.5f;
+  r.bin_slope = (float)__builtin_fmin(r.slope * (2 * kBins) / (a.shift + 2), 1e38);
   r.index_bits = 32 - __builtin_clz((unsigned)(a.vocab - 1) | 1u);
   r.k = a.top_k ? a.top_k[row] : 0;
   if (r.greedy || r.k < 0 || r.k >= a.vocab) r.k = 0;
@@ -233,10 +233,12 @@ __device__ __forceinline__ void fill_table(double* table) {
   if (N == 256 || threadIdx.x < 256) table[threadIdx.x] = exp2((double)threadIdx.x / 256);
 }
 // The weight's binades below the largest one's, shift + 2 of them in kBins bins. In float32, as all that is asked
-// of it is that it grows with the rank; tokens of the last bin have no weight.
+// of it is that it grows with the rank; tokens of the last bin have no weight. The difference is taken of halves:
+// finite logits may lie up to twice float32's largest number apart and still have weight, at a temperature as large.
+// (-infinity goes to the last bin also where an infinite temperature makes its product a NaN.)
 constexpr int kNoBin = kBins - 1;
 __device__ __forceinline__ int bin_of(const Row& r, float v) {
-  return (int)fminf((r.bin_top - v) * r.bin_slope, (float)kNoBin);
+  return (int)fminf(__builtin_fmaf(v, -0.5f, r.half_top) * r.bin_slope, (float)kNoBin);
 }
 
 // ---- cuts -----------------------------------------------------------------------------
