@@ -74,10 +74,12 @@ q4_status q4_paged_plan(const int32_t* kv_lens, const int32_t* new_lens, const i
  *   temperature, top_p, min_p: float32 [rows], top_k: int32 [rows], each NULL: 1, 1, 0, all.
  *   tokens: int32 [rows]; probs: float32 [rows] or NULL, the chosen token's w over the total
  *   of those that stayed.
- * Differences are taken in float64 and weights kept in fixed point, 2^-min(50, 62 -
- * ceil(log2(vocab))) of the largest a step (2^-45 for 131072 tokens), so that sums are exact
- * in any order and the choice is that of 64-bit arithmetic but where u * total or a cut
- * comes within about 1e-12 of a border; a token whose weight rounds to 0 is never drawn.
+ * Differences are taken in float64 and weights kept in fixed point, 2^-s of the largest a
+ * step, s = min(50, 62 - ceil(log2(vocab))) (45 for 131072 tokens), so that sums are exact
+ * in any order. A weight is off by half a step at most, so the choice is that of exact
+ * arithmetic but where u * total or a cut comes within vocab * 2^-(s + 1) of the largest weight
+ * (2e-12 for 4096 tokens, 2e-9 for 131072, 1.2e-7, two steps of a float32 u, for 2^20) and
+ * 2^-47 of the sum of a border; a token whose weight rounds to 0 is never drawn.
  * Deterministic. vocab <= 2^20, rows < 2^22, rows *
  * ceil(vocab / 4096) < 2^24 (Q4_ERR_SHAPE). `workspace` (16-byte aligned) must hold
  * q4_sample_workspace_bytes() bytes (NULL when that is 0), which serve fewer rows too. */

@@ -309,6 +309,33 @@ def test_sample_masked_and_not_finite(q4):
     check_sample(q4, to_gpu(h), [0.5, 0.5])
 
 
+@pytest.mark.parametrize("vocab", [4096, 32000, 50257, 131072, 1 << 20])
+@pytest.mark.parametrize("steps", [0.49, 1.49, 77.3, 1e6])
+def test_sample_flat_tails(q4, vocab, steps):
+    """One peak and a flat tail of `steps` weight steps each, all rounded the same way: the worst that the fixed point
+    does to a sum. The token drawn holds u * total up to vocab * 2^-(s + 1) of the peak's weight and 2^-47 of the total."""
+    say("sample, flat tail", vocab, steps)
+    s = min(50, 62 - int(np.ceil(np.log2(vocab))))
+    x = np.full(vocab, np.log(steps * 2.0 ** -s), np.float32)
+    x[5] = 0.0
+    w = np.exp(x.astype(np.longdouble))
+    upto, n = np.cumsum(w), 400
+    total = upto[-1]
+    r = np.random.default_rng(vocab)
+    # draws at the tail: one u in 2^-24 of the range reaches it where it is light
+    reach = min(1.0, 1.5 * float(total - 1) + 2.0 ** -23)
+    u = np.concatenate([1 - 2.0 ** -24 * np.arange(1, 5), 1 - r.random(n - 4) * reach]).astype(np.float32)
+    u = np.minimum(u, np.float32(1 - 2.0 ** -24))
+    tokens, _ = q4.sample(to_gpu(x[None]).expand(n, vocab), to_gpu(u))
+    tokens = to_np(tokens)
+    want = u.astype(np.longdouble) * total
+    bound = vocab * 2.0 ** -(s + 1) + 2.0 ** -47 * total
+    assert np.all((tokens >= 0) & (tokens < vocab))
+    over, under = want - upto[tokens], upto[tokens] - w[tokens] - want
+    say("  worst share of the bound", max(over.max(), under.max()) / bound, "tokens off the peak", int((tokens != 5).sum()))
+    assert np.all(over <= bound) and np.all(under <= bound), (over.max(), under.max(), bound)
+
+
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
 @pytest.mark.parametrize("vocab", [300, 17000])
 def test_sample_spreads_beyond_float32(q4, dtype, vocab):
