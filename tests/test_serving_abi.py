@@ -145,6 +145,23 @@ def test_shared_attention_refusals(lib):
     assert w(3, 2, 3, 1, 100, 3, 100, 4, 2, 96, 32) == 0 and w(3, 2, 3, 1, 100, 3, 100, 3, 2, 128, 128) == 0
 
 
+def test_shared_attention_own_keys_grid(lib):
+    """More than 256 rows of a group, own keys of 513 to 4096: a workgroup a sequence, tile and head over those, which
+    are refused from 2^24 on (2^32 threads) before anything is launched."""
+    import ctypes
+
+    w = lib.q4_paged_attention_shared_workspace_bytes
+    cache = ctypes.byref(_lib.PagedKV(FAKE, FAKE, FAKE, FAKE, 4, 32, 8, 128, 128))
+    for seqs, max_q, max_kv, fits in ((1 << 21, 1, 1000, False), (1 << 21, 2, 4096, False), ((1 << 21) - 1, 2, 4096, True),
+                                      (1 << 20, 3, 1000, True), (1 << 22, 1, 513, False), (1 << 21, 1, 4097, True)):
+        need = w(seqs, 1, seqs, max_q, max_kv, 64, 100, 64, 8, 128, 128)
+        assert (need > 0) == fits, (seqs, max_q, max_kv, need)
+        # without a workspace no call gets as far as a launch: its sizes are refused (2), or its workspace (6)
+        st = lib.q4_paged_attention_shared(FAKE, 8192, cache, FAKE, 4, FAKE, FAKE, 1, FAKE, 4, FAKE, FAKE, seqs, seqs, max_q,
+                                           max_kv, 64, 100, 64, 0.1, FAKE, None, 0, None)
+        assert st == (6 if fits else 2), (seqs, max_q, max_kv, st)
+
+
 def test_oracle_shared_attention():
     """One row, prefix of one key, one key of its own: equal scores average the two; no key is zero."""
     q = np.zeros((3, 1, 2))

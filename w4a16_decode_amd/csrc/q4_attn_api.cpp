@@ -271,7 +271,11 @@ q4_status pick_shared(int64_t groups, int64_t max_group_q, int64_t max_prefix, q
       return fail(Q4_ERR_SHAPE, "seqs * heads * max_q too large for one call");
     return Q4_OK;
   }
-  if (a->max_kv <= 4096) a->shares = 0;
+  if (a->max_kv <= 4096 && a->shares > 0) {  // then a workgroup a tile, which pick_attn has not counted
+    a->shares = 0;
+    if ((own_rows + a->rows_group - 1) / a->rows_group * heads * a->seqs > kMaxGroups256)
+      return fail(Q4_ERR_SHAPE, "seqs * heads * max_q too large for one call");
+  }
   const int64_t jobs = (rows + 127) / 128 * heads * groups;
   const int64_t slots = q4::prefix_attention_resident(d, g, 128);
   const int64_t pieces = std::max<int64_t>(1, std::min(slots / jobs, (max_prefix + 255) / 256));
