@@ -162,6 +162,18 @@ def test_shared_attention_own_keys_grid(lib):
         assert st == (6 if fits else 2), (seqs, max_q, max_kv, st)
 
 
+def test_shared_attention_line_grid(lib):
+    """Whole jobs and the pieces of the cut ones together are one grid: 419430 sequences of up to 80 rows of 8 heads a KV
+    head are 16777200 jobs, so that any cut among them (a tenth of a round's jobs at least, into two pieces or more)
+    makes 2^24 workgroups or more, which are refused: no workspace. Without a cut none is needed."""
+    w = lib.q4_paged_attention_shared_workspace_bytes
+    seqs = 419430
+    for tokens in range(1 << 24, (1 << 24) + 20000, 97):
+        assert w(seqs, 1, tokens, 80, 2000, 90, 6000, 64, 8, 128, 128) == 0, tokens
+    few = [w(1000, 1, tokens, 80, 2000, 90, 6000, 64, 8, 128, 128) for tokens in range(40000, 60000, 97)]
+    assert any(n > 0 for n in few)
+
+
 def test_oracle_shared_attention():
     """One row, prefix of one key, one key of its own: equal scores average the two; no key is zero."""
     q = np.zeros((3, 1, 2))

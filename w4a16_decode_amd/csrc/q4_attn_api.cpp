@@ -267,7 +267,8 @@ q4_status pick_shared(int64_t groups, int64_t max_group_q, int64_t max_prefix, q
     a->tail = pieces > 1 ? (int)std::min<int64_t>(rest * jobs / full, kMaxDim) : 0;
     a->pieces = pieces > 1 ? (int)pieces : 0;
     a->whole = (int)std::min(jobs - a->tail, kMaxDim);
-    if (jobs > kMaxGroups256 || a->tail * (int64_t)std::max(a->pieces, 32) > kMaxGroups256)
+    if (jobs > kMaxGroups256 || a->whole + a->tail * (int64_t)a->pieces > kMaxGroups256 ||
+        a->tail * int64_t(32) > kMaxGroups256)
       return fail(Q4_ERR_SHAPE, "seqs * heads * max_q too large for one call");
     return Q4_OK;
   }
