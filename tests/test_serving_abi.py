@@ -174,6 +174,17 @@ def test_shared_attention_line_grid(lib):
     assert any(n > 0 for n in few)
 
 
+def test_shared_attention_mixed_batch(lib):
+    """A chunk beside single tokens behind one prefix: the workspace holds what the group's rows have seen of the prefix,
+    which is read once for all of them (and not cut jobs of sequences that read it each by itself)."""
+    w = lib.q4_paged_attention_shared_workspace_bytes
+    for chunks, new in ((1, 80), (1, 512), (4, 512), (8, 100)):
+        tokens = chunks * new + 64 - chunks
+        rows = 8 * 8 * tokens * 130 * 4
+        need = w(64, 1, tokens, new, new + 300, tokens, 8190, 64, 8, 128, 128)
+        assert rows <= need <= 3 * rows + (16 << 20), (chunks, new, need, rows)
+
+
 def test_oracle_shared_attention():
     """One row, prefix of one key, one key of its own: equal scores average the two; no key is zero."""
     q = np.zeros((3, 1, 2))
