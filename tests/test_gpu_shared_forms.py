@@ -388,3 +388,13 @@ def test_mixed_batches(q4):
         for lead, sizes in ((0, [len(news)]), (1, [len(news) - 3]), (2, [20, len(news) - 22])):
             b = Shared(q4, sizes, [777, 130][:len(sizes)], lens, news, 16, 2, 128, 64, 32, seed=21 + lead, lead=lead)
             say("shared, mixed", len(news), lead, check(b, b.run()))
+
+
+@pytest.mark.parametrize("prompts", [[1100], [200], [300, 1, 40, 800], [17, 1100]])
+def test_prompts_beside_a_group(q4, prompts):
+    """Prompts in no group beside few rows behind a prefix, long and short ones."""
+    news = prompts + [1] * 8
+    lens = [n + 3 * i for i, n in enumerate(news)]
+    for sizes, prefix in (([8], [900]), ([3, 5], [70, 411])):
+        b = Shared(q4, sizes, prefix, lens, news, 32, 2, 128, 128, 16, seed=30, lead=len(prompts))
+        say("shared, prompts beside a group", prompts, sizes, check(b, b.run()))

@@ -185,6 +185,14 @@ def test_shared_attention_mixed_batch(lib):
         assert rows <= need <= 3 * rows + (16 << 20), (chunks, new, need, rows)
 
 
+def test_shared_attention_prompt_beside_a_group(lib):
+    """A prompt in no group beside a few rows behind a prefix: no partial results of the prompt's rows for each piece of
+    its keys (133 MB a piece here), only of what the last round of the chip is cut into."""
+    w = lib.q4_paged_attention_shared_workspace_bytes
+    need = w(9, 1, 4008, 4000, 4000, 8, 8190, 64, 8, 128, 128)
+    assert 8 * 64 * 130 * 4 <= need < 4008 * 64 * 130 * 4
+
+
 def test_oracle_shared_attention():
     """One row, prefix of one key, one key of its own: equal scores average the two; no key is zero."""
     q = np.zeros((3, 1, 2))

@@ -220,8 +220,11 @@ bool has_prefix(int64_t groups, int64_t tokens, int64_t max_group_q, int64_t max
 //     behind 4000 keys, 64 heads over 8: 42 -> 20 us against prefixes first and own keys from there;
 //     of 256 rows behind 8000 keys 40 -> 33, of 512 57 -> 67). Counted are the tiles that the call's rows can
 //     fill at most, not those that the bounds allow: empty ones end at once (five groups of 41 rows in all,
-//     bound 26: 50 us when the bounds' were counted).
-//   More, and 640 or more of a sequence: its rows fill tiles by themselves, so prefix and own keys are walked as
+//     bound 26: 50 us when the bounds' were counted). Not for long sequences outside the groups that are
+//     eight tiles a CU and more, each of which would convert the same codes and leave partial results (8 rows
+//     behind 8190 keys beside a prompt of 320, 640, 4000 tokens, this form / prefixes first: 80 / 100, 129 / 115,
+//     971 / 441 us; 32 rows in 8 groups beside 8 prompts of 40, 80, 640: 57 / 53, 96 / 54, 634 / 159).
+//   Else, 640 or more of a sequence: its rows fill tiles by themselves, so prefix and own keys are walked as
 //     one line of keys, 128 rows a workgroup; jobs that do not fill the chip a whole number of times are
 //     cut and joined (nine chunks of up to 251 rows behind 6001 keys: 552 us with the prefix first). Only where
 //     the sequences have a third of max_q rows each on average: a line reads its prefix by itself, for
@@ -236,7 +239,8 @@ q4_status pick_shared(int64_t groups, int64_t max_group_q, int64_t max_prefix, q
   const int heads = a->cache.kv_heads, share = a->q_heads / heads, d = a->cache.head_dim, g = a->cache.group;
   a->groups = (int)groups, a->max_group_q = (int)std::min<int64_t>(max_group_q, a->tokens), a->max_prefix = (int)max_prefix;
   const int64_t rows = (int64_t)a->max_group_q * share, own_rows = (int64_t)a->max_q * share;
-  if (rows <= 256) {
+  const bool prompts = own_rows > 256 && (int64_t)a->tokens * a->q_heads / 16 > 8 * q4::device_cu_count_cached();
+  if (rows <= 256 && !prompts) {
     a->rows_group = 16, a->shares = 0, a->whole = 0, a->tail = 0, a->pieces = 0;
     const int64_t tiles = (rows + 15) / 16, own = (own_rows + 15) / 16 * heads * a->seqs;
     const int64_t filled = (int64_t)a->tokens * share / 16;
