@@ -82,7 +82,9 @@ q4_status q4_paged_plan(const int32_t* kv_lens, const int32_t* new_lens, const i
  * 2^-47 of the sum of a border; a token whose weight rounds to 0 is never drawn.
  * Deterministic. vocab <= 2^20, rows < 2^22, rows *
  * ceil(vocab / 4096) < 2^24 (Q4_ERR_SHAPE). `workspace` (16-byte aligned) must hold
- * q4_sample_workspace_bytes() bytes (NULL when that is 0), which serve fewer rows too. */
+ * q4_sample_workspace_bytes() bytes (NULL when that is 0), which serve fewer rows too: where rows are split (above
+ * 32768 logits, or above 16384 for up to 32 rows) 8 bytes a logit for the tokens that a cut may list, with or without
+ * cuts, and some more (67 MB for 64 rows of 128256), else none. */
 typedef enum { Q4_F16 = 0, Q4_BF16 = 1, Q4_F32 = 2 } q4_dtype;
 
 size_t q4_sample_workspace_bytes(int64_t rows, int64_t vocab);

@@ -5,10 +5,13 @@ Bound of an output's error, from the arithmetic. With A = sum_t p_t |v_t| (p the
 prefix and own keys), Z = max_t sum_c |q_c k_tc| * scale:
  - weights, scores, sums and the last rounding as in attention without a prefix: 2^-11 A,
    2 (D / 32 + 8) 2^-23 (Z + 1) A, 2 (n / 32 + 32) 2^-24 A, 2^-11 |o|;
- - the prefix's output is divided by its sum and scaled again (4 roundings of 2^-24), and enters
-   with the weight 2^m, m = log2 of its sum relative to the scores' zero: |m| <= 1.45 Z + 64 (the
-   sum's own reference is at most 14 + 12 + 15 binades from the largest score, and there are
-   below 2^20 keys), three times rounded in float32: 3 * 2^-24 (1.45 Z + 64) of a weight.
+ - the parts of a row's keys (the prefix's pieces, the own keys') hold the reference m of their exponents in
+   float32, |m| <= 1.45 Z + 64 (at most 14 + 12 + 15 binades from the largest score, and there are below 2^20
+   keys), and are added up with 2^(difference): two references and their difference, rounded once each,
+   3 * 2^-24 (1.45 Z + 64) of a weight, and 4 products of 2^-24.
+
+Groups of up to 256 rows a KV head, most of the cases here, go through tiles of 16 rows; test_gpu_shared_forms.py has
+the other forms.
 """
 
 import numpy as np
@@ -309,7 +312,7 @@ def test_infinite_scores(q4):
     r = np.random.default_rng(12)
     for at_prefix, at_own in ((one, zero), (zero, one), (one, one), (zero, zero)):
         for sign in (-1.0, 1.0):
-            for new in (1, 9):                                    # 16- and 32-row tiles behind the prefix
+            for new in (1, 9):                                    # one tile of 16 rows and several
                 b = Shared(q4, [2], [40], [40, 40], [new, new], hq, hkv, d, 64, page, seed=13)
                 b.q[:] = 60000.0
                 v = [r.standard_normal((40, hkv, d)).astype(np.float16) for _ in range(3)]

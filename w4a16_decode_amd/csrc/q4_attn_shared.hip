@@ -12,11 +12,12 @@
 //           attention of q4_paged_attention over the own keys, whose rows start from the sum of
 //           those pieces as if they had seen the prefix's keys already;
 //   line    many rows of each sequence: 128-row workgroups that walk prefix and own keys as one line.
-// Bound by the vector work beside the matrix products, as attention without prefixes is. 64 rows behind 8190 keys,
-// 64 heads over 8 of 128 channels: 38 + 17 us, the prefix at 450 TFLOP/s and 14.4 vector instructions a product; its
-// 512 rows a head are 32 tiles, which fill the chip in eight pieces of 1024 keys. Nine chunks of up to
-// 251 rows behind two prefixes of up to 6001 keys: 484 us in a graph, 650 TFLOP/s. 8 rows behind 1003 keys: 11 us,
-// two launches' latency.
+// 64 rows behind 8190 keys, 64 heads over 8 of 128 channels: 38 + 17 us, the prefix at 450 TFLOP/s; its
+// 512 rows a head are 32 tiles, which fill the chip in eight pieces of 1024 keys. No unit is full meanwhile: with 14.4
+// vector instructions a product the vector units issue 40 to 46 % of the time and the matrix units work 21 %. The two
+// wavefronts a SIMD wait for each other's barrier and for their own chains (products, maximum, exponentials,
+// products); behind the prefix vector work is 30 % and the rest latency. Nine chunks of up to 251 rows behind two
+// prefixes of up to 6001 keys: 484 to 496 us, 650 TFLOP/s. 8 rows behind 1003 keys: 11 us, two launches' latency.
 #include "q4_attn_kernels.h"
 
 namespace q4 {
