@@ -154,8 +154,8 @@ q4_status q4_paged_attention(const void* q, int64_t q_stride, const q4_paged_kv*
 
 /* Attention of requests that share long prefixes (a system prompt, a document), each prefix
  * stored once and read once for all rows behind it (for each sequence's by themselves where the
- * sequences have 640 or more of a KV head's rows and are of like sizes, at least a third of max_q on
- * average): q4_paged_attention, without a window, of sequences whose first keys are their group's prefix. Sequences group_offsets[g] ..
+ * sequences have 640 or more of a KV head's rows and are of like sizes, at least a third of max_q tokens or
+ * 2048 rows on average): q4_paged_attention, without a window, of sequences whose first keys are their group's prefix. Sequences group_offsets[g] ..
  * group_offsets[g + 1] - 1 (int32 [groups + 1], ascending) are group g's; token t <
  * prefix_lens[g] (int32 [groups]) of its prefix lies in page prefix_table[g][t / page_size]
  * (int32 [groups][max_prefix_blocks]). Every row of the group sees all of them, and its own

@@ -193,6 +193,17 @@ def test_shared_attention_prompt_beside_a_group(lib):
     assert 8 * 64 * 130 * 4 <= need < 4008 * 64 * 130 * 4
 
 
+def test_shared_attention_loose_bounds(lib):
+    """Long chunks of like sizes under a loose max_q stay lines of keys: at most a round's jobs are cut, and no partial
+    results of all rows over the prefix are left. Long prompts outside the groups make no lines."""
+    w = lib.q4_paged_attention_shared_workspace_bytes
+    for new, max_q in ((300, 300), (300, 2400), (1500, 6000)):
+        rows = 8 * 8 * 7 * new * 130 * 4
+        assert w(7, 1, 7 * new, max_q, 100, 7 * new, 300, 64, 8, 128, 128) < rows, (new, max_q)
+    rows = 8 * 8 * 40 * 130 * 4
+    assert w(6, 1, 4 * 4000 + 40, 4000, 4000, 40, 300, 64, 8, 128, 128) >= rows
+
+
 def test_oracle_shared_attention():
     """One row, prefix of one key, one key of its own: equal scores average the two; no key is zero."""
     q = np.zeros((3, 1, 2))

@@ -226,11 +226,14 @@ bool has_prefix(int64_t groups, int64_t tokens, int64_t max_group_q, int64_t max
 //     971 / 441 us; 32 rows in 8 groups beside 8 prompts of 40, 80, 640: 57 / 53, 96 / 54, 634 / 159).
 //   Else, 640 or more of a sequence: its rows fill tiles by themselves, so prefix and own keys are walked as
 //     one line of keys, 128 rows a workgroup; jobs that do not fill the chip a whole number of times are
-//     cut and joined (nine chunks of up to 251 rows behind 6001 keys: 552 us with the prefix first). Only where
-//     the sequences have a third of max_q rows each on average: a line reads its prefix by itself, for
-//     one row as for 128. Of 64 sequences behind 8190 keys, lines / prefix first, us: 1 chunk of 512 tokens
-//     and 63 single ones 1302 / 465; 16 and 48 3723 / 3381; 32 and 32 6120 / 6493; 64 chunks of 100 2277 / 2553, 32
-//     and 32 single tokens 1382 / 1370.
+//     cut and joined (nine chunks of up to 251 rows behind 6001 keys: 552 us with the prefix first). A line reads its
+//     prefix by itself, for one row as for 128, so only where the sequences have a third of max_q tokens each on
+//     average, or 2048 rows (max_q may be a loose bound), and none longer than a group's lies outside the groups. Lines /
+//     prefix first, us: behind 8190 keys 1 chunk of 512 tokens and 63 single ones 1302 / 465; 16 and 48 (1030 rows on
+//     average) 3723 / 3381; 32 and 32 6120 / 6493; 64 chunks of 100 2277 / 2553, 32 and 32 single tokens 1382 /
+//     1370; 1 of 4000 and 8 single (3562 rows) 1770 / 1856; behind 4000 1 of 2000 and 8 (1784) 628 / 505, 2 and 8 (3206)
+//     918 / 976; 8 prompts of 640 in no group beside 32 single tokens 319 / 159. With max_q eight times the chunks'
+//     length: 5 of 150 262 / 230, 64 of 100 782 / 880, 6 of 300 (2400) 390 / 446.
 //   Else: 128-row workgroups over the prefixes, cut until they fill the chip, and the rows behind start
 //     from those pieces. There a workgroup takes all of a row's own keys up to 4096 (64 rows behind 8190
 //     keys, own keys up to 513: 75 us with equal shares of them and a join, 57 so; up to 2000: 90, 69).
@@ -262,7 +265,9 @@ q4_status pick_shared(int64_t groups, int64_t max_group_q, int64_t max_prefix, q
     return Q4_OK;
   }
   a->own_pieces = 0;
-  if (own_rows >= 640 && 3 * (int64_t)a->tokens >= (int64_t)a->seqs * a->max_q) {
+  const bool alike = 3 * (int64_t)a->tokens >= (int64_t)a->seqs * a->max_q ||
+                     (int64_t)a->tokens * share >= 2048 * (int64_t)a->seqs;
+  if (own_rows >= 640 && alike && a->max_group_q >= a->max_q) {
     const int64_t jobs = (own_rows + 127) / 128 * heads * a->seqs, slots = q4::line_attention_resident(d, g);
     // of these the call's rows fill about so many; the last round's share of them is cut, and a tenth of a round
     // more, so that no whole job is left for it where the lengths are ragged (9 chunks of up to 251 tokens behind 6001
